@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn.so")
@@ -24,6 +25,7 @@ EXPORTS = (
     "gdn_replay_decode", "gdn_replay_decode_noalloc",
     "gdn_replay_flush", "gdn_replay_rollback", "gdn_replay_decode_dual", "gdn_replay_flush_dual",
     "gdn_mamba2_decode_step", "gdn_mamba2_replay_decode", "gdn_mamba2_replay_flush", "gdn_mamba2_replay_rollback",
+    "gdn_layer_norm", "gdn_layer_norm_backward_workspace_bytes", "gdn_layer_norm_backward",
     "gdn_status_string", "gdn_last_error",
 )
 
@@ -68,6 +70,11 @@ class gdn_ring(ctypes.Structure):
                 ("L", ctypes.c_int32), ("dtype", ctypes.c_int)]
 
 
+class gdn_norm_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("groups", ctypes.c_int32), ("rms", ctypes.c_int32),
+                ("gate", ctypes.c_int)]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{message} [status {status}]")
@@ -86,6 +93,7 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m gated_deltanet_state_gdn_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ, INT = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    F32, pn = ctypes.c_float, ctypes.POINTER(gdn_norm_dims)
     pd, pg, pp, pr = (ctypes.POINTER(gdn_dims), ctypes.POINTER(gdn_gates), ctypes.POINTER(gdn_pool),
                       ctypes.POINTER(gdn_ring))
     pm, pmp, pmr = ctypes.POINTER(gdn_m2_dims), ctypes.POINTER(gdn_m2_params), ctypes.POINTER(gdn_m2_ring)
@@ -106,6 +114,9 @@ def lib() -> ctypes.CDLL:
         "gdn_mamba2_replay_decode": (INT, [pm, I32, I32, P, P, P, INT, pmp, pp, P, pmr, P, INT, P]),
         "gdn_mamba2_replay_flush": (INT, [pm, I32, pp, P, pmr, P]),
         "gdn_mamba2_replay_rollback": (INT, [pm, I32, P, P, pmr, P]),
+        "gdn_layer_norm": (INT, [pn, P, I64, P, I64, INT, P, P, F32, P, I64, INT, P, P, P]),
+        "gdn_layer_norm_backward_workspace_bytes": (SZ, [pn]),
+        "gdn_layer_norm_backward": (INT, [pn, P, I64, P, I64, P, I64, INT, P, P, P, P, P, I64, P, I64, P, P, P, SZ, P]),
         "gdn_status_string": (ctypes.c_char_p, [INT]),
         "gdn_last_error": (ctypes.c_char_p, []),
     }
@@ -473,3 +484,92 @@ def gdn_mamba2_replay_rollback(slot_map, num_rejected, ring: M2Ring, stream=None
     rs = ring.c_struct()
     _check(lib().gdn_mamba2_replay_rollback(ctypes.byref(dims), int(slot_map.shape[0]), _ptr(slot_map),
                                             _ptr(num_rejected), ctypes.byref(rs), _stream(stream)))
+
+
+# ------------------------------------------------------------------ norm
+class LayerNormGrads(NamedTuple):
+    """Gradients of gdn_layer_norm; dbias and dgate are None where the call had no bias or gate."""
+    dx: object
+    dweight: object  # float32 [width]
+    dbias: object    # float32 [width] or None
+    dgate: object
+
+
+def _f32(t, shape, what):
+    """A float32 parameter or statistic of the given shape, or None."""
+    if t is not None and (t.dtype != _torch().float32 or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what} must be float32 of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _rows(t, shape, dtype, what):
+    """(pointer, row stride) of a [rows, width] tensor whose rows may be apart."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the values of a row must be consecutive")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _norm_dims(x, groups, rms, gate, gate_after):
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, width]")
+    return gdn_norm_dims(int(x.shape[0]), int(x.shape[1]), int(groups), int(bool(rms)),
+                         0 if gate is None else 2 if gate_after else 1)
+
+
+def gdn_layer_norm(x, weight, bias=None, gate=None, groups=1, eps=1e-5, rms=False, gate_after=False, out=None,
+                   out_dtype=None, save_stats=False, stream=None):
+    """Layer (or RMS) norm of the `groups` slices of every row of x [rows, width], with an optional SiLU gate of
+    x's shape and dtype applied to x (or, gate_after, to the result); weight, bias float32 [width].  Rows may be
+    apart (x.stride(0)).  Returns y in out_dtype (x's by default), or (y, mean, rstd) with save_stats, float32
+    [rows, groups] for gdn_layer_norm_backward."""
+    torch = _torch()
+    dims = _norm_dims(x, groups, rms, gate, gate_after)
+    _f32(weight, x.shape[1:], "weight"), _f32(bias, x.shape[1:], "bias")
+    fresh = []
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        fresh.append(out)
+    mean = rstd = None
+    if save_stats:
+        mean, rstd = (torch.empty((x.shape[0], groups), dtype=torch.float32, device=x.device) for _ in range(2))
+        fresh += [mean, rstd]
+    _keep_for_stream(fresh, stream)
+    _check(lib().gdn_layer_norm(ctypes.byref(dims), *_rows(x, x.shape, x.dtype, "x"),
+                                *_rows(gate, x.shape, x.dtype, "gate"), dtype_code(x.dtype), _ptr(weight),
+                                _ptr(bias) if bias is not None else None, float(eps),
+                                *_rows(out, x.shape, out.dtype, "out"), dtype_code(out.dtype),
+                                _ptr(mean) if save_stats else None, _ptr(rstd) if save_stats else None,
+                                _stream(stream)))
+    return (out, mean, rstd) if save_stats else out
+
+
+def gdn_layer_norm_backward(dy, x, weight, mean, rstd, bias=None, gate=None, groups=1, rms=False, gate_after=False,
+                            workspace=None, stream=None) -> LayerNormGrads:
+    """Gradients of gdn_layer_norm for dy [rows, width] in x's dtype, from the forward call's inputs and the
+    mean and rstd that it saved.  dbias is computed when `bias` is given."""
+    torch = _torch()
+    dims = _norm_dims(x, groups, rms, gate, gate_after)
+    _f32(weight, x.shape[1:], "weight"), _f32(bias, x.shape[1:], "bias")
+    _f32(mean, (x.shape[0], groups), "mean"), _f32(rstd, (x.shape[0], groups), "rstd")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dz = torch.empty(x.shape, dtype=x.dtype, device=x.device) if gate is not None else None
+    dw = torch.empty(x.shape[1:], dtype=torch.float32, device=x.device)
+    db = torch.empty_like(dw) if bias is not None else None
+    fresh = [dx, dz, dw, db]
+    need = int(lib().gdn_layer_norm_backward_workspace_bytes(ctypes.byref(dims)))
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        fresh.append(workspace)
+    _keep_for_stream(fresh, stream)
+    _check(lib().gdn_layer_norm_backward(
+        ctypes.byref(dims), *_rows(dy, x.shape, x.dtype, "dy"), *_rows(x, x.shape, x.dtype, "x"),
+        *_rows(gate, x.shape, x.dtype, "gate"), dtype_code(x.dtype), _ptr(weight),
+        _ptr(bias) if bias is not None else None, _ptr(mean), _ptr(rstd), *_rows(dx, x.shape, x.dtype, "dx"),
+        *_rows(dz, x.shape, x.dtype, "dgate"), _ptr(dw), _ptr(db) if db is not None else None,
+        _ptr(workspace) if workspace is not None else None,
+        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+    return LayerNormGrads(dx, dw, db, dz)

@@ -599,3 +599,119 @@ gdn_status gdn_mamba2_replay_rollback(const gdn_m2_dims* dims, int32_t B, const 
   m2_ring_args(a, ring);
   return launched(gdn::launch_m2_rollback(a, static_cast<hipStream_t>(stream)));
 }
+
+// ------------------------------------------------------------------ norm
+namespace {
+
+gdn_status check_norm_dims(const gdn_norm_dims* d) {
+  GDN_REQUIRE(d != nullptr, GDN_EINVAL, "dims is NULL");
+  GDN_REQUIRE(d->rows >= 0, GDN_EINVAL, "rows=%lld must be >= 0", (long long)d->rows);
+  GDN_REQUIRE(d->width >= 1 && d->groups >= 1, GDN_EINVAL, "width=%d and groups=%d must be >= 1", d->width, d->groups);
+  GDN_REQUIRE(d->width % d->groups == 0, GDN_EINVAL, "width=%d is not a multiple of groups=%d", d->width, d->groups);
+  GDN_REQUIRE(d->gate == GDN_GATE_NONE || d->gate == GDN_GATE_BEFORE || d->gate == GDN_GATE_AFTER, GDN_EINVAL,
+              "gate %d is not a gdn_norm_gate", (int)d->gate);
+  GDN_REQUIRE(d->groups <= 65535, GDN_EUNSUPPORTED, "groups=%d: at most 65535 are supported", d->groups);
+  GDN_REQUIRE(gdn::norm_slice_fits(d->width / d->groups), GDN_EUNSUPPORTED,
+              "slices of %d values: at most 16384 are supported", d->width / d->groups);
+  return GDN_OK;
+}
+
+// A row tensor: present, aligned to its element and with rows that do not overlap.
+gdn_status check_rows(const void* p, int64_t stride, const gdn_norm_dims* d, int dt, const char* what) {
+  GDN_REQUIRE(p != nullptr && aligned(p, dtype_bytes(dt)), GDN_EINVAL, "%s is NULL or misaligned for its dtype", what);
+  GDN_REQUIRE(stride == 0 || stride >= d->width, GDN_EINVAL, "%s row stride %lld is below the width %d", what,
+              (long long)stride, d->width);
+  return GDN_OK;
+}
+
+gdn_status check_norm_io(const gdn_norm_dims* d, const void* x, int64_t xs, const void* z, int64_t zs, int dt,
+                         const float* w, const float* b) {
+  GDN_TRY(check_rows(x, xs, d, dt, "x"));
+  GDN_REQUIRE((z != nullptr) == (d->gate != GDN_GATE_NONE), GDN_EINVAL, "z must be given exactly when there is a gate");
+  if (z != nullptr) GDN_TRY(check_rows(z, zs, d, dt, "z"));
+  GDN_REQUIRE(w != nullptr && aligned(w, 4) && aligned(b, 4), GDN_EINVAL, "w is NULL, or w or b misaligned");
+  return GDN_OK;
+}
+
+int64_t row_stride(int64_t s, const gdn_norm_dims* d) { return s == 0 ? d->width : s; }
+
+gdn::NormArgs norm_args(const gdn_norm_dims* d, const void* x, int64_t xs, const void* z, int64_t zs, int dt,
+                        const float* w, const float* b) {
+  gdn::NormArgs a{};
+  a.x = x;
+  a.z = z;
+  a.w = w;
+  a.b = b;
+  a.rows = d->rows;
+  a.x_stride = row_stride(xs, d);
+  a.z_stride = row_stride(zs, d);
+  a.N = d->width;
+  a.groups = d->groups;
+  a.rms = d->rms != 0;
+  a.gate_after = d->gate == GDN_GATE_AFTER;
+  a.in_dt = dt;
+  return a;
+}
+
+}  // namespace
+
+gdn_status gdn_layer_norm(const gdn_norm_dims* dims, const void* x, int64_t x_stride, const void* z, int64_t z_stride,
+                          gdn_dtype in_dtype, const float* w, const float* b, float eps, void* y, int64_t y_stride,
+                          gdn_dtype out_dtype, float* mean, float* rstd, void* stream) {
+  GDN_TRY(check_norm_dims(dims));
+  GDN_TRY(check_dtypes(in_dtype, out_dtype));
+  GDN_REQUIRE(eps >= 0.f, GDN_EINVAL, "eps must be >= 0");
+  if (dims->rows == 0) return ok();  // nothing is read or written
+  GDN_TRY(check_norm_io(dims, x, x_stride, z, z_stride, in_dtype, w, b));
+  GDN_TRY(check_rows(y, y_stride, dims, out_dtype, "y"));
+  GDN_REQUIRE((mean != nullptr) == (rstd != nullptr) && aligned(mean, 4) && aligned(rstd, 4), GDN_EINVAL,
+              "mean and rstd must both be given or both be NULL, and aligned");
+  gdn::NormArgs a = norm_args(dims, x, x_stride, z, z_stride, in_dtype, w, b);
+  a.y = y;
+  a.y_stride = row_stride(y_stride, dims);
+  a.out_dt = out_dtype;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.eps = eps;
+  return launched(gdn::launch_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_layer_norm_backward_workspace_bytes(const gdn_norm_dims* dims) {
+  if (check_norm_dims(dims) != GDN_OK) return 0;
+  return (size_t)gdn::norm_bwd_blocks(dims->rows, dims->width, dims->groups) * 2 * (size_t)dims->width * sizeof(float);
+}
+
+gdn_status gdn_layer_norm_backward(const gdn_norm_dims* dims, const void* dy, int64_t dy_stride, const void* x,
+                                   int64_t x_stride, const void* z, int64_t z_stride, gdn_dtype in_dtype,
+                                   const float* w, const float* b, const float* mean, const float* rstd, void* dx,
+                                   int64_t dx_stride, void* dz, int64_t dz_stride, float* dw, float* db,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  GDN_TRY(check_norm_dims(dims));
+  GDN_TRY(check_dtypes(in_dtype, in_dtype));
+  GDN_REQUIRE(dw != nullptr && aligned(dw, 4) && aligned(db, 4), GDN_EINVAL, "dw is NULL, or dw or db misaligned");
+  if (dims->rows > 0) {
+    GDN_TRY(check_norm_io(dims, x, x_stride, z, z_stride, in_dtype, w, b));
+    GDN_TRY(check_rows(dy, dy_stride, dims, in_dtype, "dy"));
+    GDN_TRY(check_rows(dx, dx_stride, dims, in_dtype, "dx"));
+    GDN_REQUIRE((dz != nullptr) == (z != nullptr), GDN_EINVAL, "dz must be given exactly when there is a gate");
+    if (dz != nullptr) GDN_TRY(check_rows(dz, dz_stride, dims, in_dtype, "dz"));
+    GDN_REQUIRE(mean != nullptr && rstd != nullptr && aligned(mean, 4) && aligned(rstd, 4), GDN_EINVAL,
+                "mean or rstd is NULL or misaligned");
+    const size_t need = gdn_layer_norm_backward_workspace_bytes(dims);
+    GDN_REQUIRE(workspace != nullptr && aligned(workspace, 256) && workspace_bytes >= need, GDN_EINVAL,
+                "workspace is NULL, not 256-byte aligned or smaller than %zu bytes", need);
+  }
+  gdn::NormArgs a = norm_args(dims, x, x_stride, z, z_stride, in_dtype, w, b);
+  a.dy = dy;
+  a.dx = dx;
+  a.dz = dz;
+  a.dy_stride = row_stride(dy_stride, dims);
+  a.dx_stride = row_stride(dx_stride, dims);
+  a.dz_stride = row_stride(dz_stride, dims);
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.part = static_cast<float*>(workspace);
+  a.dw = dw;
+  a.db = db;
+  return launched(gdn::launch_norm_bwd(a, static_cast<hipStream_t>(stream)));
+}

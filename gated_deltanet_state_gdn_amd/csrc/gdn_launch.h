@@ -104,6 +104,25 @@ struct PrefillArgs {
   float scale;
 };
 
+struct NormArgs {
+  const void* x;
+  const void* z;       // the gate, or null
+  const float* w;
+  const float* b;      // or null
+  void* y;
+  float* mean;         // [rows, groups], or null
+  float* rstd;
+  const void* dy;
+  void* dx;
+  void* dz;
+  float* part;         // [blocks][2][N] partial dw and db
+  float* dw;
+  float* db;           // or null
+  int64_t rows, x_stride, z_stride, y_stride, dy_stride, dx_stride, dz_stride;
+  int32_t N, groups, rms, gate_after, in_dt, out_dt;
+  float eps;
+};
+
 // Each returns hipSuccess or the launch error.
 hipError_t launch_decode(const DecodeArgs& a, int state_dt, int D, hipStream_t s);
 // state_dt: dtype of the checkpoint pool a.d.pool; with a.read_pool set the
@@ -118,6 +137,10 @@ hipError_t launch_m2_decode(const M2Args& a, int state_dt, int P, int N, hipStre
 // fold, step (T > 0) and pointer advance; T == 0 is the flush
 hipError_t launch_m2_replay(const M2Args& a, int state_dt, int P, int N, hipStream_t s);
 hipError_t launch_m2_rollback(const M2Args& a, hipStream_t s);
+hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
+bool norm_slice_fits(int n);
+int norm_bwd_blocks(int64_t rows, int N, int groups);
 size_t m2_lds_bytes(int P, int N, int L, int T, int heads_per_group);
 
 // Dynamic LDS of the speculative-decode kernel; launches need <= kSpecMaxLds.

@@ -372,6 +372,57 @@ gdn_status gdn_mamba2_replay_rollback(const gdn_m2_dims* dims, int32_t B, const 
                                       const int32_t* num_rejected, const gdn_m2_ring* ring,
                                       void* stream);
 
+/* -------------------------------------------------------------------- norm
+ * Layer or RMS norm of the slices of a row, forward and backward: the norm in
+ * front of a recurrent block and, gated and by groups, the one behind its
+ * recurrence (the output gate that the Mamba2 and GDN entry points leave to
+ * the caller).  A row of `width` values is `groups` slices of
+ * n = width / groups.  With u = x, or x silu(z) for GDN_GATE_BEFORE:
+ *     m = mean(u) (0 when rms is set),  r = (mean((u - m)^2) + eps)^-1/2,
+ *     y = (u - m) r w + b, times silu(z) for GDN_GATE_AFTER.
+ * FP32 math and sums.  Rows of x, z, y, dy, dx and dz may be apart by any
+ * stride (in elements, >= width; 0 stands for width), the values of a row are
+ * consecutive, and any element alignment is accepted.  n <= 16384, else
+ * GDN_EUNSUPPORTED; groups <= 65535. */
+typedef enum { GDN_GATE_NONE = 0, GDN_GATE_BEFORE = 1, GDN_GATE_AFTER = 2 } gdn_norm_gate;
+
+typedef struct {
+  int64_t rows;
+  int32_t width;  /* values of a row, a multiple of groups */
+  int32_t groups;
+  int32_t rms;    /* 0: layer norm, otherwise RMS norm (no mean) */
+  gdn_norm_gate gate;
+} gdn_norm_dims;
+
+/*   x, z       [rows, width] in_dtype (z NULL exactly for GDN_GATE_NONE)
+ *   w, b       float32 [width]; b NULL for no bias
+ *   y          [rows, width] out_dtype
+ *   mean, rstd float32 [rows, groups], what the backward pass needs; both or
+ *              neither NULL (the RMS form writes zeros to mean)
+ * rows == 0 is a no-op. */
+gdn_status gdn_layer_norm(const gdn_norm_dims* dims, const void* x, int64_t x_stride, const void* z,
+                          int64_t z_stride, gdn_dtype in_dtype, const float* w, const float* b,
+                          float eps, void* y, int64_t y_stride, gdn_dtype out_dtype, float* mean,
+                          float* rstd, void* stream);
+
+/* Gradients of gdn_layer_norm from dy and the forward call's inputs and
+ * statistics.
+ *   dy, dx, dz  [rows, width] in_dtype (dz NULL exactly for GDN_GATE_NONE)
+ *   b           the forward call's bias or NULL (read for GDN_GATE_AFTER only)
+ *   dw, db      float32 [width], summed over all rows in a fixed order (equal
+ *               calls give equal bits); db NULL when it is not wanted
+ *   workspace   device scratch of at least the queried size, 256-byte aligned,
+ *               not read before it is written
+ * dx may be dy or x, and dz may be z, element for element.  rows == 0 writes
+ * zeros to dw and db. */
+size_t gdn_layer_norm_backward_workspace_bytes(const gdn_norm_dims* dims);
+gdn_status gdn_layer_norm_backward(const gdn_norm_dims* dims, const void* dy, int64_t dy_stride,
+                                   const void* x, int64_t x_stride, const void* z, int64_t z_stride,
+                                   gdn_dtype in_dtype, const float* w, const float* b,
+                                   const float* mean, const float* rstd, void* dx, int64_t dx_stride,
+                                   void* dz, int64_t dz_stride, float* dw, float* db, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* gdn_status_string(gdn_status status);
 

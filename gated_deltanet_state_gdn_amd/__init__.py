@@ -4,6 +4,7 @@ Entry points (same names as the C ABI in include/gdn.h): gdn_decode_step,
 gdn_spec_decode, gdn_copy_state_blocks, gdn_chunk_prefill, gdn_replay_decode,
 gdn_replay_flush, gdn_replay_rollback, and the Mamba2 variant gdn_mamba2_decode_step,
 gdn_mamba2_replay_decode, gdn_mamba2_replay_flush, gdn_mamba2_replay_rollback.
+Over packed sequences, forward and backward: gdn_mamba2_scan, gdn_mamba2_scan_backward.
 The block's norm: gdn_layer_norm, gdn_layer_norm_backward.
 The kernels live in libgdn.so, built in-tree by
 ``python -m gated_deltanet_state_gdn_amd.build``; importing this package does
@@ -16,5 +17,5 @@ from ._binding import (  # noqa: F401
     gdn_replay_decode, gdn_replay_decode_noalloc, gdn_replay_flush, gdn_replay_rollback, gdn_replay_workspace_bytes, gdn_spec_decode,
     gdn_status_string, lib, make_state_table, new_ring, state_refs_bytes, M2Ring, new_m2_ring,
     gdn_mamba2_decode_step, gdn_mamba2_replay_decode, gdn_mamba2_replay_flush, gdn_mamba2_replay_rollback,
-    LayerNormGrads, gdn_layer_norm, gdn_layer_norm_backward,
+    M2ScanGrads, gdn_mamba2_scan, gdn_mamba2_scan_backward, LayerNormGrads, gdn_layer_norm, gdn_layer_norm_backward,
 )

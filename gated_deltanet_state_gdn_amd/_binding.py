@@ -25,6 +25,7 @@ EXPORTS = (
     "gdn_replay_decode", "gdn_replay_decode_noalloc",
     "gdn_replay_flush", "gdn_replay_rollback", "gdn_replay_decode_dual", "gdn_replay_flush_dual",
     "gdn_mamba2_decode_step", "gdn_mamba2_replay_decode", "gdn_mamba2_replay_flush", "gdn_mamba2_replay_rollback",
+    "gdn_mamba2_scan_workspace_bytes", "gdn_mamba2_scan", "gdn_mamba2_scan_backward_workspace_bytes", "gdn_mamba2_scan_backward",
     "gdn_layer_norm", "gdn_layer_norm_backward_workspace_bytes", "gdn_layer_norm_backward",
     "gdn_status_string", "gdn_last_error",
 )
@@ -70,6 +71,10 @@ class gdn_ring(ctypes.Structure):
                 ("L", ctypes.c_int32), ("dtype", ctypes.c_int)]
 
 
+class gdn_m2_strides(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_int64), ("Bm", ctypes.c_int64), ("Cm", ctypes.c_int64), ("dt", ctypes.c_int64)]
+
+
 class gdn_norm_dims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("groups", ctypes.c_int32), ("rms", ctypes.c_int32),
                 ("gate", ctypes.c_int)]
@@ -94,6 +99,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ, INT = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
     F32, pn = ctypes.c_float, ctypes.POINTER(gdn_norm_dims)
+    pst = ctypes.POINTER(gdn_m2_strides)
     pd, pg, pp, pr = (ctypes.POINTER(gdn_dims), ctypes.POINTER(gdn_gates), ctypes.POINTER(gdn_pool),
                       ctypes.POINTER(gdn_ring))
     pm, pmp, pmr = ctypes.POINTER(gdn_m2_dims), ctypes.POINTER(gdn_m2_params), ctypes.POINTER(gdn_m2_ring)
@@ -114,6 +120,10 @@ def lib() -> ctypes.CDLL:
         "gdn_mamba2_replay_decode": (INT, [pm, I32, I32, P, P, P, INT, pmp, pp, P, pmr, P, INT, P]),
         "gdn_mamba2_replay_flush": (INT, [pm, I32, pp, P, pmr, P]),
         "gdn_mamba2_replay_rollback": (INT, [pm, I32, P, P, pmr, P]),
+        "gdn_mamba2_scan_workspace_bytes": (SZ, [pm, I32, I64]),
+        "gdn_mamba2_scan": (INT, [pm, I32, P, I64, P, P, P, INT, pst, pmp, pp, P, P, INT, P, SZ, P]),
+        "gdn_mamba2_scan_backward_workspace_bytes": (SZ, [pm, I32, I64]),
+        "gdn_mamba2_scan_backward": (INT, [pm, I32, P, I64, P, P, P, INT, pst, pmp, pp, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "gdn_layer_norm": (INT, [pn, P, I64, P, I64, INT, P, P, F32, P, I64, INT, P, P, P]),
         "gdn_layer_norm_backward_workspace_bytes": (SZ, [pn]),
         "gdn_layer_norm_backward": (INT, [pn, P, I64, P, I64, P, I64, INT, P, P, P, P, P, I64, P, I64, P, P, P, SZ, P]),
@@ -486,6 +496,117 @@ def gdn_mamba2_replay_rollback(slot_map, num_rejected, ring: M2Ring, stream=None
                                             _ptr(num_rejected), ctypes.byref(rs), _stream(stream)))
 
 
+class M2ScanGrads(NamedTuple):
+    """Gradients of gdn_mamba2_scan: dx, dBm, dCm, ddt in the inputs' dtype, the others float32."""
+    dx: object
+    dBm: object
+    dCm: object
+    ddt: object
+    dA_log: object
+    ddt_bias: object
+    dD: object
+    dinit: object  # [N, H, d, n], or None without a pool
+
+
+def _token_rows(t, tail, dtype, what):
+    """(pointer, token stride) of a [T, ...] tensor whose tokens may be apart."""
+    if t.dim() != 1 + len(tail) or tuple(t.shape[1:]) != tuple(tail) or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} of shape [T, {', '.join(map(str, tail))}], not {t.dtype} {tuple(t.shape)}")
+    dense, step = 1, []
+    for v in reversed(tail):
+        step.insert(0, dense)
+        dense *= int(v)
+    if t.numel() and any(t.shape[1 + i] > 1 and t.stride(1 + i) != v for i, v in enumerate(step)):
+        raise ValueError(f"{what}: the values of a token must be consecutive")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map):
+    """The arguments that the scan and its backward share: dims, sequences, pointers and the structs behind them."""
+    torch = _torch()
+    if x.dim() != 3 or Bm.dim() != 3:
+        raise ValueError("x must be [T, H, d] and Bm [T, G, n]")
+    T, H, d = x.shape
+    G, n = Bm.shape[1:]
+    px, sx = _token_rows(x, (H, d), x.dtype, "x")
+    pb, sb = _token_rows(Bm, (G, n), x.dtype, "Bm")
+    pc, sc = _token_rows(Cm, (G, n), x.dtype, "Cm")
+    pdt, sdt = _token_rows(dt, (H,), x.dtype, "dt")
+    if not T == Bm.shape[0] == Cm.shape[0] == dt.shape[0]:
+        raise ValueError("x, Bm, Cm and dt must have the same number of tokens")
+    for t, what in ((A_log, "A_log"), (dt_bias, "dt_bias"), (D, "D")):
+        _f32(t, (H,), what)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be int32 [N + 1]")
+    N = int(cu_seqlens.shape[0]) - 1
+    if (pool is None) != (slot_map is None):
+        raise ValueError("pool and slot_map come together or not at all")
+    if pool is not None:
+        if tuple(pool.shape[1:]) != (H, d, n):
+            raise ValueError(f"pool must be [slots, {H}, {d}, {n}], not {tuple(pool.shape)}")
+        if slot_map.dtype != torch.int32 or tuple(slot_map.shape) != (N,):
+            raise ValueError(f"slot_map must be int32 [{N}]")
+    dims = gdn_m2_dims(H, G, d, n)
+    params = gdn_m2_params(pdt, _ptr(A_log), _ptr(dt_bias), _ptr(D))
+    return (T, N, dims, [ctypes.byref(dims), N, _ptr(cu_seqlens), T, px, pb, pc, dtype_code(x.dtype),
+                         ctypes.byref(gdn_m2_strides(sx, sb, sc, sdt)), ctypes.byref(params),
+                         ctypes.byref(_pool(pool)) if pool is not None else None,
+                         _ptr(slot_map) if slot_map is not None else None])
+
+
+def gdn_mamba2_scan(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool=None, slot_map=None, out=None, out_dtype=None,
+                    workspace=None, stream=None):
+    """The Mamba2 recurrence over packed sequences: x [T, H, d]; Bm, Cm [T, G, n]; dt [T, H]; cu_seqlens int32
+    [N+1] (device).  Tokens may be apart (slices of wider rows).  With a pool [slots, H, d, n] and slot_map int32
+    [N], sequence s goes on from slot slot_map[s] and leaves its final state there; without, from zero states.
+    Returns y [T, H, d] in out_dtype (x's by default)."""
+    torch = _torch()
+    T, N, dims, args = _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map)
+    fresh = []
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        fresh.append(out)
+    elif tuple(out.shape) != tuple(x.shape):
+        raise ValueError(f"out must be {tuple(x.shape)}, not {tuple(out.shape)}")
+    if workspace is None:
+        need = int(lib().gdn_mamba2_scan_workspace_bytes(ctypes.byref(dims), N, T))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            fresh.append(workspace)
+    _keep_for_stream(fresh, stream)
+    _check(lib().gdn_mamba2_scan(*args, _ptr(out), dtype_code(out.dtype), _ptr(workspace) if workspace is not None else None,
+                                 workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+    return out
+
+
+def gdn_mamba2_scan_backward(dy, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool=None, slot_map=None, dfinal=None,
+                             workspace=None, stream=None) -> M2ScanGrads:
+    """Gradients of gdn_mamba2_scan for dy [T, H, d] in x's dtype (and dfinal, float32 [N, H, d, n], of the final
+    states).  pool and slot_map give the states that the forward call started from, as they were before it."""
+    torch = _torch()
+    T, N, dims, args = _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map)
+    H, d, G, n = dims.num_heads, dims.headdim, dims.num_groups, dims.dstate
+    if tuple(dy.shape) != tuple(x.shape) or dy.dtype != x.dtype:
+        raise ValueError(f"dy must be {x.dtype} of shape {tuple(x.shape)}, not {dy.dtype} {tuple(dy.shape)}")
+    _f32(dfinal, (N, H, d, n), "dfinal")
+    new = lambda shape, t: torch.empty(shape, dtype=t, device=x.device)  # noqa: E731
+    f32 = torch.float32
+    grads = M2ScanGrads(new((T, H, d), x.dtype), new((T, G, n), x.dtype), new((T, G, n), x.dtype), new((T, H), x.dtype),
+                        new((H,), f32), new((H,), f32), new((H,), f32), new((N, H, d, n), f32) if pool is not None else None)
+    fresh = list(grads)
+    if workspace is None:
+        need = int(lib().gdn_mamba2_scan_backward_workspace_bytes(ctypes.byref(dims), N, T))
+        if need:
+            workspace = new((need,), torch.uint8)
+            fresh.append(workspace)
+    _keep_for_stream(fresh, stream)
+    _check(lib().gdn_mamba2_scan_backward(
+        *args, _ptr(dy), _ptr(dfinal) if dfinal is not None else None, *(_ptr(t) for t in grads[:7]),
+        _ptr(grads.dinit) if pool is not None else None, _ptr(workspace) if workspace is not None else None,
+        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+    return grads
+
+
 # ------------------------------------------------------------------ norm
 class LayerNormGrads(NamedTuple):
     """Gradients of gdn_layer_norm; dbias and dgate are None where the call had no bias or gate."""
@@ -508,7 +629,7 @@ def _rows(t, shape, dtype, what):
         return None, 0
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{what}: the values of a row must be consecutive")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
 

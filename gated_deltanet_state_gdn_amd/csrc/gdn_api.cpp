@@ -715,3 +715,256 @@ gdn_status gdn_layer_norm_backward(const gdn_norm_dims* dims, const void* dy, in
   a.db = db;
   return launched(gdn::launch_norm_bwd(a, static_cast<hipStream_t>(stream)));
 }
+
+// ------------------------------------------------------------------ Mamba2 sequence scan
+namespace {
+
+// Parts of a workspace, each on a 256-byte boundary.
+struct Carve {
+  size_t used = 0;
+  size_t take(size_t bytes) {
+    const size_t at = used;
+    used += (bytes + 255) / 256 * 256;
+    return at;
+  }
+};
+
+struct ScanWs {
+  size_t gates, wt, gm, seg, seg_g, rt, fwd, rev, part, part_bc, bytes;
+  int seg_chunks, splits;
+};
+
+ScanWs scan_ws(const gdn_m2_dims* d, int32_t N, int64_t total, bool backward) {
+  ScanWs w{};
+  Carve c;
+  const size_t H = d->num_heads, G = d->num_groups, state = (size_t)d->headdim * d->dstate * 4;
+  const size_t chunks = gdn::scan_slots(N, total, 64);
+  w.seg_chunks = gdn::scan_seg_chunks(N, total, d->num_heads, d->num_groups, d->headdim);
+  w.gates = c.take(chunks * H * 3 * 64 * 4);
+  w.wt = c.take(chunks * G * d->dstate * 64 * 4);
+  w.gm = c.take(chunks * G * 64 * 64 * 4);
+  if (w.seg_chunks > 0) {
+    const size_t segs = gdn::scan_slots(N, total, (int64_t)w.seg_chunks * 64);
+    w.seg = c.take(segs * H * state);
+    w.seg_g = c.take(segs * H * 8);
+  }
+  if (backward) {
+    const size_t blocks = gdn::scan_slots(N, total, 128);
+    w.splits = gdn::grad_splits(N, total, d->num_heads, d->num_groups);
+    w.rt = c.take(chunks * G * d->dstate * 64 * 4);
+    w.fwd = c.take(blocks * H * state);
+    w.rev = c.take(blocks * H * state);
+    w.part = c.take(blocks * H * 3 * 4);
+    if (w.splits > 1) w.part_bc = c.take((size_t)w.splits * 2 * total * G * d->dstate * 4);
+  }
+  w.bytes = c.used;
+  return w;
+}
+
+gdn_status check_scan_sizes(const gdn_m2_dims* d, int32_t N, int64_t total) {
+  GDN_TRY(check_m2_dims(d));
+  GDN_REQUIRE(N >= 0 && total >= 0, GDN_EINVAL, "N=%d and total_tokens=%lld must be >= 0", N, (long long)total);
+  GDN_REQUIRE(total <= INT32_MAX, GDN_EINVAL, "total_tokens=%lld exceeds the 32-bit cu_seqlens", (long long)total);
+  GDN_REQUIRE(N > 0 || total == 0, GDN_EINVAL, "%lld tokens in no sequence", (long long)total);
+  GDN_REQUIRE(d->num_heads <= 65535, GDN_EUNSUPPORTED, "H=%d: at most 65535 heads are supported", d->num_heads);
+  GDN_REQUIRE(gdn::scan_slots(N, total, 64) * d->num_heads <= INT32_MAX, GDN_EUNSUPPORTED,
+              "64-token chunks x heads exceed the grid limit");
+  return GDN_OK;
+}
+
+gdn_status check_token_stride(int64_t s, int64_t least, int64_t unit, const char* what) {
+  GDN_REQUIRE(s == 0 || (s >= least && s % unit == 0), GDN_EINVAL, "%s stride %lld must be 0 or a multiple of %lld, >= %lld",
+              what, (long long)s, (long long)unit, (long long)least);
+  return GDN_OK;
+}
+
+gdn_status check_scan_io(const gdn_m2_dims* d, const int32_t* cu, int64_t total, const void* x, const void* Bm,
+                         const void* Cm, int in_dt, const gdn_m2_strides* st, const gdn_m2_params* p,
+                         const gdn_pool* state, const int32_t* slot_map) {
+  GDN_REQUIRE(cu != nullptr && aligned(cu, 4), GDN_EINVAL, "cu_seqlens is NULL or misaligned");
+  GDN_REQUIRE(p != nullptr && p->A_log && p->dt_bias && p->D, GDN_EINVAL, "params or one of its parameters is NULL");
+  GDN_REQUIRE(aligned(p->A_log, 4) && aligned(p->dt_bias, 4) && aligned(p->D, 4), GDN_EINVAL, "a parameter is misaligned");
+  if (total > 0) {
+    GDN_REQUIRE(x && Bm && Cm && p->dt, GDN_EINVAL, "x, Bm, Cm or dt is NULL");
+    GDN_REQUIRE(aligned(x, 16) && aligned(Bm, 16) && aligned(Cm, 16), GDN_EINVAL, "x, Bm or Cm is not 16-byte aligned");
+    GDN_REQUIRE(aligned(p->dt, dtype_bytes(in_dt)), GDN_EINVAL, "dt is misaligned for its dtype");
+  }
+  if (st != nullptr) {
+    GDN_TRY(check_token_stride(st->x, (int64_t)d->num_heads * d->headdim, 8, "x"));
+    GDN_TRY(check_token_stride(st->Bm, (int64_t)d->num_groups * d->dstate, 8, "Bm"));
+    GDN_TRY(check_token_stride(st->Cm, (int64_t)d->num_groups * d->dstate, 8, "Cm"));
+    GDN_TRY(check_token_stride(st->dt, d->num_heads, 1, "dt"));
+  }
+  GDN_REQUIRE((state != nullptr) == (slot_map != nullptr), GDN_EINVAL, "the state pool and slot_map come together or not at all");
+  if (state != nullptr) {
+    GDN_TRY(check_pool(state, "state"));
+    GDN_REQUIRE(aligned(slot_map, 4), GDN_EINVAL, "slot_map is misaligned");
+  }
+  return GDN_OK;
+}
+
+gdn_status check_scan_ws(const void* ws, size_t bytes, size_t need) {
+  GDN_REQUIRE(need == 0 || (ws != nullptr && aligned(ws, 256) && bytes >= need), GDN_EINVAL,
+              "workspace is NULL, not 256-byte aligned or smaller than %zu bytes", need);
+  return GDN_OK;
+}
+
+gdn::M2ScanArgs scan_args(const gdn_m2_dims* d, int32_t N, const int32_t* cu, int64_t total, const void* x, const void* Bm,
+                          const void* Cm, int in_dt, const gdn_m2_strides* st, const gdn_m2_params* p,
+                          const gdn_pool* state, const int32_t* slot_map, char* ws, const ScanWs& w) {
+  gdn::M2ScanArgs a{};
+  auto stride = [](const gdn_m2_strides* q, int64_t gdn_m2_strides::* f, int64_t dense) { return q != nullptr && q->*f != 0 ? q->*f : dense; };
+  a.read = Cm;
+  a.write = Bm;
+  a.in = x;
+  a.dt = p->dt;
+  a.A_log = p->A_log;
+  a.dt_bias = p->dt_bias;
+  a.Dskip = p->D;
+  a.cu = cu;
+  if (state != nullptr) {
+    a.live = slot_map;
+    a.live_slots = state->num_slots;
+    a.init = gdn::ScanStates{state->base, slot_map, (int32_t)state->dtype};
+  }
+  a.read_ts = stride(st, &gdn_m2_strides::Cm, (int64_t)d->num_groups * d->dstate);
+  a.write_ts = stride(st, &gdn_m2_strides::Bm, (int64_t)d->num_groups * d->dstate);
+  a.in_ts = stride(st, &gdn_m2_strides::x, (int64_t)d->num_heads * d->headdim);
+  a.dt_ts = stride(st, &gdn_m2_strides::dt, d->num_heads);
+  a.total = total;
+  a.N = N;
+  a.H = d->num_heads;
+  a.G = d->num_groups;
+  a.in_dt = in_dt;
+  a.gates = reinterpret_cast<float*>(ws + w.gates);
+  a.wt = ws + w.wt;
+  a.gm = reinterpret_cast<float*>(ws + w.gm);
+  a.seg = reinterpret_cast<float*>(ws + w.seg);
+  a.seg_g = reinterpret_cast<double*>(ws + w.seg_g);
+  a.seg_chunks = w.seg_chunks;
+  return a;
+}
+
+}  // namespace
+
+size_t gdn_mamba2_scan_workspace_bytes(const gdn_m2_dims* dims, int32_t N, int64_t total_tokens) {
+  if (check_scan_sizes(dims, N, total_tokens) != GDN_OK || N == 0) return 0;
+  return scan_ws(dims, N, total_tokens, false).bytes;
+}
+
+gdn_status gdn_mamba2_scan(const gdn_m2_dims* dims, int32_t N, const int32_t* cu_seqlens, int64_t total_tokens,
+                           const void* x, const void* Bm, const void* Cm, gdn_dtype in_dtype,
+                           const gdn_m2_strides* strides, const gdn_m2_params* params, const gdn_pool* state,
+                           const int32_t* slot_map, void* y, gdn_dtype out_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  GDN_TRY(check_scan_sizes(dims, N, total_tokens));
+  GDN_TRY(check_dtypes(in_dtype, out_dtype));
+  if (N == 0 || total_tokens == 0) return ok();  // nothing is read or written
+  GDN_TRY(check_scan_io(dims, cu_seqlens, total_tokens, x, Bm, Cm, in_dtype, strides, params, state, slot_map));
+  GDN_REQUIRE(y != nullptr && aligned(y, dtype_bytes(out_dtype)), GDN_EINVAL, "y is NULL or misaligned for out_dtype");
+  const ScanWs w = scan_ws(dims, N, total_tokens, false);
+  GDN_TRY(check_scan_ws(workspace, workspace_bytes, w.bytes));
+  gdn::M2ScanArgs a = scan_args(dims, N, cu_seqlens, total_tokens, x, Bm, Cm, in_dtype, strides, params, state, slot_map,
+                                static_cast<char*>(workspace), w);
+  a.out = y;
+  a.out_dt = out_dtype;
+  a.fin = a.init;
+  const bool bf = in_dtype == GDN_BF16 && out_dtype != GDN_F32;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = gdn::launch_scan_prep(a, bf, dims->dstate, s);
+  if (e == hipSuccess) e = gdn::launch_scan_walk(a, bf, dims->headdim, dims->dstate, false, true, s);
+  return launched(e);
+}
+
+size_t gdn_mamba2_scan_backward_workspace_bytes(const gdn_m2_dims* dims, int32_t N, int64_t total_tokens) {
+  if (check_scan_sizes(dims, N, total_tokens) != GDN_OK || N == 0) return 0;
+  return scan_ws(dims, N, total_tokens, true).bytes;
+}
+
+gdn_status gdn_mamba2_scan_backward(const gdn_m2_dims* dims, int32_t N, const int32_t* cu_seqlens, int64_t total_tokens,
+                                    const void* x, const void* Bm, const void* Cm, gdn_dtype in_dtype,
+                                    const gdn_m2_strides* strides, const gdn_m2_params* params, const gdn_pool* init,
+                                    const int32_t* slot_map, const void* dy, const float* dfinal, void* dx, void* dBm,
+                                    void* dCm, void* ddt, float* dA_log, float* ddt_bias, float* dD, float* dinit,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  GDN_TRY(check_scan_sizes(dims, N, total_tokens));
+  GDN_TRY(check_dtypes(in_dtype, in_dtype));
+  GDN_REQUIRE(dA_log && ddt_bias && dD && aligned(dA_log, 4) && aligned(ddt_bias, 4) && aligned(dD, 4), GDN_EINVAL,
+              "a head parameter's gradient is NULL or misaligned");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  gdn::M2GradArgs q{};
+  q.H = dims->num_heads;
+  q.dA_log = dA_log;
+  q.ddt_bias = ddt_bias;
+  q.dD = dD;
+  if (N == 0)  // the parameters' gradients are sums of nothing
+    return launched(gdn::launch_scan_grad(q, false, dims->headdim, dims->dstate, s));
+  GDN_TRY(check_scan_io(dims, cu_seqlens, total_tokens, x, Bm, Cm, in_dtype, strides, params, init, slot_map));
+  if (total_tokens > 0) {
+    const size_t eb = dtype_bytes(in_dtype);
+    GDN_REQUIRE(dy != nullptr && aligned(dy, 16), GDN_EINVAL, "dy is NULL or not 16-byte aligned");
+    GDN_REQUIRE(dx && dBm && dCm && ddt && aligned(dx, eb) && aligned(dBm, eb) && aligned(dCm, eb) && aligned(ddt, eb), GDN_EINVAL,
+                "dx, dBm, dCm or ddt is NULL or misaligned for its dtype");
+  }
+  GDN_REQUIRE(aligned(dfinal, 16) && aligned(dinit, 16), GDN_EINVAL, "dfinal or dinit is not 16-byte aligned");
+  const ScanWs w = scan_ws(dims, N, total_tokens, true);
+  GDN_TRY(check_scan_ws(workspace, workspace_bytes, w.bytes));
+  char* const ws = static_cast<char*>(workspace);
+  const bool bf = in_dtype == GDN_BF16;
+  // forward: the states before each block (the prep below writes the transposed B for it)
+  gdn::M2ScanArgs f = scan_args(dims, N, cu_seqlens, total_tokens, x, Bm, Cm, in_dtype, strides, params, init, slot_map, ws, w);
+  // in reverse: read B, write C, in dy
+  gdn::M2ScanArgs r = f;
+  r.read = Bm;
+  r.write = Cm;
+  r.read_ts = f.write_ts;
+  r.write_ts = f.read_ts;
+  r.in = dy;
+  r.in_ts = (int64_t)dims->num_heads * dims->headdim;
+  r.out = dx;
+  r.out_dt = in_dtype;
+  r.init = gdn::ScanStates{const_cast<float*>(dfinal), nullptr, GDN_F32};
+  r.fin = gdn::ScanStates{dinit, nullptr, GDN_F32};
+  r.rt = ws + w.rt;
+  r.blocks = reinterpret_cast<float*>(ws + w.rev);
+  f.wt = r.rt;
+  f.gm = nullptr;
+  f.blocks = reinterpret_cast<float*>(ws + w.fwd);
+  hipError_t e = hipSuccess;
+  if (total_tokens > 0) {
+    e = gdn::launch_scan_prep(r, bf, dims->dstate, s);
+    if (e == hipSuccess) e = gdn::launch_scan_walk(f, bf, dims->headdim, dims->dstate, false, false, s);
+  }
+  if (e == hipSuccess) e = gdn::launch_scan_walk(r, bf, dims->headdim, dims->dstate, true, true, s);
+  if (e != hipSuccess) return launched(e);
+  q.x = x;
+  q.Bm = Bm;
+  q.Cm = Cm;
+  q.dt = params->dt;
+  q.dy = dy;
+  q.A_log = params->A_log;
+  q.dt_bias = params->dt_bias;
+  q.cu = cu_seqlens;
+  q.live = f.live;
+  q.live_slots = f.live_slots;
+  q.x_ts = f.in_ts;
+  q.b_ts = f.write_ts;
+  q.c_ts = f.read_ts;
+  q.dt_ts = f.dt_ts;
+  q.total = total_tokens;
+  q.N = N;
+  q.G = dims->num_groups;
+  q.dt_in = in_dtype;
+  q.splits = w.splits;
+  q.gates = f.gates;
+  q.bt = r.rt;
+  q.ct = r.wt;
+  q.fwd = f.blocks;
+  q.rev = r.blocks;
+  q.dB = dBm;
+  q.dC = dCm;
+  q.ddt = ddt;
+  q.part_bc = reinterpret_cast<float*>(ws + w.part_bc);
+  q.part = reinterpret_cast<float*>(ws + w.part);
+  return launched(gdn::launch_scan_grad(q, bf, dims->headdim, dims->dstate, s));
+}

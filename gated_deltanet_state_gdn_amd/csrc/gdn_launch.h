@@ -104,6 +104,73 @@ struct PrefillArgs {
   float scale;
 };
 
+// States that a scan starts from or ends in: a pool's slots, or (slots null)
+// one state a sequence.
+struct ScanStates {
+  void* base;  // or null: zero states, or none written
+  const int32_t* slots;
+  int32_t dtype;
+};
+
+// The walk of the sequence scan, forward (read C, write B, in x) or in reverse
+// (read B, write C, in dy).  Strides are in elements between tokens.
+struct M2ScanArgs {
+  const void* read;   // [T, G, n]
+  const void* write;  // [T, G, n]
+  const void* in;     // [T, H, d]
+  const void* dt;     // [T, H]
+  const float* A_log;
+  const float* dt_bias;
+  const float* Dskip;
+  const int32_t* cu;    // [N + 1]
+  const int32_t* live;  // slot of each sequence: outside [0, live_slots) marks a padded one; or null
+  int64_t live_slots;
+  int64_t read_ts, write_ts, in_ts, dt_ts;
+  int64_t total;
+  int32_t N, H, G, in_dt, out_dt;
+  void* out;        // y, or dx
+  ScanStates init, fin;
+  float* gates;     // [chunk slots][H][3][64]: prefix sums of log-decays (two floats), dt'
+  void* wt;         // [chunk slots][G][n][64] transposed write vectors
+  void* rt;         // the same of the read vectors, or null
+  float* gm;        // [chunk slots][G][64][64] read . write, or null
+  float* seg;       // [segment slots][H][d][n] states at the segments' starts
+  double* seg_g;    // [segment slots][H] the segments' summed log-decays
+  float* blocks;    // [block slots][H][n][d] states that meet each 128-token block, or null
+  int32_t seg_chunks;  // 0: whole sequences
+  int32_t local;       // the segments' first walk
+};
+
+// The gradient kernel over blocks of 128 tokens.
+struct M2GradArgs {
+  const void* x;
+  const void* Bm;
+  const void* Cm;
+  const void* dt;
+  const void* dy;
+  const float* A_log;
+  const float* dt_bias;
+  const int32_t* cu;
+  const int32_t* live;
+  int64_t live_slots;
+  int64_t x_ts, b_ts, c_ts, dt_ts;
+  int64_t total;
+  int32_t N, H, G, dt_in, splits;  // dt_in: dtype of the inputs and their gradients; splits: workgroups a group
+  const float* gates;
+  const void* bt;      // transposed B and C [chunk slots][G][n][64]
+  const void* ct;
+  const float* fwd;    // [block slots][H][n][d] states before each block
+  const float* rev;    // gradients of the states after it
+  void* dB;            // [T, G, n]
+  void* dC;
+  void* ddt;           // [T, H]
+  float* part_bc;      // [splits][2][T][G][n] where splits > 1
+  float* part;         // [block slots][H][3] sums for dA_log, ddt_bias, dD
+  float* dA_log;
+  float* ddt_bias;
+  float* dD;
+};
+
 struct NormArgs {
   const void* x;
   const void* z;       // the gate, or null
@@ -137,6 +204,13 @@ hipError_t launch_m2_decode(const M2Args& a, int state_dt, int P, int N, hipStre
 // fold, step (T > 0) and pointer advance; T == 0 is the flush
 hipError_t launch_m2_replay(const M2Args& a, int state_dt, int P, int N, hipStream_t s);
 hipError_t launch_m2_rollback(const M2Args& a, hipStream_t s);
+// Slots of a packed batch cut into pieces of P tokens.
+int64_t scan_slots(int64_t N, int64_t total, int64_t P);
+int scan_seg_chunks(int64_t N, int64_t total, int H, int G, int d);
+hipError_t launch_scan_prep(const M2ScanArgs& a, bool bf, int n, hipStream_t s);
+hipError_t launch_scan_walk(M2ScanArgs a, bool bf, int d, int n, bool rev, bool out, hipStream_t s);
+int grad_splits(int64_t N, int64_t total, int H, int G);
+hipError_t launch_scan_grad(const M2GradArgs& a, bool bf, int d, int n, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
 bool norm_slice_fits(int n);

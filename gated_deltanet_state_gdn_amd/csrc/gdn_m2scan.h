@@ -1,0 +1,178 @@
+// Device pieces shared by the Mamba2 sequence scan's kernels (gdn_m2scan.hip,
+// gdn_m2grad.hip): where chunks lie, operand fragments, and the exact split of
+// an FP32 operand into bf16 terms.
+#pragma once
+
+#include "gdn_device.h"
+#include "gdn_launch.h"
+
+namespace gdn {
+
+constexpr int kScanChunk = 64;   // tokens of a chunk
+constexpr int kGradBlock = 128;  // tokens of a block of the gradient kernel, two chunks
+
+// ------------------------------------------------------------------ where chunks lie
+// Sequence s of a packed batch, cut into pieces of P tokens, owns the slots
+// s + floor(cu[s] / P) + c, c < max(1, ceil(len / P)): distinct for all
+// sequences, and below sequences + ceil(total / P).  A workgroup of slot i finds its
+// sequence as the last s with s + floor(cu[s] / P) <= i.
+struct Piece {
+  int seq;          // -1: the slot is not used
+  int index, count; // this piece, and the pieces of its sequence
+  int64_t begin;    // the sequence's first token
+  int64_t len;      // and its tokens
+};
+
+// The lanes of a wave test 64 sequences at a time.
+__device__ __forceinline__ Piece find_piece(const int32_t* cu, int N, int64_t total, int64_t slot, int P) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = N;  // the answer lies in [lo, hi): s = 0 always qualifies
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) >> 6;
+    const int s = lo + lane * step;
+    const bool in = s < hi && (int64_t)s + cu[s] / P <= slot;
+    const int n = __popcll(__ballot(in));
+    const int nlo = lo + (n - 1) * step;  // the condition holds on a prefix, and for lane 0
+    hi = min(hi, nlo + step);
+    lo = nlo;
+  }
+  Piece p;
+  const int64_t b = min((int64_t)cu[lo], total), e = min((int64_t)cu[lo + 1], total);
+  p.begin = b;
+  p.len = max(e - b, (int64_t)0);
+  p.index = (int)(slot - lo - b / P);
+  p.count = (int)max((p.len + P - 1) / P, (int64_t)1);
+  p.seq = p.index < p.count ? lo : -1;
+  return p;
+}
+
+__device__ __forceinline__ bool state_live(const int32_t* slots, int64_t num_slots, int seq) {
+  if (slots == nullptr) return true;
+  const int32_t s = slots[seq];
+  return s >= 0 && (int64_t)s < num_slots;
+}
+
+// ------------------------------------------------------------------ fragments
+// A fragment is the 8 values that a lane gives a 16 x 16 product over 32 k's:
+// lane l holds row (or column) l % 16 and the k's stored at 8 (l / 16) .. + 7.
+// bf16: one 16x16x32 MFMA.  FP32: eight 16x16x4 ones, the e-th on every lane's
+// e-th value; any order of the k's does, as both operands use the same.
+template <bool BF>
+struct Frag;
+template <>
+struct Frag<true> {
+  typedef uint16_t E;
+  u32x4 v;
+  __device__ __forceinline__ static Frag load(const E* p) { return Frag{*reinterpret_cast<const u32x4*>(p)}; }
+  __device__ __forceinline__ static Frag zero() { return Frag{u32x4{0u, 0u, 0u, 0u}}; }
+  __device__ __forceinline__ void widen(float (&f)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = unpack_lo<GDN_BF16>(v[j]);
+      f[2 * j + 1] = unpack_hi<GDN_BF16>(v[j]);
+    }
+  }
+  __device__ __forceinline__ static Frag round(const float (&f)[8]) {
+    Frag r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = pack2<GDN_BF16>(f[2 * j], f[2 * j + 1]);
+    return r;
+  }
+  // values 0..3 to p and 4..7 to p2
+  __device__ __forceinline__ void store_halves(E* p, E* p2) const {
+    *reinterpret_cast<u32x2*>(p) = u32x2{v[0], v[1]};
+    *reinterpret_cast<u32x2*>(p2) = u32x2{v[2], v[3]};
+  }
+};
+template <>
+struct Frag<false> {
+  typedef float E;
+  f32x4 a, b;
+  __device__ __forceinline__ static Frag load(const E* p) {
+    return Frag{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)};
+  }
+  __device__ __forceinline__ static Frag zero() { return Frag{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}; }
+  __device__ __forceinline__ void widen(float (&f)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[j] = a[j];
+      f[4 + j] = b[j];
+    }
+  }
+  __device__ __forceinline__ static Frag round(const float (&f)[8]) {
+    return Frag{f32x4{f[0], f[1], f[2], f[3]}, f32x4{f[4], f[5], f[6], f[7]}};
+  }
+  __device__ __forceinline__ void store_halves(E* p, E* p2) const {
+    *reinterpret_cast<f32x4*>(p) = a;
+    *reinterpret_cast<f32x4*>(p2) = b;
+  }
+};
+
+__device__ __forceinline__ f32x4 frag_mma(f32x4 acc, const Frag<true>& a, const Frag<true>& b) {
+  typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), acc, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 frag_mma(f32x4 acc, const Frag<false>& a, const Frag<false>& b) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[j], b.a[j], acc, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[j], b.b[j], acc, 0, 0, 0);
+  return acc;
+}
+
+// FP32 values as a sum of bf16 terms, each the rounding of what the ones
+// before leave: three hold the 24 bits, so a product with exact bf16 values is
+// that of the FP32 values.  FP32 mode needs one.
+template <bool BF>
+struct Split {
+  static constexpr int K = BF ? 3 : 1;
+  Frag<BF> t[K];
+  __device__ __forceinline__ static Split of(float (&f)[8]) {
+    Split s;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      s.t[k] = Frag<BF>::round(f);
+      if (k + 1 < K) {
+        float g[8];
+        s.t[k].widen(g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] -= g[e];
+      }
+    }
+    return s;
+  }
+  // a: exact in the fragment's type, the small terms first
+  __device__ __forceinline__ f32x4 mma_right(f32x4 acc, const Frag<BF>& a) const {
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) acc = frag_mma(acc, a, t[k]);
+    return acc;
+  }
+};
+
+// 8 consecutive input elements from element i as a fragment (16-byte aligned).
+template <bool BF>
+__device__ __forceinline__ Frag<BF> frag_from(const void* p, int64_t i, int dt) {
+  if constexpr (BF) {
+    return Frag<true>::load(static_cast<const uint16_t*>(p) + i);
+  } else {
+    float f[8];
+    load_vec<8>(p, i, dt, f);
+    return Frag<false>::round(f);
+  }
+}
+
+__device__ __forceinline__ float row16_sum(float x) {
+  x += dpp_mov<0xB1>(x);
+  x += dpp_mov<0x4E>(x);
+  x += dpp_mov<0x128>(x);
+  x += dpp_mov<0x124>(x);
+  return x;
+}
+
+// A prefix sum of log-decays kept as two floats: differences of far positions
+// keep FP32 accuracy.
+__device__ __forceinline__ float decay_between(float hi_to, float lo_to, float hi_from, float lo_from) {
+  return expf((hi_to - hi_from) + (lo_to - lo_from));
+}
+
+}  // namespace gdn

@@ -1,0 +1,546 @@
+// Mamba2 recurrence over packed sequences, and its reverse (the sequence form
+// of the state update of gdn_mamba2.hip, Dao and Gu's selective state-space
+// model; AREX ReplaySSM article, "bottleneck" section, for the state's shape).
+//
+// Per head, with g = -exp(A_log) dt' and dt' = softplus(dt + dt_bias):
+//     S_t = e^{g_t} S_{t-1} + dt'_t x_t B_t^T,   y_t = S_t C_t + D x_t.
+// Over a chunk of 64 tokens with c_i = g_1 + .. + g_i in it and S before it:
+//     y_i = e^{c_i} S C_i + sum_{j<=i} e^{c_i-c_j} dt'_j (C_i.B_j) x_j + D x_i
+//     S'  = e^{c_last} S + sum_j e^{c_last-c_j} dt'_j x_j B_j^T
+// and in reverse, with dS' the gradient of the state after the chunk:
+//     X_j  = e^{c_last-c_j} dS' B_j + sum_{i>=j} e^{c_i-c_j} (C_i.B_j) dy_i
+//     dx_j = dt'_j X_j + D dy_j,   dS = e^{c_last} dS' + sum_i e^{c_i} dy_i C_i^T
+// One kernel does both: tokens have a read vector (C, or B in reverse), a
+// write vector (B, or C) and an input (x, or dy).  Exponents are never positive.
+//
+// Kernels: the prep forms, once for all heads of a group, the products of read
+// and write vectors and the transposed write vectors, and each head's dt' and
+// c.  The walk keeps the states of 128 rows (two heads of 64) in accumulators
+// and goes over the chunks; the state meets the read vectors straight from its
+// accumulators, whose layout is that of an operand once the read vectors'
+// columns are stored in the same order.  Where there are too few walks for the
+// chip, sequences are cut into segments: a first walk finds each segment's own
+// end state, a small kernel chains them, the second walk starts every segment
+// from its true state.
+//
+// Rounding (bf16 inputs): products of two inputs are exact in FP32.  The state
+// is FP32, and its updates multiply e^{..} dt' x in three bf16 terms, all its
+// 24 bits, with exact B.  For the output alone the state and the decay-weighted
+// products of read and write vectors are rounded to bf16 once, as y is.
+// Other inputs or an FP32 output take the FP32 MFMA throughout.
+#include "gdn_m2scan.h"
+
+namespace gdn {
+
+// ------------------------------------------------------------------ prep
+// One workgroup a (chunk slot, group): gm[r][c] = read_r . write_c in FP32,
+// wt = write vectors transposed [n][64], rt = read vectors transposed (only
+// where asked for), and for the group's heads c as two floats and dt'.
+// Tokens past the sequence's end count as zero vectors with dt' = g = 0.
+template <bool BF, int NN>
+__global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
+  typedef typename Frag<BF>::E E;
+  constexpr int KB = (NN + 31) / 32, LD = KB * 32 + (BF ? 8 : 4);
+  __shared__ __align__(16) E s_r[kScanChunk * LD];
+  __shared__ __align__(16) E s_w[kScanChunk * LD];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+  const Piece pc = find_piece(a.cu, a.N, a.total, blockIdx.x, kScanChunk);
+  const int64_t t0 = pc.begin + (int64_t)pc.index * kScanChunk;
+  const int len = pc.seq < 0 ? 0 : (int)min((int64_t)kScanChunk, pc.begin + pc.len - t0);
+  if (len <= 0) return;
+  const int g = blockIdx.y;
+  constexpr int VPR = KB * 4;  // 8-element vectors of a row, zeros past NN
+  for (int u = tid; u < kScanChunk * VPR; u += 256) {
+    const int t = u / VPR, n0 = (u - t * VPR) * 8;
+    Frag<BF> r = Frag<BF>::zero(), w = r;
+    if (t < len && n0 < NN) {
+      r = frag_from<BF>(a.read, (t0 + t) * a.read_ts + g * NN + n0, a.in_dt);
+      w = frag_from<BF>(a.write, (t0 + t) * a.write_ts + g * NN + n0, a.in_dt);
+    }
+    *reinterpret_cast<Frag<BF>*>(s_r + t * LD + n0) = r;
+    *reinterpret_cast<Frag<BF>*>(s_w + t * LD + n0) = w;
+  }
+  // gates: a head a wave, a token a lane
+  const int hpg = a.H / a.G;
+  for (int hi = wave; hi < hpg; hi += 4) {
+    const int h = g * hpg + hi;
+    float dtp = 0.f;
+    double c = 0.0;
+    if (lane < len) {
+      dtp = softplus_f(load_elem(a.dt, (t0 + lane) * a.dt_ts + h, a.in_dt) + a.dt_bias[h]);
+      c = -(double)(expf(a.A_log[h]) * dtp);
+    }
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double o = __shfl_up(c, off, 64);
+      if (lane >= off) c += o;
+    }
+    float* gt = a.gates + ((int64_t)blockIdx.x * a.H + h) * 3 * kScanChunk;
+    const float ch = (float)c;
+    gt[lane] = ch;
+    gt[kScanChunk + lane] = (float)(c - (double)ch);
+    gt[2 * kScanChunk + lane] = dtp;
+  }
+  __syncthreads();
+  const int64_t cg = (int64_t)blockIdx.x * a.G + g;
+  if (a.gm != nullptr) {
+    float* gm = a.gm + cg * kScanChunk * kScanChunk;
+#pragma unroll
+    for (int ct = 0; ct < 4; ++ct) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        acc = frag_mma(acc, Frag<BF>::load(s_r + (16 * wave + l16) * LD + 32 * kb + 8 * q),
+                       Frag<BF>::load(s_w + (16 * ct + l16) * LD + 32 * kb + 8 * q));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) gm[(16 * wave + 4 * q + r) * kScanChunk + 16 * ct + l16] = acc[r];
+    }
+  }
+  for (int u = tid; u < NN * 8; u += 256) {
+    const int n = u % NN, tb = (u / NN) * 8;
+    Frag<BF> f;
+    E* e = reinterpret_cast<E*>(&f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = s_w[(tb + k) * LD + n];
+    *reinterpret_cast<Frag<BF>*>(static_cast<E*>(a.wt) + (cg * NN + n) * kScanChunk + tb) = f;
+    if (a.rt != nullptr) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] = s_r[(tb + k) * LD + n];
+      *reinterpret_cast<Frag<BF>*>(static_cast<E*>(a.rt) + (cg * NN + n) * kScanChunk + tb) = f;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ walk
+template <bool BF, int D, int NN, bool OUT>
+struct WalkGeom {
+  typedef typename Frag<BF>::E E;
+  static constexpr int PT = D == 16 ? 1 : 2;           // 16-row tiles of a wave
+  static constexpr int ROWS = 64 * PT;                 // state rows of the workgroup
+  static constexpr int HB = ROWS / D;                  // its heads
+  static constexpr int NT = NN / 16, KB = (NN + 31) / 32;
+  static constexpr int LDF = KB * 32 + (BF ? 8 : 4);   // read vectors [64][LDF], columns in accumulator order
+  static constexpr int LDT = kScanChunk + (BF ? 8 : 4);  // write vectors [NN][LDT], inputs [ROWS][LDT], products [HB][64][LDT]
+  static constexpr int F0 = 0, K0 = F0 + (OUT ? kScanChunk * LDF : 0), X0 = K0 + NN * LDT, P0 = X0 + ROWS * LDT;
+  static constexpr int ELEMS = P0 + (OUT ? HB * kScanChunk * LDT : 0);
+  // floats a head: c (two), dt', the input's weight, the read factor
+  static constexpr size_t LDS = ((size_t)ELEMS * sizeof(E) + 15) / 16 * 16 + (size_t)HB * 5 * kScanChunk * 4;
+};
+
+// Where (row p, token t) of the transposed inputs lies: in 16-bit form groups
+// of 8 tokens are permuted by the row's block of 8, so that the transposing
+// stores of a wave meet all banks.
+template <bool BF, int LDT>
+__device__ __forceinline__ int xt_at(int p, int t) {
+  return p * LDT + (BF ? ((((t >> 3) ^ (p >> 3)) & 7) << 3 | (t & 7)) : t);
+}
+
+template <bool BF, int D, int NN, bool REV, bool OUT>
+__global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
+  using W = WalkGeom<BF, D, NN, OUT>;
+  typedef typename W::E E;
+  constexpr int PT = W::PT, HB = W::HB, NT = W::NT, KB = W::KB, LDF = W::LDF, LDT = W::LDT, ROWS = W::ROWS, Q = kScanChunk;
+  extern __shared__ __align__(16) unsigned char smem[];
+  E* const s_f = reinterpret_cast<E*>(smem) + W::F0;
+  E* const s_k = reinterpret_cast<E*>(smem) + W::K0;
+  E* const s_x = reinterpret_cast<E*>(smem) + W::X0;
+  E* const s_p = reinterpret_cast<E*>(smem) + W::P0;
+  float* const s_g = reinterpret_cast<float*>(smem + ((size_t)W::ELEMS * sizeof(E) + 15) / 16 * 16);  // [HB][5][64]
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+  const int hpg = a.H / a.G, hbs = (hpg + HB - 1) / HB;
+  const int u = xcd_unit(blockIdx.x, gridDim.x);
+  const int slot = u / (a.G * hbs), gh = u - slot * (a.G * hbs), g = gh / hbs, hb = gh - g * hbs;
+  Piece sg;
+  if (a.seg_chunks > 0) {
+    sg = find_piece(a.cu, a.N, a.total, slot, a.seg_chunks * Q);
+    if (sg.seq < 0) return;
+  } else {
+    sg.seq = slot;
+    sg.begin = min((int64_t)a.cu[slot], a.total);
+    sg.len = max(min((int64_t)a.cu[slot + 1], a.total) - sg.begin, (int64_t)0);
+    sg.index = 0;
+    sg.count = 1;
+  }
+  const bool last_seg = REV ? sg.index == 0 : sg.index == sg.count - 1;
+  if (a.local && last_seg) return;  // nothing starts from this segment's end
+  const int chunks = (int)((sg.len + Q - 1) / Q);
+  const int c_lo = a.seg_chunks > 0 ? sg.index * a.seg_chunks : 0;
+  const int c_hi = a.seg_chunks > 0 ? min(chunks, c_lo + a.seg_chunks) : chunks;
+  const int64_t slot0 = sg.seq + sg.begin / Q;  // chunk slot of the sequence's first chunk
+
+  const int p0 = wave * 16 * PT;                // the wave's rows of the workgroup's
+  const int hl = p0 / D, hw = hb * HB + hl;     // its head of the workgroup's, and of the group's
+  const int rows_in = min(ROWS, (hpg - hb * HB) * D);
+  const bool mine = hw < hpg;
+  const int64_t col0 = ((int64_t)g * hpg + hb * HB) * D;  // the workgroup's first column of a token's inputs
+  const int h = g * hpg + min(hw, hpg - 1);
+  const int pd = p0 - hl * D;                   // the wave's rows within its head
+  const float Dh = a.Dskip[h];
+  const bool vout = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+
+  if (!state_live(a.live, a.live_slots, sg.seq)) {  // a padded sequence: zero outputs, no state
+    if (OUT)
+      for (int64_t i = tid; i < (int64_t)(c_hi - c_lo) * Q * rows_in; i += 256) {
+        const int64_t t = sg.begin + (int64_t)c_lo * Q + i / rows_in;
+        if (t < sg.begin + sg.len) store_elem(a.out, t * a.H * D + col0 + i % rows_in, 0.f, a.out_dt);
+      }
+    if (OUT && a.fin.base != nullptr && a.fin.slots == nullptr && last_seg)
+      for (int i = tid; i < rows_in * NN; i += 256) store_elem(a.fin.base, ((int64_t)sg.seq * a.H * D + col0) * NN + i, 0.f, a.fin.dtype);
+    return;
+  }
+
+  // state, transposed: S[nt][pt][r] = (n = 16 nt + 4 q + r, p = p0 + 16 pt + l16)
+  f32x4 S[NT][PT];
+  auto state_at = [&](int64_t unit, int nt, int pt) { return ((unit * a.H + h) * D + pd + 16 * pt + l16) * NN + 16 * nt + 4 * q; };
+  const int64_t seg_unit = slot;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) {
+      S[nt][pt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (a.local || !mine) continue;
+      if (a.seg_chunks > 0) {
+        S[nt][pt] = *reinterpret_cast<const f32x4*>(a.seg + state_at(seg_unit, nt, pt));
+      } else if (a.init.base != nullptr) {
+        float f[4];
+        load_vec<4>(a.init.base, state_at(a.init.slots != nullptr ? a.init.slots[sg.seq] : sg.seq, nt, pt), a.init.dtype, f);
+        S[nt][pt] = f32x4{f[0], f[1], f[2], f[3]};
+      }
+    }
+  double total_g = 0.0;
+
+  for (int step = 0; step < c_hi - c_lo; ++step) {
+    const int c = REV ? c_hi - 1 - step : c_lo + step;
+    const int64_t t0 = sg.begin + (int64_t)c * Q;
+    const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
+    const int64_t cs = slot0 + c, cg = cs * a.G + g;
+
+    if (a.blocks != nullptr && mine && (REV ? ((c & 1) || c == chunks - 1) : !(c & 1))) {
+      // the state that meets this block of two chunks, as [n][p]
+      float* o = a.blocks + ((sg.seq + sg.begin / kGradBlock + (c >> 1)) * a.H + h) * (int64_t)(D * NN);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[(16 * nt + 4 * q + r) * D + pd + 16 * pt + l16] = S[nt][pt][r];
+    }
+
+    __syncthreads();  // the chunk before is done with LDS
+    if constexpr (OUT) {
+      constexpr int VPR = NN / 8;
+      for (int i = tid; i < Q * VPR; i += 256) {
+        const int t = i / VPR, n0 = (i - t * VPR) * 8;
+        Frag<BF> f = Frag<BF>::zero();
+        if (t < len) f = frag_from<BF>(a.read, (t0 + t) * a.read_ts + g * NN + n0, a.in_dt);
+        // n = 32 k + 16 b + 4 s + r is stored at 32 k + 8 s + 4 b + r
+        E* d = s_f + t * LDF + (n0 & ~31) + 2 * (n0 & 15) + ((n0 >> 4) & 1) * 4;
+        f.store_halves(d, d + 8);
+        if (NN == 16) Frag<BF>::zero().store_halves(d + 4, d + 12);
+      }
+    }
+    for (int i = tid; i < NN * 8; i += 256)
+      *reinterpret_cast<Frag<BF>*>(s_k + (i >> 3) * LDT + (i & 7) * 8) =
+          Frag<BF>::load(static_cast<const E*>(a.wt) + cg * NN * Q + i * 8);
+    if constexpr (BF) {
+      constexpr int PB = ROWS / 8;
+#pragma unroll
+      for (int k = 0; k < 32 * PB / 256; ++k) {
+        const int i = tid + 256 * k, pb = i % PB, t = (i / PB) * 2;
+        u32x4 v0 = {0u, 0u, 0u, 0u}, v1 = v0;
+        if (8 * pb < rows_in) {
+          const uint16_t* src = static_cast<const uint16_t*>(a.in) + (t0 + t) * a.in_ts + col0 + 8 * pb;
+          if (t < len) v0 = *reinterpret_cast<const u32x4*>(src);
+          if (t + 1 < len) v1 = *reinterpret_cast<const u32x4*>(src + a.in_ts);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          *reinterpret_cast<uint32_t*>(s_x + xt_at<BF, LDT>(8 * pb + 2 * e, t)) = (v0[e] & 0xffffu) | (v1[e] << 16);
+          *reinterpret_cast<uint32_t*>(s_x + xt_at<BF, LDT>(8 * pb + 2 * e + 1, t)) = (v0[e] >> 16) | (v1[e] & 0xffff0000u);
+        }
+      }
+    } else {
+      for (int i = tid; i < Q * (ROWS / 8); i += 256) {
+        const int pb = i % (ROWS / 8), t = i / (ROWS / 8);
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (t < len && 8 * pb < rows_in) load_vec<8>(a.in, (t0 + t) * a.in_ts + col0 + 8 * pb, a.in_dt, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_x[xt_at<BF, LDT>(8 * pb + e, t)] = f[e];
+      }
+    }
+    if (tid < HB * Q) {
+      const int k = tid / Q, t = tid % Q, hh = g * hpg + min(hb * HB + k, hpg - 1);
+      const float* gt = a.gates + (cs * a.H + hh) * 3 * Q;
+      const float ch = gt[t], cl = gt[Q + t], dtp = gt[2 * Q + t];
+      const float to_end = decay_between(gt[Q - 1], gt[2 * Q - 1], ch, cl), from_start = expf(ch + cl);
+      float* o = s_g + k * 5 * Q + t;
+      o[0] = ch;
+      o[Q] = cl;
+      o[2 * Q] = dtp;
+      o[3 * Q] = t < len ? (REV ? from_start : to_end * dtp) : 0.f;
+      o[4 * Q] = REV ? to_end : from_start;
+    }
+    __syncthreads();
+
+    const float* gh_ = s_g + hl * 5 * Q;
+    f32x4 acc[PT][4];
+    if constexpr (OUT) {
+      // products of read and write vectors, weighted by decay: row r of the output, token c of the input
+      {
+        const int r = tid >> 2, c0 = (tid & 3) * 16;
+        float gm[16];
+        const float* src = a.gm + (cg * Q + r) * Q + c0;
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const f32x4 v = *reinterpret_cast<const f32x4*>(src + e);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) gm[e + j] = v[j];
+        }
+#pragma unroll
+        for (int k = 0; k < HB; ++k) {
+          const float* sg_ = s_g + k * 5 * Q;
+          const float rh = sg_[r], rl = sg_[Q + r];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int cc = c0 + 8 * half + e;
+              const bool on = REV ? cc >= r : cc <= r;
+              const float d = REV ? (sg_[cc] - rh) + (sg_[Q + cc] - rl) : (rh - sg_[cc]) + (rl - sg_[Q + cc]);
+              f[e] = on ? expf(d) * gm[8 * half + e] * (REV ? 1.f : sg_[2 * Q + cc]) : 0.f;
+            }
+            *reinterpret_cast<Frag<BF>*>(s_p + (k * Q + r) * LDT + c0 + 8 * half) = Frag<BF>::round(f);
+          }
+        }
+      }
+      // the state's part
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) acc[pt][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        Frag<BF> sf[PT];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] = S[2 * kb][pt][e];
+            f[4 + e] = 2 * kb + 1 < NT ? S[2 * kb + 1 < NT ? 2 * kb + 1 : 0][pt][e] : 0.f;
+          }
+          sf[pt] = Frag<BF>::round(f);
+        }
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const Frag<BF> ff = Frag<BF>::load(s_f + (16 * rt + l16) * LDF + 32 * kb + 8 * q);
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], sf[pt], ff);
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const float f = gh_[4 * Q + 16 * rt + l16];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) acc[pt][rt] *= f;
+      }
+      __syncthreads();  // the products are there
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        Frag<BF> xf[PT];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) xf[pt] = Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q));
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          if (REV ? (ks == 0 && rt >= 2) : (ks == 1 && rt < 2)) continue;  // all above the diagonal
+          const Frag<BF> pf = Frag<BF>::load(s_p + (hl * Q + 16 * rt + l16) * LDT + 32 * ks + 8 * q);
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[pt], pf);
+        }
+      }
+      if (mine) {
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const int t = 16 * rt + l16;
+          if (t < len) {
+            const float sc = REV ? gh_[2 * Q + t] : 1.f;
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) {
+              const int64_t off = (int64_t)h * D + pd + 16 * pt + 4 * q;
+              float v[4];
+              load_vec<4>(a.in, (t0 + t) * a.in_ts + off, a.in_dt, v);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] = acc[pt][rt][r] * sc + Dh * v[r];
+              store_vec<4>(a.out, (t0 + t) * a.H * D + off, v, a.out_dt, vout);
+            }
+          }
+        }
+      }
+    }
+    // the state after the chunk
+    const float* gt = a.gates + (cs * a.H + h) * 3 * Q;
+    const float end_h = gt[Q - 1], end_l = gt[2 * Q - 1], dec = expf(end_h + end_l);
+    total_g += (double)end_h + (double)end_l;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) S[nt][pt] *= dec;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      if (32 * ks >= len) continue;
+      Split<BF> xs[PT];
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        float f[8];
+        Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q)).widen(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= gh_[3 * Q + 32 * ks + 8 * q + e];
+        xs[pt] = Split<BF>::of(f);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const Frag<BF> kf = Frag<BF>::load(s_k + (16 * nt + l16) * LDT + 32 * ks + 8 * q);
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) S[nt][pt] = xs[pt].mma_right(S[nt][pt], kf);
+      }
+    }
+  }
+
+  if (!mine) return;
+  if (a.local) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) *reinterpret_cast<f32x4*>(a.seg + state_at(seg_unit, nt, pt)) = S[nt][pt];
+    if (pd == 0 && lane == 0) a.seg_g[(int64_t)slot * a.H + h] = total_g;
+  } else if (a.fin.base != nullptr && last_seg && (REV || sg.len > 0)) {
+    const int64_t unit = a.fin.slots != nullptr ? a.fin.slots[sg.seq] : sg.seq;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        const float f[4] = {S[nt][pt][0], S[nt][pt][1], S[nt][pt][2], S[nt][pt][3]};
+        store_vec<4>(a.fin.base, state_at(unit, nt, pt), f, a.fin.dtype, true);
+      }
+  }
+}
+
+// ------------------------------------------------------------------ chain
+// Turns the segments' own end states into the states they start from, in
+// place: per (sequence, head), four state elements a thread.
+template <bool REV>
+__global__ void __launch_bounds__(256) gdn_m2s_chain_kernel(const M2ScanArgs a, int elems) {
+  const int seq = blockIdx.z, h = blockIdx.y;
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= elems || !state_live(a.live, a.live_slots, seq)) return;
+  const int P = a.seg_chunks * kScanChunk;
+  const int64_t b = min((int64_t)a.cu[seq], a.total), e = min((int64_t)a.cu[seq + 1], a.total);
+  const int count = (int)max((e - b + P - 1) / P, (int64_t)1);
+  f32x4 S = {0.f, 0.f, 0.f, 0.f};
+  if (a.init.base != nullptr) {
+    float f[4];
+    load_vec<4>(a.init.base, ((a.init.slots != nullptr ? a.init.slots[seq] : (int64_t)seq) * a.H + h) * elems + i, a.init.dtype, f);
+    S = f32x4{f[0], f[1], f[2], f[3]};
+  }
+  const int64_t s0 = seq + b / P;
+  for (int k = 0; k < count; ++k) {
+    const int64_t unit = (s0 + (REV ? count - 1 - k : k)) * a.H + h;
+    f32x4* p = reinterpret_cast<f32x4*>(a.seg + unit * elems + i);
+    if (k + 1 < count) {
+      const f32x4 own = *p;
+      const float dec = (float)exp(a.seg_g[unit]);
+      *p = S;
+      S = S * dec + own;
+    } else {
+      *p = S;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+namespace {
+
+template <bool BF, int D, int NN, bool REV, bool OUT>
+hipError_t walk(const M2ScanArgs& a, hipStream_t s) {
+  using W = WalkGeom<BF, D, NN, OUT>;
+  const int hpg = a.H / a.G, hbs = (hpg + W::HB - 1) / W::HB;
+  const int64_t slots = a.seg_chunks > 0 ? a.N + (a.total + (int64_t)a.seg_chunks * kScanChunk - 1) / ((int64_t)a.seg_chunks * kScanChunk) : a.N;
+  auto* k = gdn_m2s_walk_kernel<BF, D, NN, REV, OUT>;
+  if (W::LDS > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)W::LDS);
+    if (e != hipSuccess) return e;
+  }
+  k<<<(unsigned)(slots * a.G * hbs), 256, W::LDS, s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool BF, int D, int NN>
+hipError_t walk_kind(const M2ScanArgs& a, bool rev, bool out, hipStream_t s) {
+  if (rev) return out ? walk<BF, D, NN, true, true>(a, s) : walk<BF, D, NN, true, false>(a, s);
+  return out ? walk<BF, D, NN, false, true>(a, s) : walk<BF, D, NN, false, false>(a, s);
+}
+
+template <bool BF, int D>
+hipError_t walk_n(const M2ScanArgs& a, int n, bool rev, bool out, hipStream_t s) {
+  if (n == 16) return walk_kind<BF, D, 16>(a, rev, out, s);
+  if (n == 64) return walk_kind<BF, D, 64>(a, rev, out, s);
+  return walk_kind<BF, D, 128>(a, rev, out, s);
+}
+
+template <bool BF>
+hipError_t walk_dn(const M2ScanArgs& a, int d, int n, bool rev, bool out, hipStream_t s) {
+  if (d == 16) return walk_n<BF, 16>(a, n, rev, out, s);
+  if (d == 64) return walk_n<BF, 64>(a, n, rev, out, s);
+  return walk_n<BF, 128>(a, n, rev, out, s);
+}
+
+template <bool BF>
+hipError_t prep(const M2ScanArgs& a, int n, hipStream_t s) {
+  const dim3 grid((unsigned)scan_slots(a.N, a.total, kScanChunk), (unsigned)a.G);
+  if (n == 16) gdn_m2s_prep_kernel<BF, 16><<<grid, 256, 0, s>>>(a);
+  else if (n == 64) gdn_m2s_prep_kernel<BF, 64><<<grid, 256, 0, s>>>(a);
+  else gdn_m2s_prep_kernel<BF, 128><<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t scan_slots(int64_t N, int64_t total, int64_t P) { return N + (total + P - 1) / P; }
+
+// Chunks a segment, 0 for whole sequences.
+int scan_seg_chunks(int64_t N, int64_t total, int H, int G, int d) {
+  const int hb = d == 128 ? 1 : d == 64 ? 2 : 4, hpg = H / G;
+  const int64_t walks = (int64_t)G * ((hpg + hb - 1) / hb), chunks = (total + kScanChunk - 1) / kScanChunk;
+  if (N * walks >= 512 || chunks <= 16) return 0;
+  int64_t per = chunks * walks / 1024;
+  per = per < 8 ? 8 : (per + 1) / 2 * 2;
+  return per >= chunks ? 0 : (int)per;
+}
+
+hipError_t launch_scan_prep(const M2ScanArgs& a, bool bf, int n, hipStream_t s) {
+  return bf ? prep<true>(a, n, s) : prep<false>(a, n, s);
+}
+
+// The walk over all sequences, with the segments' first walk and their chain
+// where a.seg_chunks is set.  out: write outputs (else states only).
+hipError_t launch_scan_walk(M2ScanArgs a, bool bf, int d, int n, bool rev, bool out, hipStream_t s) {
+  auto go = [&](const M2ScanArgs& b, bool o) { return bf ? walk_dn<true>(b, d, n, rev, o, s) : walk_dn<false>(b, d, n, rev, o, s); };
+  if (a.seg_chunks > 0) {
+    M2ScanArgs b = a;
+    b.local = 1;
+    b.blocks = nullptr;
+    hipError_t e = go(b, false);
+    if (e != hipSuccess) return e;
+    const dim3 grid((unsigned)((d * n + 1023) / 1024), (unsigned)a.H, (unsigned)a.N);
+    if (rev) gdn_m2s_chain_kernel<true><<<grid, 256, 0, s>>>(a, d * n);
+    else gdn_m2s_chain_kernel<false><<<grid, 256, 0, s>>>(a, d * n);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  a.local = 0;
+  return go(a, out);
+}
+
+}  // namespace gdn

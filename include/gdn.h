@@ -372,6 +372,67 @@ gdn_status gdn_mamba2_replay_rollback(const gdn_m2_dims* dims, int32_t B, const 
                                       const int32_t* num_rejected, const gdn_m2_ring* ring,
                                       void* stream);
 
+/* Distances between tokens in elements, for inputs that are slices of wider
+ * rows; 0 stands for dense.  x, Bm and Cm: multiples of 8. */
+typedef struct {
+  int64_t x;  /* >= H d */
+  int64_t Bm; /* >= G n */
+  int64_t Cm; /* >= G n */
+  int64_t dt; /* >= H */
+} gdn_m2_strides;
+
+/* The Mamba2 recurrence over N packed variable-length sequences (the prefill
+ * whose states gdn_mamba2_decode_step and the replay calls go on from).
+ *   cu_seqlens  device int32 [N+1], non-decreasing, cu_seqlens[0] = 0,
+ *               cu_seqlens[N] = total_tokens
+ *   x           [total_tokens, H, d] in_dtype, Bm and Cm [total_tokens, G, n],
+ *               params->dt [total_tokens, H]; x, Bm, Cm 16-byte aligned
+ *   strides     NULL: all dense
+ *   state       sequence s starts from slot slot_map[s] and its final state is
+ *               written back there, rounded once per call; a zero-length
+ *               sequence leaves its slot untouched; a slot outside the pool
+ *               marks a padded sequence (zero outputs).  NULL (and slot_map
+ *               NULL): zero initial states, and none kept
+ *   y           [total_tokens, H, d] out_dtype
+ *   workspace   device scratch of at least the queried size, 256-byte aligned,
+ *               not read before it is written; calls that share one must not
+ *               overlap
+ * bf16 inputs with a 16-bit y run on the bf16 matrix instructions (FP32 state
+ * and sums; the state and the decay-weighted B C products are rounded to bf16
+ * where they meet y, and only there); any other pair of types runs in FP32
+ * throughout.  Within 64 tokens a NaN or infinity also reaches earlier tokens
+ * of its own sequence. */
+size_t gdn_mamba2_scan_workspace_bytes(const gdn_m2_dims* dims, int32_t N, int64_t total_tokens);
+gdn_status gdn_mamba2_scan(const gdn_m2_dims* dims, int32_t N, const int32_t* cu_seqlens,
+                           int64_t total_tokens, const void* x, const void* Bm, const void* Cm,
+                           gdn_dtype in_dtype, const gdn_m2_strides* strides,
+                           const gdn_m2_params* params, const gdn_pool* state,
+                           const int32_t* slot_map, void* y, gdn_dtype out_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Gradients of gdn_mamba2_scan from dy and the forward call's inputs.
+ *   init, slot_map  the states that the forward call started from, as they
+ *               were before it (read only), or both NULL for zero states
+ *   dy          [total_tokens, H, d] in_dtype, dense, 16-byte aligned
+ *   dfinal      float32 [N, H, d, n], gradient of the final states, or NULL
+ *   dx, dBm, dCm, ddt  dense, in_dtype, shaped as the inputs
+ *   dA_log, ddt_bias, dD  float32 [H], summed in a fixed order (equal calls
+ *               give equal bits)
+ *   dinit       float32 [N, H, d, n], gradient of the initial states, or NULL
+ * A padded sequence has zero gradients; of a zero-length one dinit is dfinal.
+ * The workspace holds, beside smaller things, two FP32 states per head and 128
+ * tokens. */
+size_t gdn_mamba2_scan_backward_workspace_bytes(const gdn_m2_dims* dims, int32_t N,
+                                                int64_t total_tokens);
+gdn_status gdn_mamba2_scan_backward(const gdn_m2_dims* dims, int32_t N, const int32_t* cu_seqlens,
+                                    int64_t total_tokens, const void* x, const void* Bm,
+                                    const void* Cm, gdn_dtype in_dtype,
+                                    const gdn_m2_strides* strides, const gdn_m2_params* params,
+                                    const gdn_pool* init, const int32_t* slot_map, const void* dy,
+                                    const float* dfinal, void* dx, void* dBm, void* dCm, void* ddt,
+                                    float* dA_log, float* ddt_bias, float* dD, float* dinit,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* -------------------------------------------------------------------- norm
  * Layer or RMS norm of the slices of a row, forward and backward: the norm in
  * front of a recurrent block and, gated and by groups, the one behind its

@@ -6,3 +6,4 @@ import this package; the library never does.
 from .gdn_oracle import *  # noqa: F401,F403
 from .mamba2_oracle import *  # noqa: F401,F403
 from .norm_oracle import *  # noqa: F401,F403
+from .mamba2_scan_oracle import *  # noqa: F401,F403

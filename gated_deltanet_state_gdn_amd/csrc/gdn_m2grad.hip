@@ -23,8 +23,9 @@
 // the diagonal tile row sums and column sums are subtracted.  Diagonal
 // elements do not enter.
 //
-// A decay multiplies last, so that one close to the smallest numbers costs one
-// rounding there.  The states are split in three bf16 terms (bf16 inputs), so all sums that end
+// A decay multiplies last and is the square of a root that the hardware's
+// exponential does not flush, so that one close to the smallest numbers costs
+// two roundings there.  The states are split in three bf16 terms (bf16 inputs), so all sums that end
 // in dt's gradient and the head parameters' are FP32 sums of FP32 products.
 // Parameter sums go through one partial row a block and are added in a fixed
 // order, in 64 bits.
@@ -41,9 +42,15 @@ struct GradGeom {
   static constexpr int LDN = T + (BF ? 8 : 4);    // the summed products [128][LDN], over x and dy after the last head
   static constexpr int ELEMS = 2 * T * LDX > T * LDN ? 2 * T * LDX : T * LDN;
   static constexpr bool BOTH = NT == 8;           // each wave has a column tile of dC and of dB; else one wave has one of them
-  // floats: c (two), dt', read and write factors; row and column sums; the waves' parts
-  static constexpr int FLOATS = 5 * T + 8 * T + 4 * T + 2 * NT * T + 8 + 8;
-  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + FLOATS * 4;
+  static constexpr bool G_LDS = BF || D < 128;    // C_i.B_j in LDS, in registers where that is full
+  static constexpr bool LATE = BF;                // a head's sums are closed while the next head is under way
+  static constexpr int XV = T * DK / 8 / 512;     // vectors of 8 elements of x (and of dy) that a thread stages
+  // a head's results: column sums [8][128], row sums, the diagonal tiles' row and column sums, the diagonal, the state
+  // parts [NT][128] twice, dt', the waves' parts of <S, dS'> and of sum dy.x, e^{c_last}
+  static constexpr int RES = (8 + 4 + 2 * NT + 1) * T + 24;
+  static constexpr int GATES = 4 * T;             // c / 2 (two), e^{c_i}, e^{c_last - c_j}
+  static_assert(!BF || 2 * T * LDN * 2 <= ELEMS * 2 + 36 * 64 * 16, "both terms of the summed products fit over x, dy and C.B");
+  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + (G_LDS ? 36 * 64 * 16 : 0) + (GATES + (LATE ? 2 : 1) * RES) * 4;
 };
 
 // Sums over a 16-lane row's lanes at or after, and at or before, each lane.
@@ -67,7 +74,7 @@ __device__ __forceinline__ float row_prefix(float x) {
 }
 
 template <bool BF, int D, int NN>
-__global__ void __launch_bounds__(512) gdn_m2s_grad_kernel(const M2GradArgs a) {
+__global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a) {
   using W = GradGeom<BF, D, NN>;
   typedef typename W::E E;
   constexpr int T = W::T, NT = W::NT, LDX = W::LDX, LDN = W::LDN, DB = W::DB, Q = kScanChunk;
@@ -76,20 +83,12 @@ __global__ void __launch_bounds__(512) gdn_m2s_grad_kernel(const M2GradArgs a) {
   E* const s_x = reinterpret_cast<E*>(smem);
   E* const s_y = s_x + T * LDX;
   E* const s_n = s_x;
-  float* const s_ch = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E));
+  f32x4* const s_gt = reinterpret_cast<f32x4*>(smem + (size_t)W::ELEMS * sizeof(E));  // tile (i, j <= i) at i (i + 1) / 2 + j, by lane
+  float* const s_ch = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E) + (W::G_LDS ? 36 * 64 * 16 : 0));
   float* const s_cl = s_ch + T;
-  float* const s_dt = s_cl + T;
-  float* const s_er = s_dt + T;      // e^{c_i}
+  float* const s_er = s_cl + T;      // e^{c_i}
   float* const s_ew = s_er + T;      // e^{c_last - c_j}
-  float* const s_col = s_ew + T;     // [8][128] column sums of the tiles below the diagonal, by row block
-  float* const s_row = s_col + 8 * T;  // row sums of them
-  float* const s_rd = s_row + T;     // row and column sums inside the diagonal tiles
-  float* const s_cd = s_rd + T;
-  float* const s_dg = s_cd + T;      // the diagonal
-  float* const s_cs = s_dg + T;      // [NT][128]
-  float* const s_cv = s_cs + NT * T;
-  float* const s_q = s_cv + NT * T;  // [8] parts of <S, dS'>
-  float* const s_dd = s_q + 8;       // [8] parts of sum dy.x
+  float* const s_res = s_ew + T;
 
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -124,121 +123,290 @@ __global__ void __launch_bounds__(512) gdn_m2s_grad_kernel(const M2GradArgs a) {
   const int nt = wave % NT, n16 = 16 * nt;
   const bool do_c = wave < NT, do_b = BOTH || (wave >= NT && wave < 2 * NT);
 
-  // G for the wave's 16 rows: C_i . B_j
-  f32x4 G[8], Ns[8];
+  // the next head's tokens and states before it travel in registers while this head is under way, the gradients of the
+  // states after it while dC's part is
+  Frag<BF> vx[W::XV], vy[W::XV];
+  f32x4 vs[2 * DB], vr[2 * DB];
+  float vg[7];
+  auto fetch_tokens = [&](int h) {
 #pragma unroll
-  for (int jt = 0; jt < 8; ++jt) G[jt] = Ns[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < W::XV; ++k) {
+      const int i = tid + 512 * k, t = i / (W::DK / 8), p0 = (i - t * (W::DK / 8)) * 8;
+      vx[k] = vy[k] = Frag<BF>::zero();
+      if (t < len && p0 < D) {
+        vx[k] = frag_from<BF>(a.x, t0 * a.x_ts + (int64_t)h * D, t * (uint32_t)a.x_ts + p0, a.dt_in);
+        vy[k] = frag_from<BF>(a.dy, (t0 * a.H + h) * D, t * (uint32_t)(a.H * D) + p0, a.dt_in);
+      }
+    }
+    if (tid < T) {
+      const float* g0 = a.gates + (slot64 * a.H + h) * 3 * Q;
+      const float* g1 = g0 + (len > Q ? (int64_t)a.H * 3 * Q : 0);  // a block's second chunk, where there is one
+      const float* gt = tid < Q ? g0 : g1;
+      vg[0] = gt[tid % Q];
+      vg[1] = gt[Q + tid % Q];
+      vg[2] = gt[2 * Q + tid % Q];
+      vg[3] = g0[Q - 1];
+      vg[4] = g0[2 * Q - 1];
+      vg[5] = g1[Q - 1];
+      vg[6] = g1[2 * Q - 1];
+    }
+  };
+  auto commit_tokens = [&](float* res) {
+#pragma unroll
+    for (int k = 0; k < W::XV; ++k) {
+      const int i = tid + 512 * k, t = i / (W::DK / 8), p0 = (i - t * (W::DK / 8)) * 8;
+      *reinterpret_cast<Frag<BF>*>(s_x + t * LDX + p0) = vx[k];
+      *reinterpret_cast<Frag<BF>*>(s_y + t * LDX + p0) = vy[k];
+    }
+    if (tid < T) {
+      // prefix sums over the block: the second chunk's follow the first's total
+      const double tot0 = (double)vg[3] + (double)vg[4];
+      const double last = len > Q ? tot0 + ((double)vg[5] + (double)vg[6]) : tot0;
+      double c = (double)vg[0] + (double)vg[1];
+      float dtp = vg[2];
+      if (tid >= Q) {
+        c = len > Q ? tot0 + c : tot0;
+        dtp = len > Q ? dtp : 0.f;
+      }
+      const float ch = (float)c;
+      s_ch[tid] = 0.5f * ch;
+      s_cl[tid] = 0.5f * (float)(c - (double)ch);
+      s_er[tid] = exp2f((float)c);
+      s_ew[tid] = exp2f((float)(last - c));
+      res[(8 + 4 + 2 * NT) * T + tid] = dtp;
+      if (tid == 0) res[W::RES - 1] = exp2f((float)last);
+    }
+  };
+  // the states' rows n of this wave's columns, S^T[n][p]
+  auto fetch_state = [&](const float* base, int h, f32x4 (&v)[2 * DB]) {
+#pragma unroll
+    for (int k = 0; k < DB; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        v[2 * k + e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (D >= 32 || 8 * q < D)
+          v[2 * k + e] = *reinterpret_cast<const f32x4*>(at_bytes(base, ((int64_t)slot * a.H + h) * (D * NN) + n16 * D + 32 * k + 4 * e, l16 * D + 8 * q, 4));
+      }
+  };
+  auto split_state = [&](const f32x4 (&v)[2 * DB], Split<BF> (&o)[DB]) {
+#pragma unroll
+    for (int k = 0; k < DB; ++k) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = v[2 * k + (e >> 2)][e & 3];
+      o[k] = Split<BF>::of(f);
+    }
+  };
+
+  // G for the wave's 16 rows: C_i . B_j
+  f32x4 G[W::G_LDS ? 1 : 8], Ns[8];
   {
     const int i = 16 * wave + l16;
 #pragma unroll
-    for (int kb = 0; kb < (NN + 31) / 32; ++kb) {
-      const int n0 = 32 * kb + 8 * q;
-      Frag<BF> cf = Frag<BF>::zero();
-      if (i < len && n0 < NN) cf = frag_from<BF>(a.Cm, (t0 + i) * a.c_ts + g * NN + n0, a.dt_in);
+    for (int jt = 0; jt < 8; ++jt) {
+      Ns[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (jt > wave) continue;
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int jt = 0; jt < 8; ++jt) {
-        if (jt > wave) continue;
-        const int j = 16 * jt + l16;
-        Frag<BF> bf = Frag<BF>::zero();
-        if (j < len && n0 < NN) bf = frag_from<BF>(a.Bm, (t0 + j) * a.b_ts + g * NN + n0, a.dt_in);
-        G[jt] = frag_mma(G[jt], cf, bf);
+      for (int kb = 0; kb < (NN + 31) / 32; ++kb) {
+        const int n0 = 32 * kb + 8 * q, j = 16 * jt + l16;
+        Frag<BF> cf = Frag<BF>::zero(), bf = cf;
+        if (i < len && n0 < NN) cf = frag_from<BF>(a.Cm, t0 * a.c_ts + g * NN, i * (uint32_t)a.c_ts + n0, a.dt_in);
+        if (j < len && n0 < NN) bf = frag_from<BF>(a.Bm, t0 * a.b_ts + g * NN, j * (uint32_t)a.b_ts + n0, a.dt_in);
+        acc = frag_mma(acc, cf, bf);
       }
+      if constexpr (W::G_LDS) s_gt[(wave * (wave + 1) / 2 + jt) * 64 + lane] = acc;
+      else G[jt] = acc;
     }
   }
-  // the wave's columns of C and B in the accumulators' order, kept in the input's width
-  constexpr int CW = BF ? 2 : 4;
-  uint32_t cc[8][CW], bb[8][CW];
-#pragma unroll
-  for (int it = 0; it < 8; ++it) {
-    float cv[4], bv[4];
+  // the wave's columns of C and B in the accumulators' order, kept in the input's width (FP32: read where they are used)
+  uint32_t cc[BF ? 8 : 1][2], bb[BF ? 8 : 1][2];
+  auto column = [&](const void* m, int64_t ts, int it, float (&v)[4]) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int64_t t = t0 + 16 * it + 4 * q + r;
-      const bool in = 16 * it + 4 * q + r < len;
-      cv[r] = in ? load_elem(a.Cm, t * a.c_ts + g * NN + n16 + l16, a.dt_in) : 0.f;
-      bv[r] = in ? load_elem(a.Bm, t * a.b_ts + g * NN + n16 + l16, a.dt_in) : 0.f;
+      const int t = 16 * it + 4 * q + r;
+      v[r] = t < len ? load_elem(at_bytes(m, t0 * ts + g * NN + n16, t * (uint32_t)ts + l16, BF || a.dt_in != GDN_F32 ? 2 : 4), 0, BF ? GDN_BF16 : a.dt_in) : 0.f;
     }
-    if constexpr (BF) {
-      cc[it][0] = pack2<GDN_BF16>(cv[0], cv[1]);
-      cc[it][1] = pack2<GDN_BF16>(cv[2], cv[3]);
-      bb[it][0] = pack2<GDN_BF16>(bv[0], bv[1]);
-      bb[it][1] = pack2<GDN_BF16>(bv[2], bv[3]);
-    } else {
+  };
+  if constexpr (BF)
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      float v[4];
+      column(a.Cm, a.c_ts, it, v);
+      cc[it][0] = pack2<GDN_BF16>(v[0], v[1]);
+      cc[it][1] = pack2<GDN_BF16>(v[2], v[3]);
+      column(a.Bm, a.b_ts, it, v);
+      bb[it][0] = pack2<GDN_BF16>(v[0], v[1]);
+      bb[it][1] = pack2<GDN_BF16>(v[2], v[3]);
+    }
+
+  // closes a head: dt's gradient for the block's tokens and the head's parameter sums (one wave)
+  auto close_head = [&](int h, const float* res) {
+    const float *r_col = res, *r_row = res + 8 * T, *r_rd = r_row + T, *r_cd = r_rd + T, *r_dg = r_cd + T, *r_cs = r_dg + T,
+                *r_cv = r_cs + NT * T, *r_dt = r_cv + NT * T, *r_q = r_dt + T, *r_dd = r_q + 8;
+    // whole tiles with rows after block b and columns before it: 8 lanes a block
+    float whole = 0.f;
+    {
+      const int b = lane >> 3, sub = lane & 7;
+      for (int j = sub; j < 16 * b; j += 8)
+        for (int i = b + 1; i < tiles; ++i) whole += r_col[i * T + j];
+      whole += dpp_mov<0xB1>(whole);
+      whole += dpp_mov<0x4E>(whole);
+      whole += __shfl_xor(whole, 4, 64);
+    }
+    float qs = 0.f, dd = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      qs += i < NT ? r_q[i] : 0.f;
+      dd += i < tiles ? r_dd[i] : 0.f;
+    }
+    // token 64 k + lane, in the block of 16 tokens 4 k + q
+    float cv[2], co[2], dtp[2], pre[2], suf[2], cs_suf[2], cv_pre[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int t = 64 * k + lane, b = 4 * k + q;
+      const bool in = t < 16 * tiles;
+      float cs = 0.f;
+      cv[k] = co[k] = 0.f;
+      dtp[k] = r_dt[t];
+      if (in) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          cs += r_cs[i * T + t];
+          cv[k] += r_cv[i * T + t];
+        }
+        for (int i = b + 1; i < tiles; ++i) co[k] += r_col[i * T + t];
+      }
+      // inside the block: earlier columns of later rows, later rows of earlier columns, and the diagonal tile
+      const float r0 = in ? r_row[t] + (r_rd[t] - r_cd[t]) : 0.f;
+      pre[k] = row_shift<0x111>(row_prefix(co[k]));  // before t, not at it
+      suf[k] = row_suffix(r0);
+      cs_suf[k] = row_suffix(cs);
+      cv_pre[k] = row_prefix(cv[k]);
+      pre[k] += row_shift<0x111>(cv_pre[k]);
+    }
+    // the blocks' totals of the state parts, from both sides
+    float after = 0.f, before = 0.f;
+#pragma unroll
+    for (int k = 1; k >= 0; --k)
+#pragma unroll
+      for (int r = 3; r >= 0; --r) {
+        const float tot = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cs_suf[k]), 16 * r));
+        if (q == r) suf[k] += cs_suf[k] + after;
+        after += tot;
+      }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        cc[it][r] = __float_as_uint(cv[r]);
-        bb[it][r] = __float_as_uint(bv[r]);
+        const float tot = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cv_pre[k]), 16 * r + 15));
+        if (q == r) pre[k] += before;
+        before += tot;
+      }
+    const float A = expf(a.A_log[h]), bias = a.dt_bias[h], eq = qs * res[W::RES - 1];
+    float sa = 0.f, sb = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int t = 64 * k + lane;
+      const float wh = __shfl(whole, 8 * (4 * k + q), 64);
+      if (t < len) {
+        const float dg = ((wh + pre[k]) + suf[k]) + eq;
+        // dt' x_t.X_t over dt'; a step that underflows to zero has a slope of zero with it
+        const float own = dtp[k] > 0.f ? ((co[k] + r_cd[t]) + (r_dg[t] + cv[k])) / dtp[k] : 0.f;
+        const float raw = load_elem(a.dt, (t0 + t) * a.dt_ts + h, a.dt_in) + bias;
+        const float d = (own - A * dg) * sigmoid_f(raw);
+        store_elem(a.ddt, (t0 + t) * a.H + h, d, a.dt_in);
+        sa -= A * dtp[k] * dg;
+        sb += d;
       }
     }
-  }
-  auto value = [](const uint32_t (&w)[CW], int r) {
-    if constexpr (BF) return (r & 1) ? unpack_hi<GDN_BF16>(w[r >> 1]) : unpack_lo<GDN_BF16>(w[r >> 1]);
-    else return __uint_as_float(w[r]);
+    sa = wave_sum(sa);
+    sb = wave_sum(sb);
+    if (lane == 0) {
+      float* o = a.part + ((int64_t)slot * a.H + h) * 3;
+      o[0] = sa;
+      o[1] = sb;
+      o[2] = dd;
+    }
   };
 
   f32x4 dC[8], dB[8];
 #pragma unroll
   for (int it = 0; it < 8; ++it) dC[it] = dB[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  fetch_tokens(g * hpg + h_lo);
+  fetch_state(a.fwd, g * hpg + h_lo, vs);
   for (int hi = h_lo; hi < h_hi; ++hi) {
-    const int h = g * hpg + hi;
+    const int h = g * hpg + hi, h_next = min(h + 1, g * hpg + h_hi - 1);
+    float* const res = s_res + (W::LATE ? (hi & 1) * W::RES : 0);
+    float *r_col = res, *r_row = res + 8 * T, *r_rd = r_row + T, *r_cd = r_rd + T, *r_dg = r_cd + T, *r_cs = r_dg + T,
+          *r_cv = r_cs + NT * T, *r_q = r_cv + NT * T + T, *r_dd = r_q + 8;
     __syncthreads();  // the head before is done with LDS
-    constexpr int VPR = W::DK / 8;
-    for (int i = tid; i < T * VPR; i += 512) {
-      const int t = i / VPR, p0 = (i - t * VPR) * 8;
-      Frag<BF> xv = Frag<BF>::zero(), yv = xv;
-      if (t < len && p0 < D) {
-        xv = frag_from<BF>(a.x, (t0 + t) * a.x_ts + (int64_t)h * D + p0, a.dt_in);
-        yv = frag_from<BF>(a.dy, ((t0 + t) * a.H + h) * D + p0, a.dt_in);
-      }
-      *reinterpret_cast<Frag<BF>*>(s_x + t * LDX + p0) = xv;
-      *reinterpret_cast<Frag<BF>*>(s_y + t * LDX + p0) = yv;
-    }
-    if (tid < T) {
-      // prefix sums over the block: the second chunk's follow the first's total
-      const float* g0 = a.gates + (slot64 * a.H + h) * 3 * Q;
-      const float* g1 = g0 + (int64_t)a.H * 3 * Q;
-      const double tot0 = (double)g0[Q - 1] + (double)g0[2 * Q - 1];
-      double c = tot0, last = tot0;
-      float dtp = 0.f;
-      if (len > Q) last = tot0 + ((double)g1[Q - 1] + (double)g1[2 * Q - 1]);
-      if (tid < Q) {
-        c = (double)g0[tid] + (double)g0[Q + tid];
-        dtp = g0[2 * Q + tid];
-      } else if (len > Q) {
-        c = tot0 + ((double)g1[tid - Q] + (double)g1[tid]);
-        dtp = g1[Q + tid];
-      }
-      const float ch = (float)c;
-      s_ch[tid] = ch;
-      s_cl[tid] = (float)(c - (double)ch);
-      s_dt[tid] = dtp;
-      s_er[tid] = expf((float)c);
-      s_ew[tid] = expf((float)(last - c));
-    }
-    // the states' rows n of this wave's columns: S^T[n][p]
-    Split<BF> sc[DB], sb[DB];
-    float qs = 0.f;
-    {
-      const int64_t at = ((int64_t)slot * a.H + h) * (D * NN) + (n16 + l16) * D;
-#pragma unroll
-      for (int k = 0; k < DB; ++k) {
-        float f[8], r[8];
-        const int p0 = 32 * k + 8 * q;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = r[e] = 0.f;
-        if (p0 < D) {
-          load_vec<8>(a.fwd, at + p0, GDN_F32, f);
-          load_vec<8>(a.rev, at + p0, GDN_F32, r);
-        }
-        if (do_c)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) qs += f[e] * r[e];
-        sc[k] = Split<BF>::of(f);
-        sb[k] = Split<BF>::of(r);
-      }
-    }
+    commit_tokens(res);
     __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    fetch_state(a.rev, h, vr);
+    __builtin_amdgcn_sched_barrier(0);
+
+    // state parts of dC and dB for the wave's 16 columns
+    if (do_c) {
+      Split<BF> sc[DB];
+      split_state(vs, sc);
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        if (it >= tiles) continue;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < DB; ++k) v = sc[k].mma_right(v, Frag<BF>::load(s_y + (16 * it + l16) * LDX + 32 * k + 8 * q));
+        float s[4], col[4];
+        if constexpr (!BF) column(a.Cm, a.c_ts, it, col);
+        const f32x4 er = *reinterpret_cast<const f32x4*>(s_er + 16 * it + 4 * q);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (BF) col[r] = (r & 1) ? unpack_hi<GDN_BF16>(cc[it][r >> 1]) : unpack_lo<GDN_BF16>(cc[it][r >> 1]);
+          s[r] = er[r] * row16_sum(v[r] * col[r]);
+        }
+        dC[it] += v * er;
+        if (l16 < 4) r_cs[nt * T + 16 * it + 4 * q + l16] = l16 == 0 ? s[0] : l16 == 1 ? s[1] : l16 == 2 ? s[2] : s[3];
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (do_c) {
+      float qs = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2 * DB; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qs += vs[k][e] * vr[k][e];
+      qs = wave_sum(qs);
+      if (lane == 0) r_q[wave] = qs;
+    }
+    Split<BF> sb[DB];
+    split_state(vr, sb);
+    __builtin_amdgcn_sched_barrier(0);
+    fetch_state(a.fwd, h_next, vs);
+    fetch_tokens(h_next);
+    __builtin_amdgcn_sched_barrier(0);
+    if (do_b) {
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        if (it >= tiles) continue;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < DB; ++k) v = sb[k].mma_right(v, Frag<BF>::load(s_x + (16 * it + l16) * LDX + 32 * k + 8 * q));
+        float s[4], col[4];
+        if constexpr (!BF) column(a.Bm, a.b_ts, it, col);
+        const f32x4 ew = *reinterpret_cast<const f32x4*>(s_ew + 16 * it + 4 * q);
+        const f32x4 dtj = *reinterpret_cast<const f32x4*>(r_cv + NT * T + 16 * it + 4 * q);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (BF) col[r] = (r & 1) ? unpack_hi<GDN_BF16>(bb[it][r >> 1]) : unpack_lo<GDN_BF16>(bb[it][r >> 1]);
+          s[r] = ew[r] * (dtj[r] * row16_sum(v[r] * col[r]));
+        }
+        dB[it] += v * (ew * dtj);
+        if (l16 < 4) r_cv[nt * T + 16 * it + 4 * q + l16] = l16 == 0 ? s[0] : l16 == 1 ? s[1] : l16 == 2 ? s[2] : s[3];
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
 
     // products of dy and x for the wave's 16 rows
     if (wave < tiles) {
@@ -255,31 +423,33 @@ __global__ void __launch_bounds__(512) gdn_m2s_grad_kernel(const M2GradArgs a) {
 #pragma unroll
       for (int jt = 0; jt < 8; ++jt) {
         if (jt > wave) continue;
-        f32x4 w = {0.f, 0.f, 0.f, 0.f};
+        f32x4 w = {0.f, 0.f, 0.f, 0.f}, gt;
 #pragma unroll
         for (int k = 0; k < DB; ++k) w = frag_mma(w, yf[k], Frag<BF>::load(s_x + (16 * jt + l16) * LDX + 32 * k + 8 * q));
+        if constexpr (W::G_LDS) gt = s_gt[(wave * (wave + 1) / 2 + jt) * 64 + lane];
+        else gt = G[jt];
         const int j = 16 * jt + l16;
-        const float jh = s_ch[j], jl = s_cl[j], dtj = s_dt[j];
+        const float jh = s_ch[j], jl = s_cl[j], dtj = r_cv[NT * T + j];
+        float col = 0.f;
         if (jt < wave) {
-          float col = 0.f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float e = decay_between(ih[r], il[r], jh, jl), dw = dtj * w[r];
+            const float e2 = __builtin_amdgcn_exp2f((ih[r] - jh) + (il[r] - jl)), e = e2 * e2, dw = dtj * w[r];
             Ns[jt][r] += e * dw;
-            const float m = e * (dw * G[jt][r]);
+            const float m = e * (dw * gt[r]);
             col += m;
             rowo[r] += m;
           }
           col = xor_sum_from<16>(col);
-          if (q == 0) s_col[wave * T + j] = col;
+          if (q == 0) r_col[wave * T + j] = col;
         } else {
-          float col = 0.f, rowd[4], diag = 0.f, wd = 0.f;
+          float rowd[4], diag = 0.f, wd = 0.f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int i = i0 + r;
-            const float e = j <= i ? decay_between(ih[r], il[r], jh, jl) : 0.f, dw = dtj * w[r];
+            const float e2 = j <= i ? __builtin_amdgcn_exp2f((ih[r] - jh) + (il[r] - jl)) : 0.f, e = e2 * e2, dw = dtj * w[r];
             Ns[jt][r] += e * dw;
-            const float m = e * (dw * G[jt][r]);
+            const float m = e * (dw * gt[r]);
             if (i == j) {
               diag = m;
               wd = w[r];
@@ -293,193 +463,62 @@ __global__ void __launch_bounds__(512) gdn_m2s_grad_kernel(const M2GradArgs a) {
           diag = xor_sum_from<16>(diag);
           wd = wave_sum(wd);
           if (q == 0) {
-            s_cd[j] = col;
-            s_dg[j] = diag;
+            r_cd[j] = col;
+            r_dg[j] = diag;
           }
-          if (lane == 0) s_dd[wave] = wd;
+          if (lane == 0) r_dd[wave] = wd;
           if (l16 < 4) {
-            const float v = l16 == 0 ? rowd[0] : l16 == 1 ? rowd[1] : l16 == 2 ? rowd[2] : rowd[3];
-            const float o = l16 == 0 ? rowo[0] : l16 == 1 ? rowo[1] : l16 == 2 ? rowo[2] : rowo[3];
-            s_rd[i0 + l16] = v;
-            s_row[i0 + l16] = o;
+            r_rd[i0 + l16] = l16 == 0 ? rowd[0] : l16 == 1 ? rowd[1] : l16 == 2 ? rowd[2] : rowd[3];
+            r_row[i0 + l16] = l16 == 0 ? rowo[0] : l16 == 1 ? rowo[1] : l16 == 2 ? rowo[2] : rowo[3];
           }
         }
       }
     }
-    // state parts of dC and dB for the wave's 16 columns
-    if (do_c) {
-      qs = wave_sum(qs);
-      if (lane == 0) s_q[wave] = qs;
-#pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        if (it >= tiles) continue;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < DB; ++k) v = sc[k].mma_right(v, Frag<BF>::load(s_y + (16 * it + l16) * LDX + 32 * k + 8 * q));
-        float s[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float e = s_er[16 * it + 4 * q + r];
-          s[r] = e * row16_sum(v[r] * value(cc[it], r));
-          v[r] *= e;
-        }
-        dC[it] += v;
-        if (l16 < 4) s_cs[nt * T + 16 * it + 4 * q + l16] = l16 == 0 ? s[0] : l16 == 1 ? s[1] : l16 == 2 ? s[2] : s[3];
-      }
+    if constexpr (W::LATE) {
+      if (wave == 0 && hi > h_lo) close_head(h - 1, s_res + ((hi - 1) & 1) * W::RES);
+    } else {
+      __syncthreads();
+      if (wave == 0) close_head(h, res);
     }
-    if (do_b) {
-#pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        if (it >= tiles) continue;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < DB; ++k) v = sb[k].mma_right(v, Frag<BF>::load(s_x + (16 * it + l16) * LDX + 32 * k + 8 * q));
-        float s[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = 16 * it + 4 * q + r;
-          const float e = s_ew[j], dtj = s_dt[j];
-          s[r] = e * (dtj * row16_sum(v[r] * value(bb[it], r)));
-          v[r] *= e * dtj;
-        }
-        dB[it] += v;
-        if (l16 < 4) s_cv[nt * T + 16 * it + 4 * q + l16] = l16 == 0 ? s[0] : l16 == 1 ? s[1] : l16 == 2 ? s[2] : s[3];
-      }
-    }
+  }
+  if constexpr (W::LATE) {
     __syncthreads();
-
-    if (wave == 0) {
-      // dg: token 64 k + lane, its block of 16 b = 4 k + q
-      // whole tiles with rows after block b and columns before it: 8 lanes a block
-      float whole = 0.f;
-      {
-        const int b = lane >> 3, sub = lane & 7;
-        for (int j = sub; j < 16 * b; j += 8) {
-          float c = 0.f;
-          for (int i = b + 1; i < tiles; ++i) c += s_col[i * T + j];
-          whole += c;
-        }
-        whole += dpp_mov<0xB1>(whole);
-        whole += dpp_mov<0x4E>(whole);
-        whole += __shfl_xor(whole, 4, 64);
-      }
-      float qs_ = 0.f, dd = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        qs_ += i < NT ? s_q[i < NT ? i : 0] : 0.f;
-        dd += i < tiles ? s_dd[i] : 0.f;
-      }
-      float cs[2], cv[2], co[2], dtp[2], pre[2], suf[2], cs_suf[2], cv_pre[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int t = 64 * k + lane, b = 4 * k + q;
-        const bool in = t < 16 * tiles;
-        cs[k] = cv[k] = co[k] = 0.f;
-        dtp[k] = s_dt[t];
-        if (in) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            cs[k] += s_cs[i * T + t];
-            cv[k] += s_cv[i * T + t];
-          }
-          for (int i = b + 1; i < tiles; ++i) co[k] += s_col[i * T + t];
-        }
-        // inside the block: earlier columns of later rows, later rows of earlier columns, and the diagonal tile
-        const float r0 = in ? s_row[t] + (s_rd[t] - s_cd[t]) : 0.f;
-        pre[k] = row_shift<0x111>(row_prefix(co[k]));  // before t, not at it
-        suf[k] = row_suffix(r0);
-        cs_suf[k] = row_suffix(cs[k]);
-        cv_pre[k] = row_prefix(cv[k]);
-        pre[k] += row_shift<0x111>(cv_pre[k]);
-      }
-      // the blocks' totals of the state parts, from both sides
-      float after = 0.f, before = 0.f;
-#pragma unroll
-      for (int k = 1; k >= 0; --k)
-#pragma unroll
-        for (int r = 3; r >= 0; --r) {
-          const float tot = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cs_suf[k]), 16 * r));
-          if (q == r) suf[k] += cs_suf[k] + after;
-          after += tot;
-        }
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float tot = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cv_pre[k]), 16 * r + 15));
-          if (q == r) pre[k] += before;
-          before += tot;
-        }
-      const float A = expf(a.A_log[h]), bias = a.dt_bias[h], eq = qs_ * s_er[len - 1];
-      float sa = 0.f, sb_ = 0.f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int t = 64 * k + lane;
-        const float wh = __shfl(whole, 8 * (4 * k + q), 64);
-        if (t < len) {
-          const float dg = ((wh + pre[k]) + suf[k]) + eq;
-          // dt' x_t.X_t over dt'; a step that underflows to zero has a slope of zero with it
-          const float own = dtp[k] > 0.f ? ((co[k] + s_cd[t]) + (s_dg[t] + cv[k])) / dtp[k] : 0.f;
-          const float raw = load_elem(a.dt, (t0 + t) * a.dt_ts + h, a.dt_in) + bias;
-          const float d = (own - A * dg) * sigmoid_f(raw);
-          store_elem(a.ddt, (t0 + t) * a.H + h, d, a.dt_in);
-          sa -= A * dtp[k] * dg;
-          sb_ += d;
-        }
-      }
-      sa = wave_sum(sa);
-      sb_ = wave_sum(sb_);
-      if (lane == 0) {
-        float* o = a.part + ((int64_t)slot * a.H + h) * 3;
-        o[0] = sa;
-        o[1] = sb_;
-        o[2] = dd;
-      }
-    }
+    if (wave == 0) close_head(g * hpg + h_hi - 1, s_res + ((h_hi - 1) & 1) * W::RES);
   }
 
   // the heads' summed products with B and C, in two bf16 terms (bf16 inputs): as [i][j] for dC, as [j][i] for dB
 #pragma unroll
   for (int turn = 0; turn < 2; ++turn) {
-    f32x4 left[8];
+    constexpr int TERMS = BF ? 2 : 1;
+    __syncthreads();
 #pragma unroll
-    for (int jt = 0; jt < 8; ++jt) left[jt] = Ns[jt];
+    for (int jt = 0; jt < 8; ++jt)
 #pragma unroll
-    for (int term = 0; term < (BF ? 2 : 1); ++term) {
-      __syncthreads();
-#pragma unroll
-      for (int jt = 0; jt < 8; ++jt) {
-        E e[4];
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * wave + 4 * q + r, j = 16 * jt + l16;
+        E* d = s_n + (turn == 0 ? i * LDN + j : j * LDN + i);
         if constexpr (BF) {
-          const uint32_t w0 = pack2<GDN_BF16>(left[jt][0], left[jt][1]), w1 = pack2<GDN_BF16>(left[jt][2], left[jt][3]);
-          e[0] = (E)w0;
-          e[1] = (E)(w0 >> 16);
-          e[2] = (E)w1;
-          e[3] = (E)(w1 >> 16);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) left[jt][r] -= bf16_bits_to_f32(e[r]);
+          const uint32_t hi = pack2<GDN_BF16>(Ns[jt][r], 0.f) & 0xffffu;
+          d[0] = (E)hi;
+          d[T * LDN] = (E)pack2<GDN_BF16>(Ns[jt][r] - bf16_bits_to_f32(hi), 0.f);
         } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) e[r] = left[jt][r];
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * wave + 4 * q + r, j = 16 * jt + l16;
-          s_n[turn == 0 ? i * LDN + j : j * LDN + i] = e[r];
+          d[0] = Ns[jt][r];
         }
       }
-      __syncthreads();
-      const bool mine = turn == 0 ? do_c : do_b;
-      if (mine) {
-        const E* src = static_cast<const E*>(turn == 0 ? a.bt : a.ct);
+    __syncthreads();
+    if (turn == 0 ? do_c : do_b) {
+      const void* src = turn == 0 ? a.bt : a.ct;
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-          if (32 * kb >= len) continue;
-          const Frag<BF> f = Frag<BF>::load(src + (((slot64 + (kb >> 1)) * a.G + g) * NN + n16 + l16) * Q + 32 * (kb & 1) + 8 * q);
+      for (int kb = 0; kb < 4; ++kb) {
+        if (32 * kb >= len) continue;
+        const Frag<BF> f = Frag<BF>::load(reinterpret_cast<const E*>(
+            at_bytes(src, (((slot64 + (kb >> 1)) * a.G + g) * NN + n16) * Q + 32 * (kb & 1), l16 * Q + 8 * q, sizeof(E))));
 #pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            if (turn == 0 ? 2 * kb > it : 2 * kb + 1 < it) continue;  // no pair j <= i in the tile
-            const Frag<BF> nf = Frag<BF>::load(s_n + (16 * it + l16) * LDN + 32 * kb + 8 * q);
+        for (int it = 0; it < 8; ++it) {
+          if (turn == 0 ? 2 * kb > it : 2 * kb + 1 < it) continue;  // no pair j <= i in the tile
+#pragma unroll
+          for (int k = TERMS - 1; k >= 0; --k) {
+            const Frag<BF> nf = Frag<BF>::load(s_n + k * T * LDN + (16 * it + l16) * LDN + 32 * kb + 8 * q);
             if (turn == 0) dC[it] = frag_mma(dC[it], nf, f);
             else dB[it] = frag_mma(dB[it], nf, f);
           }

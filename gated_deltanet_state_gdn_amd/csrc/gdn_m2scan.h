@@ -52,6 +52,14 @@ __device__ __forceinline__ bool state_live(const int32_t* slots, int64_t num_slo
   return s >= 0 && (int64_t)s < num_slots;
 }
 
+// ------------------------------------------------------------------ addresses
+// A uniform 64-bit base and a 32-bit lane offset, in elements of `EB` bytes: a
+// load then takes its base from scalar registers, and a loop over many
+// addresses keeps one vector register each instead of two.
+__device__ __forceinline__ const char* at_bytes(const void* base, int64_t uniform, uint32_t lane, int eb) {
+  return static_cast<const char*>(base) + uniform * eb + (uint32_t)(lane * (uint32_t)eb);
+}
+
 // ------------------------------------------------------------------ fragments
 // A fragment is the 8 values that a lane gives a 16 x 16 product over 32 k's:
 // lane l holds row (or column) l % 16 and the k's stored at 8 (l / 16) .. + 7.
@@ -149,14 +157,15 @@ struct Split {
   }
 };
 
-// 8 consecutive input elements from element i as a fragment (16-byte aligned).
+// 8 consecutive input elements from element (uniform + lane) as a fragment
+// (16-byte aligned; BF: the input is bf16).
 template <bool BF>
-__device__ __forceinline__ Frag<BF> frag_from(const void* p, int64_t i, int dt) {
+__device__ __forceinline__ Frag<BF> frag_from(const void* p, int64_t uniform, uint32_t lane, int dt) {
   if constexpr (BF) {
-    return Frag<true>::load(static_cast<const uint16_t*>(p) + i);
+    return Frag<true>::load(reinterpret_cast<const uint16_t*>(at_bytes(p, uniform, lane, 2)));
   } else {
     float f[8];
-    load_vec<8>(p, i, dt, f);
+    load_vec<8>(at_bytes(p, uniform, lane, dt == GDN_F32 ? 4 : 2), 0, dt, f);
     return Frag<false>::round(f);
   }
 }
@@ -167,12 +176,6 @@ __device__ __forceinline__ float row16_sum(float x) {
   x += dpp_mov<0x128>(x);
   x += dpp_mov<0x124>(x);
   return x;
-}
-
-// A prefix sum of log-decays kept as two floats: differences of far positions
-// keep FP32 accuracy.
-__device__ __forceinline__ float decay_between(float hi_to, float lo_to, float hi_from, float lo_from) {
-  return expf((hi_to - hi_from) + (lo_to - lo_from));
 }
 
 }  // namespace gdn

@@ -30,6 +30,10 @@
 // Other inputs or an FP32 output take the FP32 MFMA throughout.
 #include "gdn_m2scan.h"
 
+#ifndef GDN_SEG_WALKS
+#define GDN_SEG_WALKS 768
+#endif
+
 namespace gdn {
 
 // ------------------------------------------------------------------ prep
@@ -54,8 +58,8 @@ __global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
     const int t = u / VPR, n0 = (u - t * VPR) * 8;
     Frag<BF> r = Frag<BF>::zero(), w = r;
     if (t < len && n0 < NN) {
-      r = frag_from<BF>(a.read, (t0 + t) * a.read_ts + g * NN + n0, a.in_dt);
-      w = frag_from<BF>(a.write, (t0 + t) * a.write_ts + g * NN + n0, a.in_dt);
+      r = frag_from<BF>(a.read, t0 * a.read_ts + g * NN, t * (uint32_t)a.read_ts + n0, a.in_dt);
+      w = frag_from<BF>(a.write, t0 * a.write_ts + g * NN, t * (uint32_t)a.write_ts + n0, a.in_dt);
     }
     *reinterpret_cast<Frag<BF>*>(s_r + t * LD + n0) = r;
     *reinterpret_cast<Frag<BF>*>(s_w + t * LD + n0) = w;
@@ -68,7 +72,7 @@ __global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
     double c = 0.0;
     if (lane < len) {
       dtp = softplus_f(load_elem(a.dt, (t0 + lane) * a.dt_ts + h, a.in_dt) + a.dt_bias[h]);
-      c = -(double)(expf(a.A_log[h]) * dtp);
+      c = -(double)(expf(a.A_log[h]) * dtp) * 1.4426950408889634;  // in powers of two
     }
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -112,12 +116,17 @@ __global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
 }
 
 // ------------------------------------------------------------------ walk
-template <bool BF, int D, int NN, bool OUT>
+// Waves of a walk: eight over 256 state rows (four heads of 64) share the read
+// and write vectors of a chunk; four where a group has no more rows than 128,
+// and in FP32, whose operands are twice as wide.
+template <bool BF, int D, int NN, int NW, bool OUT>
 struct WalkGeom {
   typedef typename Frag<BF>::E E;
+  static constexpr int THREADS = 64 * NW;
   static constexpr int PT = D == 16 ? 1 : 2;           // 16-row tiles of a wave
-  static constexpr int ROWS = 64 * PT;                 // state rows of the workgroup
+  static constexpr int ROWS = 16 * PT * NW;            // state rows of the workgroup
   static constexpr int HB = ROWS / D;                  // its heads
+  static constexpr int WPH = NW / HB;                  // waves of a head
   static constexpr int NT = NN / 16, KB = (NN + 31) / 32;
   static constexpr int LDF = KB * 32 + (BF ? 8 : 4);   // read vectors [64][LDF], columns in accumulator order
   static constexpr int LDT = kScanChunk + (BF ? 8 : 4);  // write vectors [NN][LDT], inputs [ROWS][LDT], products [HB][64][LDT]
@@ -125,6 +134,9 @@ struct WalkGeom {
   static constexpr int ELEMS = P0 + (OUT ? HB * kScanChunk * LDT : 0);
   // floats a head: c (two), dt', the input's weight, the read factor
   static constexpr size_t LDS = ((size_t)ELEMS * sizeof(E) + 15) / 16 * 16 + (size_t)HB * 5 * kScanChunk * 4;
+  // vectors of 8 elements that a thread stages
+  static constexpr int FV = (kScanChunk * NN / 8 + THREADS - 1) / THREADS;
+  static constexpr int XV = kScanChunk * ROWS / 8 / THREADS;
 };
 
 // Where (row p, token t) of the transposed inputs lies: in 16-bit form groups
@@ -135,11 +147,12 @@ __device__ __forceinline__ int xt_at(int p, int t) {
   return p * LDT + (BF ? ((((t >> 3) ^ (p >> 3)) & 7) << 3 | (t & 7)) : t);
 }
 
-template <bool BF, int D, int NN, bool REV, bool OUT>
-__global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
-  using W = WalkGeom<BF, D, NN, OUT>;
+template <bool BF, int D, int NN, int NW, bool REV, bool OUT>
+__global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
+  using W = WalkGeom<BF, D, NN, NW, OUT>;
   typedef typename W::E E;
   constexpr int PT = W::PT, HB = W::HB, NT = W::NT, KB = W::KB, LDF = W::LDF, LDT = W::LDT, ROWS = W::ROWS, Q = kScanChunk;
+  constexpr int THREADS = W::THREADS, WPH = W::WPH, PB = ROWS / 8;
   extern __shared__ __align__(16) unsigned char smem[];
   E* const s_f = reinterpret_cast<E*>(smem) + W::F0;
   E* const s_k = reinterpret_cast<E*>(smem) + W::K0;
@@ -147,7 +160,8 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
   E* const s_p = reinterpret_cast<E*>(smem) + W::P0;
   float* const s_g = reinterpret_cast<float*>(smem + ((size_t)W::ELEMS * sizeof(E) + 15) / 16 * 16);  // [HB][5][64]
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l16 = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hpg = a.H / a.G, hbs = (hpg + HB - 1) / HB;
   const int u = xcd_unit(blockIdx.x, gridDim.x);
   const int slot = u / (a.G * hbs), gh = u - slot * (a.G * hbs), g = gh / hbs, hb = gh - g * hbs;
@@ -170,30 +184,28 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
   const int64_t slot0 = sg.seq + sg.begin / Q;  // chunk slot of the sequence's first chunk
 
   const int p0 = wave * 16 * PT;                // the wave's rows of the workgroup's
-  const int hl = p0 / D, hw = hb * HB + hl;     // its head of the workgroup's, and of the group's
+  const int hl = wave / WPH, hw = hb * HB + hl; // its head of the workgroup's, and of the group's
   const int rows_in = min(ROWS, (hpg - hb * HB) * D);
   const bool mine = hw < hpg;
   const int64_t col0 = ((int64_t)g * hpg + hb * HB) * D;  // the workgroup's first column of a token's inputs
   const int h = g * hpg + min(hw, hpg - 1);
   const int pd = p0 - hl * D;                   // the wave's rows within its head
-  const float Dh = a.Dskip[h];
   const bool vout = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 
   if (!state_live(a.live, a.live_slots, sg.seq)) {  // a padded sequence: zero outputs, no state
     if (OUT)
-      for (int64_t i = tid; i < (int64_t)(c_hi - c_lo) * Q * rows_in; i += 256) {
+      for (int64_t i = tid; i < (int64_t)(c_hi - c_lo) * Q * rows_in; i += THREADS) {
         const int64_t t = sg.begin + (int64_t)c_lo * Q + i / rows_in;
         if (t < sg.begin + sg.len) store_elem(a.out, t * a.H * D + col0 + i % rows_in, 0.f, a.out_dt);
       }
     if (OUT && a.fin.base != nullptr && a.fin.slots == nullptr && last_seg)
-      for (int i = tid; i < rows_in * NN; i += 256) store_elem(a.fin.base, ((int64_t)sg.seq * a.H * D + col0) * NN + i, 0.f, a.fin.dtype);
+      for (int i = tid; i < rows_in * NN; i += THREADS) store_elem(a.fin.base, ((int64_t)sg.seq * a.H * D + col0) * NN + i, 0.f, a.fin.dtype);
     return;
   }
 
   // state, transposed: S[nt][pt][r] = (n = 16 nt + 4 q + r, p = p0 + 16 pt + l16)
   f32x4 S[NT][PT];
   auto state_at = [&](int64_t unit, int nt, int pt) { return ((unit * a.H + h) * D + pd + 16 * pt + l16) * NN + 16 * nt + 4 * q; };
-  const int64_t seg_unit = slot;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
       S[nt][pt] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (a.local || !mine) continue;
       if (a.seg_chunks > 0) {
-        S[nt][pt] = *reinterpret_cast<const f32x4*>(a.seg + state_at(seg_unit, nt, pt));
+        S[nt][pt] = *reinterpret_cast<const f32x4*>(a.seg + state_at(slot, nt, pt));
       } else if (a.init.base != nullptr) {
         float f[4];
         load_vec<4>(a.init.base, state_at(a.init.slots != nullptr ? a.init.slots[sg.seq] : sg.seq, nt, pt), a.init.dtype, f);
@@ -210,7 +222,102 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
     }
   double total_g = 0.0;
 
-  for (int step = 0; step < c_hi - c_lo; ++step) {
+  // the next chunk's operands travel in registers while this one's are used
+  Frag<BF> vf[OUT ? W::FV : 1], vk[W::FV], vx[W::XV];
+  float vg[5];
+  auto fetch = [&](int c) {
+    const int64_t t0 = sg.begin + (int64_t)c * Q;
+    const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
+    const int64_t cs = slot0 + c, cg = cs * a.G + g;
+#pragma unroll
+    for (int k = 0; k < W::FV; ++k) {
+      const int i = tid + k * THREADS;
+      if (i < Q * NN / 8) {
+        vk[k] = Frag<BF>::load(reinterpret_cast<const E*>(at_bytes(a.wt, cg * NN * Q, i * 8, sizeof(E))));
+        if constexpr (OUT) {
+          const int t = i / (NN / 8), n0 = (i - t * (NN / 8)) * 8;
+          vf[k] = Frag<BF>::zero();
+          if (t < len) vf[k] = frag_from<BF>(a.read, t0 * a.read_ts + g * NN, t * (uint32_t)a.read_ts + n0, a.in_dt);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < W::XV; ++k) {
+      // 16-bit: vectors 2 k and 2 k + 1 are two tokens of the same 8 columns
+      const int i = BF ? tid + (k >> 1) * THREADS : tid + k * THREADS;
+      const int pb = i % PB, t = BF ? 2 * (i / PB) + (k & 1) : i / PB;
+      vx[k] = Frag<BF>::zero();
+      if (t < len && 8 * pb < rows_in) vx[k] = frag_from<BF>(a.in, t0 * a.in_ts + col0, t * (uint32_t)a.in_ts + 8 * pb, a.in_dt);
+    }
+    if (tid < HB * Q) {
+      const int t = tid % Q;
+      const float* gt = a.gates + (cs * a.H + g * hpg + min(hb * HB + tid / Q, hpg - 1)) * 3 * Q;
+      vg[0] = gt[t];
+      vg[1] = gt[Q + t];
+      vg[2] = gt[2 * Q + t];
+      vg[3] = gt[Q - 1];
+      vg[4] = gt[2 * Q - 1];
+    }
+  };
+  auto commit = [&](int len) {
+#pragma unroll
+    for (int k = 0; k < W::FV; ++k) {
+      const int i = tid + k * THREADS;
+      if (i < Q * NN / 8) {
+        *reinterpret_cast<Frag<BF>*>(s_k + (i >> 3) * LDT + (i & 7) * 8) = vk[k];
+        if constexpr (OUT) {
+          const int t = i / (NN / 8), n0 = (i - t * (NN / 8)) * 8;
+          // n = 32 k + 16 b + 4 s + r is stored at 32 k + 8 s + 4 b + r
+          E* d = s_f + t * LDF + (n0 & ~31) + 2 * (n0 & 15) + ((n0 >> 4) & 1) * 4;
+          vf[k].store_halves(d, d + 8);
+          if (NN == 16) Frag<BF>::zero().store_halves(d + 4, d + 12);
+        }
+      }
+    }
+    if constexpr (BF) {
+#pragma unroll
+      for (int k = 0; k < W::XV / 2; ++k) {
+        const int i = tid + k * THREADS, pb = i % PB, t = 2 * (i / PB);
+        const u32x4 v0 = vx[2 * k].v, v1 = vx[2 * k + 1].v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          *reinterpret_cast<uint32_t*>(s_x + xt_at<BF, LDT>(8 * pb + 2 * e, t)) = (v0[e] & 0xffffu) | (v1[e] << 16);
+          *reinterpret_cast<uint32_t*>(s_x + xt_at<BF, LDT>(8 * pb + 2 * e + 1, t)) = (v0[e] >> 16) | (v1[e] & 0xffff0000u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < W::XV; ++k) {
+        const int i = tid + k * THREADS, pb = i % PB, t = i / PB;
+        float f[8];
+        vx[k].widen(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_x[xt_at<BF, LDT>(8 * pb + e, t)] = (E)f[e];
+      }
+    }
+    if (tid < HB * Q) {
+      const float to_end = exp2f((vg[3] - vg[0]) + (vg[4] - vg[1])), from_start = exp2f(vg[0] + vg[1]);
+      float* o = s_g + tid / Q * 5 * Q + tid % Q;
+      o[0] = vg[0];
+      o[Q] = vg[1];
+      o[2 * Q] = vg[2];
+      o[3 * Q] = tid % Q < len ? (REV ? from_start : to_end * vg[2]) : 0.f;
+      o[4 * Q] = REV ? to_end : from_start;
+    }
+  };
+
+  if constexpr (OUT)  // tiles beyond the diagonal that share a 32-token operand with one on it stay zero
+    for (int i = tid; i < HB * Q * 4; i += THREADS) {
+      const int r = i >> 2, tile = (r >> 4) & 3, c = REV ? (tile & 1 ? tile - 1 : 4) : (tile & 1 ? 4 : tile + 1);
+      if (c < 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_p[r * LDT + 16 * c + 4 * (i & 3) + e] = (E)0;
+    }
+  const int steps = c_hi - c_lo;
+  if (steps > 0) fetch(REV ? c_hi - 1 : c_lo);
+  const float* const gh_ = s_g + hl * 5 * Q;
+
+  for (int step = 0; step < steps; ++step) {
     const int c = REV ? c_hi - 1 - step : c_lo + step;
     const int64_t t0 = sg.begin + (int64_t)c * Q;
     const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
@@ -224,98 +331,32 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[(16 * nt + 4 * q + r) * D + pd + 16 * pt + l16] = S[nt][pt][r];
+          for (int r = 0; r < 4; ++r) {
+            float* ou = o + (16 * nt + r) * D + pd + 16 * pt;
+            *reinterpret_cast<float*>(reinterpret_cast<char*>(ou) + (uint32_t)(4 * (4 * q * D + l16))) = S[nt][pt][r];
+          }
     }
 
     __syncthreads();  // the chunk before is done with LDS
-    if constexpr (OUT) {
-      constexpr int VPR = NN / 8;
-      for (int i = tid; i < Q * VPR; i += 256) {
-        const int t = i / VPR, n0 = (i - t * VPR) * 8;
-        Frag<BF> f = Frag<BF>::zero();
-        if (t < len) f = frag_from<BF>(a.read, (t0 + t) * a.read_ts + g * NN + n0, a.in_dt);
-        // n = 32 k + 16 b + 4 s + r is stored at 32 k + 8 s + 4 b + r
-        E* d = s_f + t * LDF + (n0 & ~31) + 2 * (n0 & 15) + ((n0 >> 4) & 1) * 4;
-        f.store_halves(d, d + 8);
-        if (NN == 16) Frag<BF>::zero().store_halves(d + 4, d + 12);
-      }
-    }
-    for (int i = tid; i < NN * 8; i += 256)
-      *reinterpret_cast<Frag<BF>*>(s_k + (i >> 3) * LDT + (i & 7) * 8) =
-          Frag<BF>::load(static_cast<const E*>(a.wt) + cg * NN * Q + i * 8);
-    if constexpr (BF) {
-      constexpr int PB = ROWS / 8;
-#pragma unroll
-      for (int k = 0; k < 32 * PB / 256; ++k) {
-        const int i = tid + 256 * k, pb = i % PB, t = (i / PB) * 2;
-        u32x4 v0 = {0u, 0u, 0u, 0u}, v1 = v0;
-        if (8 * pb < rows_in) {
-          const uint16_t* src = static_cast<const uint16_t*>(a.in) + (t0 + t) * a.in_ts + col0 + 8 * pb;
-          if (t < len) v0 = *reinterpret_cast<const u32x4*>(src);
-          if (t + 1 < len) v1 = *reinterpret_cast<const u32x4*>(src + a.in_ts);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          *reinterpret_cast<uint32_t*>(s_x + xt_at<BF, LDT>(8 * pb + 2 * e, t)) = (v0[e] & 0xffffu) | (v1[e] << 16);
-          *reinterpret_cast<uint32_t*>(s_x + xt_at<BF, LDT>(8 * pb + 2 * e + 1, t)) = (v0[e] >> 16) | (v1[e] & 0xffff0000u);
-        }
-      }
-    } else {
-      for (int i = tid; i < Q * (ROWS / 8); i += 256) {
-        const int pb = i % (ROWS / 8), t = i / (ROWS / 8);
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (t < len && 8 * pb < rows_in) load_vec<8>(a.in, (t0 + t) * a.in_ts + col0 + 8 * pb, a.in_dt, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s_x[xt_at<BF, LDT>(8 * pb + e, t)] = f[e];
-      }
-    }
-    if (tid < HB * Q) {
-      const int k = tid / Q, t = tid % Q, hh = g * hpg + min(hb * HB + k, hpg - 1);
-      const float* gt = a.gates + (cs * a.H + hh) * 3 * Q;
-      const float ch = gt[t], cl = gt[Q + t], dtp = gt[2 * Q + t];
-      const float to_end = decay_between(gt[Q - 1], gt[2 * Q - 1], ch, cl), from_start = expf(ch + cl);
-      float* o = s_g + k * 5 * Q + t;
-      o[0] = ch;
-      o[Q] = cl;
-      o[2 * Q] = dtp;
-      o[3 * Q] = t < len ? (REV ? from_start : to_end * dtp) : 0.f;
-      o[4 * Q] = REV ? to_end : from_start;
-    }
+    commit(len);
     __syncthreads();
 
-    const float* gh_ = s_g + hl * 5 * Q;
     f32x4 acc[PT][4];
     if constexpr (OUT) {
-      // products of read and write vectors, weighted by decay: row r of the output, token c of the input
-      {
-        const int r = tid >> 2, c0 = (tid & 3) * 16;
-        float gm[16];
-        const float* src = a.gm + (cg * Q + r) * Q + c0;
+      // the decay-weighted products of read and write vectors: the tiles on and below the diagonal
+      // (above it in reverse) go round the head's waves; lane: row lane / 4, four columns
+      constexpr int PER = (10 + WPH - 1) / WPH;
+      f32x4 gm[PER];
+      int rts[PER], cts[PER];
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(src + e);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) gm[e + j] = v[j];
-        }
-#pragma unroll
-        for (int k = 0; k < HB; ++k) {
-          const float* sg_ = s_g + k * 5 * Q;
-          const float rh = sg_[r], rl = sg_[Q + r];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int cc = c0 + 8 * half + e;
-              const bool on = REV ? cc >= r : cc <= r;
-              const float d = REV ? (sg_[cc] - rh) + (sg_[Q + cc] - rl) : (rh - sg_[cc]) + (rl - sg_[Q + cc]);
-              f[e] = on ? expf(d) * gm[8 * half + e] * (REV ? 1.f : sg_[2 * Q + cc]) : 0.f;
-            }
-            *reinterpret_cast<Frag<BF>*>(s_p + (k * Q + r) * LDT + c0 + 8 * half) = Frag<BF>::round(f);
-          }
-        }
+      for (int k = 0; k < PER; ++k) {
+        const int t = min(wave % WPH + k * WPH, 9);
+        const int i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t - i * (i + 1) / 2;
+        rts[k] = REV ? j : i;
+        cts[k] = REV ? i : j;
+        gm[k] = *reinterpret_cast<const f32x4*>(at_bytes(a.gm, cg * Q * Q + 16 * rts[k] * Q + 16 * cts[k], (lane >> 2) * Q + (lane & 3) * 4, 4));
       }
-      // the state's part
+      // the state's part of the output
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
@@ -341,47 +382,37 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
         }
       }
 #pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        if (wave % WPH + k * WPH >= 10) continue;
+        const int r = 16 * rts[k] + (lane >> 2), c0 = 16 * cts[k] + 4 * (lane & 3);
+        const float rh = gh_[r], rl = gh_[Q + r];
+        const f32x4 ch = *reinterpret_cast<const f32x4*>(gh_ + c0), cl = *reinterpret_cast<const f32x4*>(gh_ + Q + c0);
+        f32x4 w = gm[k];
+        if constexpr (!REV) w *= *reinterpret_cast<const f32x4*>(gh_ + 2 * Q + c0);
+        E* d = s_p + (hl * Q + r) * LDT + c0;
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool on = REV ? c0 + e >= r : c0 + e <= r;
+          const float x = REV ? (ch[e] - rh) + (cl[e] - rl) : (rh - ch[e]) + (rl - cl[e]);
+          f[e] = on ? __builtin_amdgcn_exp2f(x) * w[e] : 0.f;
+        }
+        if constexpr (BF) *reinterpret_cast<u32x2*>(d) = u32x2{pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
+        else *reinterpret_cast<f32x4*>(d) = f32x4{f[0], f[1], f[2], f[3]};
+      }
+#pragma unroll
       for (int rt = 0; rt < 4; ++rt) {
         const float f = gh_[4 * Q + 16 * rt + l16];
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) acc[pt][rt] *= f;
       }
-      __syncthreads();  // the products are there
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        Frag<BF> xf[PT];
-#pragma unroll
-        for (int pt = 0; pt < PT; ++pt) xf[pt] = Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q));
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          if (REV ? (ks == 0 && rt >= 2) : (ks == 1 && rt < 2)) continue;  // all above the diagonal
-          const Frag<BF> pf = Frag<BF>::load(s_p + (hl * Q + 16 * rt + l16) * LDT + 32 * ks + 8 * q);
-#pragma unroll
-          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[pt], pf);
-        }
-      }
-      if (mine) {
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const int t = 16 * rt + l16;
-          if (t < len) {
-            const float sc = REV ? gh_[2 * Q + t] : 1.f;
-#pragma unroll
-            for (int pt = 0; pt < PT; ++pt) {
-              const int64_t off = (int64_t)h * D + pd + 16 * pt + 4 * q;
-              float v[4];
-              load_vec<4>(a.in, (t0 + t) * a.in_ts + off, a.in_dt, v);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] = acc[pt][rt][r] * sc + Dh * v[r];
-              store_vec<4>(a.out, (t0 + t) * a.H * D + off, v, a.out_dt, vout);
-            }
-          }
-        }
-      }
     }
+    __builtin_amdgcn_sched_barrier(0);  // keeps the next chunk's loads from being moved up, where registers are short
+    if (step + 1 < steps) fetch(REV ? c - 1 : c + 1);
+
     // the state after the chunk
     const float* gt = a.gates + (cs * a.H + h) * 3 * Q;
-    const float end_h = gt[Q - 1], end_l = gt[2 * Q - 1], dec = expf(end_h + end_l);
+    const float end_h = gt[Q - 1], end_l = gt[2 * Q - 1], dec = exp2f(end_h + end_l);
     total_g += (double)end_h + (double)end_l;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -406,6 +437,43 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
         for (int pt = 0; pt < PT; ++pt) S[nt][pt] = xs[pt].mma_right(S[nt][pt], kf);
       }
     }
+
+    if constexpr (OUT) {
+      __syncthreads();  // the products are there
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        Frag<BF> xf[PT];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) xf[pt] = Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q));
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          if (REV ? (ks == 0 && rt >= 2) : (ks == 1 && rt < 2)) continue;  // all beyond the diagonal
+          const Frag<BF> pf = Frag<BF>::load(s_p + (hl * Q + 16 * rt + l16) * LDT + 32 * ks + 8 * q);
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[pt], pf);
+        }
+      }
+      if (mine) {
+        const float Dh = a.Dskip[h];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const int t = 16 * rt + l16;
+          if (t < len) {
+            const float sc = REV ? gh_[2 * Q + t] : 1.f;
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) {
+              const int64_t off = (int64_t)h * D + pd + 16 * pt;
+              const int ib = BF || a.in_dt != GDN_F32 ? 2 : 4, ob = BF || a.out_dt != GDN_F32 ? 2 : 4;
+              float v[4];
+              load_vec<4>(at_bytes(a.in, (t0 + 16 * rt) * a.in_ts + off, l16 * (uint32_t)a.in_ts + 4 * q, ib), 0, BF ? GDN_BF16 : a.in_dt, v);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] = acc[pt][rt][r] * sc + Dh * v[r];
+              store_vec<4>(const_cast<char*>(at_bytes(a.out, (t0 + 16 * rt) * a.H * D + off, l16 * (uint32_t)(a.H * D) + 4 * q, ob)), 0, v, a.out_dt, vout);
+            }
+          }
+        }
+      }
+    }
   }
 
   if (!mine) return;
@@ -413,7 +481,7 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt) *reinterpret_cast<f32x4*>(a.seg + state_at(seg_unit, nt, pt)) = S[nt][pt];
+      for (int pt = 0; pt < PT; ++pt) *reinterpret_cast<f32x4*>(a.seg + state_at(slot, nt, pt)) = S[nt][pt];
     if (pd == 0 && lane == 0) a.seg_g[(int64_t)slot * a.H + h] = total_g;
   } else if (a.fin.base != nullptr && last_seg && (REV || sg.len > 0)) {
     const int64_t unit = a.fin.slots != nullptr ? a.fin.slots[sg.seq] : sg.seq;
@@ -450,7 +518,7 @@ __global__ void __launch_bounds__(256) gdn_m2s_chain_kernel(const M2ScanArgs a, 
     f32x4* p = reinterpret_cast<f32x4*>(a.seg + unit * elems + i);
     if (k + 1 < count) {
       const f32x4 own = *p;
-      const float dec = (float)exp(a.seg_g[unit]);
+      const float dec = (float)exp2(a.seg_g[unit]);
       *p = S;
       S = S * dec + own;
     } else {
@@ -460,33 +528,44 @@ __global__ void __launch_bounds__(256) gdn_m2s_chain_kernel(const M2ScanArgs a, 
 }
 
 // ------------------------------------------------------------------ host
+int64_t scan_slots(int64_t N, int64_t total, int64_t P) { return N + (total + P - 1) / P; }
+
 namespace {
 
-template <bool BF, int D, int NN, bool REV, bool OUT>
+int walk_waves(bool bf, int d, int hpg) { return bf && hpg * d > (d == 16 ? 64 : 128) ? 8 : 4; }
+
+template <bool BF, int D, int NN, int NW, bool REV, bool OUT>
 hipError_t walk(const M2ScanArgs& a, hipStream_t s) {
-  using W = WalkGeom<BF, D, NN, OUT>;
+  using W = WalkGeom<BF, D, NN, NW, OUT>;
   const int hpg = a.H / a.G, hbs = (hpg + W::HB - 1) / W::HB;
-  const int64_t slots = a.seg_chunks > 0 ? a.N + (a.total + (int64_t)a.seg_chunks * kScanChunk - 1) / ((int64_t)a.seg_chunks * kScanChunk) : a.N;
-  auto* k = gdn_m2s_walk_kernel<BF, D, NN, REV, OUT>;
+  const int64_t slots = a.seg_chunks > 0 ? scan_slots(a.N, a.total, (int64_t)a.seg_chunks * kScanChunk) : a.N;
+  auto* k = gdn_m2s_walk_kernel<BF, D, NN, NW, REV, OUT>;
   if (W::LDS > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)W::LDS);
     if (e != hipSuccess) return e;
   }
-  k<<<(unsigned)(slots * a.G * hbs), 256, W::LDS, s>>>(a);
+  k<<<(unsigned)(slots * a.G * hbs), W::THREADS, W::LDS, s>>>(a);
   return hipGetLastError();
 }
 
-template <bool BF, int D, int NN>
+template <bool BF, int D, int NN, int NW>
 hipError_t walk_kind(const M2ScanArgs& a, bool rev, bool out, hipStream_t s) {
-  if (rev) return out ? walk<BF, D, NN, true, true>(a, s) : walk<BF, D, NN, true, false>(a, s);
-  return out ? walk<BF, D, NN, false, true>(a, s) : walk<BF, D, NN, false, false>(a, s);
+  if (rev) return out ? walk<BF, D, NN, NW, true, true>(a, s) : walk<BF, D, NN, NW, true, false>(a, s);
+  return out ? walk<BF, D, NN, NW, false, true>(a, s) : walk<BF, D, NN, NW, false, false>(a, s);
+}
+
+template <bool BF, int D, int NN>
+hipError_t walk_nw(const M2ScanArgs& a, bool rev, bool out, hipStream_t s) {
+  if constexpr (BF)
+    if (walk_waves(true, D, a.H / a.G) == 8) return walk_kind<BF, D, NN, 8>(a, rev, out, s);
+  return walk_kind<BF, D, NN, 4>(a, rev, out, s);
 }
 
 template <bool BF, int D>
 hipError_t walk_n(const M2ScanArgs& a, int n, bool rev, bool out, hipStream_t s) {
-  if (n == 16) return walk_kind<BF, D, 16>(a, rev, out, s);
-  if (n == 64) return walk_kind<BF, D, 64>(a, rev, out, s);
-  return walk_kind<BF, D, 128>(a, rev, out, s);
+  if (n == 16) return walk_nw<BF, D, 16>(a, rev, out, s);
+  if (n == 64) return walk_nw<BF, D, 64>(a, rev, out, s);
+  return walk_nw<BF, D, 128>(a, rev, out, s);
 }
 
 template <bool BF>
@@ -507,14 +586,12 @@ hipError_t prep(const M2ScanArgs& a, int n, hipStream_t s) {
 
 }  // namespace
 
-int64_t scan_slots(int64_t N, int64_t total, int64_t P) { return N + (total + P - 1) / P; }
-
-// Chunks a segment, 0 for whole sequences.
+// Chunks a segment (even, so that blocks of two chunks do not straddle), 0 for whole sequences.
 int scan_seg_chunks(int64_t N, int64_t total, int H, int G, int d) {
-  const int hb = d == 128 ? 1 : d == 64 ? 2 : 4, hpg = H / G;
+  const int hpg = H / G, hb = walk_waves(true, d, hpg) * (d == 16 ? 16 : 32) / d;
   const int64_t walks = (int64_t)G * ((hpg + hb - 1) / hb), chunks = (total + kScanChunk - 1) / kScanChunk;
   if (N * walks >= 512 || chunks <= 16) return 0;
-  int64_t per = chunks * walks / 1024;
+  int64_t per = chunks * walks / GDN_SEG_WALKS;
   per = per < 8 ? 8 : (per + 1) / 2 * 2;
   return per >= chunks ? 0 : (int)per;
 }

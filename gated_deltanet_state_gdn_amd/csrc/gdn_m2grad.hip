@@ -43,14 +43,16 @@ struct GradGeom {
   static constexpr int ELEMS = 2 * T * LDX > T * LDN ? 2 * T * LDX : T * LDN;
   static constexpr bool BOTH = NT == 8;           // each wave has a column tile of dC and of dB; else one wave has one of them
   static constexpr bool G_LDS = BF || D < 128;    // C_i.B_j in LDS, in registers where that is full
-  static constexpr bool LATE = BF;                // a head's sums are closed while the next head is under way
+  static constexpr bool N_LDS = BF;               // the heads' summed products too
+  static constexpr bool LATE = BF && D < 128;     // a head's sums are closed while the next head is under way
   static constexpr int XV = T * DK / 8 / 512;     // vectors of 8 elements of x (and of dy) that a thread stages
   // a head's results: column sums [8][128], row sums, the diagonal tiles' row and column sums, the diagonal, the state
   // parts [NT][128] twice, dt', the waves' parts of <S, dS'> and of sum dy.x, e^{c_last}
   static constexpr int RES = (8 + 4 + 2 * NT + 1) * T + 24;
-  static constexpr int GATES = 4 * T;             // c / 2 (two), e^{c_i}, e^{c_last - c_j}
-  static_assert(!BF || 2 * T * LDN * 2 <= ELEMS * 2 + 36 * 64 * 16, "both terms of the summed products fit over x, dy and C.B");
-  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + (G_LDS ? 36 * 64 * 16 : 0) + (GATES + (LATE ? 2 : 1) * RES) * 4;
+  static constexpr int GATES = 5 * T;             // c / 2 (two), e^{c_i}, dt' e^{c_last - c_j}, dt'
+  static constexpr int TILES = 36 * 64 * 16;      // bytes of the tiles on and below the diagonal
+  static_assert(!BF || 2 * T * LDN * 2 <= ELEMS * 2 + TILES, "both terms of the summed products fit over x, dy and C.B");
+  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + (G_LDS ? TILES : 0) + (N_LDS ? TILES : 0) + (GATES + (LATE ? 2 : 1) * RES) * 4;
 };
 
 // Sums over a 16-lane row's lanes at or after, and at or before, each lane.
@@ -83,15 +85,18 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
   E* const s_x = reinterpret_cast<E*>(smem);
   E* const s_y = s_x + T * LDX;
   E* const s_n = s_x;
-  f32x4* const s_gt = reinterpret_cast<f32x4*>(smem + (size_t)W::ELEMS * sizeof(E));  // tile (i, j <= i) at i (i + 1) / 2 + j, by lane
-  float* const s_ch = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E) + (W::G_LDS ? 36 * 64 * 16 : 0));
+  int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int tile0 = wave * (wave + 1) / 2 * 64 + lane;  // tile (i, j <= i) is the i (i + 1) / 2 + j-th, a lane's four values together
+  f32x4* const s_gt = reinterpret_cast<f32x4*>(smem + (size_t)W::ELEMS * sizeof(E));
+  f32x4* const s_ns = s_gt + (W::G_LDS ? 36 * 64 : 0);
+  float* const s_ch = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E) + (W::G_LDS ? W::TILES : 0) + (W::N_LDS ? W::TILES : 0));
   float* const s_cl = s_ch + T;
   float* const s_er = s_cl + T;      // e^{c_i}
-  float* const s_ew = s_er + T;      // e^{c_last - c_j}
-  float* const s_res = s_ew + T;
+  float* const s_wd = s_er + T;      // dt'_j e^{c_last - c_j}
+  float* const s_dt = s_wd + T;
+  float* const s_res = s_dt + T;
 
-  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hpg = a.H / a.G;
   const int slot = blockIdx.x / (a.G * a.splits), rest = blockIdx.x - slot * (a.G * a.splits), g = rest / a.splits, split = rest - g * a.splits;
   const int h_lo = (int)((int64_t)hpg * split / a.splits), h_hi = (int)((int64_t)hpg * (split + 1) / a.splits);
@@ -121,7 +126,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
 
   // which part of the column work this wave has
   const int nt = wave % NT, n16 = 16 * nt;
-  const bool do_c = wave < NT, do_b = BOTH || (wave >= NT && wave < 2 * NT);
+  const bool do_c = BOTH || wave < NT, do_b = BOTH || (wave >= NT && wave < 2 * NT);
 
   // the next head's tokens and states before it travel in registers while this head is under way, the gradients of the
   // states after it while dC's part is
@@ -172,7 +177,8 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       s_ch[tid] = 0.5f * ch;
       s_cl[tid] = 0.5f * (float)(c - (double)ch);
       s_er[tid] = exp2f((float)c);
-      s_ew[tid] = exp2f((float)(last - c));
+      s_wd[tid] = dtp * exp2f((float)(last - c));
+      s_dt[tid] = dtp;
       res[(8 + 4 + 2 * NT) * T + tid] = dtp;
       if (tid == 0) res[W::RES - 1] = exp2f((float)last);
     }
@@ -198,14 +204,31 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     }
   };
 
+  // four 16-token tiles of x or dy times a split state, their terms apart: a product never follows the one it adds to
+  auto products = [&](const E* rows, int i0, const Split<BF> (&st)[DB], f32x4 (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < DB; ++k) {
+      Frag<BF> f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = Frag<BF>::load(rows + (16 * (i0 + i) + l16) * LDX + 32 * k + 8 * q);
+#pragma unroll
+      for (int t = Split<BF>::K - 1; t >= 0; --t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = frag_mma(v[i], f[i], st[k].t[t]);
+    }
+  };
+
   // G for the wave's 16 rows: C_i . B_j
-  f32x4 G[W::G_LDS ? 1 : 8], Ns[8];
+  f32x4 G[W::G_LDS ? 1 : 8], Ns[W::N_LDS ? 1 : 8];
   {
     const int i = 16 * wave + l16;
 #pragma unroll
     for (int jt = 0; jt < 8; ++jt) {
-      Ns[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (!W::N_LDS) Ns[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (jt > wave) continue;
+      if constexpr (W::N_LDS) s_ns[tile0 + jt * 64] = f32x4{0.f, 0.f, 0.f, 0.f};
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < (NN + 31) / 32; ++kb) {
@@ -215,30 +238,46 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
         if (j < len && n0 < NN) bf = frag_from<BF>(a.Bm, t0 * a.b_ts + g * NN, j * (uint32_t)a.b_ts + n0, a.dt_in);
         acc = frag_mma(acc, cf, bf);
       }
-      if constexpr (W::G_LDS) s_gt[(wave * (wave + 1) / 2 + jt) * 64 + lane] = acc;
+      if constexpr (W::G_LDS) s_gt[tile0 + jt * 64] = acc;
       else G[jt] = acc;
     }
   }
-  // the wave's columns of C and B in the accumulators' order, kept in the input's width (FP32: read where they are used)
-  uint32_t cc[BF ? 8 : 1][2], bb[BF ? 8 : 1][2];
-  auto column = [&](const void* m, int64_t ts, int it, float (&v)[4]) {
+  // four tiles of the wave's columns of C or B in the accumulators' order, from the transposed copies where the input is
+  // bf16 (four tokens together; past the second chunk there is nothing to read)
+  struct Columns {
+    u32x2 w[BF ? 8 : 1];
+  };
+  auto load_columns = [&](const void* transposed, Columns& c) {
+    if constexpr (BF)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * it + 4 * q + r;
-      v[r] = t < len ? load_elem(at_bytes(m, t0 * ts + g * NN + n16, t * (uint32_t)ts + l16, BF || a.dt_in != GDN_F32 ? 2 : 4), 0, BF ? GDN_BF16 : a.dt_in) : 0.f;
+      for (int it = 0; it < 8; ++it) {
+        c.w[it] = u32x2{0u, 0u};
+        if (16 * it < len)
+          c.w[it] = *reinterpret_cast<const u32x2*>(
+              at_bytes(transposed, (((slot64 + (it >> 2)) * a.G + g) * NN + n16) * Q + 16 * (it & 3), l16 * Q + 4 * q, 2));
+      }
+  };
+  auto column_of = [&](const void* m, int64_t ts, const Columns& c, int it, float (&v)[4]) {
+    if constexpr (BF) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = (r & 1) ? unpack_hi<GDN_BF16>(c.w[it][r >> 1]) : unpack_lo<GDN_BF16>(c.w[it][r >> 1]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * it + 4 * q + r;
+        v[r] = t < len ? load_elem(at_bytes(m, t0 * ts + g * NN + n16, t * (uint32_t)ts + l16, a.dt_in != GDN_F32 ? 2 : 4), 0, a.dt_in) : 0.f;
+      }
     }
   };
-  if constexpr (BF)
-#pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      float v[4];
-      column(a.Cm, a.c_ts, it, v);
-      cc[it][0] = pack2<GDN_BF16>(v[0], v[1]);
-      cc[it][1] = pack2<GDN_BF16>(v[2], v[3]);
-      column(a.Bm, a.b_ts, it, v);
-      bb[it][0] = pack2<GDN_BF16>(v[0], v[1]);
-      bb[it][1] = pack2<GDN_BF16>(v[2], v[3]);
-    }
+  auto pick4 = [&](float v0, float v1, float v2, float v3) {
+    const float lo = (l16 & 4) ? v1 : v0, hi = (l16 & 4) ? v3 : v2;
+    return (l16 & 8) ? hi : lo;
+  };
+  // 2^(2 x) for x = half an exponent: the square of a root that the hardware's exponential does not flush
+  auto decay_half = [](float x) {
+    const float r = __builtin_amdgcn_exp2f(x);
+    return r * r;
+  };
 
   // closes a head: dt's gradient for the block's tokens and the head's parameter sums (one wave)
   auto close_head = [&](int h, const float* res) {
@@ -338,6 +377,9 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
   fetch_state(a.fwd, g * hpg + h_lo, vs);
   for (int hi = h_lo; hi < h_hi; ++hi) {
     const int h = g * hpg + hi, h_next = min(h + 1, g * hpg + h_hi - 1);
+    // the lane's places are not known to be the ones of the head before: what follows from them is formed anew, in a few
+    // instructions, where it would otherwise be kept in registers that the loop has not got
+    asm volatile("" : "+v"(tid), "+v"(lane), "+v"(l16), "+v"(q), "+v"(tile0));
     float* const res = s_res + (W::LATE ? (hi & 1) * W::RES : 0);
     float *r_col = res, *r_row = res + 8 * T, *r_rd = r_row + T, *r_cd = r_rd + T, *r_dg = r_cd + T, *r_cs = r_dg + T,
           *r_cv = r_cs + NT * T, *r_q = r_cv + NT * T + T, *r_dd = r_q + 8;
@@ -345,29 +387,31 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     commit_tokens(res);
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
+    Columns cc, bb;
+    if (do_c) load_columns(a.ct, cc);  // first: loads are waited for in order
     fetch_state(a.rev, h, vr);
     __builtin_amdgcn_sched_barrier(0);
 
-    // state parts of dC and dB for the wave's 16 columns
+    // state parts of dC and dB for the wave's 16 columns; row l16 / 4 of four tiles, token 4 q + l16 % 4 of it
+    const int own = 16 * (l16 >> 2) + 4 * q + (l16 & 3);
     if (do_c) {
       Split<BF> sc[DB];
       split_state(vs, sc);
 #pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        if (it >= tiles) continue;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      for (int i0 = 0; i0 < 8; i0 += 4) {
+        if (i0 >= tiles) continue;
+        f32x4 v[4];
+        products(s_y, i0, sc, v);
+        float dots[4];
 #pragma unroll
-        for (int k = 0; k < DB; ++k) v = sc[k].mma_right(v, Frag<BF>::load(s_y + (16 * it + l16) * LDX + 32 * k + 8 * q));
-        float s[4], col[4];
-        if constexpr (!BF) column(a.Cm, a.c_ts, it, col);
-        const f32x4 er = *reinterpret_cast<const f32x4*>(s_er + 16 * it + 4 * q);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (BF) col[r] = (r & 1) ? unpack_hi<GDN_BF16>(cc[it][r >> 1]) : unpack_lo<GDN_BF16>(cc[it][r >> 1]);
-          s[r] = er[r] * row16_sum(v[r] * col[r]);
+        for (int i = 0; i < 4; ++i) {
+          float col[4];
+          column_of(a.Cm, a.c_ts, cc, i0 + i, col);
+          dots[i] = row16_sum4(v[i][0] * col[0], v[i][1] * col[1], v[i][2] * col[2], v[i][3] * col[3]);
+          dC[i0 + i] += v[i] * *reinterpret_cast<const f32x4*>(s_er + 16 * (i0 + i) + 4 * q);
         }
-        dC[it] += v * er;
-        if (l16 < 4) r_cs[nt * T + 16 * it + 4 * q + l16] = l16 == 0 ? s[0] : l16 == 1 ? s[1] : l16 == 2 ? s[2] : s[3];
+        r_cs[nt * T + 16 * i0 + own] = s_er[16 * i0 + own] * pick4(dots[0], dots[1], dots[2], dots[3]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -380,97 +424,109 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       qs = wave_sum(qs);
       if (lane == 0) r_q[wave] = qs;
     }
+    if (do_b) load_columns(a.bt, bb);
     Split<BF> sb[DB];
     split_state(vr, sb);
+    __builtin_amdgcn_sched_barrier(0);
+    if (do_b) {
+#pragma unroll
+      for (int i0 = 0; i0 < 8; i0 += 4) {
+        if (i0 >= tiles) continue;
+        f32x4 v[4];
+        products(s_x, i0, sb, v);
+        float dots[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float col[4];
+          column_of(a.Bm, a.b_ts, bb, i0 + i, col);
+          dots[i] = row16_sum4(v[i][0] * col[0], v[i][1] * col[1], v[i][2] * col[2], v[i][3] * col[3]);
+          dB[i0 + i] += v[i] * *reinterpret_cast<const f32x4*>(s_wd + 16 * (i0 + i) + 4 * q);
+        }
+        r_cv[nt * T + 16 * i0 + own] = s_wd[16 * i0 + own] * pick4(dots[0], dots[1], dots[2], dots[3]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
     __builtin_amdgcn_sched_barrier(0);
     fetch_state(a.fwd, h_next, vs);
     fetch_tokens(h_next);
     __builtin_amdgcn_sched_barrier(0);
-    if (do_b) {
-#pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        if (it >= tiles) continue;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < DB; ++k) v = sb[k].mma_right(v, Frag<BF>::load(s_x + (16 * it + l16) * LDX + 32 * k + 8 * q));
-        float s[4], col[4];
-        if constexpr (!BF) column(a.Bm, a.b_ts, it, col);
-        const f32x4 ew = *reinterpret_cast<const f32x4*>(s_ew + 16 * it + 4 * q);
-        const f32x4 dtj = *reinterpret_cast<const f32x4*>(r_cv + NT * T + 16 * it + 4 * q);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if constexpr (BF) col[r] = (r & 1) ? unpack_hi<GDN_BF16>(bb[it][r >> 1]) : unpack_lo<GDN_BF16>(bb[it][r >> 1]);
-          s[r] = ew[r] * (dtj[r] * row16_sum(v[r] * col[r]));
-        }
-        dB[it] += v * (ew * dtj);
-        if (l16 < 4) r_cv[nt * T + 16 * it + 4 * q + l16] = l16 == 0 ? s[0] : l16 == 1 ? s[1] : l16 == 2 ? s[2] : s[3];
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
 
-    // products of dy and x for the wave's 16 rows
+    // products of dy and x for the wave's 16 rows; off the diagonal tile the decay is that down to the rows' first
+    // token times that from there
     if (wave < tiles) {
       Frag<BF> yf[DB];
 #pragma unroll
       for (int k = 0; k < DB; ++k) yf[k] = Frag<BF>::load(s_y + (16 * wave + l16) * LDX + 32 * k + 8 * q);
       const int i0 = 16 * wave + 4 * q;
-      float ih[4], il[4], rowo[4] = {0.f, 0.f, 0.f, 0.f};
+      const f32x4 ih = *reinterpret_cast<const f32x4*>(s_ch + i0), il = *reinterpret_cast<const f32x4*>(s_cl + i0);
+      const float mh = s_ch[16 * wave], ml = s_cl[16 * wave];
+      f32x4 rowo = {0.f, 0.f, 0.f, 0.f}, down;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        ih[r] = s_ch[i0 + r];
-        il[r] = s_cl[i0 + r];
-      }
-#pragma unroll
-      for (int jt = 0; jt < 8; ++jt) {
-        if (jt > wave) continue;
-        f32x4 w = {0.f, 0.f, 0.f, 0.f}, gt;
-#pragma unroll
-        for (int k = 0; k < DB; ++k) w = frag_mma(w, yf[k], Frag<BF>::load(s_x + (16 * jt + l16) * LDX + 32 * k + 8 * q));
-        if constexpr (W::G_LDS) gt = s_gt[(wave * (wave + 1) / 2 + jt) * 64 + lane];
-        else gt = G[jt];
+      for (int r = 0; r < 4; ++r) down[r] = decay_half((ih[r] - mh) + (il[r] - ml));
+      auto tile = [&](int jt, f32x4& ns, const f32x4& gt, auto on_diagonal) {
         const int j = 16 * jt + l16;
-        const float jh = s_ch[j], jl = s_cl[j], dtj = r_cv[NT * T + j];
-        float col = 0.f;
-        if (jt < wave) {
+        f32x4 w = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < DB; ++k) w = frag_mma(w, yf[k], Frag<BF>::load(s_x + j * LDX + 32 * k + 8 * q));
+        const float jh = s_ch[j], jl = s_cl[j], dtj = s_dt[j];
+        if constexpr (!decltype(on_diagonal)::value) {
+          const float from = dtj * decay_half((mh - jh) + (ml - jl));
+          float col = 0.f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float e2 = __builtin_amdgcn_exp2f((ih[r] - jh) + (il[r] - jl)), e = e2 * e2, dw = dtj * w[r];
-            Ns[jt][r] += e * dw;
-            const float m = e * (dw * gt[r]);
+            const float e = down[r] * from, m = e * (w[r] * gt[r]);
+            ns[r] += e * w[r];
             col += m;
             rowo[r] += m;
           }
           col = xor_sum_from<16>(col);
           if (q == 0) r_col[wave * T + j] = col;
         } else {
-          float rowd[4], diag = 0.f, wd = 0.f;
+          f32x4 off;
+          float diag = 0.f, wd = 0.f, cd = 0.f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int i = i0 + r;
-            const float e2 = j <= i ? __builtin_amdgcn_exp2f((ih[r] - jh) + (il[r] - jl)) : 0.f, e = e2 * e2, dw = dtj * w[r];
-            Ns[jt][r] += e * dw;
-            const float m = e * (dw * gt[r]);
-            if (i == j) {
+            const float e = j <= i0 + r ? dtj * decay_half((ih[r] - jh) + (il[r] - jl)) : 0.f, m = e * (w[r] * gt[r]);
+            ns[r] += e * w[r];
+            if (j == i0 + r) {
               diag = m;
               wd = w[r];
             }
-            const float off = i == j ? 0.f : m;
-            col += off;
-            rowd[r] = row16_sum(off);
-            rowo[r] = row16_sum(rowo[r]);
+            off[r] = j == i0 + r ? 0.f : m;
+            cd += off[r];
           }
-          col = xor_sum_from<16>(col);
-          diag = xor_sum_from<16>(diag);
-          wd = wave_sum(wd);
-          if (q == 0) {
-            r_cd[j] = col;
-            r_dg[j] = diag;
-          }
-          if (lane == 0) r_dd[wave] = wd;
+          const float rd = row16_sum4(off[0], off[1], off[2], off[3]), ro = row16_sum4(rowo[0], rowo[1], rowo[2], rowo[3]);
+          const float z = rows_sum4(cd, diag, wd, 0.f);  // the rows of 16 lanes get the three sums over the tile's rows
           if (l16 < 4) {
-            r_rd[i0 + l16] = l16 == 0 ? rowd[0] : l16 == 1 ? rowd[1] : l16 == 2 ? rowd[2] : rowd[3];
-            r_row[i0 + l16] = l16 == 0 ? rowo[0] : l16 == 1 ? rowo[1] : l16 == 2 ? rowo[2] : rowo[3];
+            r_rd[i0 + l16] = rd;
+            r_row[i0 + l16] = ro;
           }
+          if (q < 2) (q == 0 ? r_cd : r_dg)[j] = z;
+          const float dd = row16_sum(z);
+          if (lane == 32) r_dd[wave] = dd;
+        }
+      };
+      if constexpr (W::N_LDS) {
+        f32x4 ns;
+#pragma unroll 1
+        for (int jt = 0; jt < wave; ++jt) {
+          ns = s_ns[tile0 + jt * 64];
+          tile(jt, ns, s_gt[tile0 + jt * 64], std::false_type{});
+          s_ns[tile0 + jt * 64] = ns;
+        }
+        ns = s_ns[tile0 + wave * 64];
+        tile(wave, ns, s_gt[tile0 + wave * 64], std::true_type{});
+        s_ns[tile0 + wave * 64] = ns;
+      } else {
+#pragma unroll
+        for (int jt = 0; jt < 8; ++jt) {
+          f32x4 gt = {0.f, 0.f, 0.f, 0.f};
+          if (jt <= wave) {
+            if constexpr (W::G_LDS) gt = s_gt[tile0 + jt * 64];
+            else gt = G[jt];
+          }
+          if (jt < wave) tile(jt, Ns[jt], gt, std::false_type{});
+          else if (jt == wave) tile(jt, Ns[jt], gt, std::true_type{});
         }
       }
     }
@@ -492,19 +548,25 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     constexpr int TERMS = BF ? 2 : 1;
     __syncthreads();
 #pragma unroll
-    for (int jt = 0; jt < 8; ++jt)
+    for (int jt = 0; jt < 8; ++jt) {
+      f32x4 ns = {0.f, 0.f, 0.f, 0.f};
+      if (jt <= wave) {
+        if constexpr (W::N_LDS) ns = s_ns[tile0 + jt * 64];
+        else ns = Ns[jt];
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = 16 * wave + 4 * q + r, j = 16 * jt + l16;
         E* d = s_n + (turn == 0 ? i * LDN + j : j * LDN + i);
         if constexpr (BF) {
-          const uint32_t hi = pack2<GDN_BF16>(Ns[jt][r], 0.f) & 0xffffu;
+          const uint32_t hi = pack2<GDN_BF16>(ns[r], 0.f) & 0xffffu;
           d[0] = (E)hi;
-          d[T * LDN] = (E)pack2<GDN_BF16>(Ns[jt][r] - bf16_bits_to_f32(hi), 0.f);
+          d[T * LDN] = (E)pack2<GDN_BF16>(ns[r] - bf16_bits_to_f32(hi), 0.f);
         } else {
-          d[0] = Ns[jt][r];
+          d[0] = ns[r];
         }
       }
+    }
     __syncthreads();
     if (turn == 0 ? do_c : do_b) {
       const void* src = turn == 0 ? a.bt : a.ct;
@@ -526,22 +588,23 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       }
     }
   }
+  auto write = [&](const f32x4 (&v)[8], void* out, int which) {
+    const int64_t at = (t0 * a.G + g) * NN + n16;
+    const int64_t part = (int64_t)(2 * split + which) * a.total * a.G * NN + at;
 #pragma unroll
-  for (int it = 0; it < 8; ++it)
+    for (int it = 0; it < 8; ++it)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * it + 4 * q + r;
-      if (t >= len) continue;
-      const int64_t at = ((t0 + t) * a.G + g) * NN + n16 + l16;
-      if (a.splits > 1) {
-        const int64_t each = a.total * a.G * NN;
-        if (do_b) a.part_bc[(int64_t)(2 * split) * each + at] = dB[it][r];
-        if (do_c) a.part_bc[(int64_t)(2 * split + 1) * each + at] = dC[it][r];
-      } else {
-        if (do_b) store_elem(a.dB, at, dB[it][r], a.dt_in);
-        if (do_c) store_elem(a.dC, at, dC[it][r], a.dt_in);
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * it + 4 * q + r;
+        const uint32_t off = t * (uint32_t)(a.G * NN) + l16;
+        if (t >= len) continue;
+        if (a.splits > 1) *reinterpret_cast<float*>(const_cast<char*>(at_bytes(a.part_bc, part, off, 4))) = v[it][r];
+        else if constexpr (BF) *reinterpret_cast<__bf16*>(const_cast<char*>(at_bytes(out, at, off, 2))) = (__bf16)v[it][r];
+        else store_elem(out, at + off, v[it][r], a.dt_in);
       }
-    }
+  };
+  if (do_b) write(dB, a.dB, 0);
+  if (do_c) write(dC, a.dC, 1);
 }
 
 // dB and dC from the splits' parts, in order.

@@ -23,6 +23,11 @@ struct Piece {
   int64_t len;      // and its tokens
 };
 
+// cu[i], inside the batch, in a scalar register (i is uniform).
+__device__ __forceinline__ int64_t token_at(const int32_t* cu, int i, int64_t total) {
+  return __builtin_amdgcn_readfirstlane((int)min((int64_t)cu[i], total));
+}
+
 // The lanes of a wave test 64 sequences at a time.
 __device__ __forceinline__ Piece find_piece(const int32_t* cu, int N, int64_t total, int64_t slot, int P) {
   const int lane = threadIdx.x & 63;
@@ -33,11 +38,11 @@ __device__ __forceinline__ Piece find_piece(const int32_t* cu, int N, int64_t to
     const bool in = s < hi && (int64_t)s + cu[s] / P <= slot;
     const int n = __popcll(__ballot(in));
     const int nlo = lo + (n - 1) * step;  // the condition holds on a prefix, and for lane 0
-    hi = min(hi, nlo + step);
-    lo = nlo;
+    hi = __builtin_amdgcn_readfirstlane(min(hi, nlo + step));
+    lo = __builtin_amdgcn_readfirstlane(nlo);  // the same in every lane, and in scalar registers with all that follows from it
   }
   Piece p;
-  const int64_t b = min((int64_t)cu[lo], total), e = min((int64_t)cu[lo + 1], total);
+  const int64_t b = token_at(cu, lo, total), e = token_at(cu, lo + 1, total);
   p.begin = b;
   p.len = max(e - b, (int64_t)0);
   p.index = (int)(slot - lo - b / P);
@@ -149,12 +154,6 @@ struct Split {
     }
     return s;
   }
-  // a: exact in the fragment's type, the small terms first
-  __device__ __forceinline__ f32x4 mma_right(f32x4 acc, const Frag<BF>& a) const {
-#pragma unroll
-    for (int k = K - 1; k >= 0; --k) acc = frag_mma(acc, a, t[k]);
-    return acc;
-  }
 };
 
 // 8 consecutive input elements from element (uniform + lane) as a fragment
@@ -170,12 +169,51 @@ __device__ __forceinline__ Frag<BF> frag_from(const void* p, int64_t uniform, ui
   }
 }
 
+// ------------------------------------------------------------------ sums across lanes
+// x from the lane that CTRL names, in a form that folds into the addition
+// that uses it.
+template <int CTRL>
+__device__ __forceinline__ float dpp_zero(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
 __device__ __forceinline__ float row16_sum(float x) {
-  x += dpp_mov<0xB1>(x);
-  x += dpp_mov<0x4E>(x);
-  x += dpp_mov<0x128>(x);
-  x += dpp_mov<0x124>(x);
+  x += dpp_zero<0xB1>(x);
+  x += dpp_zero<0x4E>(x);
+  x += dpp_zero<0x128>(x);
+  x += dpp_zero<0x124>(x);
   return x;
+}
+// Sums of four values over each row of 16 lanes: lane l gets that of value l % 4.
+__device__ __forceinline__ float row16_sum4(float a, float b, float c, float d) {
+  const int l = threadIdx.x;
+  const bool odd = l & 1, two = l & 2;
+  const float p = (odd ? b : a) + dpp_zero<0xB1>(odd ? a : b);
+  const float r = (odd ? d : c) + dpp_zero<0xB1>(odd ? c : d);
+  float x = (two ? r : p) + dpp_zero<0x4E>(two ? p : r);
+  x += dpp_zero<0x128>(x);
+  x += dpp_zero<0x124>(x);
+  return x;
+}
+// Sums of four values over the four rows of 16 lanes: lane l gets, for its
+// place l % 16, that of value l / 16.
+__device__ __forceinline__ float rows_sum4(float a, float b, float c, float d) {
+  auto join = [](float x, float y, auto wide) {  // halves (pairs of rows) of x, then of y, added
+    const unsigned p = __builtin_bit_cast(unsigned, x), r = __builtin_bit_cast(unsigned, y);
+    unsigned u, v;
+    if constexpr (decltype(wide)::value) {
+      const auto t = __builtin_amdgcn_permlane32_swap(p, r, false, false);
+      u = t[0];
+      v = t[1];
+    } else {
+      const auto t = __builtin_amdgcn_permlane16_swap(p, r, false, false);
+      u = t[0];
+      v = t[1];
+    }
+    return __builtin_bit_cast(float, u) + __builtin_bit_cast(float, v);
+  };
+  // after the 32-lane swap the low half holds the first value's sum over halves, the high half the second's
+  const float x = join(a, c, std::true_type{}), y = join(b, d, std::true_type{});
+  return join(x, y, std::false_type{});
 }
 
 }  // namespace gdn

@@ -131,7 +131,9 @@ struct WalkGeom {
   static constexpr int LDF = KB * 32 + (BF ? 8 : 4);   // read vectors [64][LDF], columns in accumulator order
   static constexpr int LDT = kScanChunk + (BF ? 8 : 4);  // write vectors [NN][LDT], inputs [ROWS][LDT], products [HB][64][LDT]
   static constexpr int F0 = 0, K0 = F0 + (OUT ? kScanChunk * LDF : 0), X0 = K0 + NN * LDT, P0 = X0 + ROWS * LDT;
-  static constexpr int ELEMS = P0 + (OUT ? HB * kScanChunk * LDT : 0);
+  static constexpr int LDV = ROWS + 8;                 // inputs as they come [64][LDV], for D x (16-bit form)
+  static constexpr int V0 = P0 + (OUT ? HB * kScanChunk * LDT : 0);
+  static constexpr int ELEMS = V0 + (OUT && BF ? kScanChunk * LDV : 0);
   // floats a head: c (two), dt', the input's weight, the read factor
   static constexpr size_t LDS = ((size_t)ELEMS * sizeof(E) + 15) / 16 * 16 + (size_t)HB * 5 * kScanChunk * 4;
   // vectors of 8 elements that a thread stages
@@ -158,9 +160,10 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
   E* const s_k = reinterpret_cast<E*>(smem) + W::K0;
   E* const s_x = reinterpret_cast<E*>(smem) + W::X0;
   E* const s_p = reinterpret_cast<E*>(smem) + W::P0;
+  E* const s_v = reinterpret_cast<E*>(smem) + W::V0;
   float* const s_g = reinterpret_cast<float*>(smem + ((size_t)W::ELEMS * sizeof(E) + 15) / 16 * 16);  // [HB][5][64]
 
-  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
+  int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hpg = a.H / a.G, hbs = (hpg + HB - 1) / HB;
   const int u = xcd_unit(blockIdx.x, gridDim.x);
@@ -171,8 +174,8 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
     if (sg.seq < 0) return;
   } else {
     sg.seq = slot;
-    sg.begin = min((int64_t)a.cu[slot], a.total);
-    sg.len = max(min((int64_t)a.cu[slot + 1], a.total) - sg.begin, (int64_t)0);
+    sg.begin = token_at(a.cu, slot, a.total);
+    sg.len = max(token_at(a.cu, slot + 1, a.total) - sg.begin, (int64_t)0);
     sg.index = 0;
     sg.count = 1;
   }
@@ -222,9 +225,24 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
     }
   double total_g = 0.0;
 
+  // 16-bit inputs are staged as pairs of tokens by blocks of 8 columns: eight blocks, then eight pairs, a wave
+  auto pair_block = [](int i) { return (i & 7) | (i / 256) << 3; };
+  auto pair_of = [](int i) { return (i >> 3) & 31; };
   // the next chunk's operands travel in registers while this one's are used
   Frag<BF> vf[OUT ? W::FV : 1], vk[W::FV], vx[W::XV];
   float vg[5];
+  // the products of read and write vectors: the 16 x 16 tiles on and below the diagonal (above it in reverse) go round
+  // the head's waves; lane: row lane / 4, four columns
+  constexpr int PER = (10 + WPH - 1) / WPH;
+  f32x4 gm[OUT ? PER : 1];
+  int rts[PER], cts[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int t = min(wave % WPH + k * WPH, 9);
+    const int i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t - i * (i + 1) / 2;
+    rts[k] = REV ? j : i;
+    cts[k] = REV ? i : j;
+  }
   auto fetch = [&](int c) {
     const int64_t t0 = sg.begin + (int64_t)c * Q;
     const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
@@ -245,10 +263,14 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
     for (int k = 0; k < W::XV; ++k) {
       // 16-bit: vectors 2 k and 2 k + 1 are two tokens of the same 8 columns
       const int i = BF ? tid + (k >> 1) * THREADS : tid + k * THREADS;
-      const int pb = i % PB, t = BF ? 2 * (i / PB) + (k & 1) : i / PB;
+      const int pb = BF ? pair_block(i) : i % PB, t = BF ? 2 * pair_of(i) + (k & 1) : i / PB;
       vx[k] = Frag<BF>::zero();
       if (t < len && 8 * pb < rows_in) vx[k] = frag_from<BF>(a.in, t0 * a.in_ts + col0, t * (uint32_t)a.in_ts + 8 * pb, a.in_dt);
     }
+    if constexpr (OUT)
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        gm[k] = *reinterpret_cast<const f32x4*>(at_bytes(a.gm, cg * Q * Q + 16 * rts[k] * Q + 16 * cts[k], (lane >> 2) * Q + (lane & 3) * 4, 4));
     if (tid < HB * Q) {
       const int t = tid % Q;
       const float* gt = a.gates + (cs * a.H + g * hpg + min(hb * HB + tid / Q, hpg - 1)) * 3 * Q;
@@ -277,8 +299,12 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
     if constexpr (BF) {
 #pragma unroll
       for (int k = 0; k < W::XV / 2; ++k) {
-        const int i = tid + k * THREADS, pb = i % PB, t = 2 * (i / PB);
+        const int i = tid + k * THREADS, pb = pair_block(i), t = 2 * pair_of(i);
         const u32x4 v0 = vx[2 * k].v, v1 = vx[2 * k + 1].v;
+        if constexpr (OUT) {
+          *reinterpret_cast<u32x4*>(s_v + t * W::LDV + 8 * pb) = v0;
+          *reinterpret_cast<u32x4*>(s_v + (t + 1) * W::LDV + 8 * pb) = v1;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           *reinterpret_cast<uint32_t*>(s_x + xt_at<BF, LDT>(8 * pb + 2 * e, t)) = (v0[e] & 0xffffu) | (v1[e] << 16);
@@ -321,7 +347,10 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
     const int c = REV ? c_hi - 1 - step : c_lo + step;
     const int64_t t0 = sg.begin + (int64_t)c * Q;
     const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
-    const int64_t cs = slot0 + c, cg = cs * a.G + g;
+    const int64_t cs = slot0 + c;
+    // the lane's places are not known to be the ones of the chunk before: what follows from them is formed anew, in a few
+    // instructions, where it would otherwise be kept in registers that the loop has not got
+    asm volatile("" : "+v"(tid), "+v"(lane), "+v"(l16), "+v"(q));
 
     if (a.blocks != nullptr && mine && (REV ? ((c & 1) || c == chunks - 1) : !(c & 1))) {
       // the state that meets this block of two chunks, as [n][p]
@@ -343,19 +372,6 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
 
     f32x4 acc[PT][4];
     if constexpr (OUT) {
-      // the decay-weighted products of read and write vectors: the tiles on and below the diagonal
-      // (above it in reverse) go round the head's waves; lane: row lane / 4, four columns
-      constexpr int PER = (10 + WPH - 1) / WPH;
-      f32x4 gm[PER];
-      int rts[PER], cts[PER];
-#pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int t = min(wave % WPH + k * WPH, 9);
-        const int i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t - i * (i + 1) / 2;
-        rts[k] = REV ? j : i;
-        cts[k] = REV ? i : j;
-        gm[k] = *reinterpret_cast<const f32x4*>(at_bytes(a.gm, cg * Q * Q + 16 * rts[k] * Q + 16 * cts[k], (lane >> 2) * Q + (lane & 3) * 4, 4));
-      }
       // the state's part of the output
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt)
@@ -430,11 +446,19 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
         for (int e = 0; e < 8; ++e) f[e] *= gh_[3 * Q + 32 * ks + 8 * q + e];
         xs[pt] = Split<BF>::of(f);
       }
+      // four tiles of n at a time, their terms apart: a product never follows the one it adds to
+      constexpr int NG = NT < 4 ? NT : 4;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const Frag<BF> kf = Frag<BF>::load(s_k + (16 * nt + l16) * LDT + 32 * ks + 8 * q);
+      for (int ng = 0; ng < NT; ng += NG) {
+        Frag<BF> kf[NG];
 #pragma unroll
-        for (int pt = 0; pt < PT; ++pt) S[nt][pt] = xs[pt].mma_right(S[nt][pt], kf);
+        for (int i = 0; i < NG; ++i) kf[i] = Frag<BF>::load(s_k + (16 * (ng + i) + l16) * LDT + 32 * ks + 8 * q);
+#pragma unroll
+        for (int k = Split<BF>::K - 1; k >= 0; --k)
+#pragma unroll
+          for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) S[ng + i][pt] = frag_mma(S[ng + i][pt], kf[i], xs[pt].t[k]);
       }
     }
 
@@ -463,9 +487,15 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
 #pragma unroll
             for (int pt = 0; pt < PT; ++pt) {
               const int64_t off = (int64_t)h * D + pd + 16 * pt;
-              const int ib = BF || a.in_dt != GDN_F32 ? 2 : 4, ob = BF || a.out_dt != GDN_F32 ? 2 : 4;
+              const int ob = BF || a.out_dt != GDN_F32 ? 2 : 4;
               float v[4];
-              load_vec<4>(at_bytes(a.in, (t0 + 16 * rt) * a.in_ts + off, l16 * (uint32_t)a.in_ts + 4 * q, ib), 0, BF ? GDN_BF16 : a.in_dt, v);
+              if constexpr (BF) {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(s_v + t * W::LDV + p0 + 16 * pt + 4 * q);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = (r & 1) ? unpack_hi<GDN_BF16>(w[r >> 1]) : unpack_lo<GDN_BF16>(w[r >> 1]);
+              } else {
+                load_vec<4>(at_bytes(a.in, (t0 + 16 * rt) * a.in_ts + off, l16 * (uint32_t)a.in_ts + 4 * q, a.in_dt == GDN_F32 ? 4 : 2), 0, a.in_dt, v);
+              }
 #pragma unroll
               for (int r = 0; r < 4; ++r) v[r] = acc[pt][rt][r] * sc + Dh * v[r];
               store_vec<4>(const_cast<char*>(at_bytes(a.out, (t0 + 16 * rt) * a.H * D + off, l16 * (uint32_t)(a.H * D) + 4 * q, ob)), 0, v, a.out_dt, vout);
@@ -504,7 +534,7 @@ __global__ void __launch_bounds__(256) gdn_m2s_chain_kernel(const M2ScanArgs a, 
   const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= elems || !state_live(a.live, a.live_slots, seq)) return;
   const int P = a.seg_chunks * kScanChunk;
-  const int64_t b = min((int64_t)a.cu[seq], a.total), e = min((int64_t)a.cu[seq + 1], a.total);
+  const int64_t b = token_at(a.cu, seq, a.total), e = token_at(a.cu, seq + 1, a.total);
   const int count = (int)max((e - b + P - 1) / P, (int64_t)1);
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (a.init.base != nullptr) {

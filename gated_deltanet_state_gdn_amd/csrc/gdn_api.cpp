@@ -861,7 +861,7 @@ gdn_status gdn_mamba2_scan(const gdn_m2_dims* dims, int32_t N, const int32_t* cu
   GDN_TRY(check_dtypes(in_dtype, out_dtype));
   if (N == 0 || total_tokens == 0) return ok();  // nothing is read or written
   GDN_TRY(check_scan_io(dims, cu_seqlens, total_tokens, x, Bm, Cm, in_dtype, strides, params, state, slot_map));
-  GDN_REQUIRE(y != nullptr && aligned(y, dtype_bytes(out_dtype)), GDN_EINVAL, "y is NULL or misaligned for out_dtype");
+  GDN_REQUIRE(y != nullptr && aligned(y, 16), GDN_EINVAL, "y is NULL or not 16-byte aligned");
   const ScanWs w = scan_ws(dims, N, total_tokens, false);
   GDN_TRY(check_scan_ws(workspace, workspace_bytes, w.bytes));
   gdn::M2ScanArgs a = scan_args(dims, N, cu_seqlens, total_tokens, x, Bm, Cm, in_dtype, strides, params, state, slot_map,
@@ -869,7 +869,7 @@ gdn_status gdn_mamba2_scan(const gdn_m2_dims* dims, int32_t N, const int32_t* cu
   a.out = y;
   a.out_dt = out_dtype;
   a.fin = a.init;
-  const bool bf = in_dtype == GDN_BF16 && out_dtype != GDN_F32;
+  const bool bf = in_dtype == GDN_BF16 && out_dtype == GDN_BF16;
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = gdn::launch_scan_prep(a, bf, dims->dstate, s);
   if (e == hipSuccess) e = gdn::launch_scan_walk(a, bf, dims->headdim, dims->dstate, false, true, s);
@@ -903,8 +903,8 @@ gdn_status gdn_mamba2_scan_backward(const gdn_m2_dims* dims, int32_t N, const in
   if (total_tokens > 0) {
     const size_t eb = dtype_bytes(in_dtype);
     GDN_REQUIRE(dy != nullptr && aligned(dy, 16), GDN_EINVAL, "dy is NULL or not 16-byte aligned");
-    GDN_REQUIRE(dx && dBm && dCm && ddt && aligned(dx, eb) && aligned(dBm, eb) && aligned(dCm, eb) && aligned(ddt, eb), GDN_EINVAL,
-                "dx, dBm, dCm or ddt is NULL or misaligned for its dtype");
+    GDN_REQUIRE(dx && dBm && dCm && ddt && aligned(dx, 16) && aligned(dBm, eb) && aligned(dCm, eb) && aligned(ddt, eb), GDN_EINVAL,
+                "dx, dBm, dCm or ddt is NULL, dx not 16-byte aligned or another misaligned for its dtype");
   }
   GDN_REQUIRE(aligned(dfinal, 16) && aligned(dinit, 16), GDN_EINVAL, "dfinal or dinit is not 16-byte aligned");
   const ScanWs w = scan_ws(dims, N, total_tokens, true);
@@ -940,17 +940,14 @@ gdn_status gdn_mamba2_scan_backward(const gdn_m2_dims* dims, int32_t N, const in
   q.x = x;
   q.Bm = Bm;
   q.Cm = Cm;
-  q.dt = params->dt;
   q.dy = dy;
   q.A_log = params->A_log;
-  q.dt_bias = params->dt_bias;
   q.cu = cu_seqlens;
   q.live = f.live;
   q.live_slots = f.live_slots;
   q.x_ts = f.in_ts;
   q.b_ts = f.write_ts;
   q.c_ts = f.read_ts;
-  q.dt_ts = f.dt_ts;
   q.total = total_tokens;
   q.N = N;
   q.G = dims->num_groups;

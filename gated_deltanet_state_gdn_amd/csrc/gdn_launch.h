@@ -136,7 +136,7 @@ struct M2ScanArgs {
   float* gm;        // [chunk slots][G][64][64] read . write, or null
   float* seg;       // [segment slots][H][d][n] states at the segments' starts
   double* seg_g;    // [segment slots][H] the segments' summed log-decays
-  float* blocks;    // [block slots][H][n][d] states that meet each 128-token block, or null
+  float* blocks;    // states that meet each 128-token block, [block slots][H] of [n][d] (in reverse [d][n]), or null
   int32_t seg_chunks;  // 0: whole sequences
   int32_t local;       // the segments' first walk
 };
@@ -146,21 +146,19 @@ struct M2GradArgs {
   const void* x;
   const void* Bm;
   const void* Cm;
-  const void* dt;
   const void* dy;
   const float* A_log;
-  const float* dt_bias;
   const int32_t* cu;
   const int32_t* live;
   int64_t live_slots;
-  int64_t x_ts, b_ts, c_ts, dt_ts;
+  int64_t x_ts, b_ts, c_ts;
   int64_t total;
   int32_t N, H, G, dt_in, splits;  // dt_in: dtype of the inputs and their gradients; splits: workgroups a group
   const float* gates;
   const void* bt;      // transposed B and C [chunk slots][G][n][64]
   const void* ct;
   const float* fwd;    // [block slots][H][n][d] states before each block
-  const float* rev;    // gradients of the states after it
+  const float* rev;    // [block slots][H][d][n] gradients of the states after it
   void* dB;            // [T, G, n]
   void* dC;
   void* ddt;           // [T, H]

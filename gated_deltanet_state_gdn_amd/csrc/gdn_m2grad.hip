@@ -47,7 +47,7 @@ struct GradGeom {
   static constexpr bool LATE = BF && D < 128;     // a head's sums are closed while the next head is under way
   static constexpr int XV = T * DK / 8 / 512;     // vectors of 8 elements of x (and of dy) that a thread stages
   // a head's results: column sums [8][128], row sums, the diagonal tiles' row and column sums, the diagonal, the state
-  // parts [NT][128] twice, dt', the waves' parts of <S, dS'> and of sum dy.x, e^{c_last}
+  // parts [NT][128] twice, dt', the waves' parts of <S, dS'> and of sum dy.x, exp(A_log), e^{c_last}
   static constexpr int RES = (8 + 4 + 2 * NT + 1) * T + 24;
   static constexpr int GATES = 5 * T;             // c / 2 (two), e^{c_i}, dt' e^{c_last - c_j}, dt'
   static constexpr int TILES = 36 * 64 * 16;      // bytes of the tiles on and below the diagonal
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
   // states after it while dC's part is
   Frag<BF> vx[W::XV], vy[W::XV];
   f32x4 vs[2 * DB], vr[2 * DB];
-  float vg[7];
+  float vg[8];
   auto fetch_tokens = [&](int h) {
 #pragma unroll
     for (int k = 0; k < W::XV; ++k) {
@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       vg[4] = g0[2 * Q - 1];
       vg[5] = g1[Q - 1];
       vg[6] = g1[2 * Q - 1];
+      vg[7] = a.A_log[h];
     }
   };
   auto commit_tokens = [&](float* res) {
@@ -180,18 +181,28 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       s_wd[tid] = dtp * exp2f((float)(last - c));
       s_dt[tid] = dtp;
       res[(8 + 4 + 2 * NT) * T + tid] = dtp;
-      if (tid == 0) res[W::RES - 1] = exp2f((float)last);
+      if (tid == 0) {
+        res[W::RES - 1] = exp2f((float)last);
+        res[W::RES - 2] = expf(vg[7]);
+      }
     }
   };
-  // the states' rows n of this wave's columns, S^T[n][p]
-  auto fetch_state = [&](const float* base, int h, f32x4 (&v)[2 * DB]) {
+  // a state's column n of this wave's, 8 rows p at a time: from [n][p], or from [p][n]
+  auto fetch_state = [&](const float* base, int h, f32x4 (&v)[2 * DB], auto by_p) {
+    const int64_t at = ((int64_t)slot * a.H + h) * (D * NN);
 #pragma unroll
     for (int k = 0; k < DB; ++k)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         v[2 * k + e] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (D >= 32 || 8 * q < D)
-          v[2 * k + e] = *reinterpret_cast<const f32x4*>(at_bytes(base, ((int64_t)slot * a.H + h) * (D * NN) + n16 * D + 32 * k + 4 * e, l16 * D + 8 * q, 4));
+        if (D < 32 && 8 * q >= D) continue;
+        if constexpr (decltype(by_p)::value) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            v[2 * k + e][r] = *reinterpret_cast<const float*>(at_bytes(base, at + (32 * k + 4 * e + r) * NN + n16, 8 * q * NN + l16, 4));
+        } else {
+          v[2 * k + e] = *reinterpret_cast<const f32x4*>(at_bytes(base, at + n16 * D + 32 * k + 4 * e, l16 * D + 8 * q, 4));
+        }
       }
   };
   auto split_state = [&](const f32x4 (&v)[2 * DB], Split<BF> (&o)[DB]) {
@@ -342,7 +353,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
         if (q == r) pre[k] += before;
         before += tot;
       }
-    const float A = expf(a.A_log[h]), bias = a.dt_bias[h], eq = qs * res[W::RES - 1];
+    const float A = res[W::RES - 2], eq = qs * res[W::RES - 1];
     float sa = 0.f, sb = 0.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -352,8 +363,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
         const float dg = ((wh + pre[k]) + suf[k]) + eq;
         // dt' x_t.X_t over dt'; a step that underflows to zero has a slope of zero with it
         const float own = dtp[k] > 0.f ? ((co[k] + r_cd[t]) + (r_dg[t] + cv[k])) / dtp[k] : 0.f;
-        const float raw = load_elem(a.dt, (t0 + t) * a.dt_ts + h, a.dt_in) + bias;
-        const float d = (own - A * dg) * sigmoid_f(raw);
+        const float d = (own - A * dg) * -expm1f(-dtp[k]);  // softplus' = sigmoid = 1 - e^-softplus
         store_elem(a.ddt, (t0 + t) * a.H + h, d, a.dt_in);
         sa -= A * dtp[k] * dg;
         sb += d;
@@ -374,7 +384,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
   for (int it = 0; it < 8; ++it) dC[it] = dB[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   fetch_tokens(g * hpg + h_lo);
-  fetch_state(a.fwd, g * hpg + h_lo, vs);
+  fetch_state(a.fwd, g * hpg + h_lo, vs, std::false_type{});
   for (int hi = h_lo; hi < h_hi; ++hi) {
     const int h = g * hpg + hi, h_next = min(h + 1, g * hpg + h_hi - 1);
     // the lane's places are not known to be the ones of the head before: what follows from them is formed anew, in a few
@@ -389,7 +399,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     __builtin_amdgcn_sched_barrier(0);
     Columns cc, bb;
     if (do_c) load_columns(a.ct, cc);  // first: loads are waited for in order
-    fetch_state(a.rev, h, vr);
+    fetch_state(a.rev, h, vr, std::true_type{});
     __builtin_amdgcn_sched_barrier(0);
 
     // state parts of dC and dB for the wave's 16 columns; row l16 / 4 of four tiles, token 4 q + l16 % 4 of it
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    fetch_state(a.fwd, h_next, vs);
+    fetch_state(a.fwd, h_next, vs, std::false_type{});
     fetch_tokens(h_next);
     __builtin_amdgcn_sched_barrier(0);
 
@@ -486,7 +496,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
           float diag = 0.f, wd = 0.f, cd = 0.f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float e = j <= i0 + r ? dtj * decay_half((ih[r] - jh) + (il[r] - jl)) : 0.f, m = e * (w[r] * gt[r]);
+            const float e = dtj * decay_half(j <= i0 + r ? (ih[r] - jh) + (il[r] - jl) : -INFINITY), m = e * (w[r] * gt[r]);
             ns[r] += e * w[r];
             if (j == i0 + r) {
               diag = m;

@@ -23,11 +23,11 @@
 // end state, a small kernel chains them, the second walk starts every segment
 // from its true state.
 //
-// Rounding (bf16 inputs): products of two inputs are exact in FP32.  The state
+// Rounding (bf16 inputs and outputs): products of two inputs are exact in FP32.  The state
 // is FP32, and its updates multiply e^{..} dt' x in three bf16 terms, all its
 // 24 bits, with exact B.  For the output alone the state and the decay-weighted
 // products of read and write vectors are rounded to bf16 once, as y is.
-// Other inputs or an FP32 output take the FP32 MFMA throughout.
+// Any other types take the FP32 MFMA throughout.
 #include "gdn_m2scan.h"
 
 #ifndef GDN_SEG_WALKS
@@ -193,7 +193,6 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
   const int64_t col0 = ((int64_t)g * hpg + hb * HB) * D;  // the workgroup's first column of a token's inputs
   const int h = g * hpg + min(hw, hpg - 1);
   const int pd = p0 - hl * D;                   // the wave's rows within its head
-  const bool vout = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 
   if (!state_live(a.live, a.live_slots, sg.seq)) {  // a padded sequence: zero outputs, no state
     if (OUT)
@@ -206,24 +205,47 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
     return;
   }
 
-  // state, transposed: S[nt][pt][r] = (n = 16 nt + 4 q + r, p = p0 + 16 pt + l16)
+  // The state in accumulators.  With outputs it is transposed, S[nt][pt][r] = (n = 16 nt + 4 q + r, p = 16 pt + l16), the
+  // order in which it meets the read vectors; without, (n = 16 nt + l16, p = 16 pt + 4 q + r), which gives blocks [n][p]
+  // four values at a time.  In memory a state is [p][n].
   f32x4 S[NT][PT];
-  auto state_at = [&](int64_t unit, int nt, int pt) { return ((unit * a.H + h) * D + pd + 16 * pt + l16) * NN + 16 * nt + 4 * q; };
+  auto load_state = [&](const void* base, int64_t unit, int dt) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        const int64_t at = ((unit * a.H + h) * D + pd + 16 * pt) * NN + 16 * nt;
+        float f[4];
+        if constexpr (OUT) load_vec<4>(base, at + l16 * NN + 4 * q, dt, f);
+        else
+#pragma unroll
+          for (int r = 0; r < 4; ++r) f[r] = load_elem(base, at + (4 * q + r) * NN + l16, dt);
+        S[nt][pt] = f32x4{f[0], f[1], f[2], f[3]};
+      }
+  };
+  auto store_state = [&](void* base, int64_t unit, int dt) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        const int64_t at = ((unit * a.H + h) * D + pd + 16 * pt) * NN + 16 * nt;
+        const float f[4] = {S[nt][pt][0], S[nt][pt][1], S[nt][pt][2], S[nt][pt][3]};
+        if constexpr (OUT) store_vec<4>(base, at + l16 * NN + 4 * q, f, dt, true);
+        else
+#pragma unroll
+          for (int r = 0; r < 4; ++r) store_elem(base, at + (4 * q + r) * NN + l16, f[r], dt);
+      }
+  };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int pt = 0; pt < PT; ++pt) {
-      S[nt][pt] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (a.local || !mine) continue;
-      if (a.seg_chunks > 0) {
-        S[nt][pt] = *reinterpret_cast<const f32x4*>(a.seg + state_at(slot, nt, pt));
-      } else if (a.init.base != nullptr) {
-        float f[4];
-        load_vec<4>(a.init.base, state_at(a.init.slots != nullptr ? a.init.slots[sg.seq] : sg.seq, nt, pt), a.init.dtype, f);
-        S[nt][pt] = f32x4{f[0], f[1], f[2], f[3]};
-      }
-    }
+    for (int pt = 0; pt < PT; ++pt) S[nt][pt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (!a.local && mine) {
+    if (a.seg_chunks > 0) load_state(a.seg, slot, GDN_F32);
+    else if (a.init.base != nullptr) load_state(a.init.base, a.init.slots != nullptr ? a.init.slots[sg.seq] : sg.seq, a.init.dtype);
+  }
   double total_g = 0.0;
+  const float Dh = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, a.Dskip[h])));
 
   // 16-bit inputs are staged as pairs of tokens by blocks of 8 columns: eight blocks, then eight pairs, a wave
   auto pair_block = [](int i) { return (i & 7) | (i / 256) << 3; };
@@ -236,9 +258,10 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
   constexpr int PER = (10 + WPH - 1) / WPH;
   f32x4 gm[OUT ? PER : 1];
   int rts[PER], cts[PER];
+  const int sub = wave & (WPH - 1);
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
-    const int t = min(wave % WPH + k * WPH, 9);
+    const int t = min(sub + k * WPH, 9);
     const int i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t - i * (i + 1) / 2;
     rts[k] = REV ? j : i;
     cts[k] = REV ? i : j;
@@ -352,20 +375,6 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
     // instructions, where it would otherwise be kept in registers that the loop has not got
     asm volatile("" : "+v"(tid), "+v"(lane), "+v"(l16), "+v"(q));
 
-    if (a.blocks != nullptr && mine && (REV ? ((c & 1) || c == chunks - 1) : !(c & 1))) {
-      // the state that meets this block of two chunks, as [n][p]
-      float* o = a.blocks + ((sg.seq + sg.begin / kGradBlock + (c >> 1)) * a.H + h) * (int64_t)(D * NN);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float* ou = o + (16 * nt + r) * D + pd + 16 * pt;
-            *reinterpret_cast<float*>(reinterpret_cast<char*>(ou) + (uint32_t)(4 * (4 * q * D + l16))) = S[nt][pt][r];
-          }
-    }
-
     __syncthreads();  // the chunk before is done with LDS
     commit(len);
     __syncthreads();
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
       }
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        if (wave % WPH + k * WPH >= 10) continue;
+        if (10 % WPH != 0 && sub + k * WPH >= 10) continue;
         const int r = 16 * rts[k] + (lane >> 2), c0 = 16 * cts[k] + 4 * (lane & 3);
         const float rh = gh_[r], rl = gh_[Q + r];
         const f32x4 ch = *reinterpret_cast<const f32x4*>(gh_ + c0), cl = *reinterpret_cast<const f32x4*>(gh_ + Q + c0);
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
         for (int e = 0; e < 4; ++e) {
           const bool on = REV ? c0 + e >= r : c0 + e <= r;
           const float x = REV ? (ch[e] - rh) + (cl[e] - rl) : (rh - ch[e]) + (rl - cl[e]);
-          f[e] = on ? __builtin_amdgcn_exp2f(x) * w[e] : 0.f;
+          f[e] = __builtin_amdgcn_exp2f(on ? x : -INFINITY) * w[e];
         }
         if constexpr (BF) *reinterpret_cast<u32x2*>(d) = u32x2{pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
         else *reinterpret_cast<f32x4*>(d) = f32x4{f[0], f[1], f[2], f[3]};
@@ -422,13 +431,66 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) acc[pt][rt] *= f;
       }
+
+      __syncthreads();  // the products are there
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        Frag<BF> xf[PT];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) xf[pt] = Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q));
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          if (REV ? (ks == 0 && rt >= 2) : (ks == 1 && rt < 2)) continue;  // all beyond the diagonal
+          const Frag<BF> pf = Frag<BF>::load(s_p + (hl * Q + 16 * rt + l16) * LDT + 32 * ks + 8 * q);
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[pt], pf);
+        }
+      }
+      if (mine) {
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const int t = 16 * rt + l16;
+          if (t < len) {
+            const float sc = REV ? gh_[2 * Q + t] : 1.f;
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) {
+              const int64_t off = (int64_t)h * D + pd + 16 * pt;
+              float v[4];
+              if constexpr (BF) {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(s_v + t * W::LDV + p0 + 16 * pt + 4 * q);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = (r & 1) ? unpack_hi<GDN_BF16>(w[r >> 1]) : unpack_lo<GDN_BF16>(w[r >> 1]);
+              } else {
+                load_vec<4>(at_bytes(a.in, (t0 + 16 * rt) * a.in_ts + off, l16 * (uint32_t)a.in_ts + 4 * q, a.in_dt == GDN_F32 ? 4 : 2), 0, a.in_dt, v);
+              }
+#pragma unroll
+              for (int r = 0; r < 4; ++r) v[r] = acc[pt][rt][r] * sc + Dh * v[r];
+              store_vec<4>(const_cast<char*>(at_bytes(a.out, (t0 + 16 * rt) * a.H * D + off, l16 * (uint32_t)(a.H * D) + 4 * q, BF || a.out_dt != GDN_F32 ? 2 : 4)), 0, v,
+                           BF ? GDN_BF16 : a.out_dt, true);
+            }
+          }
+        }
+      }
     }
-    __builtin_amdgcn_sched_barrier(0);  // keeps the next chunk's loads from being moved up, where registers are short
+
+    if (a.blocks != nullptr && mine && (REV ? ((c & 1) || c == chunks - 1) : !(c & 1))) {
+      // the state that meets this block of two chunks: [p][n] in reverse, [n][p] forward
+      float* o = a.blocks + ((sg.seq + sg.begin / kGradBlock + (c >> 1)) * a.H + h) * (int64_t)(D * NN);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          const int64_t at = OUT ? (pd + 16 * pt) * NN + 16 * nt : 16 * nt * D + pd + 16 * pt;
+          *reinterpret_cast<f32x4*>(const_cast<char*>(at_bytes(o, at, l16 * (OUT ? NN : D) + 4 * q, 4))) = S[nt][pt];
+        }
+    }
+    // the next chunk's loads come after this one's stores: memory operations are waited for in order
+    __builtin_amdgcn_sched_barrier(0);
     if (step + 1 < steps) fetch(REV ? c - 1 : c + 1);
+    __builtin_amdgcn_sched_barrier(0);
 
     // the state after the chunk
-    const float* gt = a.gates + (cs * a.H + h) * 3 * Q;
-    const float end_h = gt[Q - 1], end_l = gt[2 * Q - 1], dec = exp2f(end_h + end_l);
+    const float end_h = gh_[Q - 1], end_l = gh_[2 * Q - 1], dec = exp2f(end_h + end_l);
     total_g += (double)end_h + (double)end_l;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -458,70 +520,18 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
 #pragma unroll
           for (int i = 0; i < NG; ++i)
 #pragma unroll
-            for (int pt = 0; pt < PT; ++pt) S[ng + i][pt] = frag_mma(S[ng + i][pt], kf[i], xs[pt].t[k]);
-      }
-    }
-
-    if constexpr (OUT) {
-      __syncthreads();  // the products are there
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        Frag<BF> xf[PT];
-#pragma unroll
-        for (int pt = 0; pt < PT; ++pt) xf[pt] = Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q));
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          if (REV ? (ks == 0 && rt >= 2) : (ks == 1 && rt < 2)) continue;  // all beyond the diagonal
-          const Frag<BF> pf = Frag<BF>::load(s_p + (hl * Q + 16 * rt + l16) * LDT + 32 * ks + 8 * q);
-#pragma unroll
-          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[pt], pf);
-        }
-      }
-      if (mine) {
-        const float Dh = a.Dskip[h];
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const int t = 16 * rt + l16;
-          if (t < len) {
-            const float sc = REV ? gh_[2 * Q + t] : 1.f;
-#pragma unroll
-            for (int pt = 0; pt < PT; ++pt) {
-              const int64_t off = (int64_t)h * D + pd + 16 * pt;
-              const int ob = BF || a.out_dt != GDN_F32 ? 2 : 4;
-              float v[4];
-              if constexpr (BF) {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(s_v + t * W::LDV + p0 + 16 * pt + 4 * q);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = (r & 1) ? unpack_hi<GDN_BF16>(w[r >> 1]) : unpack_lo<GDN_BF16>(w[r >> 1]);
-              } else {
-                load_vec<4>(at_bytes(a.in, (t0 + 16 * rt) * a.in_ts + off, l16 * (uint32_t)a.in_ts + 4 * q, a.in_dt == GDN_F32 ? 4 : 2), 0, a.in_dt, v);
-              }
-#pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] = acc[pt][rt][r] * sc + Dh * v[r];
-              store_vec<4>(const_cast<char*>(at_bytes(a.out, (t0 + 16 * rt) * a.H * D + off, l16 * (uint32_t)(a.H * D) + 4 * q, ob)), 0, v, a.out_dt, vout);
-            }
-          }
-        }
+            for (int pt = 0; pt < PT; ++pt)
+              S[ng + i][pt] = OUT ? frag_mma(S[ng + i][pt], kf[i], xs[pt].t[k]) : frag_mma(S[ng + i][pt], xs[pt].t[k], kf[i]);
       }
     }
   }
 
   if (!mine) return;
   if (a.local) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt) *reinterpret_cast<f32x4*>(a.seg + state_at(slot, nt, pt)) = S[nt][pt];
+    store_state(a.seg, slot, GDN_F32);
     if (pd == 0 && lane == 0) a.seg_g[(int64_t)slot * a.H + h] = total_g;
   } else if (a.fin.base != nullptr && last_seg && (REV || sg.len > 0)) {
-    const int64_t unit = a.fin.slots != nullptr ? a.fin.slots[sg.seq] : sg.seq;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt) {
-        const float f[4] = {S[nt][pt][0], S[nt][pt][1], S[nt][pt][2], S[nt][pt][3]};
-        store_vec<4>(a.fin.base, state_at(unit, nt, pt), f, a.fin.dtype, true);
-      }
+    store_state(a.fin.base, a.fin.slots != nullptr ? a.fin.slots[sg.seq] : sg.seq, a.fin.dtype);
   }
 }
 

@@ -393,11 +393,11 @@ typedef struct {
  *               sequence leaves its slot untouched; a slot outside the pool
  *               marks a padded sequence (zero outputs).  NULL (and slot_map
  *               NULL): zero initial states, and none kept
- *   y           [total_tokens, H, d] out_dtype
+ *   y           [total_tokens, H, d] out_dtype, 16-byte aligned
  *   workspace   device scratch of at least the queried size, 256-byte aligned,
  *               not read before it is written; calls that share one must not
  *               overlap
- * bf16 inputs with a 16-bit y run on the bf16 matrix instructions (FP32 state
+ * bf16 inputs with a bf16 y run on the bf16 matrix instructions (FP32 state
  * and sums; the state and the decay-weighted B C products are rounded to bf16
  * where they meet y, and only there); any other pair of types runs in FP32
  * throughout.  Within 64 tokens a NaN or infinity also reaches earlier tokens
@@ -415,7 +415,7 @@ gdn_status gdn_mamba2_scan(const gdn_m2_dims* dims, int32_t N, const int32_t* cu
  *               were before it (read only), or both NULL for zero states
  *   dy          [total_tokens, H, d] in_dtype, dense, 16-byte aligned
  *   dfinal      float32 [N, H, d, n], gradient of the final states, or NULL
- *   dx, dBm, dCm, ddt  dense, in_dtype, shaped as the inputs
+ *   dx, dBm, dCm, ddt  dense, in_dtype, shaped as the inputs; dx 16-byte aligned
  *   dA_log, ddt_bias, dD  float32 [H], summed in a fixed order (equal calls
  *               give equal bits)
  *   dinit       float32 [N, H, d, n], gradient of the initial states, or NULL

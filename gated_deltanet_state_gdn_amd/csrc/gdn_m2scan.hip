@@ -31,7 +31,7 @@
 #include "gdn_m2scan.h"
 
 #ifndef GDN_SEG_WALKS
-#define GDN_SEG_WALKS 768
+#define GDN_SEG_WALKS 1024
 #endif
 
 namespace gdn {
@@ -116,12 +116,15 @@ __global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
 }
 
 // ------------------------------------------------------------------ walk
-// Waves of a walk: eight over 256 state rows (four heads of 64) share the read
-// and write vectors of a chunk; four where a group has no more rows than 128,
-// and in FP32, whose operands are twice as wide.
-template <bool BF, int D, int NN, int NW, bool OUT>
+// Four waves over 128 state rows (two heads of 64), two workgroups on a compute
+// unit: one's vector work then runs beside the other's matrix work.  Eight
+// waves over 256 rows, one workgroup, share the read and write vectors of a
+// chunk among twice the heads but keep in step: a prefill of 20,408 tokens
+// through 128 heads took 789 us that way, 678 us this way.
+template <bool BF, int D, int NN, bool OUT>
 struct WalkGeom {
   typedef typename Frag<BF>::E E;
+  static constexpr int NW = 4;
   static constexpr int THREADS = 64 * NW;
   static constexpr int PT = D == 16 ? 1 : 2;           // 16-row tiles of a wave
   static constexpr int ROWS = 16 * PT * NW;            // state rows of the workgroup
@@ -131,9 +134,7 @@ struct WalkGeom {
   static constexpr int LDF = KB * 32 + (BF ? 8 : 4);   // read vectors [64][LDF], columns in accumulator order
   static constexpr int LDT = kScanChunk + (BF ? 8 : 4);  // write vectors [NN][LDT], inputs [ROWS][LDT], products [HB][64][LDT]
   static constexpr int F0 = 0, K0 = F0 + (OUT ? kScanChunk * LDF : 0), X0 = K0 + NN * LDT, P0 = X0 + ROWS * LDT;
-  static constexpr int LDV = ROWS + 8;                 // inputs as they come [64][LDV], for D x (16-bit form)
-  static constexpr int V0 = P0 + (OUT ? HB * kScanChunk * LDT : 0);
-  static constexpr int ELEMS = V0 + (OUT && BF ? kScanChunk * LDV : 0);
+  static constexpr int ELEMS = P0 + (OUT ? HB * kScanChunk * LDT : 0);
   // floats a head: c (two), dt', the input's weight, the read factor
   static constexpr size_t LDS = ((size_t)ELEMS * sizeof(E) + 15) / 16 * 16 + (size_t)HB * 5 * kScanChunk * 4;
   // vectors of 8 elements that a thread stages
@@ -149,9 +150,9 @@ __device__ __forceinline__ int xt_at(int p, int t) {
   return p * LDT + (BF ? ((((t >> 3) ^ (p >> 3)) & 7) << 3 | (t & 7)) : t);
 }
 
-template <bool BF, int D, int NN, int NW, bool REV, bool OUT>
-__global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
-  using W = WalkGeom<BF, D, NN, NW, OUT>;
+template <bool BF, int D, int NN, bool REV, bool OUT>
+__global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
+  using W = WalkGeom<BF, D, NN, OUT>;
   typedef typename W::E E;
   constexpr int PT = W::PT, HB = W::HB, NT = W::NT, KB = W::KB, LDF = W::LDF, LDT = W::LDT, ROWS = W::ROWS, Q = kScanChunk;
   constexpr int THREADS = W::THREADS, WPH = W::WPH, PB = ROWS / 8;
@@ -160,7 +161,6 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
   E* const s_k = reinterpret_cast<E*>(smem) + W::K0;
   E* const s_x = reinterpret_cast<E*>(smem) + W::X0;
   E* const s_p = reinterpret_cast<E*>(smem) + W::P0;
-  E* const s_v = reinterpret_cast<E*>(smem) + W::V0;
   float* const s_g = reinterpret_cast<float*>(smem + ((size_t)W::ELEMS * sizeof(E) + 15) / 16 * 16);  // [HB][5][64]
 
   int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
@@ -247,12 +247,13 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
   double total_g = 0.0;
   const float Dh = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, a.Dskip[h])));
 
-  // 16-bit inputs are staged as pairs of tokens by blocks of 8 columns: eight blocks, then eight pairs, a wave
-  auto pair_block = [](int i) { return (i & 7) | (i / 256) << 3; };
-  auto pair_of = [](int i) { return (i >> 3) & 31; };
-  // the next chunk's operands travel in registers while this one's are used
+  // A chunk's operands are fetched a chunk ahead, in registers.  What a thread stages: vectors of 8 along n of the read
+  // vectors (token t, and t + 256 / (NN / 8) for the next), of 8 tokens of the transposed write vectors, and of 8 columns of
+  // the inputs, in 16-bit form for two neighbouring tokens (eight column blocks, then eight pairs, a wave).
+  constexpr int VPR = NN / 8, FSTEP = 256 / VPR;
+  static_assert(256 % VPR == 0 && NN * 8 % 64 == 0, "whole rows of vectors");
   Frag<BF> vf[OUT ? W::FV : 1], vk[W::FV], vx[W::XV];
-  float vg[5];
+  float vg[3];
   // the products of read and write vectors: the 16 x 16 tiles on and below the diagonal (above it in reverse) go round
   // the head's waves; lane: row lane / 4, four columns
   constexpr int PER = (10 + WPH - 1) / WPH;
@@ -270,87 +271,95 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
     const int64_t t0 = sg.begin + (int64_t)c * Q;
     const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
     const int64_t cs = slot0 + c, cg = cs * a.G + g;
+    const char* pk = static_cast<const char*>(a.wt) + cg * (NN * Q * (int)sizeof(E));
 #pragma unroll
-    for (int k = 0; k < W::FV; ++k) {
-      const int i = tid + k * THREADS;
-      if (i < Q * NN / 8) {
-        vk[k] = Frag<BF>::load(reinterpret_cast<const E*>(at_bytes(a.wt, cg * NN * Q, i * 8, sizeof(E))));
-        if constexpr (OUT) {
-          const int t = i / (NN / 8), n0 = (i - t * (NN / 8)) * 8;
-          vf[k] = Frag<BF>::zero();
-          if (t < len) vf[k] = frag_from<BF>(a.read, t0 * a.read_ts + g * NN, t * (uint32_t)a.read_ts + n0, a.in_dt);
-        }
+    for (int k = 0; k < W::FV; ++k)
+      if (NN * 8 % 256 == 0 || tid + 256 * k < NN * 8)
+        vk[k] = Frag<BF>::load(reinterpret_cast<const E*>(pk + k * 256 * 8 * sizeof(E) + (uint32_t)(tid * 8 * sizeof(E))));
+    if constexpr (OUT) {
+      const int t = tid / VPR;
+      const uint32_t off = t * (uint32_t)a.read_ts + tid % VPR * 8;
+      const int64_t at = t0 * a.read_ts + g * NN;
+#pragma unroll
+      for (int k = 0; k < W::FV; ++k) {
+        vf[k] = Frag<BF>::zero();
+        if (t + k * FSTEP < len) vf[k] = frag_from<BF>(a.read, at + k * FSTEP * a.read_ts, off, a.in_dt);
       }
     }
+    {
+      const int t = BF ? 2 * (tid >> 3 & 31) : tid / PB, pb = BF ? tid & 7 : tid % PB;
+      const uint32_t off = t * (uint32_t)a.in_ts + 8 * pb;
+      const int64_t at = t0 * a.in_ts + col0;
 #pragma unroll
-    for (int k = 0; k < W::XV; ++k) {
-      // 16-bit: vectors 2 k and 2 k + 1 are two tokens of the same 8 columns
-      const int i = BF ? tid + (k >> 1) * THREADS : tid + k * THREADS;
-      const int pb = BF ? pair_block(i) : i % PB, t = BF ? 2 * pair_of(i) + (k & 1) : i / PB;
-      vx[k] = Frag<BF>::zero();
-      if (t < len && 8 * pb < rows_in) vx[k] = frag_from<BF>(a.in, t0 * a.in_ts + col0, t * (uint32_t)a.in_ts + 8 * pb, a.in_dt);
+      for (int k = 0; k < W::XV; ++k) {
+        // BF: vectors 2 k and 2 k + 1 are two tokens of block pb + 8 k; else the token is 256 / PB further on
+        const int dt = BF ? (k & 1) : k * (256 / PB), dp = BF ? 8 * (k >> 1) : 0;
+        vx[k] = Frag<BF>::zero();
+        if (t + dt < len && 8 * (pb + dp) < rows_in) vx[k] = frag_from<BF>(a.in, at + dt * a.in_ts + 8 * dp, off, a.in_dt);
+      }
     }
-    if constexpr (OUT)
+    if constexpr (OUT) {
+      const char* pg = reinterpret_cast<const char*>(a.gm + cg * Q * Q);
 #pragma unroll
       for (int k = 0; k < PER; ++k)
-        gm[k] = *reinterpret_cast<const f32x4*>(at_bytes(a.gm, cg * Q * Q + 16 * rts[k] * Q + 16 * cts[k], (lane >> 2) * Q + (lane & 3) * 4, 4));
-    if (tid < HB * Q) {
-      const int t = tid % Q;
-      const float* gt = a.gates + (cs * a.H + g * hpg + min(hb * HB + tid / Q, hpg - 1)) * 3 * Q;
-      vg[0] = gt[t];
-      vg[1] = gt[Q + t];
-      vg[2] = gt[2 * Q + t];
-      vg[3] = gt[Q - 1];
-      vg[4] = gt[2 * Q - 1];
+        gm[k] = *reinterpret_cast<const f32x4*>(pg + (16 * rts[k] * Q + 16 * cts[k]) * 4 + (uint32_t)(((lane >> 2) * Q + (lane & 3) * 4) * 4));
+    }
+    if (wave < HB) {  // a wave a head, a token a lane
+      const char* gt = reinterpret_cast<const char*>(a.gates + (cs * a.H + g * hpg + min(hb * HB + wave, hpg - 1)) * 3 * Q);
+      vg[0] = *reinterpret_cast<const float*>(gt + (uint32_t)(4 * lane));
+      vg[1] = *reinterpret_cast<const float*>(gt + 4 * Q + (uint32_t)(4 * lane));
+      vg[2] = *reinterpret_cast<const float*>(gt + 8 * Q + (uint32_t)(4 * lane));
     }
   };
   auto commit = [&](int len) {
+    {
+      E* d = s_k + (tid >> 3) * LDT + (tid & 7) * 8;
 #pragma unroll
-    for (int k = 0; k < W::FV; ++k) {
-      const int i = tid + k * THREADS;
-      if (i < Q * NN / 8) {
-        *reinterpret_cast<Frag<BF>*>(s_k + (i >> 3) * LDT + (i & 7) * 8) = vk[k];
-        if constexpr (OUT) {
-          const int t = i / (NN / 8), n0 = (i - t * (NN / 8)) * 8;
-          // n = 32 k + 16 b + 4 s + r is stored at 32 k + 8 s + 4 b + r
-          E* d = s_f + t * LDF + (n0 & ~31) + 2 * (n0 & 15) + ((n0 >> 4) & 1) * 4;
-          vf[k].store_halves(d, d + 8);
-          if (NN == 16) Frag<BF>::zero().store_halves(d + 4, d + 12);
+      for (int k = 0; k < W::FV; ++k)
+        if (NN * 8 % 256 == 0 || tid + 256 * k < NN * 8) *reinterpret_cast<Frag<BF>*>(d + k * 32 * LDT) = vk[k];
+    }
+    if constexpr (OUT) {
+      // n = 32 k + 16 b + 4 s + r is stored at 32 k + 8 s + 4 b + r
+      const int t = tid / VPR, n0 = tid % VPR * 8;
+      E* d = s_f + t * LDF + (n0 & ~31) + 2 * (n0 & 15) + ((n0 >> 4) & 1) * 4;
+#pragma unroll
+      for (int k = 0; k < W::FV; ++k)
+        if (Q * VPR % 256 == 0 || t + k * FSTEP < Q) {
+          vf[k].store_halves(d + k * FSTEP * LDF, d + k * FSTEP * LDF + 8);
+          if (NN == 16) Frag<BF>::zero().store_halves(d + k * FSTEP * LDF + 4, d + k * FSTEP * LDF + 12);
         }
-      }
     }
     if constexpr (BF) {
+      // 64 rows on, a row's block of 8 has the same place in the permutation
+      E* d = s_x + xt_at<BF, LDT>(8 * (tid & 7), 2 * (tid >> 3 & 31));
 #pragma unroll
       for (int k = 0; k < W::XV / 2; ++k) {
-        const int i = tid + k * THREADS, pb = pair_block(i), t = 2 * pair_of(i);
         const u32x4 v0 = vx[2 * k].v, v1 = vx[2 * k + 1].v;
-        if constexpr (OUT) {
-          *reinterpret_cast<u32x4*>(s_v + t * W::LDV + 8 * pb) = v0;
-          *reinterpret_cast<u32x4*>(s_v + (t + 1) * W::LDV + 8 * pb) = v1;
-        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          *reinterpret_cast<uint32_t*>(s_x + xt_at<BF, LDT>(8 * pb + 2 * e, t)) = (v0[e] & 0xffffu) | (v1[e] << 16);
-          *reinterpret_cast<uint32_t*>(s_x + xt_at<BF, LDT>(8 * pb + 2 * e + 1, t)) = (v0[e] >> 16) | (v1[e] & 0xffff0000u);
+          *reinterpret_cast<uint32_t*>(d + (64 * k + 2 * e) * LDT) = __builtin_amdgcn_perm(v1[e], v0[e], 0x05040100u);
+          *reinterpret_cast<uint32_t*>(d + (64 * k + 2 * e + 1) * LDT) = __builtin_amdgcn_perm(v1[e], v0[e], 0x07060302u);
         }
       }
     } else {
 #pragma unroll
       for (int k = 0; k < W::XV; ++k) {
-        const int i = tid + k * THREADS, pb = i % PB, t = i / PB;
+        const int pb = tid % PB, t = tid / PB + k * (256 / PB);
         float f[8];
         vx[k].widen(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s_x[xt_at<BF, LDT>(8 * pb + e, t)] = (E)f[e];
       }
     }
-    if (tid < HB * Q) {
-      const float to_end = exp2f((vg[3] - vg[0]) + (vg[4] - vg[1])), from_start = exp2f(vg[0] + vg[1]);
-      float* o = s_g + tid / Q * 5 * Q + tid % Q;
+    if (wave < HB) {
+      const float end_h = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vg[0]), 63));
+      const float end_l = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, vg[1]), 63));
+      const float to_end = exp2f((end_h - vg[0]) + (end_l - vg[1])), from_start = exp2f(vg[0] + vg[1]);
+      float* o = s_g + wave * 5 * Q + lane;
       o[0] = vg[0];
       o[Q] = vg[1];
       o[2 * Q] = vg[2];
-      o[3 * Q] = tid % Q < len ? (REV ? from_start : to_end * vg[2]) : 0.f;
+      o[3 * Q] = lane < len ? (REV ? from_start : to_end * vg[2]) : 0.f;
       o[4 * Q] = REV ? to_end : from_start;
     }
   };
@@ -381,6 +390,23 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
 
     f32x4 acc[PT][4];
     if constexpr (OUT) {
+      // the inputs once more, for D x, before anything that would hold these loads up
+      InVec<BF ? GDN_BF16 : GDN_F32, 4> vin[PT][4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          const int64_t at = (t0 + 16 * rt) * a.in_ts + (int64_t)h * D + pd + 16 * pt;
+          const uint32_t off = l16 * (uint32_t)a.in_ts + 4 * q;
+          if constexpr (BF) {
+            if (16 * rt + l16 < len) vin[pt][rt].load(at_bytes(a.in, at, off, 2), 0);
+          } else {
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+            if (16 * rt + l16 < len) load_vec<4>(at_bytes(a.in, at, off, a.in_dt == GDN_F32 ? 4 : 2), 0, a.in_dt, f);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) vin[pt][rt].w[r] = __float_as_uint(f[r]);
+          }
+        }
       // the state's part of the output
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt)
@@ -410,8 +436,11 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
       for (int k = 0; k < PER; ++k) {
         if (10 % WPH != 0 && sub + k * WPH >= 10) continue;
         const int r = 16 * rts[k] + (lane >> 2), c0 = 16 * cts[k] + 4 * (lane & 3);
-        const float rh = gh_[r], rl = gh_[Q + r];
-        const f32x4 ch = *reinterpret_cast<const f32x4*>(gh_ + c0), cl = *reinterpret_cast<const f32x4*>(gh_ + Q + c0);
+        // (the low parts of c are below what is left of these products once they are bf16)
+        const float rh = gh_[r], rl = BF ? 0.f : gh_[Q + r];
+        const f32x4 ch = *reinterpret_cast<const f32x4*>(gh_ + c0);
+        f32x4 cl = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (!BF) cl = *reinterpret_cast<const f32x4*>(gh_ + Q + c0);
         f32x4 w = gm[k];
         if constexpr (!REV) w *= *reinterpret_cast<const f32x4*>(gh_ + 2 * Q + c0);
         E* d = s_p + (hl * Q + r) * LDT + c0;
@@ -419,7 +448,8 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const bool on = REV ? c0 + e >= r : c0 + e <= r;
-          const float x = REV ? (ch[e] - rh) + (cl[e] - rl) : (rh - ch[e]) + (rl - cl[e]);
+          float x = REV ? ch[e] - rh : rh - ch[e];
+          if constexpr (!BF) x += REV ? cl[e] - rl : rl - cl[e];
           f[e] = __builtin_amdgcn_exp2f(on ? x : -INFINITY) * w[e];
         }
         if constexpr (BF) *reinterpret_cast<u32x2*>(d) = u32x2{pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
@@ -456,13 +486,7 @@ __global__ void __launch_bounds__(64 * NW, BF ? 2 : 1) gdn_m2s_walk_kernel(const
             for (int pt = 0; pt < PT; ++pt) {
               const int64_t off = (int64_t)h * D + pd + 16 * pt;
               float v[4];
-              if constexpr (BF) {
-                const u32x2 w = *reinterpret_cast<const u32x2*>(s_v + t * W::LDV + p0 + 16 * pt + 4 * q);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = (r & 1) ? unpack_hi<GDN_BF16>(w[r >> 1]) : unpack_lo<GDN_BF16>(w[r >> 1]);
-              } else {
-                load_vec<4>(at_bytes(a.in, (t0 + 16 * rt) * a.in_ts + off, l16 * (uint32_t)a.in_ts + 4 * q, a.in_dt == GDN_F32 ? 4 : 2), 0, a.in_dt, v);
-              }
+              vin[pt][rt].widen(v);
 #pragma unroll
               for (int r = 0; r < 4; ++r) v[r] = acc[pt][rt][r] * sc + Dh * v[r];
               store_vec<4>(const_cast<char*>(at_bytes(a.out, (t0 + 16 * rt) * a.H * D + off, l16 * (uint32_t)(a.H * D) + 4 * q, BF || a.out_dt != GDN_F32 ? 2 : 4)), 0, v,
@@ -572,14 +596,15 @@ int64_t scan_slots(int64_t N, int64_t total, int64_t P) { return N + (total + P 
 
 namespace {
 
-int walk_waves(bool bf, int d, int hpg) { return bf && hpg * d > (d == 16 ? 64 : 128) ? 8 : 4; }
+// Heads of a walk's workgroup.
+int walk_heads(int d) { return (d == 16 ? 64 : 128) / d; }
 
-template <bool BF, int D, int NN, int NW, bool REV, bool OUT>
+template <bool BF, int D, int NN, bool REV, bool OUT>
 hipError_t walk(const M2ScanArgs& a, hipStream_t s) {
-  using W = WalkGeom<BF, D, NN, NW, OUT>;
+  using W = WalkGeom<BF, D, NN, OUT>;
   const int hpg = a.H / a.G, hbs = (hpg + W::HB - 1) / W::HB;
   const int64_t slots = a.seg_chunks > 0 ? scan_slots(a.N, a.total, (int64_t)a.seg_chunks * kScanChunk) : a.N;
-  auto* k = gdn_m2s_walk_kernel<BF, D, NN, NW, REV, OUT>;
+  auto* k = gdn_m2s_walk_kernel<BF, D, NN, REV, OUT>;
   if (W::LDS > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)W::LDS);
     if (e != hipSuccess) return e;
@@ -588,24 +613,17 @@ hipError_t walk(const M2ScanArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool BF, int D, int NN, int NW>
-hipError_t walk_kind(const M2ScanArgs& a, bool rev, bool out, hipStream_t s) {
-  if (rev) return out ? walk<BF, D, NN, NW, true, true>(a, s) : walk<BF, D, NN, NW, true, false>(a, s);
-  return out ? walk<BF, D, NN, NW, false, true>(a, s) : walk<BF, D, NN, NW, false, false>(a, s);
-}
-
 template <bool BF, int D, int NN>
-hipError_t walk_nw(const M2ScanArgs& a, bool rev, bool out, hipStream_t s) {
-  if constexpr (BF)
-    if (walk_waves(true, D, a.H / a.G) == 8) return walk_kind<BF, D, NN, 8>(a, rev, out, s);
-  return walk_kind<BF, D, NN, 4>(a, rev, out, s);
+hipError_t walk_kind(const M2ScanArgs& a, bool rev, bool out, hipStream_t s) {
+  if (rev) return out ? walk<BF, D, NN, true, true>(a, s) : walk<BF, D, NN, true, false>(a, s);
+  return out ? walk<BF, D, NN, false, true>(a, s) : walk<BF, D, NN, false, false>(a, s);
 }
 
 template <bool BF, int D>
 hipError_t walk_n(const M2ScanArgs& a, int n, bool rev, bool out, hipStream_t s) {
-  if (n == 16) return walk_nw<BF, D, 16>(a, rev, out, s);
-  if (n == 64) return walk_nw<BF, D, 64>(a, rev, out, s);
-  return walk_nw<BF, D, 128>(a, rev, out, s);
+  if (n == 16) return walk_kind<BF, D, 16>(a, rev, out, s);
+  if (n == 64) return walk_kind<BF, D, 64>(a, rev, out, s);
+  return walk_kind<BF, D, 128>(a, rev, out, s);
 }
 
 template <bool BF>
@@ -628,7 +646,10 @@ hipError_t prep(const M2ScanArgs& a, int n, hipStream_t s) {
 
 // Chunks a segment (even, so that blocks of two chunks do not straddle), 0 for whole sequences.
 int scan_seg_chunks(int64_t N, int64_t total, int H, int G, int d) {
-  const int hpg = H / G, hb = walk_waves(true, d, hpg) * (d == 16 ? 16 : 32) / d;
+#ifdef GDN_SEG_FORCE
+  if (GDN_SEG_FORCE >= 0) return GDN_SEG_FORCE;
+#endif
+  const int hpg = H / G, hb = walk_heads(d);
   const int64_t walks = (int64_t)G * ((hpg + hb - 1) / hb), chunks = (total + kScanChunk - 1) / kScanChunk;
   if (N * walks >= 512 || chunks <= 16) return 0;
   int64_t per = chunks * walks / GDN_SEG_WALKS;

@@ -731,7 +731,8 @@ struct Carve {
 
 struct ScanWs {
   size_t gates, wt, gm, seg, seg_g, rt, fwd, rev, part, part_bc, bytes;
-  int seg_chunks, splits;
+  gdn::ScanPlan plan;
+  int splits;
 };
 
 ScanWs scan_ws(const gdn_m2_dims* d, int32_t N, int64_t total, bool backward) {
@@ -739,12 +740,12 @@ ScanWs scan_ws(const gdn_m2_dims* d, int32_t N, int64_t total, bool backward) {
   Carve c;
   const size_t H = d->num_heads, G = d->num_groups, state = (size_t)d->headdim * d->dstate * 4;
   const size_t chunks = gdn::scan_slots(N, total, 64);
-  w.seg_chunks = gdn::scan_seg_chunks(N, total, d->num_heads, d->num_groups, d->headdim);
+  w.plan = gdn::scan_plan(N, total, d->num_heads, d->num_groups, d->headdim);
   w.gates = c.take(chunks * H * 3 * 64 * 4);
   w.wt = c.take(chunks * G * d->dstate * 64 * 4);
   w.gm = c.take(chunks * G * 64 * 64 * 4);
-  if (w.seg_chunks > 0) {
-    const size_t segs = gdn::scan_slots(N, total, (int64_t)w.seg_chunks * 64);
+  if (w.plan.seg_chunks > 0) {
+    const size_t segs = gdn::scan_slots(N, total, (int64_t)w.plan.seg_chunks * 64);
     w.seg = c.take(segs * H * state);
     w.seg_g = c.take(segs * H * 8);
   }
@@ -761,12 +762,17 @@ ScanWs scan_ws(const gdn_m2_dims* d, int32_t N, int64_t total, bool backward) {
   return w;
 }
 
+// A block's 128 tokens are reached by 32-bit byte offsets.
+constexpr int64_t kMaxTokenStride = 1 << 22;
+
 gdn_status check_scan_sizes(const gdn_m2_dims* d, int32_t N, int64_t total) {
   GDN_TRY(check_m2_dims(d));
   GDN_REQUIRE(N >= 0 && total >= 0, GDN_EINVAL, "N=%d and total_tokens=%lld must be >= 0", N, (long long)total);
   GDN_REQUIRE(total <= INT32_MAX, GDN_EINVAL, "total_tokens=%lld exceeds the 32-bit cu_seqlens", (long long)total);
   GDN_REQUIRE(N > 0 || total == 0, GDN_EINVAL, "%lld tokens in no sequence", (long long)total);
   GDN_REQUIRE(d->num_heads <= 65535, GDN_EUNSUPPORTED, "H=%d: at most 65535 heads are supported", d->num_heads);
+  GDN_REQUIRE((int64_t)d->num_heads * d->headdim <= kMaxTokenStride && (int64_t)d->num_groups * d->dstate <= kMaxTokenStride,
+              GDN_EUNSUPPORTED, "H d and G n must be at most 2^22");
   GDN_REQUIRE(gdn::scan_slots(N, total, 64) * d->num_heads <= INT32_MAX, GDN_EUNSUPPORTED,
               "64-token chunks x heads exceed the grid limit");
   return GDN_OK;
@@ -841,7 +847,8 @@ gdn::M2ScanArgs scan_args(const gdn_m2_dims* d, int32_t N, const int32_t* cu, in
   a.gm = reinterpret_cast<float*>(ws + w.gm);
   a.seg = reinterpret_cast<float*>(ws + w.seg);
   a.seg_g = reinterpret_cast<double*>(ws + w.seg_g);
-  a.seg_chunks = w.seg_chunks;
+  a.seg_chunks = w.plan.seg_chunks;
+  a.narrow = w.plan.narrow;
   return a;
 }
 

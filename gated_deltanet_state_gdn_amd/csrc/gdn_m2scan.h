@@ -65,6 +65,15 @@ __device__ __forceinline__ const char* at_bytes(const void* base, int64_t unifor
   return static_cast<const char*>(base) + uniform * eb + (uint32_t)(lane * (uint32_t)eb);
 }
 
+// A window of `bytes` from a uniform element: reads past its end give zero and
+// writes past it are dropped, so a chunk's last tokens need no branches, and
+// the number of memory operations in flight is known to the compiler.  All of
+// an access's offset goes into its lane offset, which is what is compared with
+// the window's size.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window16(const void* base, int64_t elem, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(base)) + 2 * elem, 0, (int)bytes, 0x00027000);
+}
+
 // ------------------------------------------------------------------ fragments
 // A fragment is the 8 values that a lane gives a 16 x 16 product over 32 k's:
 // lane l holds row (or column) l % 16 and the k's stored at 8 (l / 16) .. + 7.

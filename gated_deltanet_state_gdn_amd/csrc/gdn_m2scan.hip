@@ -30,10 +30,6 @@
 // Any other types take the FP32 MFMA throughout.
 #include "gdn_m2scan.h"
 
-#ifndef GDN_SEG_WALKS
-#define GDN_SEG_WALKS 1024
-#endif
-
 namespace gdn {
 
 // ------------------------------------------------------------------ prep
@@ -121,12 +117,12 @@ __global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
 // waves over 256 rows, one workgroup, share the read and write vectors of a
 // chunk among twice the heads but keep in step: a prefill of 20,408 tokens
 // through 128 heads took 789 us that way, 678 us this way.
-template <bool BF, int D, int NN, bool OUT>
+template <bool BF, int D, int NN, int PT_, bool OUT>
 struct WalkGeom {
   typedef typename Frag<BF>::E E;
   static constexpr int NW = 4;
   static constexpr int THREADS = 64 * NW;
-  static constexpr int PT = D == 16 ? 1 : 2;           // 16-row tiles of a wave
+  static constexpr int PT = PT_;                       // 16-row tiles of a wave
   static constexpr int ROWS = 16 * PT * NW;            // state rows of the workgroup
   static constexpr int HB = ROWS / D;                  // its heads
   static constexpr int WPH = NW / HB;                  // waves of a head
@@ -150,11 +146,11 @@ __device__ __forceinline__ int xt_at(int p, int t) {
   return p * LDT + (BF ? ((((t >> 3) ^ (p >> 3)) & 7) << 3 | (t & 7)) : t);
 }
 
-template <bool BF, int D, int NN, bool REV, bool OUT>
+template <bool BF, int D, int NN, int PT, bool REV, bool OUT>
 __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
-  using W = WalkGeom<BF, D, NN, OUT>;
+  using W = WalkGeom<BF, D, NN, PT, OUT>;
   typedef typename W::E E;
-  constexpr int PT = W::PT, HB = W::HB, NT = W::NT, KB = W::KB, LDF = W::LDF, LDT = W::LDT, ROWS = W::ROWS, Q = kScanChunk;
+  constexpr int HB = W::HB, NT = W::NT, KB = W::KB, LDF = W::LDF, LDT = W::LDT, ROWS = W::ROWS, Q = kScanChunk;
   constexpr int THREADS = W::THREADS, WPH = W::WPH, PB = ROWS / 8;
   extern __shared__ __align__(16) unsigned char smem[];
   E* const s_f = reinterpret_cast<E*>(smem) + W::F0;
@@ -276,7 +272,12 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
     for (int k = 0; k < W::FV; ++k)
       if (NN * 8 % 256 == 0 || tid + 256 * k < NN * 8)
         vk[k] = Frag<BF>::load(reinterpret_cast<const E*>(pk + k * 256 * 8 * sizeof(E) + (uint32_t)(tid * 8 * sizeof(E))));
-    if constexpr (OUT) {
+    if constexpr (OUT && BF) {
+      const auto w = window16(a.read, t0 * a.read_ts + g * NN, 2 * ((len - 1) * a.read_ts + NN));
+      const int off = 2 * (tid / VPR * (int)a.read_ts + tid % VPR * 8);
+#pragma unroll
+      for (int k = 0; k < W::FV; ++k) vf[k].v = __builtin_amdgcn_raw_buffer_load_b128(w, off + 2 * k * FSTEP * (int)a.read_ts, 0, 0);
+    } else if constexpr (OUT) {
       const int t = tid / VPR;
       const uint32_t off = t * (uint32_t)a.read_ts + tid % VPR * 8;
       const int64_t at = t0 * a.read_ts + g * NN;
@@ -286,23 +287,23 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
         if (t + k * FSTEP < len) vf[k] = frag_from<BF>(a.read, at + k * FSTEP * a.read_ts, off, a.in_dt);
       }
     }
-    {
-      const int t = BF ? 2 * (tid >> 3 & 31) : tid / PB, pb = BF ? tid & 7 : tid % PB;
+    if constexpr (BF) {
+      // rows past the group's heads read what lies there, or zero: no output depends on them
+      const auto w = window16(a.in, t0 * a.in_ts + col0, 2 * ((len - 1) * a.in_ts + rows_in));
+      const int off = 2 * (2 * (tid >> 3 & 31) * (int)a.in_ts + 8 * (tid & 7));
+#pragma unroll
+      for (int k = 0; k < W::XV; ++k)  // 2 k and 2 k + 1 are two tokens of the same block of columns
+        vx[k].v = __builtin_amdgcn_raw_buffer_load_b128(w, off + 2 * ((k & 1) * (int)a.in_ts + 64 * (k >> 1)), 0, 0);
+    } else {
+      const int t = tid / PB, pb = tid % PB;
       const uint32_t off = t * (uint32_t)a.in_ts + 8 * pb;
       const int64_t at = t0 * a.in_ts + col0;
 #pragma unroll
       for (int k = 0; k < W::XV; ++k) {
-        // BF: vectors 2 k and 2 k + 1 are two tokens of block pb + 8 k; else the token is 256 / PB further on
-        const int dt = BF ? (k & 1) : k * (256 / PB), dp = BF ? 8 * (k >> 1) : 0;
+        const int dt = k * (256 / PB);
         vx[k] = Frag<BF>::zero();
-        if (t + dt < len && 8 * (pb + dp) < rows_in) vx[k] = frag_from<BF>(a.in, at + dt * a.in_ts + 8 * dp, off, a.in_dt);
+        if (t + dt < len && 8 * pb < rows_in) vx[k] = frag_from<BF>(a.in, at + dt * a.in_ts, off, a.in_dt);
       }
-    }
-    if constexpr (OUT) {
-      const char* pg = reinterpret_cast<const char*>(a.gm + cg * Q * Q);
-#pragma unroll
-      for (int k = 0; k < PER; ++k)
-        gm[k] = *reinterpret_cast<const f32x4*>(pg + (16 * rts[k] * Q + 16 * cts[k]) * 4 + (uint32_t)(((lane >> 2) * Q + (lane & 3) * 4) * 4));
     }
     if (wave < HB) {  // a wave a head, a token a lane
       const char* gt = reinterpret_cast<const char*>(a.gates + (cs * a.H + g * hpg + min(hb * HB + wave, hpg - 1)) * 3 * Q);
@@ -310,6 +311,12 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
       vg[1] = *reinterpret_cast<const float*>(gt + 4 * Q + (uint32_t)(4 * lane));
       vg[2] = *reinterpret_cast<const float*>(gt + 8 * Q + (uint32_t)(4 * lane));
     }
+  };
+  auto fetch_products = [&](int c) {
+    const char* pg = reinterpret_cast<const char*>(a.gm + ((slot0 + c) * a.G + g) * Q * Q);
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+      gm[k] = *reinterpret_cast<const f32x4*>(pg + (16 * rts[k] * Q + 16 * cts[k]) * 4 + (uint32_t)(((lane >> 2) * Q + (lane & 3) * 4) * 4));
   };
   auto commit = [&](int len) {
     {
@@ -372,7 +379,10 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
         for (int e = 0; e < 4; ++e) s_p[r * LDT + 16 * c + 4 * (i & 3) + e] = (E)0;
     }
   const int steps = c_hi - c_lo;
-  if (steps > 0) fetch(REV ? c_hi - 1 : c_lo);
+  if (steps > 0) {
+    fetch(REV ? c_hi - 1 : c_lo);
+    if constexpr (OUT) fetch_products(REV ? c_hi - 1 : c_lo);
+  }
   const float* const gh_ = s_g + hl * 5 * Q;
 
   for (int step = 0; step < steps; ++step) {
@@ -388,25 +398,40 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
     commit(len);
     __syncthreads();
 
+    // Memory operations are waited for in order: the inputs once more (for D x) first, then the next chunk's operands,
+    // which have the whole chunk to arrive, then, once this chunk's are used, the next products, and last the stores.
+    const int c_next = min(max(REV ? c - 1 : c + 1, c_lo), c_hi - 1);
     f32x4 acc[PT][4];
+    InVec<BF ? GDN_BF16 : GDN_F32, 4> vin[PT][4];
     if constexpr (OUT) {
-      // the inputs once more, for D x, before anything that would hold these loads up
-      InVec<BF ? GDN_BF16 : GDN_F32, 4> vin[PT][4];
+      if constexpr (BF) {
+        const auto w = window16(a.in, t0 * a.in_ts + (int64_t)h * D + pd, 2 * ((len - 1) * a.in_ts + 16 * PT));
+        const int off = 2 * (l16 * (int)a.in_ts + 4 * q);
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
+        for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-        for (int pt = 0; pt < PT; ++pt) {
-          const int64_t at = (t0 + 16 * rt) * a.in_ts + (int64_t)h * D + pd + 16 * pt;
-          const uint32_t off = l16 * (uint32_t)a.in_ts + 4 * q;
-          if constexpr (BF) {
-            if (16 * rt + l16 < len) vin[pt][rt].load(at_bytes(a.in, at, off, 2), 0);
-          } else {
+          for (int pt = 0; pt < PT; ++pt) {
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(w, off + 2 * (16 * rt * (int)a.in_ts + 16 * pt), 0, 0);
+            vin[pt][rt].w[0] = v[0];
+            vin[pt][rt].w[1] = v[1];
+          }
+      } else {
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) {
+            const int64_t at = (t0 + 16 * rt) * a.in_ts + (int64_t)h * D + pd + 16 * pt;
             float f[4] = {0.f, 0.f, 0.f, 0.f};
-            if (16 * rt + l16 < len) load_vec<4>(at_bytes(a.in, at, off, a.in_dt == GDN_F32 ? 4 : 2), 0, a.in_dt, f);
+            if (16 * rt + l16 < len) load_vec<4>(at_bytes(a.in, at, l16 * (uint32_t)a.in_ts + 4 * q, a.in_dt == GDN_F32 ? 4 : 2), 0, a.in_dt, f);
 #pragma unroll
             for (int r = 0; r < 4; ++r) vin[pt][rt].w[r] = __float_as_uint(f[r]);
           }
-        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(c_next);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (OUT) {
       // the state's part of the output
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt)
@@ -462,6 +487,9 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
         for (int pt = 0; pt < PT; ++pt) acc[pt][rt] *= f;
       }
 
+      __builtin_amdgcn_sched_barrier(0);
+      fetch_products(c_next);
+      __builtin_amdgcn_sched_barrier(0);
       __syncthreads();  // the products are there
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
@@ -476,7 +504,23 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
           for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[pt], pf);
         }
       }
-      if (mine) {
+      if constexpr (BF) {
+        const auto w = window16(a.out, (t0 * a.H + h) * D + pd, mine ? 2 * ((len - 1) * (a.H * D) + 16 * PT) : 0);
+        const int off = 2 * (l16 * (a.H * D) + 4 * q);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const float sc = REV ? gh_[2 * Q + 16 * rt + l16] : 1.f;
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) {
+            float v[4];
+            vin[pt][rt].widen(v);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = acc[pt][rt][r] * sc + Dh * v[r];
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2<GDN_BF16>(v[0], v[1]), pack2<GDN_BF16>(v[2], v[3])}, w,
+                                                  off + 2 * (16 * rt * (a.H * D) + 16 * pt), 0, 0);
+          }
+        }
+      } else if (mine) {
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
           const int t = 16 * rt + l16;
@@ -484,13 +528,12 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
             const float sc = REV ? gh_[2 * Q + t] : 1.f;
 #pragma unroll
             for (int pt = 0; pt < PT; ++pt) {
-              const int64_t off = (int64_t)h * D + pd + 16 * pt;
               float v[4];
               vin[pt][rt].widen(v);
 #pragma unroll
               for (int r = 0; r < 4; ++r) v[r] = acc[pt][rt][r] * sc + Dh * v[r];
-              store_vec<4>(const_cast<char*>(at_bytes(a.out, (t0 + 16 * rt) * a.H * D + off, l16 * (uint32_t)(a.H * D) + 4 * q, BF || a.out_dt != GDN_F32 ? 2 : 4)), 0, v,
-                           BF ? GDN_BF16 : a.out_dt, true);
+              store_vec<4>(const_cast<char*>(at_bytes(a.out, (t0 + 16 * rt) * a.H * D + (int64_t)h * D + pd + 16 * pt,
+                                                      l16 * (uint32_t)(a.H * D) + 4 * q, a.out_dt != GDN_F32 ? 2 : 4)), 0, v, a.out_dt, true);
             }
           }
         }
@@ -508,11 +551,6 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
           *reinterpret_cast<f32x4*>(const_cast<char*>(at_bytes(o, at, l16 * (OUT ? NN : D) + 4 * q, 4))) = S[nt][pt];
         }
     }
-    // the next chunk's loads come after this one's stores: memory operations are waited for in order
-    __builtin_amdgcn_sched_barrier(0);
-    if (step + 1 < steps) fetch(REV ? c - 1 : c + 1);
-    __builtin_amdgcn_sched_barrier(0);
-
     // the state after the chunk
     const float end_h = gh_[Q - 1], end_l = gh_[2 * Q - 1], dec = exp2f(end_h + end_l);
     total_g += (double)end_h + (double)end_l;
@@ -596,15 +634,12 @@ int64_t scan_slots(int64_t N, int64_t total, int64_t P) { return N + (total + P 
 
 namespace {
 
-// Heads of a walk's workgroup.
-int walk_heads(int d) { return (d == 16 ? 64 : 128) / d; }
-
-template <bool BF, int D, int NN, bool REV, bool OUT>
+template <bool BF, int D, int NN, int PT, bool REV, bool OUT>
 hipError_t walk(const M2ScanArgs& a, hipStream_t s) {
-  using W = WalkGeom<BF, D, NN, OUT>;
+  using W = WalkGeom<BF, D, NN, PT, OUT>;
   const int hpg = a.H / a.G, hbs = (hpg + W::HB - 1) / W::HB;
   const int64_t slots = a.seg_chunks > 0 ? scan_slots(a.N, a.total, (int64_t)a.seg_chunks * kScanChunk) : a.N;
-  auto* k = gdn_m2s_walk_kernel<BF, D, NN, REV, OUT>;
+  auto* k = gdn_m2s_walk_kernel<BF, D, NN, PT, REV, OUT>;
   if (W::LDS > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)W::LDS);
     if (e != hipSuccess) return e;
@@ -613,17 +648,23 @@ hipError_t walk(const M2ScanArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool BF, int D, int NN>
+template <bool BF, int D, int NN, int PT>
 hipError_t walk_kind(const M2ScanArgs& a, bool rev, bool out, hipStream_t s) {
-  if (rev) return out ? walk<BF, D, NN, true, true>(a, s) : walk<BF, D, NN, true, false>(a, s);
-  return out ? walk<BF, D, NN, false, true>(a, s) : walk<BF, D, NN, false, false>(a, s);
+  if (rev) return out ? walk<BF, D, NN, PT, true, true>(a, s) : walk<BF, D, NN, PT, true, false>(a, s);
+  return out ? walk<BF, D, NN, PT, false, true>(a, s) : walk<BF, D, NN, PT, false, false>(a, s);
+}
+
+template <bool BF, int D, int NN>
+hipError_t walk_pt(const M2ScanArgs& a, bool rev, bool out, hipStream_t s) {
+  if constexpr (D == 64) return a.narrow ? walk_kind<BF, D, NN, 1>(a, rev, out, s) : walk_kind<BF, D, NN, 2>(a, rev, out, s);
+  else return walk_kind<BF, D, NN, D == 16 ? 1 : 2>(a, rev, out, s);
 }
 
 template <bool BF, int D>
 hipError_t walk_n(const M2ScanArgs& a, int n, bool rev, bool out, hipStream_t s) {
-  if (n == 16) return walk_kind<BF, D, 16>(a, rev, out, s);
-  if (n == 64) return walk_kind<BF, D, 64>(a, rev, out, s);
-  return walk_kind<BF, D, 128>(a, rev, out, s);
+  if (n == 16) return walk_pt<BF, D, 16>(a, rev, out, s);
+  if (n == 64) return walk_pt<BF, D, 64>(a, rev, out, s);
+  return walk_pt<BF, D, 128>(a, rev, out, s);
 }
 
 template <bool BF>
@@ -644,17 +685,21 @@ hipError_t prep(const M2ScanArgs& a, int n, hipStream_t s) {
 
 }  // namespace
 
-// Chunks a segment (even, so that blocks of two chunks do not straddle), 0 for whole sequences.
-int scan_seg_chunks(int64_t N, int64_t total, int H, int G, int d) {
+ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d) {
+  const int hpg = H / G;
+  const int64_t chunks = (total + kScanChunk - 1) / kScanChunk;
+  ScanPlan p{0, 0};
 #ifdef GDN_SEG_FORCE
-  if (GDN_SEG_FORCE >= 0) return GDN_SEG_FORCE;
+  p.seg_chunks = GDN_SEG_FORCE % 1000;
+  p.narrow = GDN_SEG_FORCE / 1000;
+  return p;
 #endif
-  const int hpg = H / G, hb = walk_heads(d);
-  const int64_t walks = (int64_t)G * ((hpg + hb - 1) / hb), chunks = (total + kScanChunk - 1) / kScanChunk;
-  if (N * walks >= 512 || chunks <= 16) return 0;
-  int64_t per = chunks * walks / GDN_SEG_WALKS;
+  const int64_t walks = (int64_t)G * ((hpg * d + 127) / 128);
+  if (N * walks >= 512 || chunks <= 16) return p;
+  int64_t per = chunks * walks / 1024;
   per = per < 8 ? 8 : (per + 1) / 2 * 2;
-  return per >= chunks ? 0 : (int)per;
+  p.seg_chunks = per >= chunks ? 0 : (int)per;
+  return p;
 }
 
 hipError_t launch_scan_prep(const M2ScanArgs& a, bool bf, int n, hipStream_t s) {

@@ -373,7 +373,7 @@ gdn_status gdn_mamba2_replay_rollback(const gdn_m2_dims* dims, int32_t B, const 
                                       void* stream);
 
 /* Distances between tokens in elements, for inputs that are slices of wider
- * rows; 0 stands for dense.  x, Bm and Cm: multiples of 8. */
+ * rows; 0 stands for dense.  x, Bm and Cm: multiples of 8; at most 2^22. */
 typedef struct {
   int64_t x;  /* >= H d */
   int64_t Bm; /* >= G n */

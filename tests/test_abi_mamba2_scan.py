@@ -60,6 +60,8 @@ BAD = [
     (dict(st=bd.gdn_m2_strides(8 * 64 + 4, 0, 0, 0)), gdn.GDN_EINVAL),
     (dict(st=bd.gdn_m2_strides(0, 0, 2 * 128 - 8, 0)), gdn.GDN_EINVAL),
     (dict(st=bd.gdn_m2_strides(0, 0, 0, 7)), gdn.GDN_EINVAL),
+    (dict(st=bd.gdn_m2_strides((1 << 22) + 8, 0, 0, 0)), gdn.GDN_EUNSUPPORTED),   # past 32-bit offsets in a block
+    (dict(dims=dict(H=40000, G=1, d=128)), gdn.GDN_EUNSUPPORTED),
     (dict(st=bd.gdn_m2_strides(0, -256, 0, 0)), gdn.GDN_EINVAL),
     (dict(pool=None), gdn.GDN_EINVAL),                            # slots and no pool
     (dict(sm=None), gdn.GDN_EINVAL),

@@ -128,49 +128,68 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
   const int nt = wave % NT, n16 = 16 * nt;
   const bool do_c = BOTH || wave < NT, do_b = BOTH || (wave >= NT && wave < 2 * NT);
 
-  // the next head's tokens and states before it travel in registers while this head is under way, the gradients of the
-  // states after it while dC's part is
+  // the next head's operands travel in registers while this head's are used
   Frag<BF> vx[W::XV], vy[W::XV];
-  f32x4 vs[2 * DB], vr[2 * DB];
-  float vg[8];
+  f32x4 vs[2 * DB];
+  float vr[8 * DB];
+  float vg[3], tot[5];  // a token's c (two) and dt'; the chunks' totals (two each) and A_log
   auto fetch_tokens = [&](int h) {
+    constexpr int VPR = W::DK / 8;
+    if constexpr (BF) {
+      const auto wx = window(a.x, t0 * a.x_ts + (int64_t)h * D, 2, 2 * ((len - 1) * a.x_ts + D));
+      const auto wy = window(a.dy, (t0 * a.H + h) * D, 2, 2 * ((len - 1) * (int64_t)(a.H * D) + D));
+      const int t = tid / VPR, p0 = tid % VPR * 8;
+      // (of d = 16, the vectors past the row's end lie outside the window's rows)
 #pragma unroll
-    for (int k = 0; k < W::XV; ++k) {
-      const int i = tid + 512 * k, t = i / (W::DK / 8), p0 = (i - t * (W::DK / 8)) * 8;
-      vx[k] = vy[k] = Frag<BF>::zero();
-      if (t < len && p0 < D) {
-        vx[k] = frag_from<BF>(a.x, t0 * a.x_ts + (int64_t)h * D, t * (uint32_t)a.x_ts + p0, a.dt_in);
-        vy[k] = frag_from<BF>(a.dy, (t0 * a.H + h) * D, t * (uint32_t)(a.H * D) + p0, a.dt_in);
+      for (int k = 0; k < W::XV; ++k) {
+        const int tk = t + k * (512 / VPR);
+        vx[k] = vy[k] = Frag<BF>::zero();
+        if (D >= 32 || p0 < D) {
+          vx[k].v = __builtin_amdgcn_raw_buffer_load_b128(wx, 2 * (tk * (int)a.x_ts + p0), 0, 0);
+          vy[k].v = __builtin_amdgcn_raw_buffer_load_b128(wy, 2 * (tk * a.H * D + p0), 0, 0);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < W::XV; ++k) {
+        const int i = tid + 512 * k, t = i / VPR, p0 = (i - t * VPR) * 8;
+        vx[k] = vy[k] = Frag<BF>::zero();
+        if (t < len && p0 < D) {
+          vx[k] = frag_from<BF>(a.x, t0 * a.x_ts + (int64_t)h * D, t * (uint32_t)a.x_ts + p0, a.dt_in);
+          vy[k] = frag_from<BF>(a.dy, (t0 * a.H + h) * D, t * (uint32_t)(a.H * D) + p0, a.dt_in);
+        }
       }
     }
-    if (tid < T) {
+  };
+  auto fetch_gates = [&](int h) {
+    if (wave < 2) {  // the first wave has the first chunk's tokens, the second the second's, where there is one
       const float* g0 = a.gates + (slot64 * a.H + h) * 3 * Q;
-      const float* g1 = g0 + (len > Q ? (int64_t)a.H * 3 * Q : 0);  // a block's second chunk, where there is one
-      const float* gt = tid < Q ? g0 : g1;
-      vg[0] = gt[tid % Q];
-      vg[1] = gt[Q + tid % Q];
-      vg[2] = gt[2 * Q + tid % Q];
-      vg[3] = g0[Q - 1];
-      vg[4] = g0[2 * Q - 1];
-      vg[5] = g1[Q - 1];
-      vg[6] = g1[2 * Q - 1];
-      vg[7] = a.A_log[h];
+      const float* g1 = g0 + (len > Q ? (int64_t)a.H * 3 * Q : 0);
+      const auto w = window(wave == 0 ? g0 : g1, 0, 4, 12 * Q);
+      vg[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(w, 4 * lane, 0, 0));
+      vg[1] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(w, 4 * lane + 4 * Q, 0, 0));
+      vg[2] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(w, 4 * lane + 8 * Q, 0, 0));
+      tot[0] = scalar_read(g0 + Q - 1);
+      tot[1] = scalar_read(g0 + 2 * Q - 1);
+      tot[2] = scalar_read(g1 + Q - 1);
+      tot[3] = scalar_read(g1 + 2 * Q - 1);
+      tot[4] = scalar_read(a.A_log + h);
     }
   };
   auto commit_tokens = [&](float* res) {
 #pragma unroll
     for (int k = 0; k < W::XV; ++k) {
-      const int i = tid + 512 * k, t = i / (W::DK / 8), p0 = (i - t * (W::DK / 8)) * 8;
-      *reinterpret_cast<Frag<BF>*>(s_x + t * LDX + p0) = vx[k];
-      *reinterpret_cast<Frag<BF>*>(s_y + t * LDX + p0) = vy[k];
+      const int at = (tid / (W::DK / 8) + k * (512 / (W::DK / 8))) * LDX + tid % (W::DK / 8) * 8;
+      *reinterpret_cast<Frag<BF>*>(s_x + at) = vx[k];
+      *reinterpret_cast<Frag<BF>*>(s_y + at) = vy[k];
     }
-    if (tid < T) {
+    if (wave < 2) {
       // prefix sums over the block: the second chunk's follow the first's total
-      const double tot0 = (double)vg[3] + (double)vg[4];
-      const double last = len > Q ? tot0 + ((double)vg[5] + (double)vg[6]) : tot0;
+      const double tot0 = (double)tot[0] + (double)tot[1];
+      const double last = len > Q ? tot0 + ((double)tot[2] + (double)tot[3]) : tot0;
       double c = (double)vg[0] + (double)vg[1];
       float dtp = vg[2];
-      if (tid >= Q) {
+      if (wave == 1) {
         c = len > Q ? tot0 + c : tot0;
         dtp = len > Q ? dtp : 0.f;
       }
@@ -183,38 +202,29 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       res[(8 + 4 + 2 * NT) * T + tid] = dtp;
       if (tid == 0) {
         res[W::RES - 1] = exp2f((float)last);
-        res[W::RES - 2] = expf(vg[7]);
+        res[W::RES - 2] = expf(tot[4]);
       }
     }
   };
   // a state's column n of this wave's, 8 rows p at a time: from [n][p], or from [p][n]
-  auto fetch_state = [&](const float* base, int h, f32x4 (&v)[2 * DB], auto by_p) {
-    const int64_t at = ((int64_t)slot * a.H + h) * (D * NN);
+  auto fetch_fwd = [&](int h) {
+    const auto w = window(a.fwd, ((int64_t)slot * a.H + h) * (D * NN), 4, 4 * D * NN);
 #pragma unroll
-    for (int k = 0; k < DB; ++k)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        v[2 * k + e] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (D < 32 && 8 * q >= D) continue;
-        if constexpr (decltype(by_p)::value) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            v[2 * k + e][r] = *reinterpret_cast<const float*>(at_bytes(base, at + (32 * k + 4 * e + r) * NN + n16, 8 * q * NN + l16, 4));
-        } else {
-          v[2 * k + e] = *reinterpret_cast<const f32x4*>(at_bytes(base, at + n16 * D + 32 * k + 4 * e, l16 * D + 8 * q, 4));
-        }
-      }
-  };
-  auto split_state = [&](const f32x4 (&v)[2 * DB], Split<BF> (&o)[DB]) {
-#pragma unroll
-    for (int k = 0; k < DB; ++k) {
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = v[2 * k + (e >> 2)][e & 3];
-      o[k] = Split<BF>::of(f);
+    for (int k = 0; k < 2 * DB; ++k) {
+      vs[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (D >= 32 || 8 * q < D)
+        vs[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(w, 4 * (l16 * D + 8 * q) + 4 * (32 * (k >> 1) + 4 * (k & 1)), 4 * n16 * D, 0));
     }
   };
-
+  auto fetch_rev = [&](int h) {
+    const auto w = window(a.rev, ((int64_t)slot * a.H + h) * (D * NN), 4, 4 * D * NN);
+#pragma unroll
+    for (int k = 0; k < 8 * DB; ++k) {
+      vr[k] = 0.f;
+      if (D >= 32 || 8 * q < D)
+        vr[k] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(w, 4 * (8 * q * NN + l16) + 4 * (32 * (k >> 3) + (k & 7)) * NN, 4 * n16, 0));
+    }
+  };
   // four 16-token tiles of x or dy times a split state, their terms apart: a product never follows the one it adds to
   auto products = [&](const E* rows, int i0, const Split<BF> (&st)[DB], f32x4 (&v)[4]) {
 #pragma unroll
@@ -231,18 +241,45 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     }
   };
 
-  // G for the wave's 16 rows: C_i . B_j
+  // G for the wave's 16 rows: C_i . B_j.  bf16: both rows through LDS, over the places of x and dy and of the summed
+  // products; FP32: straight from memory
   f32x4 G[W::G_LDS ? 1 : 8], Ns[W::N_LDS ? 1 : 8];
-  {
+  constexpr int KB = (NN + 31) / 32, LDC = KB * 32 + 8;
+  if constexpr (BF) {
+    E* const s_c = s_x;
+    E* const s_b = reinterpret_cast<E*>(s_ns);
+    static_assert(T * LDC <= W::ELEMS && 2 * T * LDC <= W::TILES, "the rows of C and of B fit");
+    const auto wc = window(a.Cm, t0 * a.c_ts + g * NN, 2, 2 * ((len - 1) * a.c_ts + NN));
+    const auto wb = window(a.Bm, t0 * a.b_ts + g * NN, 2, 2 * ((len - 1) * a.b_ts + NN));
+    for (int i = tid; i < T * KB * 4; i += 512) {
+      const int t = i / (KB * 4), n0 = i % (KB * 4) * 8;
+      Frag<BF> c = Frag<BF>::zero(), b = c;
+      if (NN >= 32 || n0 < NN) {
+        c.v = __builtin_amdgcn_raw_buffer_load_b128(wc, 2 * (t * (int)a.c_ts + n0), 0, 0);
+        b.v = __builtin_amdgcn_raw_buffer_load_b128(wb, 2 * (t * (int)a.b_ts + n0), 0, 0);
+      }
+      *reinterpret_cast<Frag<BF>*>(s_c + t * LDC + n0) = c;
+      *reinterpret_cast<Frag<BF>*>(s_b + t * LDC + n0) = b;
+    }
+    __syncthreads();
+    for (int jt = 0; jt <= wave; ++jt) {
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        acc = frag_mma(acc, Frag<BF>::load(s_c + (16 * wave + l16) * LDC + 32 * kb + 8 * q), Frag<BF>::load(s_b + (16 * jt + l16) * LDC + 32 * kb + 8 * q));
+      s_gt[tile0 + jt * 64] = acc;
+    }
+    __syncthreads();
+    for (int jt = 0; jt <= wave; ++jt) s_ns[tile0 + jt * 64] = f32x4{0.f, 0.f, 0.f, 0.f};
+  } else {
     const int i = 16 * wave + l16;
 #pragma unroll
     for (int jt = 0; jt < 8; ++jt) {
-      if constexpr (!W::N_LDS) Ns[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      Ns[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (jt > wave) continue;
-      if constexpr (W::N_LDS) s_ns[tile0 + jt * 64] = f32x4{0.f, 0.f, 0.f, 0.f};
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int kb = 0; kb < (NN + 31) / 32; ++kb) {
+      for (int kb = 0; kb < KB; ++kb) {
         const int n0 = 32 * kb + 8 * q, j = 16 * jt + l16;
         Frag<BF> cf = Frag<BF>::zero(), bf = cf;
         if (i < len && n0 < NN) cf = frag_from<BF>(a.Cm, t0 * a.c_ts + g * NN, i * (uint32_t)a.c_ts + n0, a.dt_in);
@@ -262,10 +299,8 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     if constexpr (BF)
 #pragma unroll
       for (int it = 0; it < 8; ++it) {
-        c.w[it] = u32x2{0u, 0u};
-        if (16 * it < len)
-          c.w[it] = *reinterpret_cast<const u32x2*>(
-              at_bytes(transposed, (((slot64 + (it >> 2)) * a.G + g) * NN + n16) * Q + 16 * (it & 3), l16 * Q + 4 * q, 2));
+        const auto w = window(transposed, (((slot64 + (it >> 2)) * a.G + g) * NN + n16) * Q, 2, it < 4 || len > Q ? 2 * 16 * Q : 0);
+        c.w[it] = __builtin_amdgcn_raw_buffer_load_b64(w, 2 * (l16 * Q + 4 * q) + 32 * (it & 3), 0, 0);
       }
   };
   auto column_of = [&](const void* m, int64_t ts, const Columns& c, int it, float (&v)[4]) {
@@ -384,7 +419,9 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
   for (int it = 0; it < 8; ++it) dC[it] = dB[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   fetch_tokens(g * hpg + h_lo);
-  fetch_state(a.fwd, g * hpg + h_lo, vs, std::false_type{});
+  fetch_gates(g * hpg + h_lo);
+  fetch_fwd(g * hpg + h_lo);
+  fetch_rev(g * hpg + h_lo);
   for (int hi = h_lo; hi < h_hi; ++hi) {
     const int h = g * hpg + hi, h_next = min(h + 1, g * hpg + h_hi - 1);
     // the lane's places are not known to be the ones of the head before: what follows from them is formed anew, in a few
@@ -398,15 +435,20 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
     Columns cc, bb;
-    if (do_c) load_columns(a.ct, cc);  // first: loads are waited for in order
-    fetch_state(a.rev, h, vr, std::true_type{});
+    if (do_c) load_columns(a.ct, cc);
     __builtin_amdgcn_sched_barrier(0);
 
     // state parts of dC and dB for the wave's 16 columns; row l16 / 4 of four tiles, token 4 q + l16 % 4 of it
     const int own = 16 * (l16 >> 2) + 4 * q + (l16 & 3);
     if (do_c) {
       Split<BF> sc[DB];
-      split_state(vs, sc);
+#pragma unroll
+      for (int k = 0; k < DB; ++k) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = vs[2 * k + (e >> 2)][e & 3];
+        sc[k] = Split<BF>::of(f);
+      }
 #pragma unroll
       for (int i0 = 0; i0 < 8; i0 += 4) {
         if (i0 >= tiles) continue;
@@ -428,15 +470,23 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     if (do_c) {
       float qs = 0.f;
 #pragma unroll
-      for (int k = 0; k < 2 * DB; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) qs += vs[k][e] * vr[k][e];
+      for (int k = 0; k < 8 * DB; ++k) qs += vs[k >> 2][k & 3] * vr[k];
       qs = wave_sum(qs);
       if (lane == 0) r_q[wave] = qs;
     }
-    if (do_b) load_columns(a.bt, bb);
+    if (do_b) load_columns(a.bt, bb);  // before the next head's loads: these are waited for in order
     Split<BF> sb[DB];
-    split_state(vr, sb);
+#pragma unroll
+    for (int k = 0; k < DB; ++k) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = vr[8 * k + e];
+      sb[k] = Split<BF>::of(f);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    fetch_fwd(h_next);
+    fetch_rev(h_next);
+    fetch_tokens(h_next);
     __builtin_amdgcn_sched_barrier(0);
     if (do_b) {
 #pragma unroll
@@ -457,9 +507,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    fetch_state(a.fwd, h_next, vs, std::false_type{});
-    fetch_tokens(h_next);
-    __builtin_amdgcn_sched_barrier(0);
+    fetch_gates(h_next);
 
     // products of dy and x for the wave's 16 rows; off the diagonal tile the decay is that down to the rows' first
     // token times that from there

@@ -70,8 +70,13 @@ __device__ __forceinline__ const char* at_bytes(const void* base, int64_t unifor
 // the number of memory operations in flight is known to the compiler.  All of
 // an access's offset goes into its lane offset, which is what is compared with
 // the window's size.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t window16(const void* base, int64_t elem, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(base)) + 2 * elem, 0, (int)bytes, 0x00027000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void* base, int64_t elem, int eb, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(base)) + eb * elem, 0, (int)bytes, 0x00027000);
+}
+
+// A uniform read through the scalar cache, of what no kernel writes meanwhile.
+__device__ __forceinline__ float scalar_read(const float* p) {
+  return *reinterpret_cast<const float __attribute__((address_space(4)))*>(reinterpret_cast<uintptr_t>(p));
 }
 
 // ------------------------------------------------------------------ fragments

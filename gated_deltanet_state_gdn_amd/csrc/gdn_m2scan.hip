@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
       if (NN * 8 % 256 == 0 || tid + 256 * k < NN * 8)
         vk[k] = Frag<BF>::load(reinterpret_cast<const E*>(pk + k * 256 * 8 * sizeof(E) + (uint32_t)(tid * 8 * sizeof(E))));
     if constexpr (OUT && BF) {
-      const auto w = window16(a.read, t0 * a.read_ts + g * NN, 2 * ((len - 1) * a.read_ts + NN));
+      const auto w = window(a.read, t0 * a.read_ts + g * NN, 2, 2 * ((len - 1) * a.read_ts + NN));
       const int off = 2 * (tid / VPR * (int)a.read_ts + tid % VPR * 8);
 #pragma unroll
       for (int k = 0; k < W::FV; ++k) vf[k].v = __builtin_amdgcn_raw_buffer_load_b128(w, off + 2 * k * FSTEP * (int)a.read_ts, 0, 0);
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
     }
     if constexpr (BF) {
       // rows past the group's heads read what lies there, or zero: no output depends on them
-      const auto w = window16(a.in, t0 * a.in_ts + col0, 2 * ((len - 1) * a.in_ts + rows_in));
+      const auto w = window(a.in, t0 * a.in_ts + col0, 2, 2 * ((len - 1) * a.in_ts + rows_in));
       const int off = 2 * (2 * (tid >> 3 & 31) * (int)a.in_ts + 8 * (tid & 7));
 #pragma unroll
       for (int k = 0; k < W::XV; ++k)  // 2 k and 2 k + 1 are two tokens of the same block of columns
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
     InVec<BF ? GDN_BF16 : GDN_F32, 4> vin[PT][4];
     if constexpr (OUT) {
       if constexpr (BF) {
-        const auto w = window16(a.in, t0 * a.in_ts + (int64_t)h * D + pd, 2 * ((len - 1) * a.in_ts + 16 * PT));
+        const auto w = window(a.in, t0 * a.in_ts + (int64_t)h * D + pd, 2, 2 * ((len - 1) * a.in_ts + 16 * PT));
         const int off = 2 * (l16 * (int)a.in_ts + 4 * q);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
         }
       }
       if constexpr (BF) {
-        const auto w = window16(a.out, (t0 * a.H + h) * D + pd, mine ? 2 * ((len - 1) * (a.H * D) + 16 * PT) : 0);
+        const auto w = window(a.out, (t0 * a.H + h) * D + pd, 2, mine ? 2 * ((len - 1) * (a.H * D) + 16 * PT) : 0);
         const int off = 2 * (l16 * (a.H * D) + 4 * q);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {

@@ -46,13 +46,15 @@ struct GradGeom {
   static constexpr bool N_LDS = BF;               // the heads' summed products too
   static constexpr bool LATE = BF && D < 128;     // a head's sums are closed while the next head is under way
   static constexpr int XV = T * DK / 8 / 512;     // vectors of 8 elements of x (and of dy) that a thread stages
-  // a head's results: column sums [8][128], row sums, the diagonal tiles' row and column sums, the diagonal, the state
-  // parts [NT][128] twice, dt', the waves' parts of <S, dS'> and of sum dy.x, exp(A_log), e^{c_last}
-  static constexpr int RES = (8 + 4 + 2 * NT + 1) * T + 24;
-  static constexpr int GATES = 5 * T;             // c / 2 (two), e^{c_i}, dt' e^{c_last - c_j}, dt'
+  // a head's results: column sums [8][128], row sums in two parts, the diagonal tiles' row and column sums, the diagonal, the state
+  // parts [NT][128] twice, the waves' parts of <S, dS'> and of sum dy.x
+  static constexpr int RES = (8 + 5 + 2 * NT) * T + 16;
+  // a head's gates: c / 2 (two), e^{c_i}, dt' e^{c_last - c_j}, dt', exp(A_log), e^{c_last}; of the head under way, the one
+  // before it, which is being closed, and the next
+  static constexpr int GATES = 5 * T + 4, RING = LATE ? 3 : 1;
   static constexpr int TILES = 36 * 64 * 16;      // bytes of the tiles on and below the diagonal
   static_assert(!BF || 2 * T * LDN * 2 <= ELEMS * 2 + TILES, "both terms of the summed products fit over x, dy and C.B");
-  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + (G_LDS ? TILES : 0) + (N_LDS ? TILES : 0) + (GATES + (LATE ? 2 : 1) * RES) * 4;
+  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + (G_LDS ? TILES : 0) + (N_LDS ? TILES : 0) + (RING * GATES + (LATE ? 2 : 1) * RES) * 4;
 };
 
 // Sums over a 16-lane row's lanes at or after, and at or before, each lane.
@@ -90,12 +92,8 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
   int tile0 = wave * (wave + 1) / 2 * 64 + lane;  // tile (i, j <= i) is the i (i + 1) / 2 + j-th, a lane's four values together
   f32x4* const s_gt = reinterpret_cast<f32x4*>(smem + (size_t)W::ELEMS * sizeof(E));
   f32x4* const s_ns = s_gt + (W::G_LDS ? 36 * 64 : 0);
-  float* const s_ch = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E) + (W::G_LDS ? W::TILES : 0) + (W::N_LDS ? W::TILES : 0));
-  float* const s_cl = s_ch + T;
-  float* const s_er = s_cl + T;      // e^{c_i}
-  float* const s_wd = s_er + T;      // dt'_j e^{c_last - c_j}
-  float* const s_dt = s_wd + T;
-  float* const s_res = s_dt + T;
+  float* const s_gates = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E) + (W::G_LDS ? W::TILES : 0) + (W::N_LDS ? W::TILES : 0));
+  float* const s_res = s_gates + W::RING * W::GATES;
 
   const int hpg = a.H / a.G;
   const int slot = blockIdx.x / (a.G * a.splits), rest = blockIdx.x - slot * (a.G * a.splits), g = rest / a.splits, split = rest - g * a.splits;
@@ -176,13 +174,15 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       tot[4] = scalar_read(a.A_log + h);
     }
   };
-  auto commit_tokens = [&](float* res) {
+  auto commit_tokens = [&]() {
 #pragma unroll
     for (int k = 0; k < W::XV; ++k) {
       const int at = (tid / (W::DK / 8) + k * (512 / (W::DK / 8))) * LDX + tid % (W::DK / 8) * 8;
       *reinterpret_cast<Frag<BF>*>(s_x + at) = vx[k];
       *reinterpret_cast<Frag<BF>*>(s_y + at) = vy[k];
     }
+  };
+  auto store_gates = [&](float* out) {
     if (wave < 2) {
       // prefix sums over the block: the second chunk's follow the first's total
       const double tot0 = (double)tot[0] + (double)tot[1];
@@ -194,15 +194,14 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
         dtp = len > Q ? dtp : 0.f;
       }
       const float ch = (float)c;
-      s_ch[tid] = 0.5f * ch;
-      s_cl[tid] = 0.5f * (float)(c - (double)ch);
-      s_er[tid] = exp2f((float)c);
-      s_wd[tid] = dtp * exp2f((float)(last - c));
-      s_dt[tid] = dtp;
-      res[(8 + 4 + 2 * NT) * T + tid] = dtp;
+      out[tid] = 0.5f * ch;
+      out[T + tid] = 0.5f * (float)(c - (double)ch);
+      out[2 * T + tid] = exp2f((float)c);
+      out[3 * T + tid] = dtp * exp2f((float)(last - c));
+      out[4 * T + tid] = dtp;
       if (tid == 0) {
-        res[W::RES - 1] = exp2f((float)last);
-        res[W::RES - 2] = expf(tot[4]);
+        out[5 * T] = expf(tot[4]);
+        out[5 * T + 1] = exp2f((float)last);
       }
     }
   };
@@ -251,15 +250,25 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     static_assert(T * LDC <= W::ELEMS && 2 * T * LDC <= W::TILES, "the rows of C and of B fit");
     const auto wc = window(a.Cm, t0 * a.c_ts + g * NN, 2, 2 * ((len - 1) * a.c_ts + NN));
     const auto wb = window(a.Bm, t0 * a.b_ts + g * NN, 2, 2 * ((len - 1) * a.b_ts + NN));
-    for (int i = tid; i < T * KB * 4; i += 512) {
-      const int t = i / (KB * 4), n0 = i % (KB * 4) * 8;
-      Frag<BF> c = Frag<BF>::zero(), b = c;
+    Frag<BF> c[KB], b[KB];
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int t = (tid + 512 * k) / (KB * 4), n0 = (tid + 512 * k) % (KB * 4) * 8;
+      c[k] = b[k] = Frag<BF>::zero();
       if (NN >= 32 || n0 < NN) {
-        c.v = __builtin_amdgcn_raw_buffer_load_b128(wc, 2 * (t * (int)a.c_ts + n0), 0, 0);
-        b.v = __builtin_amdgcn_raw_buffer_load_b128(wb, 2 * (t * (int)a.b_ts + n0), 0, 0);
+        c[k].v = __builtin_amdgcn_raw_buffer_load_b128(wc, 2 * (t * (int)a.c_ts + n0), 0, 0);
+        b[k].v = __builtin_amdgcn_raw_buffer_load_b128(wb, 2 * (t * (int)a.b_ts + n0), 0, 0);
       }
-      *reinterpret_cast<Frag<BF>*>(s_c + t * LDC + n0) = c;
-      *reinterpret_cast<Frag<BF>*>(s_b + t * LDC + n0) = b;
+    }
+    fetch_gates(g * hpg + h_lo);
+    fetch_fwd(g * hpg + h_lo);
+    fetch_rev(g * hpg + h_lo);
+    fetch_tokens(g * hpg + h_lo);
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int at = (tid + 512 * k) / (KB * 4) * LDC + (tid + 512 * k) % (KB * 4) * 8;
+      *reinterpret_cast<Frag<BF>*>(s_c + at) = c[k];
+      *reinterpret_cast<Frag<BF>*>(s_b + at) = b[k];
     }
     __syncthreads();
     for (int jt = 0; jt <= wave; ++jt) {
@@ -326,9 +335,9 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
   };
 
   // closes a head: dt's gradient for the block's tokens and the head's parameter sums (one wave)
-  auto close_head = [&](int h, const float* res) {
-    const float *r_col = res, *r_row = res + 8 * T, *r_rd = r_row + T, *r_cd = r_rd + T, *r_dg = r_cd + T, *r_cs = r_dg + T,
-                *r_cv = r_cs + NT * T, *r_dt = r_cv + NT * T, *r_q = r_dt + T, *r_dd = r_q + 8;
+  auto close_head = [&](int h, const float* res, const float* gates) {
+    const float *r_col = res, *r_row = res + 8 * T, *r_rd = r_row + T, *r_cd = r_rd + T, *r_dg = r_cd + T, *r_help = r_dg + T, *r_cs = r_help + T,
+                *r_cv = r_cs + NT * T, *r_q = r_cv + NT * T, *r_dd = r_q + 8;
     // whole tiles with rows after block b and columns before it: 8 lanes a block
     float whole = 0.f;
     {
@@ -353,7 +362,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       const bool in = t < 16 * tiles;
       float cs = 0.f;
       cv[k] = co[k] = 0.f;
-      dtp[k] = r_dt[t];
+      dtp[k] = gates[4 * T + t];
       if (in) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
         for (int i = b + 1; i < tiles; ++i) co[k] += r_col[i * T + t];
       }
       // inside the block: earlier columns of later rows, later rows of earlier columns, and the diagonal tile
-      const float r0 = in ? r_row[t] + (r_rd[t] - r_cd[t]) : 0.f;
+      const float r0 = in ? r_row[t] + (r_rd[t] - r_cd[t]) + (W::N_LDS && b > 4 ? r_help[t] : 0.f) : 0.f;
       pre[k] = row_shift<0x111>(row_prefix(co[k]));  // before t, not at it
       suf[k] = row_suffix(r0);
       cs_suf[k] = row_suffix(cs);
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
         if (q == r) pre[k] += before;
         before += tot;
       }
-    const float A = res[W::RES - 2], eq = qs * res[W::RES - 1];
+    const float A = gates[5 * T], eq = qs * gates[5 * T + 1];
     float sa = 0.f, sb = 0.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -418,20 +427,26 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
 #pragma unroll
   for (int it = 0; it < 8; ++it) dC[it] = dB[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  fetch_tokens(g * hpg + h_lo);
-  fetch_gates(g * hpg + h_lo);
-  fetch_fwd(g * hpg + h_lo);
-  fetch_rev(g * hpg + h_lo);
+  if constexpr (!BF) {
+    fetch_tokens(g * hpg + h_lo);
+    fetch_gates(g * hpg + h_lo);
+    fetch_fwd(g * hpg + h_lo);
+    fetch_rev(g * hpg + h_lo);
+  }
+  float *g_before = nullptr, *g_now = s_gates, *g_next = s_gates + (W::LATE ? W::GATES : 0);
+  if constexpr (W::LATE) store_gates(g_now);
   for (int hi = h_lo; hi < h_hi; ++hi) {
     const int h = g * hpg + hi, h_next = min(h + 1, g * hpg + h_hi - 1);
     // the lane's places are not known to be the ones of the head before: what follows from them is formed anew, in a few
     // instructions, where it would otherwise be kept in registers that the loop has not got
     asm volatile("" : "+v"(tid), "+v"(lane), "+v"(l16), "+v"(q), "+v"(tile0));
     float* const res = s_res + (W::LATE ? (hi & 1) * W::RES : 0);
-    float *r_col = res, *r_row = res + 8 * T, *r_rd = r_row + T, *r_cd = r_rd + T, *r_dg = r_cd + T, *r_cs = r_dg + T,
-          *r_cv = r_cs + NT * T, *r_q = r_cv + NT * T + T, *r_dd = r_q + 8;
+    float *r_col = res, *r_row = res + 8 * T, *r_rd = r_row + T, *r_cd = r_rd + T, *r_dg = r_cd + T, *r_help = r_dg + T, *r_cs = r_help + T,
+          *r_cv = r_cs + NT * T, *r_q = r_cv + NT * T, *r_dd = r_q + 8;
     __syncthreads();  // the head before is done with LDS
-    commit_tokens(res);
+    commit_tokens();
+    if constexpr (!W::LATE) store_gates(g_now);
+    const float *s_ch = g_now, *s_cl = s_ch + T, *s_er = s_cl + T, *s_wd = s_er + T, *s_dt = s_wd + T;
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
     Columns cc, bb;
@@ -485,7 +500,6 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     }
     __builtin_amdgcn_sched_barrier(0);
     fetch_fwd(h_next);
-    fetch_rev(h_next);
     fetch_tokens(h_next);
     __builtin_amdgcn_sched_barrier(0);
     if (do_b) {
@@ -507,103 +521,125 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    fetch_gates(h_next);
+    fetch_rev(h_next);
+    if constexpr (W::LATE) fetch_gates(h_next);
 
-    // products of dy and x for the wave's 16 rows; off the diagonal tile the decay is that down to the rows' first
-    // token times that from there
-    if (wave < tiles) {
+    // products of dy and x, a row of 16 x 16 tiles a wave; off the diagonal tile the decay is that down to the rows'
+    // first token times that from there
+    auto tile_row = [&](int it, int j_lo, int j_hi, bool owner) {
       Frag<BF> yf[DB];
 #pragma unroll
-      for (int k = 0; k < DB; ++k) yf[k] = Frag<BF>::load(s_y + (16 * wave + l16) * LDX + 32 * k + 8 * q);
-      const int i0 = 16 * wave + 4 * q;
+      for (int k = 0; k < DB; ++k) yf[k] = Frag<BF>::load(s_y + (16 * it + l16) * LDX + 32 * k + 8 * q);
+      const int i0 = 16 * it + 4 * q, base = it * (it + 1) / 2 * 64 + lane;
       const f32x4 ih = *reinterpret_cast<const f32x4*>(s_ch + i0), il = *reinterpret_cast<const f32x4*>(s_cl + i0);
-      const float mh = s_ch[16 * wave], ml = s_cl[16 * wave];
+      const float mh = s_ch[16 * it], ml = s_cl[16 * it];
       f32x4 rowo = {0.f, 0.f, 0.f, 0.f}, down;
 #pragma unroll
       for (int r = 0; r < 4; ++r) down[r] = decay_half((ih[r] - mh) + (il[r] - ml));
-      auto tile = [&](int jt, f32x4& ns, const f32x4& gt, auto on_diagonal) {
-        const int j = 16 * jt + l16;
+      auto product = [&](int j) {
         f32x4 w = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < DB; ++k) w = frag_mma(w, yf[k], Frag<BF>::load(s_x + j * LDX + 32 * k + 8 * q));
-        const float jh = s_ch[j], jl = s_cl[j], dtj = s_dt[j];
-        if constexpr (!decltype(on_diagonal)::value) {
-          const float from = dtj * decay_half((mh - jh) + (ml - jl));
-          float col = 0.f;
+        return w;
+      };
+      auto below = [&](int jt, f32x4& ns, const f32x4& gt) {
+        const int j = 16 * jt + l16;
+        const f32x4 w = product(j);
+        const float from = s_dt[j] * decay_half((mh - s_ch[j]) + (ml - s_cl[j]));
+        float col = 0.f;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float e = down[r] * from, m = e * (w[r] * gt[r]);
-            ns[r] += e * w[r];
-            col += m;
-            rowo[r] += m;
-          }
-          col = xor_sum_from<16>(col);
-          if (q == 0) r_col[wave * T + j] = col;
-        } else {
-          f32x4 off;
-          float diag = 0.f, wd = 0.f, cd = 0.f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float e = dtj * decay_half(j <= i0 + r ? (ih[r] - jh) + (il[r] - jl) : -INFINITY), m = e * (w[r] * gt[r]);
-            ns[r] += e * w[r];
-            if (j == i0 + r) {
-              diag = m;
-              wd = w[r];
-            }
-            off[r] = j == i0 + r ? 0.f : m;
-            cd += off[r];
-          }
-          const float rd = row16_sum4(off[0], off[1], off[2], off[3]), ro = row16_sum4(rowo[0], rowo[1], rowo[2], rowo[3]);
-          const float z = rows_sum4(cd, diag, wd, 0.f);  // the rows of 16 lanes get the three sums over the tile's rows
-          if (l16 < 4) {
-            r_rd[i0 + l16] = rd;
-            r_row[i0 + l16] = ro;
-          }
-          if (q < 2) (q == 0 ? r_cd : r_dg)[j] = z;
-          const float dd = row16_sum(z);
-          if (lane == 32) r_dd[wave] = dd;
+        for (int r = 0; r < 4; ++r) {
+          const float e = down[r] * from, m = e * (w[r] * gt[r]);
+          ns[r] += e * w[r];
+          col += m;
+          rowo[r] += m;
         }
+        col = xor_sum_from<16>(col);
+        if (q == 0) r_col[it * T + j] = col;
+      };
+      auto diagonal = [&](f32x4& ns, const f32x4& gt) {
+        const int j = 16 * it + l16;
+        const f32x4 w = product(j);
+        const float jh = s_ch[j], jl = s_cl[j], dtj = s_dt[j];
+        f32x4 off;
+        float diag = 0.f, wd = 0.f, cd = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = dtj * decay_half(j <= i0 + r ? (ih[r] - jh) + (il[r] - jl) : -INFINITY), m = e * (w[r] * gt[r]);
+          ns[r] += e * w[r];
+          diag = j == i0 + r ? m : diag;
+          wd = j == i0 + r ? w[r] : wd;
+          off[r] = j == i0 + r ? 0.f : m;
+          cd += off[r];
+        }
+        const float rd = row16_sum4(off[0], off[1], off[2], off[3]);
+        const float z = rows_sum4(cd, diag, wd, 0.f);  // the rows of 16 lanes get the three sums over the tile's rows
+        if (l16 < 4) r_rd[i0 + l16] = rd;
+        if (q < 2) (q == 0 ? r_cd : r_dg)[j] = z;
+        const float dd = row16_sum(z);
+        if (lane == 32) r_dd[it] = dd;
       };
       if constexpr (W::N_LDS) {
         f32x4 ns;
 #pragma unroll 1
-        for (int jt = 0; jt < wave; ++jt) {
-          ns = s_ns[tile0 + jt * 64];
-          tile(jt, ns, s_gt[tile0 + jt * 64], std::false_type{});
-          s_ns[tile0 + jt * 64] = ns;
+        for (int jt = j_lo; jt < j_hi; ++jt) {
+          ns = s_ns[base + jt * 64];
+          below(jt, ns, s_gt[base + jt * 64]);
+          s_ns[base + jt * 64] = ns;
         }
-        ns = s_ns[tile0 + wave * 64];
-        tile(wave, ns, s_gt[tile0 + wave * 64], std::true_type{});
-        s_ns[tile0 + wave * 64] = ns;
+        if (owner) {
+          ns = s_ns[base + it * 64];
+          diagonal(ns, s_gt[base + it * 64]);
+          s_ns[base + it * 64] = ns;
+        }
       } else {
 #pragma unroll
         for (int jt = 0; jt < 8; ++jt) {
           f32x4 gt = {0.f, 0.f, 0.f, 0.f};
-          if (jt <= wave) {
-            if constexpr (W::G_LDS) gt = s_gt[tile0 + jt * 64];
+          if (jt <= it) {
+            if constexpr (W::G_LDS) gt = s_gt[base + jt * 64];
             else gt = G[jt];
           }
-          if (jt < wave) tile(jt, Ns[jt], gt, std::false_type{});
-          else if (jt == wave) tile(jt, Ns[jt], gt, std::true_type{});
+          if (jt < it) below(jt, Ns[jt], gt);
+          else if (jt == it) diagonal(Ns[jt], gt);
         }
       }
-    }
+      const float ro = row16_sum4(rowo[0], rowo[1], rowo[2], rowo[3]);
+      if (l16 < 4) (owner ? r_row : r_help)[i0 + l16] = ro;
+    };
+    // Rows 5, 6 and 7 give their first 1, 2 and 3 tiles to waves 3, 2 and 1, which leaves five tiles a wave and one for
+    // the first, which closes heads (where the tiles' sums are in registers every wave keeps its row).
+    const int given = W::N_LDS && wave > 4 ? wave - 4 : 0;
+    if (wave < tiles) tile_row(wave, given, wave, true);
+    if (W::N_LDS && wave >= 1 && wave < 4 && 8 - wave < tiles) tile_row(8 - wave, 0, 4 - wave, false);
     if constexpr (W::LATE) {
-      if (wave == 0 && hi > h_lo) close_head(h - 1, s_res + ((hi - 1) & 1) * W::RES);
+      store_gates(g_next);
+      if (wave == 0 && hi > h_lo) close_head(h - 1, s_res + ((hi - 1) & 1) * W::RES, g_before);
+      g_before = g_now;
+      g_now = g_next;
+      g_next = s_gates + ((hi - h_lo + 2) % 3) * W::GATES;
     } else {
       __syncthreads();
-      if (wave == 0) close_head(h, res);
+      if (wave == 0) close_head(h, res, g_now);
+      fetch_gates(h_next);
     }
   }
   if constexpr (W::LATE) {
     __syncthreads();
-    if (wave == 0) close_head(g * hpg + h_hi - 1, s_res + ((h_hi - 1) & 1) * W::RES);
+    if (wave == 0) close_head(g * hpg + h_hi - 1, s_res + ((h_hi - 1) & 1) * W::RES, g_before);
   }
 
   // the heads' summed products with B and C, in two bf16 terms (bf16 inputs): as [i][j] for dC, as [j][i] for dB
 #pragma unroll
   for (int turn = 0; turn < 2; ++turn) {
     constexpr int TERMS = BF ? 2 : 1;
+    Frag<BF> f[4];
+    if (turn == 0 ? do_c : do_b)
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb)
+        f[kb] = 32 * kb >= len ? Frag<BF>::zero()
+                               : Frag<BF>::load(reinterpret_cast<const E*>(at_bytes(
+                                     turn == 0 ? a.bt : a.ct, (((slot64 + (kb >> 1)) * a.G + g) * NN + n16) * Q + 32 * (kb & 1), l16 * Q + 8 * q, sizeof(E))));
     __syncthreads();
 #pragma unroll
     for (int jt = 0; jt < 8; ++jt) {
@@ -627,20 +663,17 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
     }
     __syncthreads();
     if (turn == 0 ? do_c : do_b) {
-      const void* src = turn == 0 ? a.bt : a.ct;
 #pragma unroll
       for (int kb = 0; kb < 4; ++kb) {
         if (32 * kb >= len) continue;
-        const Frag<BF> f = Frag<BF>::load(reinterpret_cast<const E*>(
-            at_bytes(src, (((slot64 + (kb >> 1)) * a.G + g) * NN + n16) * Q + 32 * (kb & 1), l16 * Q + 8 * q, sizeof(E))));
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
           if (turn == 0 ? 2 * kb > it : 2 * kb + 1 < it) continue;  // no pair j <= i in the tile
 #pragma unroll
           for (int k = TERMS - 1; k >= 0; --k) {
             const Frag<BF> nf = Frag<BF>::load(s_n + k * T * LDN + (16 * it + l16) * LDN + 32 * kb + 8 * q);
-            if (turn == 0) dC[it] = frag_mma(dC[it], nf, f);
-            else dB[it] = frag_mma(dB[it], nf, f);
+            if (turn == 0) dC[it] = frag_mma(dC[it], nf, f[kb]);
+            else dB[it] = frag_mma(dB[it], nf, f[kb]);
           }
         }
       }

@@ -205,19 +205,38 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
   // order in which it meets the read vectors; without, (n = 16 nt + l16, p = 16 pt + 4 q + r), which gives blocks [n][p]
   // four values at a time.  In memory a state is [p][n].
   f32x4 S[NT][PT];
-  auto load_state = [&](const void* base, int64_t unit, int dt) {
+  auto load_as = [&](const void* base, int64_t unit, auto type) {  // all loads before the first use
+    constexpr int DT = decltype(type)::value, EB = DT == GDN_F32 ? 4 : 2;
+    const int64_t at = ((unit * a.H + h) * D + pd) * NN;
+    InVec<DT, 4> v[OUT ? NT : 1][PT];
+    uint32_t e[OUT ? 1 : NT][PT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt) {
-        const int64_t at = ((unit * a.H + h) * D + pd + 16 * pt) * NN + 16 * nt;
+        if constexpr (OUT) {
+          v[nt][pt].load(at_bytes(base, at + 16 * pt * NN + 16 * nt, l16 * NN + 4 * q, EB), 0);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) e[nt][pt][r] = in_bits<DT>(at_bytes(base, at + (16 * pt + r) * NN + 16 * nt, 4 * q * NN + l16, EB), 0);
+        }
+      }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
         float f[4];
-        if constexpr (OUT) load_vec<4>(base, at + l16 * NN + 4 * q, dt, f);
+        if constexpr (OUT) v[nt][pt].widen(f);
         else
 #pragma unroll
-          for (int r = 0; r < 4; ++r) f[r] = load_elem(base, at + (4 * q + r) * NN + l16, dt);
+          for (int r = 0; r < 4; ++r) f[r] = in_value<DT>(e[nt][pt][r]);
         S[nt][pt] = f32x4{f[0], f[1], f[2], f[3]};
       }
+  };
+  auto load_state = [&](const void* base, int64_t unit, int dt) {
+    if (dt == GDN_F32) load_as(base, unit, std::integral_constant<int, GDN_F32>{});
+    else if (dt == GDN_BF16) load_as(base, unit, std::integral_constant<int, GDN_BF16>{});
+    else load_as(base, unit, std::integral_constant<int, GDN_F16>{});
   };
   auto store_state = [&](void* base, int64_t unit, int dt) {
 #pragma unroll
@@ -236,10 +255,6 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int pt = 0; pt < PT; ++pt) S[nt][pt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (!a.local && mine) {
-    if (a.seg_chunks > 0) load_state(a.seg, slot, GDN_F32);
-    else if (a.init.base != nullptr) load_state(a.init.base, a.init.slots != nullptr ? a.init.slots[sg.seq] : sg.seq, a.init.dtype);
-  }
   double total_g = 0.0;
   const float Dh = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, a.Dskip[h])));
 
@@ -382,6 +397,10 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
   if (steps > 0) {
     fetch(REV ? c_hi - 1 : c_lo);
     if constexpr (OUT) fetch_products(REV ? c_hi - 1 : c_lo);
+  }
+  if (!a.local && mine) {
+    if (a.seg_chunks > 0) load_state(a.seg, slot, GDN_F32);
+    else if (a.init.base != nullptr) load_state(a.init.base, a.init.slots != nullptr ? a.init.slots[sg.seq] : sg.seq, a.init.dtype);
   }
   const float* const gh_ = s_g + hl * 5 * Q;
 

@@ -128,8 +128,9 @@ struct WalkGeom {
   static constexpr int WPH = NW / HB;                  // waves of a head
   static constexpr int NT = NN / 16, KB = (NN + 31) / 32;
   static constexpr int LDF = KB * 32 + (BF ? 8 : 4);   // read vectors [64][LDF], columns in accumulator order
-  static constexpr int LDT = kScanChunk + (BF ? 8 : 4);  // write vectors [NN][LDT], inputs [ROWS][LDT], products [HB][64][LDT]
-  static constexpr int F0 = 0, K0 = F0 + (OUT ? kScanChunk * LDF : 0), X0 = K0 + NN * LDT, P0 = X0 + ROWS * LDT;
+  static constexpr int LDK = kScanChunk + (BF ? 0 : 4);  // write vectors [NN][LDK] (16-bit form: groups of 8 tokens permuted by the row)
+  static constexpr int LDT = kScanChunk + (BF ? 8 : 4);  // inputs [ROWS][LDT], products [HB][64][LDT]
+  static constexpr int F0 = 0, K0 = F0 + (OUT ? kScanChunk * LDF : 0), X0 = K0 + NN * LDK, P0 = X0 + ROWS * LDT;
   static constexpr int ELEMS = P0 + (OUT ? HB * kScanChunk * LDT : 0);
   // floats a head: c (two), dt', the input's weight, the read factor
   static constexpr size_t LDS = ((size_t)ELEMS * sizeof(E) + 15) / 16 * 16 + (size_t)HB * 5 * kScanChunk * 4;
@@ -144,6 +145,11 @@ struct WalkGeom {
 template <bool BF, int LDT>
 __device__ __forceinline__ int xt_at(int p, int t) {
   return p * LDT + (BF ? ((((t >> 3) ^ (p >> 3)) & 7) << 3 | (t & 7)) : t);
+}
+
+template <bool BF, int LDK>
+__device__ __forceinline__ int kt_at(int n, int t) {
+  return n * LDK + (BF ? ((t >> 3) ^ (n & 7)) << 3 : t);  // t: a multiple of 8
 }
 
 template <bool BF, int D, int NN, int PT, bool REV, bool OUT>
@@ -335,10 +341,10 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
   };
   auto commit = [&](int len) {
     {
-      E* d = s_k + (tid >> 3) * LDT + (tid & 7) * 8;
+      E* d = s_k + kt_at<BF, W::LDK>(tid >> 3, (tid & 7) * 8);  // 32 rows on, the same place in the permutation
 #pragma unroll
       for (int k = 0; k < W::FV; ++k)
-        if (NN * 8 % 256 == 0 || tid + 256 * k < NN * 8) *reinterpret_cast<Frag<BF>*>(d + k * 32 * LDT) = vk[k];
+        if (NN * 8 % 256 == 0 || tid + 256 * k < NN * 8) *reinterpret_cast<Frag<BF>*>(d + k * 32 * W::LDK) = vk[k];
     }
     if constexpr (OUT) {
       // n = 32 k + 16 b + 4 s + r is stored at 32 k + 8 s + 4 b + r
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
       for (int ng = 0; ng < NT; ng += NG) {
         Frag<BF> kf[NG];
 #pragma unroll
-        for (int i = 0; i < NG; ++i) kf[i] = Frag<BF>::load(s_k + (16 * (ng + i) + l16) * LDT + 32 * ks + 8 * q);
+        for (int i = 0; i < NG; ++i) kf[i] = Frag<BF>::load(s_k + kt_at<BF, W::LDK>(16 * (ng + i) + l16, 32 * ks + 8 * q));
 #pragma unroll
         for (int k = Split<BF>::K - 1; k >= 0; --k)
 #pragma unroll
@@ -704,20 +710,27 @@ hipError_t prep(const M2ScanArgs& a, int n, hipStream_t s) {
 
 }  // namespace
 
+// Sizes decide two things (bf16, d = 64, n = 128; us for the whole call, whole
+// sequences unless a number of chunks is given):
+//  - Waves of 16 state rows, a head a workgroup, where the waves of 32 would be
+//    fewer than two workgroups a compute unit: four prompts (20,408 tokens) x
+//    128 heads 604 narrow, 722 wide; 32 x 1024 tokens x 128 heads 670 and 609.
+//  - Segments only where there are few walks, as they cost a second walk and the
+//    states' way through memory: backward of 4 x 4096 tokens x 128 heads (512
+//    walks) 1386 whole, 1847 in segments of 14; of 16,385 tokens x 32 heads (32
+//    walks) 1616 whole, 559 in segments of 12, 608 of 8.  Their length leaves
+//    704 workgroups, close to three a compute unit.
 ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d) {
-  const int hpg = H / G;
-  const int64_t chunks = (total + kScanChunk - 1) / kScanChunk;
-  ScanPlan p{0, 0};
-#ifdef GDN_SEG_FORCE
-  p.seg_chunks = GDN_SEG_FORCE % 1000;
-  p.narrow = GDN_SEG_FORCE / 1000;
-  return p;
-#endif
-  const int64_t walks = (int64_t)G * ((hpg * d + 127) / 128);
-  if (N * walks >= 512 || chunks <= 16) return p;
-  int64_t per = chunks * walks / 1024;
-  per = per < 8 ? 8 : (per + 1) / 2 * 2;
-  p.seg_chunks = per >= chunks ? 0 : (int)per;
+  const int hpg = H / G, wide_heads = (d == 16 ? 64 : 128) / d;
+  const int64_t chunks = (total + kScanChunk - 1) / kScanChunk, wide = (int64_t)G * ((hpg + wide_heads - 1) / wide_heads);
+  ScanPlan p;
+  p.narrow = d == 64 && N * wide < 512;
+  const int64_t walks = p.narrow ? H : wide;
+  p.seg_chunks = 0;
+  if (N * walks < 384 && chunks > 8) {
+    const int64_t per = (chunks * walks / 704 + 1) / 2 * 2;
+    p.seg_chunks = per < 4 ? 4 : (int)per;
+  }
   return p;
 }
 

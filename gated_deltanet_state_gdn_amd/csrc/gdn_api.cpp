@@ -781,6 +781,7 @@ gdn_status check_scan_sizes(const gdn_m2_dims* d, int32_t N, int64_t total) {
 gdn_status check_token_stride(int64_t s, int64_t least, int64_t unit, const char* what) {
   GDN_REQUIRE(s == 0 || (s >= least && s % unit == 0), GDN_EINVAL, "%s stride %lld must be 0 or a multiple of %lld, >= %lld",
               what, (long long)s, (long long)unit, (long long)least);
+  GDN_REQUIRE(s <= kMaxTokenStride, GDN_EUNSUPPORTED, "%s stride %lld: at most 2^22 is supported", what, (long long)s);
   return GDN_OK;
 }
 

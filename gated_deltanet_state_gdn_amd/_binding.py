@@ -9,6 +9,7 @@ an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import NamedTuple
@@ -150,12 +151,16 @@ def _torch():
     return torch
 
 
+_codes = {}
+
+
 def dtype_code(dt) -> int:
-    torch = _torch()
-    codes = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float16: GDN_F16}
-    if dt not in codes:
+    if not _codes:
+        torch = _torch()
+        _codes.update({torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float16: GDN_F16})
+    if dt not in _codes:
         raise TypeError(f"unsupported dtype {dt}")
-    return codes[dt]
+    return _codes[dt]
 
 
 def _ptr(t) -> int:
@@ -166,8 +171,8 @@ def _ptr(t) -> int:
 
 def _stream(stream) -> int:
     torch = _torch()
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: building a Stream object costs several microseconds a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -512,6 +517,8 @@ def _token_rows(t, tail, dtype, what):
     """(pointer, token stride) of a [T, ...] tensor whose tokens may be apart."""
     if t.dim() != 1 + len(tail) or tuple(t.shape[1:]) != tuple(tail) or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} of shape [T, {', '.join(map(str, tail))}], not {t.dtype} {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
     dense, step = 1, []
     for v in reversed(tail):
         step.insert(0, dense)
@@ -554,6 +561,13 @@ def _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map):
                          _ptr(slot_map) if slot_map is not None else None])
 
 
+@functools.lru_cache(maxsize=1024)
+def _scan_workspace(backward, H, G, d, n, N, T) -> int:
+    dims = gdn_m2_dims(H, G, d, n)
+    f = lib().gdn_mamba2_scan_backward_workspace_bytes if backward else lib().gdn_mamba2_scan_workspace_bytes
+    return int(f(ctypes.byref(dims), N, T))
+
+
 def gdn_mamba2_scan(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool=None, slot_map=None, out=None, out_dtype=None,
                     workspace=None, stream=None):
     """The Mamba2 recurrence over packed sequences: x [T, H, d]; Bm, Cm [T, G, n]; dt [T, H]; cu_seqlens int32
@@ -569,7 +583,7 @@ def gdn_mamba2_scan(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool=None, slo
     elif tuple(out.shape) != tuple(x.shape):
         raise ValueError(f"out must be {tuple(x.shape)}, not {tuple(out.shape)}")
     if workspace is None:
-        need = int(lib().gdn_mamba2_scan_workspace_bytes(ctypes.byref(dims), N, T))
+        need = _scan_workspace(False, dims.num_heads, dims.num_groups, dims.headdim, dims.dstate, N, T)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
             fresh.append(workspace)
@@ -595,7 +609,7 @@ def gdn_mamba2_scan_backward(dy, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, p
                         new((H,), f32), new((H,), f32), new((H,), f32), new((N, H, d, n), f32) if pool is not None else None)
     fresh = list(grads)
     if workspace is None:
-        need = int(lib().gdn_mamba2_scan_backward_workspace_bytes(ctypes.byref(dims), N, T))
+        need = _scan_workspace(True, H, G, d, n, N, T)
         if need:
             workspace = new((need,), torch.uint8)
             fresh.append(workspace)
@@ -627,8 +641,10 @@ def _rows(t, shape, dtype, what):
     """(pointer, row stride) of a [rows, width] tensor whose rows may be apart."""
     if t is None:
         return None, 0
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
     if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{what}: the values of a row must be consecutive")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
@@ -656,7 +672,7 @@ def gdn_layer_norm(x, weight, bias=None, gate=None, groups=1, eps=1e-5, rms=Fals
         fresh.append(out)
     mean = rstd = None
     if save_stats:
-        mean, rstd = (torch.empty((x.shape[0], groups), dtype=torch.float32, device=x.device) for _ in range(2))
+        mean, rstd = torch.empty((2, x.shape[0], groups), dtype=torch.float32, device=x.device)
         fresh += [mean, rstd]
     _keep_for_stream(fresh, stream)
     _check(lib().gdn_layer_norm(ctypes.byref(dims), *_rows(x, x.shape, x.dtype, "x"),

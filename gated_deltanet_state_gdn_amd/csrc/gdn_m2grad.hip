@@ -738,10 +738,9 @@ template <bool BF, int D, int NN>
 hipError_t grad(const M2GradArgs& a, int64_t slots, hipStream_t s) {
   using W = GradGeom<BF, D, NN>;
   auto* k = gdn_m2s_grad_kernel<BF, D, NN>;
-  if (W::LDS > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)W::LDS);
-    if (e != hipSuccess) return e;
-  }
+  static std::atomic<uint64_t> allowed{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(k), W::LDS, allowed);
+  if (e != hipSuccess) return e;
   k<<<(unsigned)(slots * a.G * a.splits), 512, W::LDS, s>>>(a);
   return hipGetLastError();
 }

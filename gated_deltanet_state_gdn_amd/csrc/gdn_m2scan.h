@@ -3,6 +3,8 @@
 // an FP32 operand into bf16 terms.
 #pragma once
 
+#include <atomic>
+
 #include "gdn_device.h"
 #include "gdn_launch.h"
 
@@ -10,6 +12,20 @@ namespace gdn {
 
 constexpr int kScanChunk = 64;   // tokens of a chunk
 constexpr int kGradBlock = 128;  // tokens of a block of the gradient kernel, two chunks
+
+// Lets a kernel take more than 64 KiB of dynamic LDS, once a device (`done`: a
+// bit a device; a device past 63 is asked every time).
+inline hipError_t allow_lds(const void* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  if (bytes <= 65536) return hipSuccess;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // ------------------------------------------------------------------ where chunks lie
 // Sequence s of a packed batch, cut into pieces of P tokens, owns the slots

@@ -665,10 +665,9 @@ hipError_t walk(const M2ScanArgs& a, hipStream_t s) {
   const int hpg = a.H / a.G, hbs = (hpg + W::HB - 1) / W::HB;
   const int64_t slots = a.seg_chunks > 0 ? scan_slots(a.N, a.total, (int64_t)a.seg_chunks * kScanChunk) : a.N;
   auto* k = gdn_m2s_walk_kernel<BF, D, NN, PT, REV, OUT>;
-  if (W::LDS > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, (int)W::LDS);
-    if (e != hipSuccess) return e;
-  }
+  static std::atomic<uint64_t> allowed{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(k), W::LDS, allowed);
+  if (e != hipSuccess) return e;
   k<<<(unsigned)(slots * a.G * hbs), W::THREADS, W::LDS, s>>>(a);
   return hipGetLastError();
 }

@@ -15,8 +15,8 @@
 //
 // Kernels: the prep forms, once for all heads of a group, the products of read
 // and write vectors and the transposed write vectors, and each head's dt' and
-// c.  The walk keeps the states of 128 rows (two heads of 64) in accumulators
-// and goes over the chunks; the state meets the read vectors straight from its
+// c.  The walk keeps the states of 128 rows (two heads of 64; 64 rows, one head,
+// where walks are few) in accumulators and goes over the chunks; the state meets the read vectors straight from its
 // accumulators, whose layout is that of an operand once the read vectors'
 // columns are stored in the same order.  Where there are too few walks for the
 // chip, sequences are cut into segments: a first walk finds each segment's own
@@ -28,6 +28,11 @@
 // 24 bits, with exact B.  For the output alone the state and the decay-weighted
 // products of read and write vectors are rounded to bf16 once, as y is.
 // Any other types take the FP32 MFMA throughout.
+//
+// Measured (bf16, heads of 64 x 128): prompts of 1024, 3000 and twice 8192
+// tokens through 128 heads 608 us (prep 51, walk 557), 1.3 TB/s of what has to
+// move: the chain of 128 chunks, 4.4 us each, is what bounds it.  Matrix units are
+// busy 13% of the time.  16,384 tokens, states only, 222 us; in reverse with dx 428.
 #include "gdn_m2scan.h"
 
 namespace gdn {
@@ -112,7 +117,7 @@ __global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
 }
 
 // ------------------------------------------------------------------ walk
-// Four waves over 128 state rows (two heads of 64), two workgroups on a compute
+// Four waves over 128 state rows (two heads of 64) or 64, two workgroups on a compute
 // unit: one's vector work then runs beside the other's matrix work.  Eight
 // waves over 256 rows, one workgroup, share the read and write vectors of a
 // chunk among twice the heads but keep in step: a prefill of 20,408 tokens

@@ -849,6 +849,7 @@ gdn::M2ScanArgs scan_args(const gdn_m2_dims* d, int32_t N, const int32_t* cu, in
   a.seg = reinterpret_cast<float*>(ws + w.seg);
   a.seg_g = reinterpret_cast<double*>(ws + w.seg_g);
   a.seg_chunks = w.plan.seg_chunks;
+  a.whole = w.plan.whole;
   a.narrow = w.plan.narrow;
   return a;
 }

@@ -137,7 +137,7 @@ struct M2ScanArgs {
   float* seg;       // [segment slots][H][d][n] states at the segments' starts
   double* seg_g;    // [segment slots][H] the segments' summed log-decays
   float* blocks;    // states that meet each 128-token block, [block slots][H] of [n][d] (in reverse [d][n]), or null
-  int32_t seg_chunks, narrow;  // ScanPlan
+  int32_t seg_chunks, whole, narrow;  // ScanPlan
   int32_t local;       // the segments' first walk
 };
 
@@ -204,10 +204,10 @@ hipError_t launch_m2_replay(const M2Args& a, int state_dt, int P, int N, hipStre
 hipError_t launch_m2_rollback(const M2Args& a, hipStream_t s);
 // Slots of a packed batch cut into pieces of P tokens.
 int64_t scan_slots(int64_t N, int64_t total, int64_t P);
-// How a walk is cut: chunks a segment (even, so that blocks of two chunks do not straddle; 0 for whole sequences), and
-// whether a wave has 16 state rows (narrow; d = 64 only) or 32.
+// How a walk is cut: chunks a segment (even, so that blocks of two chunks do not straddle; 0 for whole sequences), the
+// most segments that a sequence may have and stay whole, and whether a wave has 16 state rows (narrow; d = 64 only) or 32.
 struct ScanPlan {
-  int seg_chunks, narrow;
+  int seg_chunks, whole, narrow;
 };
 ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d);
 hipError_t launch_scan_prep(const M2ScanArgs& a, bool bf, int n, hipStream_t s);

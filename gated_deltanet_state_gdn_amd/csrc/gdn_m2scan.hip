@@ -179,6 +179,10 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
   if (a.seg_chunks > 0) {
     sg = find_piece(a.cu, a.N, a.total, slot, a.seg_chunks * Q);
     if (sg.seq < 0) return;
+    if (sg.count <= a.whole) {  // its first segment's workgroup takes it whole
+      if (sg.index > 0) return;
+      sg.count = 1;
+    }
   } else {
     sg.seq = slot;
     sg.begin = token_at(a.cu, slot, a.total);
@@ -189,8 +193,8 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
   const bool last_seg = REV ? sg.index == 0 : sg.index == sg.count - 1;
   if (a.local && last_seg) return;  // nothing starts from this segment's end
   const int chunks = (int)((sg.len + Q - 1) / Q);
-  const int c_lo = a.seg_chunks > 0 ? sg.index * a.seg_chunks : 0;
-  const int c_hi = a.seg_chunks > 0 ? min(chunks, c_lo + a.seg_chunks) : chunks;
+  const int c_lo = sg.index * a.seg_chunks;
+  const int c_hi = sg.count > 1 ? min(chunks, c_lo + a.seg_chunks) : chunks;
   const int64_t slot0 = sg.seq + sg.begin / Q;  // chunk slot of the sequence's first chunk
 
   const int p0 = wave * 16 * PT;                // the wave's rows of the workgroup's
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
     if constexpr (OUT) fetch_products(REV ? c_hi - 1 : c_lo);
   }
   if (!a.local && mine) {
-    if (a.seg_chunks > 0) load_state(a.seg, slot, GDN_F32);
+    if (sg.count > 1) load_state(a.seg, slot, GDN_F32);
     else if (a.init.base != nullptr) load_state(a.init.base, a.init.slots != nullptr ? a.init.slots[sg.seq] : sg.seq, a.init.dtype);
   }
   const float* const gh_ = s_g + hl * 5 * Q;
@@ -638,6 +642,7 @@ __global__ void __launch_bounds__(256) gdn_m2s_chain_kernel(const M2ScanArgs a, 
   const int P = a.seg_chunks * kScanChunk;
   const int64_t b = token_at(a.cu, seq, a.total), e = token_at(a.cu, seq + 1, a.total);
   const int count = (int)max((e - b + P - 1) / P, (int64_t)1);
+  if (count <= a.whole) return;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (a.init.base != nullptr) {
     float f[4];
@@ -724,6 +729,12 @@ hipError_t prep(const M2ScanArgs& a, int n, hipStream_t s) {
 //    walks) 1386 whole, 1847 in segments of 14; of 16,385 tokens x 32 heads (32
 //    walks) 1616 whole, 559 in segments of 12, 608 of 8.  Their length leaves
 //    704 workgroups, close to three a compute unit.
+//    Walks enough but of little work (3 to 12 chunks a workgroup of the 704) are
+//    likely to be ragged, and then the longest sequence decides: sequences of
+//    more than two segments are cut, and batches of equal lengths have none.  20
+//    sequences of 0 to 1500 tokens x 32 heads 91 whole, 75 cut; 12 of 1 to 3000 x
+//    64 heads 211 and 143; where nothing is cut the two launches cost 8 (20 of
+//    245 tokens 42 and 50, 20 of 500 65 and 73).
 ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d) {
   const int hpg = H / G, wide_heads = (d == 16 ? 64 : 128) / d;
   const int64_t chunks = (total + kScanChunk - 1) / kScanChunk, wide = (int64_t)G * ((hpg + wide_heads - 1) / wide_heads);
@@ -731,7 +742,9 @@ ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d) {
   p.narrow = d == 64 && N * wide < 512;
   const int64_t walks = p.narrow ? H : wide;
   p.seg_chunks = 0;
-  if (N * walks < 384 && chunks > 8) {
+  const bool few = N * walks < 384;
+  p.whole = few ? 1 : 2;
+  if (chunks > 8 && (few || (chunks * walks >= 3 * 704 && chunks * walks <= 12 * 704))) {
     const int64_t per = (chunks * walks / 704 + 1) / 2 * 2;
     p.seg_chunks = per < 4 ? 4 : (int)per;
   }

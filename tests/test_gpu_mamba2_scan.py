@@ -153,6 +153,14 @@ def test_segments(dt):
     check_backward([1500], 3, 3, 16, 16, dt)
 
 
+def test_ragged_batch_in_segments():
+    """Walks enough, of uneven lengths: the two longest sequences are cut, the others (of two segments too) are not."""
+    lens = [1300, 1, 0, 200, 700, 512, 129]
+    check_scan(lens, 64, 2, 64, 16, "bf16", "f32")
+    check_backward(lens, 64, 2, 64, 16, "bf16", "f32", dfinal=True)
+    check_scan(lens, 64, 2, 64, 16, "f32")
+
+
 def test_tokens_apart():
     """Inputs that are slices of wider rows (the gaps hold NaN)."""
     check_scan([70, 61], 4, 2, 64, 128, "bf16", "f32", wide=24)

@@ -729,7 +729,8 @@ hipError_t prep(const M2ScanArgs& a, int n, hipStream_t s) {
 //    walks) 1386 whole, 1847 in segments of 14; of 16,385 tokens x 32 heads (32
 //    walks) 1616 whole, 559 in segments of 12, 608 of 8.  Their length leaves
 //    704 workgroups, close to three a compute unit.
-//    Walks enough but of little work (3 to 12 chunks a workgroup of the 704) are
+//    Walks enough but of little work (3 to 12 chunks a workgroup of the 704,
+//    sequences that average a chunk or more: N within a grid's third bound) are
 //    likely to be ragged, and then the longest sequence decides: sequences of
 //    more than two segments are cut, and batches of equal lengths have none.  20
 //    sequences of 0 to 1500 tokens x 32 heads 91 whole, 75 cut; 12 of 1 to 3000 x
@@ -744,7 +745,7 @@ ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d) {
   p.seg_chunks = 0;
   const bool few = N * walks < 384;
   p.whole = few ? 1 : 2;
-  if (chunks > 8 && (few || (chunks * walks >= 3 * 704 && chunks * walks <= 12 * 704))) {
+  if (chunks > 8 && (few || (N <= chunks && chunks * walks >= 3 * 704 && chunks * walks <= 12 * 704))) {
     const int64_t per = (chunks * walks / 704 + 1) / 2 * 2;
     p.seg_chunks = per < 4 ? 4 : (int)per;
   }

@@ -161,6 +161,27 @@ def test_ragged_batch_in_segments():
     check_scan(lens, 64, 2, 64, 16, "f32")
 
 
+def test_more_sequences_than_a_grid_side():
+    """70,000 sequences of one token: y and dx against the formula of one token."""
+    import torch
+    import gated_deltanet_state_gdn_amd as gdn
+    N, H, d, n = 70_000, 4, 16, 16
+    gen = torch.Generator().manual_seed(5)
+    x, Bm, Cm, dt = (torch.randn(*s, generator=gen).to(DEV) for s in ((N, H, d), (N, 1, n), (N, 1, n), (N, H)))
+    A_log, dt_bias, D = (torch.randn(H, generator=gen).to(DEV) for _ in range(3))
+    cu = torch.arange(N + 1, dtype=torch.int32, device=DEV)
+    y = gdn.gdn_mamba2_scan(x, Bm, Cm, dt, A_log, dt_bias, D, cu)
+    g = gdn.gdn_mamba2_scan_backward(torch.ones_like(x), x, Bm, Cm, dt, A_log, dt_bias, D, cu)
+    torch.cuda.synchronize()
+    x, Bm, Cm, dt, dt_bias, D = (t.double() for t in (x, Bm, Cm, dt, dt_bias, D))
+    step = torch.nn.functional.softplus(dt + dt_bias)
+    scale = step * (Bm * Cm).sum(-1)
+    size = step * (Bm * Cm).abs().sum(-1) + D.abs()
+    # n products, their sum, dt' (a logarithm and an exponential, 8 units), two products and a sum: under 32 roundings of the terms' sizes
+    assert ((y - (scale + D)[..., None] * x).abs() <= 32 * 2.0 ** -24 * size[..., None] * x.abs()).all()
+    assert ((g.dx - (scale + D)[..., None]).abs() <= 32 * 2.0 ** -24 * size[..., None]).all()
+
+
 def test_tokens_apart():
     """Inputs that are slices of wider rows (the gaps hold NaN)."""
     check_scan([70, 61], 4, 2, 64, 128, "bf16", "f32", wide=24)

@@ -18,8 +18,8 @@
 // eight values and moved.  Measured, layer form with a bias in
 // bf16 where not said (a copy reaches 5.1 to 5.4 TB/s): forward 20,408 rows of
 // 4096 values 65 us, 5.2 TB/s; backward 16,384 rows of 4096 84 us, 4.8 TB/s;
-// backward 16,384 rows of 8 slices of 1024, RMS with the gate before, 262 us,
-// 5.1 TB/s; backward 40,001 rows of 128, RMS in FP32 with the gate behind, 22 us,
+// backward 16,384 rows of 8 slices of 1024, RMS with the gate before, 267 us,
+// 5.0 TB/s; backward 40,001 rows of 128, RMS in FP32 with the gate behind, 22 us,
 // 4.6 TB/s; backward 20,001 rows of 2047, which no vector fits, 62 us, 3.9 TB/s;
 // backward 4000 rows of 16,384 with the gate before 249 us, 2.6 TB/s (its
 // arithmetic spills); three rows of 8 slices: the call's latency, 13 us.
@@ -172,13 +172,16 @@ __device__ __forceinline__ float slice_sum(float x, float* part) {
   }
 }
 
-// sigmoid, without expf's steps for its range: e^-x as 2^t 2^lo, t + lo = -x log2 e,
-// 2^lo to first order.  Past +-100 it is 0 or 1 to the last bit.
+// sigmoid from a = e^-|x|, which cannot overflow: 1 / (1 + a), or a / (1 + a) for
+// x < 0.  Without expf's steps for its range: a = (2^t 2^lo)^2, t + lo = -|x| log2 e / 2,
+// 2^lo to first order; the hardware's exponential does not flush this root, so a
+// keeps to the smallest numbers.  From 110 on a is zero.
 __device__ __forceinline__ float norm_sigmoid(float x) {
-  const float v = __builtin_amdgcn_fmed3f(-x, -100.f, 100.f), t = v * 1.44269504f;
-  const float lo = fmaf(v, 1.44269504f, -t) + v * 1.92596303e-8f;  // log2 e = 1.44269504 (in FP32) + 1.926e-8
-  const float p = __builtin_amdgcn_exp2f(t);
-  return __builtin_amdgcn_rcpf(1.f + fmaf(p, lo * 0.693147181f, p));
+  const float v = fmaxf(-fabsf(x), -110.f), t = v * 0.72134752f;
+  const float lo = fmaf(v, 0.72134752f, -t) + v * 9.62981514e-9f;  // log2 e / 2 = 0.72134752 (in FP32) + 9.630e-9
+  const float root = __builtin_amdgcn_exp2f(t), p = root * root;
+  const float a = fmaf(p, lo * 1.38629436f, p), s = __builtin_amdgcn_rcpf(1.f + a);
+  return x < 0.f ? a * s : s;
 }
 
 template <int IDT, int LPU, int CH, int GATE>

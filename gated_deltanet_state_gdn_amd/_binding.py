@@ -513,49 +513,78 @@ class M2ScanGrads(NamedTuple):
     dinit: object  # [N, H, d, n], or None without a pool
 
 
-def _token_rows(t, tail, dtype, what):
-    """(pointer, token stride) of a [T, ...] tensor whose tokens may be apart."""
-    if t.dim() != 1 + len(tail) or tuple(t.shape[1:]) != tuple(tail) or t.dtype != dtype:
+def _one_row(t):
+    """Whether a tensor's rows are all one row: an expanded tensor, such as autograd's gradient behind a sum over rows.  (The
+    library takes a stride of 0 for dense rows.)"""
+    return t.shape[0] > 1 and t.stride(0) == 0 and t.numel() > 0
+
+
+def _own_rows(t, copies, stream):
+    """A copy of an input whose rows are all one, made on the call's stream and kept in `copies` until the launch."""
+    torch = _torch()
+    if stream is None:
+        t = t.contiguous()
+    else:
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+            t = t.contiguous()
+    copies.append(t)
+    return t.data_ptr(), 0
+
+
+def _row_stride(t, what):
+    """Elements between the rows of a tensor that is not dense."""
+    if _one_row(t):
+        raise ValueError(f"{what}: its rows share their memory")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _token_rows(t, tail, dtype, what, copies=None, stream=None):
+    """(pointer, token stride) of a [T, ...] tensor whose tokens may be apart; an expanded one is copied if `copies` are kept."""
+    if t.dim() != 1 + len(tail) or t.shape[1:] != tail or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} of shape [T, {', '.join(map(str, tail))}], not {t.dtype} {tuple(t.shape)}")
     if t.is_contiguous():
         return t.data_ptr(), 0
+    if copies is not None and _one_row(t):
+        return _own_rows(t, copies, stream)
     dense, step = 1, []
     for v in reversed(tail):
         step.insert(0, dense)
         dense *= int(v)
     if t.numel() and any(t.shape[1 + i] > 1 and t.stride(1 + i) != v for i, v in enumerate(step)):
         raise ValueError(f"{what}: the values of a token must be consecutive")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+    return t.data_ptr(), _row_stride(t, what)
 
 
-def _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map):
+def _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, copies, stream):
     """The arguments that the scan and its backward share: dims, sequences, pointers and the structs behind them."""
     torch = _torch()
     if x.dim() != 3 or Bm.dim() != 3:
         raise ValueError("x must be [T, H, d] and Bm [T, G, n]")
     T, H, d = x.shape
     G, n = Bm.shape[1:]
-    px, sx = _token_rows(x, (H, d), x.dtype, "x")
-    pb, sb = _token_rows(Bm, (G, n), x.dtype, "Bm")
-    pc, sc = _token_rows(Cm, (G, n), x.dtype, "Cm")
-    pdt, sdt = _token_rows(dt, (H,), x.dtype, "dt")
+    dtype = x.dtype
+    px, sx = _token_rows(x, (H, d), dtype, "x", copies, stream)
+    pb, sb = _token_rows(Bm, (G, n), dtype, "Bm", copies, stream)
+    pc, sc = _token_rows(Cm, (G, n), dtype, "Cm", copies, stream)
+    pdt, sdt = _token_rows(dt, (H,), dtype, "dt", copies, stream)
     if not T == Bm.shape[0] == Cm.shape[0] == dt.shape[0]:
         raise ValueError("x, Bm, Cm and dt must have the same number of tokens")
+    heads = (H,)
     for t, what in ((A_log, "A_log"), (dt_bias, "dt_bias"), (D, "D")):
-        _f32(t, (H,), what)
+        _f32(t, heads, what)
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be int32 [N + 1]")
     N = int(cu_seqlens.shape[0]) - 1
     if (pool is None) != (slot_map is None):
         raise ValueError("pool and slot_map come together or not at all")
     if pool is not None:
-        if tuple(pool.shape[1:]) != (H, d, n):
+        if pool.shape[1:] != (H, d, n):
             raise ValueError(f"pool must be [slots, {H}, {d}, {n}], not {tuple(pool.shape)}")
-        if slot_map.dtype != torch.int32 or tuple(slot_map.shape) != (N,):
+        if slot_map.dtype != torch.int32 or slot_map.shape != (N,):
             raise ValueError(f"slot_map must be int32 [{N}]")
     dims = gdn_m2_dims(H, G, d, n)
     params = gdn_m2_params(pdt, _ptr(A_log), _ptr(dt_bias), _ptr(D))
-    return (T, N, dims, [ctypes.byref(dims), N, _ptr(cu_seqlens), T, px, pb, pc, dtype_code(x.dtype),
+    return (T, N, dims, [ctypes.byref(dims), N, _ptr(cu_seqlens), T, px, pb, pc, dtype_code(dtype),
                          ctypes.byref(gdn_m2_strides(sx, sb, sc, sdt)), ctypes.byref(params),
                          ctypes.byref(_pool(pool)) if pool is not None else None,
                          _ptr(slot_map) if slot_map is not None else None])
@@ -571,16 +600,17 @@ def _scan_workspace(backward, H, G, d, n, N, T) -> int:
 def gdn_mamba2_scan(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool=None, slot_map=None, out=None, out_dtype=None,
                     workspace=None, stream=None):
     """The Mamba2 recurrence over packed sequences: x [T, H, d]; Bm, Cm [T, G, n]; dt [T, H]; cu_seqlens int32
-    [N+1] (device).  Tokens may be apart (slices of wider rows).  With a pool [slots, H, d, n] and slot_map int32
+    [N+1] (device).  Tokens may be apart (slices of wider rows; an expanded tensor is copied).  With a pool [slots, H, d, n] and slot_map int32
     [N], sequence s goes on from slot slot_map[s] and leaves its final state there; without, from zero states.
     Returns y [T, H, d] in out_dtype (x's by default)."""
     torch = _torch()
-    T, N, dims, args = _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map)
+    copies = []
+    T, N, dims, args = _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, copies, stream)
     fresh = []
     if out is None:
         out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
         fresh.append(out)
-    elif tuple(out.shape) != tuple(x.shape):
+    elif out.shape != x.shape:
         raise ValueError(f"out must be {tuple(x.shape)}, not {tuple(out.shape)}")
     if workspace is None:
         need = _scan_workspace(False, dims.num_heads, dims.num_groups, dims.headdim, dims.dstate, N, T)
@@ -598,10 +628,12 @@ def gdn_mamba2_scan_backward(dy, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, p
     """Gradients of gdn_mamba2_scan for dy [T, H, d] in x's dtype (and dfinal, float32 [N, H, d, n], of the final
     states).  pool and slot_map give the states that the forward call started from, as they were before it."""
     torch = _torch()
-    T, N, dims, args = _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map)
+    copies = []
+    T, N, dims, args = _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, copies, stream)
     H, d, G, n = dims.num_heads, dims.headdim, dims.num_groups, dims.dstate
-    if tuple(dy.shape) != tuple(x.shape) or dy.dtype != x.dtype:
+    if dy.shape != x.shape or dy.dtype != x.dtype:
         raise ValueError(f"dy must be {x.dtype} of shape {tuple(x.shape)}, not {dy.dtype} {tuple(dy.shape)}")
+    pdy = _own_rows(dy, copies, stream)[0] if not dy.is_contiguous() and _one_row(dy) else _ptr(dy)
     _f32(dfinal, (N, H, d, n), "dfinal")
     new = lambda shape, t: torch.empty(shape, dtype=t, device=x.device)  # noqa: E731
     f32 = torch.float32
@@ -615,7 +647,7 @@ def gdn_mamba2_scan_backward(dy, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, p
             fresh.append(workspace)
     _keep_for_stream(fresh, stream)
     _check(lib().gdn_mamba2_scan_backward(
-        *args, _ptr(dy), _ptr(dfinal) if dfinal is not None else None, *(_ptr(t) for t in grads[:7]),
+        *args, pdy, _ptr(dfinal) if dfinal is not None else None, *(_ptr(t) for t in grads[:7]),
         _ptr(grads.dinit) if pool is not None else None, _ptr(workspace) if workspace is not None else None,
         workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
     return grads
@@ -632,22 +664,24 @@ class LayerNormGrads(NamedTuple):
 
 def _f32(t, shape, what):
     """A float32 parameter or statistic of the given shape, or None."""
-    if t is not None and (t.dtype != _torch().float32 or tuple(t.shape) != tuple(shape)):
+    if t is not None and (t.dtype != _torch().float32 or t.shape != shape):
         raise ValueError(f"{what} must be float32 of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
     return t
 
 
-def _rows(t, shape, dtype, what):
-    """(pointer, row stride) of a [rows, width] tensor whose rows may be apart."""
+def _rows(t, shape, dtype, what, copies=None, stream=None):
+    """(pointer, row stride) of a [rows, width] tensor whose rows may be apart; an expanded one is copied if `copies` are kept."""
     if t is None:
         return None, 0
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
     if t.is_contiguous():
         return t.data_ptr(), 0
+    if copies is not None and _one_row(t):
+        return _own_rows(t, copies, stream)
     if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{what}: the values of a row must be consecutive")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), _row_stride(t, what)
 
 
 def _norm_dims(x, groups, rms, gate, gate_after):
@@ -661,12 +695,12 @@ def gdn_layer_norm(x, weight, bias=None, gate=None, groups=1, eps=1e-5, rms=Fals
                    out_dtype=None, save_stats=False, stream=None):
     """Layer (or RMS) norm of the `groups` slices of every row of x [rows, width], with an optional SiLU gate of
     x's shape and dtype applied to x (or, gate_after, to the result); weight, bias float32 [width].  Rows may be
-    apart (x.stride(0)).  Returns y in out_dtype (x's by default), or (y, mean, rstd) with save_stats, float32
+    apart (x.stride(0); an expanded tensor is copied).  Returns y in out_dtype (x's by default), or (y, mean, rstd) with save_stats, float32
     [rows, groups] for gdn_layer_norm_backward."""
     torch = _torch()
     dims = _norm_dims(x, groups, rms, gate, gate_after)
     _f32(weight, x.shape[1:], "weight"), _f32(bias, x.shape[1:], "bias")
-    fresh = []
+    fresh, copies = [], []
     if out is None:
         out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
         fresh.append(out)
@@ -675,8 +709,8 @@ def gdn_layer_norm(x, weight, bias=None, gate=None, groups=1, eps=1e-5, rms=Fals
         mean, rstd = torch.empty((2, x.shape[0], groups), dtype=torch.float32, device=x.device)
         fresh += [mean, rstd]
     _keep_for_stream(fresh, stream)
-    _check(lib().gdn_layer_norm(ctypes.byref(dims), *_rows(x, x.shape, x.dtype, "x"),
-                                *_rows(gate, x.shape, x.dtype, "gate"), dtype_code(x.dtype), _ptr(weight),
+    _check(lib().gdn_layer_norm(ctypes.byref(dims), *_rows(x, x.shape, x.dtype, "x", copies, stream),
+                                *_rows(gate, x.shape, x.dtype, "gate", copies, stream), dtype_code(x.dtype), _ptr(weight),
                                 _ptr(bias) if bias is not None else None, float(eps),
                                 *_rows(out, x.shape, out.dtype, "out"), dtype_code(out.dtype),
                                 _ptr(mean) if save_stats else None, _ptr(rstd) if save_stats else None,
@@ -696,15 +730,15 @@ def gdn_layer_norm_backward(dy, x, weight, mean, rstd, bias=None, gate=None, gro
     dz = torch.empty(x.shape, dtype=x.dtype, device=x.device) if gate is not None else None
     dw = torch.empty(x.shape[1:], dtype=torch.float32, device=x.device)
     db = torch.empty_like(dw) if bias is not None else None
-    fresh = [dx, dz, dw, db]
+    fresh, copies = [dx, dz, dw, db], []
     need = int(lib().gdn_layer_norm_backward_workspace_bytes(ctypes.byref(dims)))
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
         fresh.append(workspace)
     _keep_for_stream(fresh, stream)
     _check(lib().gdn_layer_norm_backward(
-        ctypes.byref(dims), *_rows(dy, x.shape, x.dtype, "dy"), *_rows(x, x.shape, x.dtype, "x"),
-        *_rows(gate, x.shape, x.dtype, "gate"), dtype_code(x.dtype), _ptr(weight),
+        ctypes.byref(dims), *_rows(dy, x.shape, x.dtype, "dy", copies, stream), *_rows(x, x.shape, x.dtype, "x", copies, stream),
+        *_rows(gate, x.shape, x.dtype, "gate", copies, stream), dtype_code(x.dtype), _ptr(weight),
         _ptr(bias) if bias is not None else None, _ptr(mean), _ptr(rstd), *_rows(dx, x.shape, x.dtype, "dx"),
         *_rows(dz, x.shape, x.dtype, "dgate"), _ptr(dw), _ptr(db) if db is not None else None,
         _ptr(workspace) if workspace is not None else None,

@@ -26,7 +26,10 @@
 // Rounding (bf16 inputs and outputs): products of two inputs are exact in FP32.  The state
 // is FP32, and its updates multiply e^{..} dt' x in three bf16 terms, all its
 // 24 bits, with exact B.  For the output alone the state and the decay-weighted
-// products of read and write vectors are rounded to bf16 once, as y is.
+// products of read and write vectors are taken in two bf16 terms, off by 2^-16 of
+// each, where y's own rounding is 2^-8: 99.8% of y then is the exact value's
+// rounding, against half of it with one term.  (The prefill below takes 665 us
+// with two terms, 604 with one.)
 // Any other types take the FP32 MFMA throughout.
 //
 // Measured (bf16, heads of 64 x 128): prompts of 1024, 3000 and twice 8192
@@ -117,8 +120,8 @@ __global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
 }
 
 // ------------------------------------------------------------------ walk
-// Four waves over 128 state rows (two heads of 64) or 64, two workgroups on a compute
-// unit: one's vector work then runs beside the other's matrix work.  Eight
+// Four waves over 128 state rows (two heads of 64), two workgroups on a compute unit, or 64, three
+// (which the bound on registers keeps: 20 x 500 tokens x 32 heads 80 us with it, 91 without): one's vector work then runs beside the other's matrix work.  Eight
 // waves over 256 rows, one workgroup, share the read and write vectors of a
 // chunk among twice the heads but keep in step: a prefill of 20,408 tokens
 // through 128 heads took 789 us that way, 678 us this way.
@@ -135,8 +138,10 @@ struct WalkGeom {
   static constexpr int LDF = KB * 32 + (BF ? 8 : 4);   // read vectors [64][LDF], columns in accumulator order
   static constexpr int LDK = kScanChunk + (BF ? 0 : 4);  // write vectors [NN][LDK] (16-bit form: groups of 8 tokens permuted by the row)
   static constexpr int LDT = kScanChunk + (BF ? 8 : 4);  // inputs [ROWS][LDT], products [HB][64][LDT]
-  static constexpr int F0 = 0, K0 = F0 + (OUT ? kScanChunk * LDF : 0), X0 = K0 + NN * LDK, P0 = X0 + ROWS * LDT;
-  static constexpr int ELEMS = P0 + (OUT ? HB * kScanChunk * LDT : 0);
+  // the products' second bf16 terms lie over the read vectors
+  static constexpr int PE = HB * kScanChunk * LDT, FE = BF && PE > kScanChunk * LDF ? PE : kScanChunk * LDF;
+  static constexpr int F0 = 0, K0 = F0 + (OUT ? FE : 0), X0 = K0 + NN * LDK, P0 = X0 + ROWS * LDT;
+  static constexpr int ELEMS = P0 + (OUT ? PE : 0);
   // floats a head: c (two), dt', the input's weight, the read factor
   static constexpr size_t LDS = ((size_t)ELEMS * sizeof(E) + 15) / 16 * 16 + (size_t)HB * 5 * kScanChunk * 4;
   // vectors of 8 elements that a thread stages
@@ -158,7 +163,7 @@ __device__ __forceinline__ int kt_at(int n, int t) {
 }
 
 template <bool BF, int D, int NN, int PT, bool REV, bool OUT>
-__global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
+__global__ void __launch_bounds__(256, BF ? (D == 64 && PT == 1 ? 3 : 2) : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
   using W = WalkGeom<BF, D, NN, PT, OUT>;
   typedef typename W::E E;
   constexpr int HB = W::HB, NT = W::NT, KB = W::KB, LDF = W::LDF, LDT = W::LDT, ROWS = W::ROWS, Q = kScanChunk;
@@ -280,16 +285,16 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
   static_assert(256 % VPR == 0 && NN * 8 % 64 == 0, "whole rows of vectors");
   Frag<BF> vf[OUT ? W::FV : 1], vk[W::FV], vx[W::XV];
   float vg[3];
-  // the products of read and write vectors: the 16 x 16 tiles on and below the diagonal (above it in reverse) go round
-  // the head's waves; lane: row lane / 4, four columns
-  constexpr int PER = (10 + WPH - 1) / WPH;
+  // the products of read and write vectors: the 16 x 16 tiles on and below the diagonal (above it in reverse) and the two
+  // beyond it that share a 32-token operand with one on it go round the head's waves; lane: row lane / 4, four columns
+  constexpr int PER = 12 / WPH;
   f32x4 gm[OUT ? PER : 1];
   int rts[PER], cts[PER];
   const int sub = wave & (WPH - 1);
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
-    const int t = min(sub + k * WPH, 9);
-    const int i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t - i * (i + 1) / 2;
+    const int t = sub + k * WPH;
+    const int i = t >= 10 ? 2 * (t - 10) : t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t >= 10 ? i + 1 : t - i * (i + 1) / 2;
     rts[k] = REV ? j : i;
     cts[k] = REV ? i : j;
   }
@@ -401,13 +406,6 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
     }
   };
 
-  if constexpr (OUT)  // tiles beyond the diagonal that share a 32-token operand with one on it stay zero
-    for (int i = tid; i < HB * Q * 4; i += THREADS) {
-      const int r = i >> 2, tile = (r >> 4) & 3, c = REV ? (tile & 1 ? tile - 1 : 4) : (tile & 1 ? 4 : tile + 1);
-      if (c < 4)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s_p[r * LDT + 16 * c + 4 * (i & 3) + e] = (E)0;
-    }
   const int steps = c_hi - c_lo;
   if (steps > 0) {
     fetch(REV ? c_hi - 1 : c_lo);
@@ -423,7 +421,6 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
     const int c = REV ? c_hi - 1 - step : c_lo + step;
     const int64_t t0 = sg.begin + (int64_t)c * Q;
     const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
-    const int64_t cs = slot0 + c;
     // the lane's places are not known to be the ones of the chunk before: what follows from them is formed anew, in a few
     // instructions, where it would otherwise be kept in registers that the loop has not got
     asm volatile("" : "+v"(tid), "+v"(lane), "+v"(l16), "+v"(q));
@@ -465,7 +462,37 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
     __builtin_amdgcn_sched_barrier(0);
     fetch(c_next);
     __builtin_amdgcn_sched_barrier(0);
+    Frag<BF> xf[2][PT];  // the wave's inputs
     if constexpr (OUT) {
+      u32x2 low[BF ? PER : 1];  // the products' second terms
+      // above -128 a c without its low part is off by 2^-18 at most, and a decay by no more than the second terms are
+      const bool far = !BF || __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, gh_[Q - 1]))) < -128.f;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int r = 16 * rts[k] + (lane >> 2), c0 = 16 * cts[k] + 4 * (lane & 3);
+        f32x4 x = *reinterpret_cast<const f32x4*>(gh_ + c0) - gh_[r];  // c of the column less that of the row
+        if (far) x += *reinterpret_cast<const f32x4*>(gh_ + Q + c0) - gh_[Q + r];
+        f32x4 w = gm[k];
+        if constexpr (!REV) w *= *reinterpret_cast<const f32x4*>(gh_ + 2 * Q + c0);
+        E* d = s_p + (hl * Q + r) * LDT + c0;
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool on = REV ? c0 + e >= r : c0 + e <= r;
+          const float v = __builtin_amdgcn_exp2f(REV ? x[e] : -x[e]) * w[e];
+          f[e] = on ? v : 0.f;
+        }
+        if constexpr (BF) {
+          const u32x2 high = {pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
+          *reinterpret_cast<u32x2*>(d) = high;
+          bf16_rest(high[0], f[0], f[1]);
+          bf16_rest(high[1], f[2], f[3]);
+          low[k] = u32x2{pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
+        } else {
+          *reinterpret_cast<f32x4*>(d) = f32x4{f[0], f[1], f[2], f[3]};
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
       // the state's part of the output
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt)
@@ -473,7 +500,8 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
         for (int rt = 0; rt < 4; ++rt) acc[pt][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        Frag<BF> sf[PT];
+        typedef Split<BF, 2> Terms;
+        Terms sf[PT];
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
           float f[8];
@@ -482,37 +510,17 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
             f[e] = S[2 * kb][pt][e];
             f[4 + e] = 2 * kb + 1 < NT ? S[2 * kb + 1 < NT ? 2 * kb + 1 : 0][pt][e] : 0.f;
           }
-          sf[pt] = Frag<BF>::round(f);
+          sf[pt] = Terms::template of<true>(f);
         }
+        Frag<BF> ff[4];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const Frag<BF> ff = Frag<BF>::load(s_f + (16 * rt + l16) * LDF + 32 * kb + 8 * q);
+        for (int rt = 0; rt < 4; ++rt) ff[rt] = Frag<BF>::load(s_f + (16 * rt + l16) * LDF + 32 * kb + 8 * q);
 #pragma unroll
-          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], sf[pt], ff);
-        }
-      }
+        for (int k = Terms::K - 1; k >= 0; --k)
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        if (10 % WPH != 0 && sub + k * WPH >= 10) continue;
-        const int r = 16 * rts[k] + (lane >> 2), c0 = 16 * cts[k] + 4 * (lane & 3);
-        // (the low parts of c are below what is left of these products once they are bf16)
-        const float rh = gh_[r], rl = BF ? 0.f : gh_[Q + r];
-        const f32x4 ch = *reinterpret_cast<const f32x4*>(gh_ + c0);
-        f32x4 cl = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (!BF) cl = *reinterpret_cast<const f32x4*>(gh_ + Q + c0);
-        f32x4 w = gm[k];
-        if constexpr (!REV) w *= *reinterpret_cast<const f32x4*>(gh_ + 2 * Q + c0);
-        E* d = s_p + (hl * Q + r) * LDT + c0;
-        float f[4];
+          for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool on = REV ? c0 + e >= r : c0 + e <= r;
-          float x = REV ? ch[e] - rh : rh - ch[e];
-          if constexpr (!BF) x += REV ? cl[e] - rl : rl - cl[e];
-          f[e] = __builtin_amdgcn_exp2f(on ? x : -INFINITY) * w[e];
-        }
-        if constexpr (BF) *reinterpret_cast<u32x2*>(d) = u32x2{pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
-        else *reinterpret_cast<f32x4*>(d) = f32x4{f[0], f[1], f[2], f[3]};
+            for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], sf[pt].t[k], ff[rt]);
       }
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) {
@@ -524,19 +532,31 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
       __builtin_amdgcn_sched_barrier(0);
       fetch_products(c_next);
       __builtin_amdgcn_sched_barrier(0);
-      __syncthreads();  // the products are there
+      auto take_products = [&](const E* p) {
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        Frag<BF> xf[PT];
+        for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
-        for (int pt = 0; pt < PT; ++pt) xf[pt] = Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q));
+          for (int rt = 0; rt < 4; ++rt) {
+            if (REV ? (ks == 0 && rt >= 2) : (ks == 1 && rt < 2)) continue;  // all beyond the diagonal
+            const Frag<BF> pf = Frag<BF>::load(p + (hl * Q + 16 * rt + l16) * LDT + 32 * ks + 8 * q);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          if (REV ? (ks == 0 && rt >= 2) : (ks == 1 && rt < 2)) continue;  // all beyond the diagonal
-          const Frag<BF> pf = Frag<BF>::load(s_p + (hl * Q + 16 * rt + l16) * LDT + 32 * ks + 8 * q);
-#pragma unroll
-          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[pt], pf);
+            for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[ks][pt], pf);
+          }
         }
+      };
+      __syncthreads();  // the products are there, and the read vectors done with
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) xf[ks][pt] = Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q));
+      if constexpr (BF)
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+          *reinterpret_cast<u32x2*>(s_f + (hl * Q + 16 * rts[k] + (lane >> 2)) * LDT + 16 * cts[k] + 4 * (lane & 3)) = low[k];
+      take_products(s_p);
+      if constexpr (BF) {
+        __syncthreads();  // and their second terms
+        take_products(s_f);
       }
       if constexpr (BF) {
         const auto w = window(a.out, (t0 * a.H + h) * D + pd, 2, mine ? 2 * ((len - 1) * (a.H * D) + 16 * PT) : 0);
@@ -599,10 +619,11 @@ __global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2S
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt) {
         float f[8];
-        Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q)).widen(f);
+        if constexpr (OUT) xf[ks][pt].widen(f);
+        else Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q)).widen(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= gh_[3 * Q + 32 * ks + 8 * q + e];
-        xs[pt] = Split<BF>::of(f);
+        xs[pt] = Split<BF>::template of<true>(f);
       }
       // four tiles of n at a time, their terms apart: a product never follows the one it adds to
       constexpr int NG = NT < 4 ? NT : 4;

@@ -398,8 +398,8 @@ typedef struct {
  *               not read before it is written; calls that share one must not
  *               overlap
  * bf16 inputs with a bf16 y run on the bf16 matrix instructions (FP32 state
- * and sums; the state and the decay-weighted B C products are rounded to bf16
- * where they meet y, and only there); any other pair of types runs in FP32
+ * and sums; the state and the decay-weighted B C products meet y in two bf16
+ * terms, to 2^-16 of each, and dx is formed alike); any other pair of types runs in FP32
  * throughout.  Within 64 tokens a NaN or infinity also reaches earlier tokens
  * of its own sequence. */
 size_t gdn_mamba2_scan_workspace_bytes(const gdn_m2_dims* dims, int32_t N, int64_t total_tokens);

@@ -19,9 +19,10 @@
 //
 // dg's first sum is taken without differences of larger sums: tiles of 16 x 16
 // with a whole block of rows after t and of columns before t count whole, those
-// that share t's rows or columns by sums from the far side, and only inside
-// the diagonal tile row sums and column sums are subtracted.  Diagonal
-// elements do not enter.
+// that share t's rows or columns by sums from the far side, and inside the
+// diagonal tile each row's sum of the columns before t counts where the row is
+// not.  So where a step clears the state its dg is as small as the decay, and
+// what stands behind it leaves nothing there.  Diagonal elements do not enter.
 //
 // A decay multiplies last and is the square of a root that the hardware's
 // exponential does not flush, so that one close to the smallest numbers costs
@@ -52,7 +53,7 @@ struct GradGeom {
   static constexpr bool N_LDS = BF;               // the heads' summed products too
   static constexpr bool LATE = BF && D < 128;     // a head's sums are closed while the next head is under way
   static constexpr int XV = T * DK / 8 / 512;     // vectors of 8 elements of x (and of dy) that a thread stages
-  // a head's results: column sums [8][128], row sums in two parts, the diagonal tiles' row and column sums, the diagonal, the state
+  // a head's results: column sums [8][128], row sums in two parts, the diagonal tiles' part of dg and column sums, the diagonal, the state
   // parts [NT][128] twice, the waves' parts of <S, dS'> and of sum dy.x
   static constexpr int RES = (8 + 5 + 2 * NT) * T + 16;
   // a head's gates: c / 2 (two), e^{c_i}, dt' e^{c_last - c_j}, dt', exp(A_log), e^{c_last}; of the head under way, the one
@@ -377,8 +378,8 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
         }
         for (int i = b + 1; i < tiles; ++i) co[k] += r_col[i * T + t];
       }
-      // inside the block: earlier columns of later rows, later rows of earlier columns, and the diagonal tile
-      const float r0 = in ? r_row[t] + (r_rd[t] - r_cd[t]) + (W::N_LDS && b > 4 ? r_help[t] : 0.f) : 0.f;
+      // inside the block: earlier columns of later rows, and later rows of earlier columns
+      const float r0 = in ? r_row[t] + (W::N_LDS && b > 4 ? r_help[t] : 0.f) : 0.f;
       pre[k] = row_shift<0x111>(row_prefix(co[k]));  // before t, not at it
       suf[k] = row_suffix(r0);
       cs_suf[k] = row_suffix(cs);
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
       const int t = 64 * k + lane;
       const float wh = __shfl(whole, 8 * (4 * k + q), 64);
       if (t < len) {
-        const float dg = ((wh + pre[k]) + suf[k]) + eq;
+        const float dg = ((wh + pre[k]) + (suf[k] + r_rd[t])) + eq;
         // dt' x_t.X_t over dt'; a step that underflows to zero has a slope of zero with it
         const float own = dtp[k] > 0.f ? ((co[k] + r_cd[t]) + (r_dg[t] + cv[k])) / dtp[k] : 0.f;
         const float d = (own - A * dg) * -expm1f(-dtp[k]);  // softplus' = sigmoid = 1 - e^-softplus
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
         const f32x4 w = product(j);
         const float jh = s_ch[j], jl = s_cl[j], dtj = s_dt[j];
         f32x4 off;
-        float diag = 0.f, wd = 0.f, cd = 0.f;
+        float diag = 0.f, wd = 0.f, cd = 0.f, dg = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float e = dtj * decay_half(j <= i0 + r ? (ih[r] - jh) + (il[r] - jl) : -INFINITY), m = e * (w[r] * gt[r]);
@@ -578,10 +579,13 @@ __global__ void __launch_bounds__(512, 2) gdn_m2s_grad_kernel(const M2GradArgs a
           off[r] = j == i0 + r ? 0.f : m;
           cd += off[r];
         }
-        const float rd = row16_sum4(off[0], off[1], off[2], off[3]);
-        const float z = rows_sum4(cd, diag, wd, 0.f);  // the rows of 16 lanes get the three sums over the tile's rows
-        if (l16 < 4) r_rd[i0 + l16] = rd;
-        if (q < 2) (q == 0 ? r_cd : r_dg)[j] = z;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {  // the columns before j, of j's row and later ones
+          const float before = row_prefix(row_shift<0x111>(off[r]));
+          dg += j <= i0 + r ? before : 0.f;
+        }
+        const float z = rows_sum4(cd, diag, wd, dg);  // the rows of 16 lanes get the four sums over the tile's rows
+        if (q != 2) (q == 0 ? r_cd : q == 1 ? r_dg : r_rd)[j] = z;
         const float dd = row16_sum(z);
         if (lane == 32) r_dd[it] = dd;
       };

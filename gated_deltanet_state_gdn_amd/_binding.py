@@ -513,6 +513,18 @@ class M2ScanGrads(NamedTuple):
     dinit: object  # [N, H, d, n], or None without a pool
 
 
+def _on_gpu(stream, x, *others):
+    """The stream's handle for a launch, once all its tensors are known to lie on x's GPU (others may be None): the library
+    takes their addresses as they are."""
+    gpu = x.get_device()
+    if gpu < 0:
+        raise ValueError(f"tensors must lie on a GPU, not on {x.device}")
+    for t in others:
+        if t is not None and t.get_device() != gpu:
+            raise ValueError(f"all tensors must lie on {x.device}, not on {t.device}")
+    return _stream(stream)
+
+
 def _one_row(t):
     """Whether a tensor's rows are all one row: an expanded tensor, such as autograd's gradient behind a sum over rows.  (The
     library takes a stride of 0 for dense rows.)"""
@@ -619,7 +631,8 @@ def gdn_mamba2_scan(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool=None, slo
             fresh.append(workspace)
     _keep_for_stream(fresh, stream)
     _check(lib().gdn_mamba2_scan(*args, _ptr(out), dtype_code(out.dtype), _ptr(workspace) if workspace is not None else None,
-                                 workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+                                 workspace.nbytes if workspace is not None else 0,
+                                 _on_gpu(stream, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, out, workspace)))
     return out
 
 
@@ -649,7 +662,8 @@ def gdn_mamba2_scan_backward(dy, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, p
     _check(lib().gdn_mamba2_scan_backward(
         *args, pdy, _ptr(dfinal) if dfinal is not None else None, *(_ptr(t) for t in grads[:7]),
         _ptr(grads.dinit) if pool is not None else None, _ptr(workspace) if workspace is not None else None,
-        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+        workspace.nbytes if workspace is not None else 0,
+        _on_gpu(stream, x, dy, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, dfinal, workspace)))
     return grads
 
 
@@ -714,7 +728,7 @@ def gdn_layer_norm(x, weight, bias=None, gate=None, groups=1, eps=1e-5, rms=Fals
                                 _ptr(bias) if bias is not None else None, float(eps),
                                 *_rows(out, x.shape, out.dtype, "out"), dtype_code(out.dtype),
                                 _ptr(mean) if save_stats else None, _ptr(rstd) if save_stats else None,
-                                _stream(stream)))
+                                _on_gpu(stream, x, gate, weight, bias, out)))
     return (out, mean, rstd) if save_stats else out
 
 
@@ -742,5 +756,5 @@ def gdn_layer_norm_backward(dy, x, weight, mean, rstd, bias=None, gate=None, gro
         _ptr(bias) if bias is not None else None, _ptr(mean), _ptr(rstd), *_rows(dx, x.shape, x.dtype, "dx"),
         *_rows(dz, x.shape, x.dtype, "dgate"), _ptr(dw), _ptr(db) if db is not None else None,
         _ptr(workspace) if workspace is not None else None,
-        workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+        workspace.nbytes if workspace is not None else 0, _on_gpu(stream, x, dy, gate, weight, bias, mean, rstd, workspace)))
     return LayerNormGrads(dx, dw, db, dz)

@@ -5,6 +5,7 @@
 // is kept between calls except the calling thread's last-error text.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -765,7 +766,7 @@ ScanWs scan_ws(const gdn_m2_dims* d, int32_t N, int64_t total, bool backward) {
 // A block's 128 tokens are reached by 32-bit byte offsets.
 constexpr int64_t kMaxTokenStride = 1 << 22;
 
-gdn_status check_scan_sizes(const gdn_m2_dims* d, int32_t N, int64_t total) {
+gdn_status check_scan_sizes(const gdn_m2_dims* d, int32_t N, int64_t total, bool backward) {
   GDN_TRY(check_m2_dims(d));
   GDN_REQUIRE(N >= 0 && total >= 0, GDN_EINVAL, "N=%d and total_tokens=%lld must be >= 0", N, (long long)total);
   GDN_REQUIRE(total <= INT32_MAX, GDN_EINVAL, "total_tokens=%lld exceeds the 32-bit cu_seqlens", (long long)total);
@@ -775,6 +776,10 @@ gdn_status check_scan_sizes(const gdn_m2_dims* d, int32_t N, int64_t total) {
               GDN_EUNSUPPORTED, "H d and G n must be at most 2^22");
   GDN_REQUIRE(gdn::scan_slots(N, total, 64) * d->num_heads <= INT32_MAX, GDN_EUNSUPPORTED,
               "64-token chunks x heads exceed the grid limit");
+  const int64_t items = total == 0 ? 0 : std::max(gdn::scan_work_items(N, total, d->num_heads, d->num_groups, d->headdim),
+                                                  backward ? gdn::grad_work_items(N, total, d->num_heads, d->num_groups) : 0);
+  GDN_REQUIRE(items <= UINT32_MAX, GDN_EUNSUPPORTED,
+              "N=%d and total_tokens=%lld make a launch of %lld threads: at most 2^32 - 1 are supported", N, (long long)total, (long long)items);
   return GDN_OK;
 }
 
@@ -857,7 +862,7 @@ gdn::M2ScanArgs scan_args(const gdn_m2_dims* d, int32_t N, const int32_t* cu, in
 }  // namespace
 
 size_t gdn_mamba2_scan_workspace_bytes(const gdn_m2_dims* dims, int32_t N, int64_t total_tokens) {
-  if (check_scan_sizes(dims, N, total_tokens) != GDN_OK || N == 0) return 0;
+  if (check_scan_sizes(dims, N, total_tokens, false) != GDN_OK || N == 0) return 0;
   return scan_ws(dims, N, total_tokens, false).bytes;
 }
 
@@ -866,7 +871,7 @@ gdn_status gdn_mamba2_scan(const gdn_m2_dims* dims, int32_t N, const int32_t* cu
                            const gdn_m2_strides* strides, const gdn_m2_params* params, const gdn_pool* state,
                            const int32_t* slot_map, void* y, gdn_dtype out_dtype, void* workspace,
                            size_t workspace_bytes, void* stream) {
-  GDN_TRY(check_scan_sizes(dims, N, total_tokens));
+  GDN_TRY(check_scan_sizes(dims, N, total_tokens, false));
   GDN_TRY(check_dtypes(in_dtype, out_dtype));
   if (N == 0 || total_tokens == 0) return ok();  // nothing is read or written
   GDN_TRY(check_scan_io(dims, cu_seqlens, total_tokens, x, Bm, Cm, in_dtype, strides, params, state, slot_map));
@@ -886,7 +891,7 @@ gdn_status gdn_mamba2_scan(const gdn_m2_dims* dims, int32_t N, const int32_t* cu
 }
 
 size_t gdn_mamba2_scan_backward_workspace_bytes(const gdn_m2_dims* dims, int32_t N, int64_t total_tokens) {
-  if (check_scan_sizes(dims, N, total_tokens) != GDN_OK || N == 0) return 0;
+  if (check_scan_sizes(dims, N, total_tokens, true) != GDN_OK || N == 0) return 0;
   return scan_ws(dims, N, total_tokens, true).bytes;
 }
 
@@ -896,7 +901,7 @@ gdn_status gdn_mamba2_scan_backward(const gdn_m2_dims* dims, int32_t N, const in
                                     const int32_t* slot_map, const void* dy, const float* dfinal, void* dx, void* dBm,
                                     void* dCm, void* ddt, float* dA_log, float* ddt_bias, float* dD, float* dinit,
                                     void* workspace, size_t workspace_bytes, void* stream) {
-  GDN_TRY(check_scan_sizes(dims, N, total_tokens));
+  GDN_TRY(check_scan_sizes(dims, N, total_tokens, true));
   GDN_TRY(check_dtypes(in_dtype, in_dtype));
   GDN_REQUIRE(dA_log && ddt_bias && dD && aligned(dA_log, 4) && aligned(ddt_bias, 4) && aligned(dD, 4), GDN_EINVAL,
               "a head parameter's gradient is NULL or misaligned");

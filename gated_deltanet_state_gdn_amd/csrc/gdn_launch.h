@@ -210,6 +210,9 @@ struct ScanPlan {
   int seg_chunks, whole, narrow;
 };
 ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d);
+// Threads along x of the largest launch of a scan, and of the gradient kernel; a launch takes fewer than 2^32.
+int64_t scan_work_items(int64_t N, int64_t total, int H, int G, int d);
+int64_t grad_work_items(int64_t N, int64_t total, int H, int G);
 hipError_t launch_scan_prep(const M2ScanArgs& a, bool bf, int n, hipStream_t s);
 hipError_t launch_scan_walk(M2ScanArgs a, bool bf, int d, int n, bool rev, bool out, hipStream_t s);
 int grad_splits(int64_t N, int64_t total, int H, int G);

@@ -780,6 +780,10 @@ int grad_splits(int64_t N, int64_t total, int H, int G) {
   return s < 1 ? 1 : (int)s;
 }
 
+int64_t grad_work_items(int64_t N, int64_t total, int H, int G) {
+  return scan_slots(N, total, kGradBlock) * G * grad_splits(N, total, H, G) * 512;
+}
+
 hipError_t launch_scan_grad(const M2GradArgs& a, bool bf, int d, int n, hipStream_t s) {
   const int64_t slots = scan_slots(a.N, a.total, kGradBlock);
   if (a.total > 0) {

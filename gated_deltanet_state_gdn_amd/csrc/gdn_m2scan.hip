@@ -36,6 +36,8 @@
 // tokens through 128 heads 608 us (prep 51, walk 557), 1.3 TB/s of what has to
 // move: the chain of 128 chunks, 4.4 us each, is what bounds it.  Matrix units are
 // busy 13% of the time.  16,384 tokens, states only, 222 us; in reverse with dx 428.
+#include <algorithm>
+
 #include "gdn_m2scan.h"
 
 namespace gdn {
@@ -771,6 +773,13 @@ ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d) {
     p.seg_chunks = per < 4 ? 4 : (int)per;
   }
   return p;
+}
+
+int64_t scan_work_items(int64_t N, int64_t total, int H, int G, int d) {
+  const ScanPlan p = scan_plan(N, total, H, G, d);
+  const int heads = p.narrow ? 1 : (d == 16 ? 64 : 128) / d;  // a workgroup's
+  const int64_t slots = p.seg_chunks > 0 ? scan_slots(N, total, (int64_t)p.seg_chunks * kScanChunk) : N;
+  return std::max(scan_slots(N, total, kScanChunk), slots * G * ((H / G + heads - 1) / heads)) * 256;
 }
 
 hipError_t launch_scan_prep(const M2ScanArgs& a, bool bf, int n, hipStream_t s) {

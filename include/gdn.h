@@ -401,7 +401,9 @@ typedef struct {
  * and sums; the state and the decay-weighted B C products meet y in two bf16
  * terms, to 2^-16 of each, and dx is formed alike); any other pair of types runs in FP32
  * throughout.  Within 64 tokens a NaN or infinity also reaches earlier tokens
- * of its own sequence. */
+ * of its own sequence.  Sizes at which a launch would have 2^32 threads (some
+ * 10^7 sequences x workgroups of heads) are refused with GDN_EUNSUPPORTED, in
+ * the size queries by 0. */
 size_t gdn_mamba2_scan_workspace_bytes(const gdn_m2_dims* dims, int32_t N, int64_t total_tokens);
 gdn_status gdn_mamba2_scan(const gdn_m2_dims* dims, int32_t N, const int32_t* cu_seqlens,
                            int64_t total_tokens, const void* x, const void* Bm, const void* Cm,

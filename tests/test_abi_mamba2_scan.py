@@ -133,3 +133,29 @@ def test_binding_refuses_shapes_and_types():
     for bad in (dict(dy=z(T, H, d + 1)), dict(dy=z(T, H, d).bfloat16()), dict(dfinal=z(N, H, d, n).bfloat16()), dict(dfinal=z(N + 1, H, d, n))):
         with pytest.raises(ValueError):
             gdn.gdn_mamba2_scan_backward(**dict(good, **dict(dict(dy=z(T, H, d)), **bad)))
+
+
+# Sizes at which a kernel's launch would have 2^32 threads: (N, T, dims, forward is refused, backward is refused).
+LAUNCHES = [
+    (300_000, 300_000, dict(H=128, G=8), True, True),                   # walks of two heads
+    (1 << 24, 1 << 24, dict(H=1, G=1), True, True),                     # chunks, one token each
+    ((1 << 24) - 1, 64, dict(H=1, G=1), True, True),
+    (1 << 23, 64, dict(H=1, G=1), False, True),                         # the gradient kernel has 512 threads a workgroup
+    (70_000, 70_000, dict(H=128, G=8), False, False),
+    (1_100_000, 1_100_000, dict(H=8, G=8, d=16, n=16), False, True),
+    (1_100_000, 1_100_000, dict(H=16, G=16, d=16, n=16), True, True),
+    ((1 << 31) - 1, 0, dict(H=1, G=1), False, None),                    # no token: nothing to launch
+]
+
+
+@pytest.mark.parametrize("N,T,dims,fwd,bwd", LAUNCHES)
+def test_launches_past_2_32_threads(L, N, T, dims, fwd, bwd):
+    q = ctypes.byref(bd.gdn_m2_dims(*dict(DIMS, **dims).values()))
+    for refused, size, call in ((fwd, L.gdn_mamba2_scan_workspace_bytes, _fwd), (bwd, L.gdn_mamba2_scan_backward_workspace_bytes, _bwd)):
+        if refused is None:
+            continue
+        assert (size(q, N, T) == 0) == refused
+        # without a workspace nothing is launched either way; only the reason differs
+        st = call(L, N=N, T=T, dims=dims, ws=None)
+        assert st == (gdn.GDN_EUNSUPPORTED if refused else gdn.GDN_OK if T == 0 else gdn.GDN_EINVAL), gdn.gdn_last_error()
+        assert not refused or "threads" in gdn.gdn_last_error()

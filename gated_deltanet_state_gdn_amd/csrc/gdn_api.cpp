@@ -677,8 +677,19 @@ gdn_status gdn_layer_norm(const gdn_norm_dims* dims, const void* x, int64_t x_st
   return launched(gdn::launch_norm(a, static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+
+gdn_status check_norm_bwd_dims(const gdn_norm_dims* d) {
+  GDN_TRY(check_norm_dims(d));
+  GDN_REQUIRE(gdn::norm_sum_work_items(d->width) <= UINT32_MAX, GDN_EUNSUPPORTED,
+              "width=%d: at most 67108848 is supported backward", d->width);
+  return GDN_OK;
+}
+
+}  // namespace
+
 size_t gdn_layer_norm_backward_workspace_bytes(const gdn_norm_dims* dims) {
-  if (check_norm_dims(dims) != GDN_OK) return 0;
+  if (check_norm_bwd_dims(dims) != GDN_OK) return 0;
   return (size_t)gdn::norm_bwd_blocks(dims->rows, dims->width, dims->groups) * 2 * (size_t)dims->width * sizeof(float);
 }
 
@@ -687,7 +698,7 @@ gdn_status gdn_layer_norm_backward(const gdn_norm_dims* dims, const void* dy, in
                                    const float* w, const float* b, const float* mean, const float* rstd, void* dx,
                                    int64_t dx_stride, void* dz, int64_t dz_stride, float* dw, float* db,
                                    void* workspace, size_t workspace_bytes, void* stream) {
-  GDN_TRY(check_norm_dims(dims));
+  GDN_TRY(check_norm_bwd_dims(dims));
   GDN_TRY(check_dtypes(in_dtype, in_dtype));
   GDN_REQUIRE(dw != nullptr && aligned(dw, 4) && aligned(db, 4), GDN_EINVAL, "dw is NULL, or dw or db misaligned");
   if (dims->rows > 0) {

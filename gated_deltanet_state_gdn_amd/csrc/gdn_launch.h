@@ -221,6 +221,7 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
 bool norm_slice_fits(int n);
 int norm_bwd_blocks(int64_t rows, int N, int groups);
+int64_t norm_sum_work_items(int N);  // threads of the kernel that adds dw and db: fewer than 2^32
 size_t m2_lds_bytes(int P, int N, int L, int T, int heads_per_group);
 
 // Dynamic LDS of the speculative-decode kernel; launches need <= kSpecMaxLds.

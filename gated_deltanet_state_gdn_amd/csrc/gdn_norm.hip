@@ -502,6 +502,8 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+int64_t norm_sum_work_items(int N) { return (2 * (int64_t)N + 31) / 32 * 1024; }
+
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
   const NormGeom q = norm_geom(a.N / a.groups);
   const int blocks = norm_bwd_blocks(a.rows, a.N, a.groups);
@@ -511,7 +513,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  gdn_norm_sum_kernel<<<(2 * a.N + 31) / 32, 1024, 0, s>>>(a.part, blocks, a.N, a.dw, a.db);
+  gdn_norm_sum_kernel<<<(unsigned)(norm_sum_work_items(a.N) / 1024), 1024, 0, s>>>(a.part, blocks, a.N, a.dw, a.db);
   return hipGetLastError();
 }
 

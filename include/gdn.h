@@ -446,7 +446,7 @@ gdn_status gdn_mamba2_scan_backward(const gdn_m2_dims* dims, int32_t N, const in
  * FP32 math and sums.  Rows of x, z, y, dy, dx and dz may be apart by any
  * stride (in elements, >= width; 0 stands for width), the values of a row are
  * consecutive, and any element alignment is accepted.  n <= 16384, else
- * GDN_EUNSUPPORTED; groups <= 65535. */
+ * GDN_EUNSUPPORTED; groups <= 65535; backward, width <= 67108848. */
 typedef enum { GDN_GATE_NONE = 0, GDN_GATE_BEFORE = 1, GDN_GATE_AFTER = 2 } gdn_norm_gate;
 
 typedef struct {

@@ -104,3 +104,12 @@ def test_binding_refuses_shapes_and_layouts():
                  lambda: gdn.gdn_layer_norm_backward(x.bfloat16(), x, w, x[:, :1], x[:, :1])):
         with pytest.raises((ValueError, gdn.GdnError)):
             call()
+
+
+@pytest.mark.parametrize("width,groups,fits", [(16 * 3 * 23 * 89 * 683, 16 * 3 * 89, True), (1 << 26, 4096, False), (65535 * 16384, 65535, False)])
+def test_backward_width_past_a_launch(L, width, groups, fits):
+    """The kernel that adds dw and db has 64 threads a column: widths at which they pass 2^32 are refused before any launch."""
+    dims = bd.gdn_norm_dims(2, width, groups, 0, 0)
+    assert (L.gdn_layer_norm_backward_workspace_bytes(ctypes.byref(dims)) > 0) == fits
+    assert _bwd(L, rows=2, width=width, groups=groups, ws=None, wsb=0) == (gdn.GDN_EINVAL if fits else gdn.GDN_EUNSUPPORTED)
+    assert _fwd(L, rows=2, width=width, groups=groups, y=None) == gdn.GDN_EINVAL  # the forward pass takes any width

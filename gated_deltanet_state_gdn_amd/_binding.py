@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import warnings
 from dataclasses import dataclass
 from typing import NamedTuple
 
@@ -525,6 +526,16 @@ def _on_gpu(stream, x, *others):
     return _stream(stream)
 
 
+def _says_no_graph(name, *inputs):
+    """Warns where autograd would be expected to record the call, which it cannot."""
+    if _torch().is_grad_enabled():
+        for t in inputs:
+            if t is not None and t.requires_grad:
+                warnings.warn(f"{name} records no gradients: its result has no graph, although an input requires grad.  Call it in a "
+                              f"torch.autograd.Function with {name}_backward, or under torch.no_grad()", stacklevel=3)
+                return
+
+
 def _one_row(t):
     """Whether a tensor's rows are all one row: an expanded tensor, such as autograd's gradient behind a sum over rows.  (The
     library takes a stride of 0 for dense rows.)"""
@@ -614,8 +625,10 @@ def gdn_mamba2_scan(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool=None, slo
     """The Mamba2 recurrence over packed sequences: x [T, H, d]; Bm, Cm [T, G, n]; dt [T, H]; cu_seqlens int32
     [N+1] (device).  Tokens may be apart (slices of wider rows; an expanded tensor is copied).  With a pool [slots, H, d, n] and slot_map int32
     [N], sequence s goes on from slot slot_map[s] and leaves its final state there; without, from zero states.
-    Returns y [T, H, d] in out_dtype (x's by default)."""
+    Returns y [T, H, d] in out_dtype (x's by default).  Autograd does not record it: gradients come from
+    gdn_mamba2_scan_backward."""
     torch = _torch()
+    _says_no_graph("gdn_mamba2_scan", x, Bm, Cm, dt, A_log, dt_bias, D, pool)
     copies = []
     T, N, dims, args = _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, copies, stream)
     fresh = []
@@ -710,8 +723,9 @@ def gdn_layer_norm(x, weight, bias=None, gate=None, groups=1, eps=1e-5, rms=Fals
     """Layer (or RMS) norm of the `groups` slices of every row of x [rows, width], with an optional SiLU gate of
     x's shape and dtype applied to x (or, gate_after, to the result); weight, bias float32 [width].  Rows may be
     apart (x.stride(0); an expanded tensor is copied).  Returns y in out_dtype (x's by default), or (y, mean, rstd) with save_stats, float32
-    [rows, groups] for gdn_layer_norm_backward."""
+    [rows, groups] for gdn_layer_norm_backward.  Autograd does not record it: gradients come from that call."""
     torch = _torch()
+    _says_no_graph("gdn_layer_norm", x, weight, bias, gate)
     dims = _norm_dims(x, groups, rms, gate, gate_after)
     _f32(weight, x.shape[1:], "weight"), _f32(bias, x.shape[1:], "bias")
     fresh, copies = [], []

@@ -75,3 +75,36 @@ def test_block_serves():
         out.append(b.decode(x[t:t + 1], states, slot))
     close("y", torch.cat(out), want)
     assert not states[0].any() and not states[2].any()
+
+
+# In bf16, the block's own type, sums are FP32 and each of the ten stages rounds what it hands on by at most 2^-8 of it, with the
+# same 3 for the factors between them; a head's sums over tokens of either sign (A_log, dt_bias, D) keep a third or less of what
+# they add.
+TOL_BF16 = 10 * 3 * 2.0 ** -8
+
+
+def test_block_in_bf16():
+    torch.manual_seed(8)
+    b = Mamba2Block(64, heads=4, headdim=16, groups=2, dstate=64)
+    p = {k: v.detach().double().cpu().requires_grad_() for k, v in b.named_parameters()}
+    cu = [0, 70, 71, 71, 140]
+    x = torch.randn(140, 64, device="cuda").bfloat16().requires_grad_()
+    dy = torch.randn(140, 64, device="cuda").bfloat16()
+    x64 = x.detach().double().cpu().requires_grad_()
+    y = b(x, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    y.backward(dy)
+    want = reference(p, b, x64, cu)
+    want.backward(dy.double().cpu())
+    grads = [("y", y.detach(), want.detach()), ("dx", x.grad, x64.grad)] + [(k, v.grad, p[k].grad) for k, v in b.named_parameters()]
+    for name, got, ref in grads:
+        err = ((got.double().cpu() - ref).norm() / ref.norm()).item()
+        print(f"{name}: {err:.2e}", flush=True)
+        assert err <= TOL_BF16 * (3 if name in ("A_log", "dt_bias", "D") else 1), name
+    # serving: a prompt, then single tokens
+    states, slot = b.new_states(3), torch.tensor([1], dtype=torch.int32, device="cuda")
+    x = x.detach()
+    out = [b.prefill(x[:70], torch.tensor([0, 70], dtype=torch.int32, device="cuda"), states, slot)]
+    out += [b.decode(x[t:t + 1], states, slot) for t in range(70, 75)]
+    want = reference(p, b, x64[:75], [0, 75]).detach()
+    err = ((torch.cat(out).double().cpu() - want).norm() / want.norm()).item()
+    assert err <= TOL_BF16

@@ -180,7 +180,10 @@ __global__ void __launch_bounds__(256, BF ? (D == 64 && PT == 1 ? 3 : 2) : 1) gd
   int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hpg = a.H / a.G, hbs = (hpg + HB - 1) / HB;
-  const int u = xcd_unit(blockIdx.x, gridDim.x);
+  // Whole sequences: each XCD takes a run of them, so that a chunk's heads share its L2.  Segments: round the XCDs, as the
+  // slots behind a sequence that is not cut have no work, and runs of them would leave some XCDs with half the others' (10
+  // x 500 to 1000 tokens x 64 heads 117 us round, 151 in runs; equal lengths, 20 x 500 x 32 heads, 82 and 80).
+  const int u = a.seg_chunks > 0 ? blockIdx.x : xcd_unit(blockIdx.x, gridDim.x);
   const int slot = u / (a.G * hbs), gh = u - slot * (a.G * hbs), g = gh / hbs, hb = gh - g * hbs;
   Piece sg;
   if (a.seg_chunks > 0) {
@@ -467,13 +470,11 @@ __global__ void __launch_bounds__(256, BF ? (D == 64 && PT == 1 ? 3 : 2) : 1) gd
     Frag<BF> xf[2][PT];  // the wave's inputs
     if constexpr (OUT) {
       u32x2 low[BF ? PER : 1];  // the products' second terms
-      // above -128 a c without its low part is off by 2^-18 at most, and a decay by no more than the second terms are
-      const bool far = !BF || __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, gh_[Q - 1]))) < -128.f;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
         const int r = 16 * rts[k] + (lane >> 2), c0 = 16 * cts[k] + 4 * (lane & 3);
-        f32x4 x = *reinterpret_cast<const f32x4*>(gh_ + c0) - gh_[r];  // c of the column less that of the row
-        if (far) x += *reinterpret_cast<const f32x4*>(gh_ + Q + c0) - gh_[Q + r];
+        // c of the column less that of the row
+        const f32x4 x = (*reinterpret_cast<const f32x4*>(gh_ + c0) - gh_[r]) + (*reinterpret_cast<const f32x4*>(gh_ + Q + c0) - gh_[Q + r]);
         f32x4 w = gm[k];
         if constexpr (!REV) w *= *reinterpret_cast<const f32x4*>(gh_ + 2 * Q + c0);
         E* d = s_p + (hl * Q + r) * LDT + c0;
@@ -746,19 +747,23 @@ hipError_t prep(const M2ScanArgs& a, int n, hipStream_t s) {
 // sequences unless a number of chunks is given):
 //  - Waves of 16 state rows, a head a workgroup, where the waves of 32 would be
 //    fewer than two workgroups a compute unit: four prompts (20,408 tokens) x
-//    128 heads 604 narrow, 722 wide; 32 x 1024 tokens x 128 heads 670 and 609.
+//    128 heads 665 narrow, 767 wide; 32 x 1024 tokens x 128 heads 713 and 685.
 //  - Segments only where there are few walks, as they cost a second walk and the
 //    states' way through memory: backward of 4 x 4096 tokens x 128 heads (512
-//    walks) 1386 whole, 1847 in segments of 14; of 16,385 tokens x 32 heads (32
-//    walks) 1616 whole, 559 in segments of 12, 608 of 8.  Their length leaves
-//    704 workgroups, close to three a compute unit.
-//    Walks enough but of little work (3 to 12 chunks a workgroup of the 704,
-//    sequences that average a chunk or more: N within a grid's third bound) are
-//    likely to be ragged, and then the longest sequence decides: sequences of
-//    more than two segments are cut, and batches of equal lengths have none.  20
-//    sequences of 0 to 1500 tokens x 32 heads 91 whole, 75 cut; 12 of 1 to 3000 x
-//    64 heads 211 and 143; where nothing is cut the two launches cost 8 (20 of
-//    245 tokens 42 and 50, 20 of 500 65 and 73).
+//    walks) 1415 whole, 1910 in segments of 58; the four prompts 665 and 917; of
+//    16,385 tokens x 32 heads (32 walks) 1745 whole, 558 in segments of 12.
+//    Their length leaves 704 workgroups, close to three a compute unit.
+//    Walks enough for that, but not for two workgroups of 128 rows a compute
+//    unit, and of little work (3 to 12 chunks a workgroup of the 704, sequences
+//    that average a chunk or more): if they are ragged, the longest sequence
+//    decides, so sequences of more than two segments are cut.  The lengths lie
+//    on the device.  Whole and cut: 20 sequences of 0 to 1500 tokens x 32 heads
+//    106 and 75; 12 of 1 to 3000 x 64 heads 244 and 114; 8 of 1 to 6000 x 32
+//    heads 310 and 142; 30 of 1 to 4000 x 32 heads 202 and 208.  Where nothing
+//    is cut the two launches more cost 5 to 11: 10 of 500 to 1000 x 64 heads 112
+//    and 117, 20 of 245 x 32 heads 45 and 55, 20 of 500 71 and 82.  With more
+//    walks: 24 of 0 to 800 x 48 heads 164 and 200, 16 of 100 to 1500 x 64 heads
+//    213 and 226, so those stay whole.
 ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d) {
   const int hpg = H / G, wide_heads = (d == 16 ? 64 : 128) / d;
   const int64_t chunks = (total + kScanChunk - 1) / kScanChunk, wide = (int64_t)G * ((hpg + wide_heads - 1) / wide_heads);
@@ -768,7 +773,7 @@ ScanPlan scan_plan(int64_t N, int64_t total, int H, int G, int d) {
   p.seg_chunks = 0;
   const bool few = N * walks < 384;
   p.whole = few ? 1 : 2;
-  if (chunks > 8 && (few || (N <= chunks && chunks * walks >= 3 * 704 && chunks * walks <= 12 * 704))) {
+  if (chunks > 8 && (few || (N * wide < 512 && N <= chunks && chunks * walks >= 3 * 704 && chunks * walks <= 12 * 704))) {
     const int64_t per = (chunks * walks / 704 + 1) / 2 * 2;
     p.seg_chunks = per < 4 ? 4 : (int)per;
   }

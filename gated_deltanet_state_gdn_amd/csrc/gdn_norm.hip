@@ -497,7 +497,10 @@ int norm_bwd_blocks(int64_t rows, int N, int groups) {
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   const NormGeom q = norm_geom(a.N / a.groups);
-  const dim3 grid((unsigned)row_blocks(a.rows, q.lpu, a.groups, q.lpu == 128 ? 4096 : 2048), (unsigned)a.groups);
+  // workgroups over all groups: 20,408 rows of 8 slices of 1024 with a gate take 201 us with 2048 and 223 with 4096, 10,000
+  // rows of 8192 85 and 89; 4096 is the better for 40,000 rows of 512 (16.1 and 14.7) and 20,408 of 2048 (33 and 28), and
+  // other widths from 96 to 4096 take the same
+  const dim3 grid((unsigned)row_blocks(a.rows, q.lpu, a.groups, 2048), (unsigned)a.groups);
   GDN_NORM_TYPE(gdn_norm_fwd_kernel);
   return hipGetLastError();
 }

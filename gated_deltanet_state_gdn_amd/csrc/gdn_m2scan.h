@@ -164,7 +164,9 @@ __device__ __forceinline__ f32x4 frag_mma(f32x4 acc, const Frag<false>& a, const
 }
 
 // What two bf16 roundings leave of a and b, exactly: a dot product with (-1, 0)
-// and (0, -1), one instruction each in place of an unpacking and a subtraction.
+// and (0, -1), one instruction each in place of an unpacking and a subtraction
+// (prefill of 20,408 tokens x 128 heads 663 us so, 678 with those; backward of
+// 16,384 tokens 1404 and 1411).
 // (The factors come from registers, since the immediate -1.0 would stand for
 // the second one in both.  An infinity or NaN reaches its neighbour's rest too.)
 __device__ __forceinline__ void bf16_rest(uint32_t pair, float& a, float& b) {
@@ -183,24 +185,15 @@ template <bool BF, int TERMS = 3>
 struct Split {
   static constexpr int K = BF ? TERMS : 1;
   Frag<BF> t[K];
-  // DOT: rests by dot products, for the walk (prefill of 20,408 tokens x 128 heads 670 us with them, 685 without); the
-  // gradient kernel, whose vector units are the busier, is slower with them (training backward 1417 us with, 1398 without)
-  template <bool DOT = false>
   __device__ __forceinline__ static Split of(float (&f)[8]) {
     Split s;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       s.t[k] = Frag<BF>::round(f);
-      if (k + 1 == K) continue;
-      if constexpr (BF && DOT) {
+      if constexpr (BF)
+        if (k + 1 < K)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bf16_rest(s.t[k].v[j], f[2 * j], f[2 * j + 1]);
-      } else {
-        float g[8];
-        s.t[k].widen(g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] -= g[e];
-      }
+          for (int j = 0; j < 4; ++j) bf16_rest(s.t[k].v[j], f[2 * j], f[2 * j + 1]);
     }
     return s;
   }

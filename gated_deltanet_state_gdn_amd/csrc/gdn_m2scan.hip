@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
 }
 
 // ------------------------------------------------------------------ walk
-// Four waves over 128 state rows (two heads of 64), two workgroups on a compute unit, or 64, three
-// (which the bound on registers keeps: 20 x 500 tokens x 32 heads 80 us with it, 91 without): one's vector work then runs beside the other's matrix work.  Eight
+// Four waves over 128 state rows (two heads of 64), two workgroups on a compute
+// unit, or 64, three: one's vector work then runs beside the other's matrix work.  Eight
 // waves over 256 rows, one workgroup, share the read and write vectors of a
 // chunk among twice the heads but keep in step: a prefill of 20,408 tokens
 // through 128 heads took 789 us that way, 678 us this way.
@@ -165,7 +165,7 @@ __device__ __forceinline__ int kt_at(int n, int t) {
 }
 
 template <bool BF, int D, int NN, int PT, bool REV, bool OUT>
-__global__ void __launch_bounds__(256, BF ? (D == 64 && PT == 1 ? 3 : 2) : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
+__global__ void __launch_bounds__(256, BF ? 2 : 1) gdn_m2s_walk_kernel(const M2ScanArgs a) {
   using W = WalkGeom<BF, D, NN, PT, OUT>;
   typedef typename W::E E;
   constexpr int HB = W::HB, NT = W::NT, KB = W::KB, LDF = W::LDF, LDT = W::LDT, ROWS = W::ROWS, Q = kScanChunk;
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(256, BF ? (D == 64 && PT == 1 ? 3 : 2) : 1) gd
             f[e] = S[2 * kb][pt][e];
             f[4 + e] = 2 * kb + 1 < NT ? S[2 * kb + 1 < NT ? 2 * kb + 1 : 0][pt][e] : 0.f;
           }
-          sf[pt] = Terms::template of<true>(f);
+          sf[pt] = Terms::of(f);
         }
         Frag<BF> ff[4];
 #pragma unroll
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(256, BF ? (D == 64 && PT == 1 ? 3 : 2) : 1) gd
         else Frag<BF>::load(s_x + xt_at<BF, LDT>(p0 + 16 * pt + l16, 32 * ks + 8 * q)).widen(f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= gh_[3 * Q + 32 * ks + 8 * q + e];
-        xs[pt] = Split<BF>::template of<true>(f);
+        xs[pt] = Split<BF>::of(f);
       }
       // four tiles of n at a time, their terms apart: a product never follows the one it adds to
       constexpr int NG = NT < 4 ? NT : 4;

@@ -32,7 +32,7 @@
 // order, in 64 bits.
 //
 // Measured (bf16, heads of 64 x 128, 16 heads a group): 16,384 tokens x 128
-// heads 783 us, 2.7 GB read and 0.13 written, 3.6 TB/s.  One workgroup of eight
+// heads 806 us in a kernel trace, 2.7 GB read and 0.13 written, 3.5 TB/s.  One workgroup of eight
 // waves fits a compute unit, as the summed products and C.B of a block lie in
 // LDS; its parts (products of a head, the state parts, the sums that close a
 // head) wait for memory and LDS in turn.  Matrix units are busy 13% of the time.

@@ -28,14 +28,15 @@
 // 24 bits, with exact B.  For the output alone the state and the decay-weighted
 // products of read and write vectors are taken in two bf16 terms, off by 2^-16 of
 // each, where y's own rounding is 2^-8: 99.8% of y then is the exact value's
-// rounding, against half of it with one term.  (The prefill below takes 665 us
+// rounding, against half of it with one term.  (The prefill below takes 663 us
 // with two terms, 604 with one.)
 // Any other types take the FP32 MFMA throughout.
 //
 // Measured (bf16, heads of 64 x 128): prompts of 1024, 3000 and twice 8192
-// tokens through 128 heads 608 us (prep 51, walk 557), 1.3 TB/s of what has to
-// move: the chain of 128 chunks, 4.4 us each, is what bounds it.  Matrix units are
-// busy 13% of the time.  16,384 tokens, states only, 222 us; in reverse with dx 428.
+// tokens through 128 heads 663 us a call, of which the prep takes 50, 1.2 TB/s of
+// what has to move: the chain of 128 chunks, 4.8 us each, is what bounds it.
+// Matrix units are busy 15% of the time, vector units 27%.  In a kernel trace,
+// 16,384 tokens, states only, 222 us; in reverse with dx 451.
 #include <algorithm>
 
 #include "gdn_m2scan.h"
@@ -126,7 +127,8 @@ __global__ void __launch_bounds__(256) gdn_m2s_prep_kernel(const M2ScanArgs a) {
 // unit, or 64, three: one's vector work then runs beside the other's matrix work.  Eight
 // waves over 256 rows, one workgroup, share the read and write vectors of a
 // chunk among twice the heads but keep in step: a prefill of 20,408 tokens
-// through 128 heads took 789 us that way, 678 us this way.
+// through 128 heads took 789 us that way, 678 us this way (the read-out with one
+// bf16 term in both).
 template <bool BF, int D, int NN, int PT_, bool OUT>
 struct WalkGeom {
   typedef typename Frag<BF>::E E;

@@ -17,11 +17,12 @@
 // alignment, and one that would pass the slice's end is read from its last
 // eight values and moved.  Measured, layer form with a bias in
 // bf16 where not said (a copy reaches 5.1 to 5.4 TB/s): forward 20,408 rows of
-// 4096 values 65 us, 5.2 TB/s; backward 16,384 rows of 4096 84 us, 4.8 TB/s;
-// backward 16,384 rows of 8 slices of 1024, RMS with the gate before, 267 us,
+// 4096 values 65 us, 5.2 TB/s, and of 8 slices of 1024, RMS with the gate
+// before, 205 us, 4.9 TB/s; backward 16,384 rows of 4096 84 us, 4.8 TB/s;
+// backward 16,384 rows of 8 slices of 1024, RMS with the gate before, 268 us,
 // 5.0 TB/s; backward 40,001 rows of 128, RMS in FP32 with the gate behind, 22 us,
-// 4.6 TB/s; backward 20,001 rows of 2047, which no vector fits, 62 us, 3.9 TB/s;
-// backward 4000 rows of 16,384 with the gate before 249 us, 2.6 TB/s (its
+// 4.6 TB/s; backward 20,001 rows of 2047, which no vector fits, 63 us, 3.9 TB/s;
+// backward 4000 rows of 16,384 with the gate before 255 us, 2.6 TB/s (its
 // arithmetic spills); three rows of 8 slices: the call's latency, 13 us.
 // The variance is taken from the deviations, not from a difference of sums.
 // All sums are FP32.  The backward pass writes one row of partial dw and db a

@@ -29,6 +29,9 @@ EXPORTS = (
     "gdn_mamba2_decode_step", "gdn_mamba2_replay_decode", "gdn_mamba2_replay_flush", "gdn_mamba2_replay_rollback",
     "gdn_mamba2_scan_workspace_bytes", "gdn_mamba2_scan", "gdn_mamba2_scan_backward_workspace_bytes", "gdn_mamba2_scan_backward",
     "gdn_layer_norm", "gdn_layer_norm_backward_workspace_bytes", "gdn_layer_norm_backward",
+    "gdn_linear_decode_step", "gdn_linear_scan_workspace_bytes", "gdn_linear_scan", "gdn_linear_scan_backward_workspace_bytes",
+    "gdn_linear_scan_backward",
+    "gdn_qk_norm_rope", "gdn_qk_norm_rope_backward_workspace_bytes", "gdn_qk_norm_rope_backward",
     "gdn_status_string", "gdn_last_error",
 )
 
@@ -82,6 +85,21 @@ class gdn_norm_dims(ctypes.Structure):
                 ("gate", ctypes.c_int)]
 
 
+class gdn_linear_dims(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_k_heads", ctypes.c_int32),
+                ("num_v_heads", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class gdn_linear_strides(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_int64), ("k", ctypes.c_int64), ("v", ctypes.c_int64)]
+
+
+class gdn_qk_dims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("num_q_heads", ctypes.c_int32), ("num_k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("neighbours", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("pair_axis", ctypes.c_char_p)]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{message} [status {status}]")
@@ -102,6 +120,7 @@ def lib() -> ctypes.CDLL:
     P, I32, I64, SZ, INT = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
     F32, pn = ctypes.c_float, ctypes.POINTER(gdn_norm_dims)
     pst = ctypes.POINTER(gdn_m2_strides)
+    pl, pls, pq = ctypes.POINTER(gdn_linear_dims), ctypes.POINTER(gdn_linear_strides), ctypes.POINTER(gdn_qk_dims)
     pd, pg, pp, pr = (ctypes.POINTER(gdn_dims), ctypes.POINTER(gdn_gates), ctypes.POINTER(gdn_pool),
                       ctypes.POINTER(gdn_ring))
     pm, pmp, pmr = ctypes.POINTER(gdn_m2_dims), ctypes.POINTER(gdn_m2_params), ctypes.POINTER(gdn_m2_ring)
@@ -129,6 +148,14 @@ def lib() -> ctypes.CDLL:
         "gdn_layer_norm": (INT, [pn, P, I64, P, I64, INT, P, P, F32, P, I64, INT, P, P, P]),
         "gdn_layer_norm_backward_workspace_bytes": (SZ, [pn]),
         "gdn_layer_norm_backward": (INT, [pn, P, I64, P, I64, P, I64, INT, P, P, P, P, P, I64, P, I64, P, P, P, SZ, P]),
+        "gdn_linear_decode_step": (INT, [pl, I32, P, P, P, INT, pls, P, pp, P, P, INT, P]),
+        "gdn_linear_scan_workspace_bytes": (SZ, [pl, I32, I64]),
+        "gdn_linear_scan": (INT, [pl, I32, P, I64, P, P, P, INT, pls, P, pp, P, P, INT, P, SZ, P]),
+        "gdn_linear_scan_backward_workspace_bytes": (SZ, [pl, I32, I64]),
+        "gdn_linear_scan_backward": (INT, [pl, I32, P, I64, P, P, P, INT, pls, P, pp, P, P, P, P, P, P, P, P, SZ, P]),
+        "gdn_qk_norm_rope": (INT, [pq, P, I64, P, I64, INT, P, P, F32, P, P, P, I64, P, I64, P]),
+        "gdn_qk_norm_rope_backward_workspace_bytes": (SZ, [pq]),
+        "gdn_qk_norm_rope_backward": (INT, [pq, P, I64, P, I64, P, I64, P, I64, INT, P, P, F32, P, P, P, I64, P, I64, P, P, P, SZ, P]),
         "gdn_status_string": (ctypes.c_char_p, [INT]),
         "gdn_last_error": (ctypes.c_char_p, []),
     }
@@ -772,3 +799,262 @@ def gdn_layer_norm_backward(dy, x, weight, mean, rstd, bias=None, gate=None, gro
         _ptr(workspace) if workspace is not None else None,
         workspace.nbytes if workspace is not None else 0, _on_gpu(stream, x, dy, gate, weight, bias, mean, rstd, workspace)))
     return LayerNormGrads(dx, dw, db, dz)
+
+
+# ------------------------------------------------------------------ linear attention
+class _launch_on:
+    """The stream's handle for a launch whose tensors all lie on x's GPU, which is made the current one meanwhile."""
+
+    __slots__ = ("stream", "tensors", "guard")
+
+    def __init__(self, stream, *tensors):
+        self.stream, self.tensors, self.guard = stream, tensors, None
+
+    def __enter__(self):
+        torch = _torch()
+        gpu = self.tensors[0].get_device()
+        if gpu >= 0 and gpu != torch.cuda.current_device():
+            self.guard = torch.cuda.device(gpu)
+            self.guard.__enter__()
+        return _on_gpu(self.stream, *self.tensors)
+
+    def __exit__(self, *error):
+        if self.guard is not None:
+            self.guard.__exit__(*error)
+
+
+class LinearScanGrads(NamedTuple):
+    """Gradients of gdn_linear_scan: dq, dk, dv in the inputs' dtype and shapes."""
+    dq: object
+    dk: object
+    dv: object
+    dinit: object  # float32 [N, H, dk, dv], or None without a pool
+
+
+def _linear_args(q, k, v, log_decay, scale, copies, stream):
+    """Dims, tokens, pointers and strides of q [T, Hq, dk], k [T, Hk, dk] and v [T, Hv, dv]."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or log_decay.dim() != 1:
+        raise ValueError("q, k and v must be [tokens, heads, dim] and log_decay [heads]")
+    T, Hq, dk = q.shape
+    Hk, Hv, dv = k.shape[1], v.shape[1], v.shape[2]
+    dtype = q.dtype
+    pq, sq = _token_rows(q, (Hq, dk), dtype, "q", copies, stream)
+    pk, sk = _token_rows(k, (Hk, dk), dtype, "k", copies, stream)
+    pv, sv = _token_rows(v, (Hv, dv), dtype, "v", copies, stream)
+    if not T == k.shape[0] == v.shape[0]:
+        raise ValueError("q, k and v must have the same number of tokens")
+    if scale is not None and not 0.0 < scale < float("inf"):
+        raise ValueError(f"scale must be positive and finite, not {scale}")
+    H = int(log_decay.shape[0])
+    _f32(log_decay, (H,), "log_decay")
+    dims = gdn_linear_dims(H, Hq, Hk, Hv, dk, dv, float(scale) if scale is not None else 0.0)
+    return dims, T, [pq, pk, pv, dtype_code(dtype), ctypes.byref(gdn_linear_strides(sq, sk, sv)), _ptr(log_decay)]
+
+
+def _linear_pool(pool, slot_map, dims, N):
+    torch = _torch()
+    if pool.dim() != 4 or pool.shape[1:] != (dims.num_heads, dims.dk, dims.dv):
+        raise ValueError(f"pool must be [slots, {dims.num_heads}, {dims.dk}, {dims.dv}], not {tuple(pool.shape)}")
+    if slot_map.dtype != torch.int32 or slot_map.shape != (N,):
+        raise ValueError(f"slot_map must be int32 [{N}]")
+    return ctypes.byref(_pool(pool)), _ptr(slot_map)
+
+
+def gdn_linear_decode_step(q, k, v, log_decay, pool, slot_map, scale=None, out=None, out_dtype=None, stream=None):
+    """One token of linear attention for each of B sequences: S <- e^g S + k v^T, o = scale S^T q.  q [B, Hq, dk];
+    k [B, Hk, dk]; v [B, Hv, dv]; log_decay float32 [H]; pool [slots, H, dk, dv]; Hq, Hk and Hv divide H.  Tokens may
+    be apart (slices of wider rows).  Returns o [B, H, dv], float32 by default."""
+    torch = _torch()
+    copies = []
+    dims, B, args = _linear_args(q, k, v, log_decay, scale, copies, stream)
+    shape = (B, dims.num_heads, dims.dv)
+    fresh = []
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or torch.float32, device=q.device)
+        fresh.append(out)
+    elif out.shape != shape:
+        raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
+    state, slots = _linear_pool(pool, slot_map, dims, B)
+    _keep_for_stream(fresh + copies, stream)
+    with _launch_on(stream, q, k, v, log_decay, pool, slot_map, out) as handle:
+        _check(lib().gdn_linear_decode_step(ctypes.byref(dims), B, *args, state, slots, _ptr(out), dtype_code(out.dtype), handle))
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_workspace(backward, H, Hq, Hk, Hv, d, N, T) -> int:
+    dims = gdn_linear_dims(H, Hq, Hk, Hv, d, d, 0.0)
+    f = lib().gdn_linear_scan_backward_workspace_bytes if backward else lib().gdn_linear_scan_workspace_bytes
+    return int(f(ctypes.byref(dims), N, T))
+
+
+def _linear_scan_args(q, k, v, log_decay, cu_seqlens, pool, slot_map, scale, copies, stream):
+    """The arguments that the scan and its backward share."""
+    torch = _torch()
+    dims, T, args = _linear_args(q, k, v, log_decay, scale, copies, stream)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must be int32 [N + 1]")
+    N = int(cu_seqlens.shape[0]) - 1
+    if (pool is None) != (slot_map is None):
+        raise ValueError("pool and slot_map come together or not at all")
+    state, slots = _linear_pool(pool, slot_map, dims, N) if pool is not None else (None, None)
+    return dims, N, T, [ctypes.byref(dims), N, _ptr(cu_seqlens), T, *args, state, slots]
+
+
+def _linear_scratch(backward, dims, N, T, workspace, device, fresh):
+    """(tensor, pointer, bytes) of the workspace given, or of one made for the call."""
+    if workspace is None:
+        need = _linear_workspace(backward, dims.num_heads, dims.num_q_heads, dims.num_k_heads, dims.num_v_heads, dims.dk, N, T)
+        if not need:
+            return None, None, 0
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+        fresh.append(workspace)
+    return workspace, _ptr(workspace), workspace.nbytes
+
+
+def gdn_linear_scan(q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, scale=None, out=None, out_dtype=None,
+                    workspace=None, stream=None):
+    """Linear attention with a fixed decay a head over packed sequences: q [T, Hq, dk]; k [T, Hk, dk]; v [T, Hv, dv];
+    log_decay float32 [H], a constant without a gradient; cu_seqlens int32 [N+1] (device); Hq, Hk and Hv divide H.
+    Tokens may be apart (slices of wider rows; an expanded tensor is copied).  With a pool [slots, H, dk, dv] and slot_map int32 [N],
+    sequence s goes on from slot slot_map[s] and leaves its final state there; without, from zero states.  Returns
+    o [T, H, dv] in out_dtype (q's by default).  Autograd does not record it: gradients come from
+    gdn_linear_scan_backward."""
+    torch = _torch()
+    _says_no_graph("gdn_linear_scan", q, k, v, pool)
+    copies, fresh = [], []
+    dims, N, T, args = _linear_scan_args(q, k, v, log_decay, cu_seqlens, pool, slot_map, scale, copies, stream)
+    shape = (T, dims.num_heads, dims.dv)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=q.device)
+        fresh.append(out)
+    elif out.shape != shape:
+        raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
+    workspace, pw, nw = _linear_scratch(False, dims, N, T, workspace, q.device, fresh)
+    _keep_for_stream(fresh + copies, stream)
+    with _launch_on(stream, q, k, v, log_decay, cu_seqlens, pool, slot_map, out, workspace) as handle:
+        _check(lib().gdn_linear_scan(*args, _ptr(out), dtype_code(out.dtype), pw, nw, handle))
+    return out
+
+
+def gdn_linear_scan_backward(do, q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, dfinal=None, scale=None,
+                             workspace=None, stream=None) -> LinearScanGrads:
+    """Gradients of gdn_linear_scan for do [T, H, dv] in q's dtype (and dfinal, float32 [N, H, dk, dv], of the final
+    states).  pool and slot_map give the states that the forward call started from, as they were before it."""
+    torch = _torch()
+    copies = []
+    dims, N, T, args = _linear_scan_args(q, k, v, log_decay, cu_seqlens, pool, slot_map, scale, copies, stream)
+    H, d = dims.num_heads, dims.dv
+    if do.shape != (T, H, d) or do.dtype != q.dtype:
+        raise ValueError(f"do must be {q.dtype} of shape {(T, H, d)}, not {do.dtype} {tuple(do.shape)}")
+    pdo = _own_rows(do, copies, stream)[0] if not do.is_contiguous() and _one_row(do) else _ptr(do)
+    _f32(dfinal, (N, H, dims.dk, d), "dfinal")
+    new = lambda shape, t: torch.empty(shape, dtype=t, device=q.device)  # noqa: E731
+    grads = LinearScanGrads(new(q.shape, q.dtype), new(k.shape, q.dtype), new(v.shape, q.dtype),
+                            new((N, H, dims.dk, d), torch.float32) if pool is not None else None)
+    fresh = list(grads)
+    workspace, pw, nw = _linear_scratch(True, dims, N, T, workspace, q.device, fresh)
+    _keep_for_stream(fresh + copies, stream)
+    with _launch_on(stream, q, do, k, v, log_decay, cu_seqlens, pool, slot_map, dfinal, workspace) as handle:
+        _check(lib().gdn_linear_scan_backward(
+            *args, pdo, _ptr(dfinal) if dfinal is not None else None, *(_ptr(t) for t in grads[:3]),
+            _ptr(grads.dinit) if pool is not None else None, pw, nw, handle))
+    return grads
+
+
+# ------------------------------------------------------------------ norm and rotation of q and k
+class QkGrads(NamedTuple):
+    """Gradients of gdn_qk_norm_rope: dq and dk in the inputs' dtype, the weights' float32 [head_dim]."""
+    dq: object
+    dk: object
+    dq_weight: object
+    dk_weight: object
+
+
+@functools.lru_cache(maxsize=64)
+def _pair_axes(axes) -> bytes:
+    if any(not 0 <= v < 4 for v in axes):
+        raise ValueError("axes must be indices of positions' rows, at most 4")
+    return bytes(axes)
+
+
+def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, neighbours, axes, copies, stream):
+    """Dims, and what both directions share: (pointer, stride) of q and k, and the parameters from the dtype on."""
+    torch = _torch()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, head_dim]")
+    T, Hq, d = q.shape
+    Hk, dtype = k.shape[1], q.dtype
+    rq, rk = _token_rows(q, (Hq, d), dtype, "q", copies, stream), _token_rows(k, (Hk, d), dtype, "k", copies, stream)
+    if k.shape[0] != T:
+        raise ValueError("q and k must have the same number of tokens")
+    _f32(q_weight, (d,), "q_weight"), _f32(k_weight, (d,), "k_weight")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be float32 [rotary_dim / 2]")
+    P = int(inv_freq.shape[0])
+    _f32(inv_freq, (P,), "inv_freq")
+    if positions.dtype != torch.int32 or positions.dim() not in (1, 2) or positions.shape[-1] != T:
+        raise ValueError(f"positions must be int32 [{T}], or [axes, {T}]")
+    rows = int(positions.shape[0]) if positions.dim() == 2 else 1
+    if axes is not None:
+        axes = _pair_axes(tuple(axes))
+        if len(axes) != P:
+            raise ValueError(f"axes must name one of positions' rows for each of the {P} pairs")
+    elif rows != 1:
+        raise ValueError("positions of several axes need `axes`")
+    dims = gdn_qk_dims(T, Hq, Hk, d, 2 * P, int(bool(neighbours)), rows, axes)
+    return dims, (*rq, *rk), [dtype_code(dtype), _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq)]
+
+
+def gdn_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, neighbours=False, axes=None, q_out=None,
+                     k_out=None, stream=None):
+    """RMS norm of every head of q [T, Hq, d] and k [T, Hk, d], with weights float32 [d], and the rotation of the first
+    2 P values of each head by the token's position: pair i turns by positions[t] inv_freq[i] (positions int32 [T],
+    inv_freq float32 [P]).  Pair i is (i, i + P), or (2 i, 2 i + 1) with `neighbours`.  With several axes (time,
+    height, width) positions is int32 [axes, T] and `axes` names the row that each of the P pairs follows.  Tokens may
+    be apart (slices of wider rows; an expanded tensor is copied).  Returns (q, k) anew, or in q_out and k_out, which may be q and k.
+    Autograd does not record it: gradients come from gdn_qk_norm_rope_backward."""
+    torch = _torch()
+    _says_no_graph("gdn_qk_norm_rope", q, k, q_weight, k_weight)
+    copies, fresh = [], []
+    dims, rows, params = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, neighbours, axes, copies, stream)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        fresh.append(q_out)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        fresh.append(k_out)
+    outs = (*_token_rows(q_out, q.shape[1:], q.dtype, "q_out"), *_token_rows(k_out, k.shape[1:], q.dtype, "k_out"))
+    if q_out.shape[0] != q.shape[0] or k_out.shape[0] != q.shape[0]:
+        raise ValueError("q_out and k_out must have as many tokens as q and k")
+    _keep_for_stream(fresh + copies, stream)
+    with _launch_on(stream, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out) as handle:
+        _check(lib().gdn_qk_norm_rope(ctypes.byref(dims), *rows, *params, *outs, handle))
+    return q_out, k_out
+
+
+def gdn_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, neighbours=False,
+                              axes=None, workspace=None, stream=None) -> QkGrads:
+    """Gradients of gdn_qk_norm_rope from those of its results, in q's dtype, and its inputs."""
+    torch = _torch()
+    copies = []
+    dims, rows, params = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, neighbours, axes, copies, stream)
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise ValueError("dq_out and dk_out must be shaped as q and k")
+    dys = (*_token_rows(dq_out, q.shape[1:], q.dtype, "dq_out", copies, stream),
+           *_token_rows(dk_out, k.shape[1:], q.dtype, "dk_out", copies, stream))
+    new = lambda shape, t: torch.empty(shape, dtype=t, device=q.device)  # noqa: E731
+    d = q.shape[2:]
+    grads = QkGrads(new(q.shape, q.dtype), new(k.shape, q.dtype), new(d, torch.float32), new(d, torch.float32))
+    fresh = list(grads)
+    need = int(lib().gdn_qk_norm_rope_backward_workspace_bytes(ctypes.byref(dims)))
+    if workspace is None and need:
+        workspace = new((need,), torch.uint8)
+        fresh.append(workspace)
+    _keep_for_stream(fresh + copies, stream)
+    with _launch_on(stream, q, k, dq_out, dk_out, q_weight, k_weight, positions, inv_freq, workspace) as handle:
+        _check(lib().gdn_qk_norm_rope_backward(
+            ctypes.byref(dims), *dys, *rows, *params, grads.dq.data_ptr(), 0, grads.dk.data_ptr(), 0, _ptr(grads.dq_weight),
+            _ptr(grads.dk_weight), _ptr(workspace) if workspace is not None else None,
+            workspace.nbytes if workspace is not None else 0, handle))
+    return grads

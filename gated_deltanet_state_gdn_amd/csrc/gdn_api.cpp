@@ -990,3 +990,378 @@ gdn_status gdn_mamba2_scan_backward(const gdn_m2_dims* dims, int32_t N, const in
   q.part = reinterpret_cast<float*>(ws + w.part);
   return launched(gdn::launch_scan_grad(q, bf, dims->headdim, dims->dstate, s));
 }
+
+// ------------------------------------------------------------------ linear attention
+namespace {
+
+gdn_status check_linear_dims(const gdn_linear_dims* d) {
+  GDN_REQUIRE(d != nullptr, GDN_EINVAL, "dims is NULL");
+  GDN_REQUIRE(d->num_heads >= 1 && d->num_q_heads >= 1 && d->num_k_heads >= 1 && d->num_v_heads >= 1, GDN_EINVAL,
+              "head counts must be >= 1 (H=%d Hq=%d Hk=%d Hv=%d)", d->num_heads, d->num_q_heads, d->num_k_heads, d->num_v_heads);
+  GDN_REQUIRE(d->num_heads % d->num_q_heads == 0 && d->num_heads % d->num_k_heads == 0 && d->num_heads % d->num_v_heads == 0,
+              GDN_EINVAL, "H=%d is not a multiple of Hq=%d, Hk=%d and Hv=%d", d->num_heads, d->num_q_heads, d->num_k_heads, d->num_v_heads);
+  GDN_REQUIRE(d->dk >= 1 && d->dv >= 1, GDN_EINVAL, "head dims must be >= 1 (dk=%d dv=%d)", d->dk, d->dv);
+  GDN_REQUIRE(d->dk == d->dv && (d->dk == 16 || d->dk == 32 || d->dk == 64 || d->dk == 128), GDN_EUNSUPPORTED,
+              "head dims dk=%d dv=%d: compiled for dk == dv in {16, 32, 64, 128}", d->dk, d->dv);
+  GDN_REQUIRE(!(d->scale > 0.f) || d->scale <= 3.4028235e38f, GDN_EINVAL, "scale must be finite");
+  GDN_REQUIRE((int64_t)d->num_heads * d->dk <= kMaxTokenStride, GDN_EUNSUPPORTED, "H dk must be at most 2^22");
+  return GDN_OK;
+}
+
+float linear_scale(const gdn_linear_dims* d) { return d->scale > 0.f ? d->scale : 1.0f / sqrtf((float)d->dk); }
+
+int64_t linear_stride(const gdn_linear_strides* st, int64_t gdn_linear_strides::* f, int64_t dense) {
+  return st != nullptr && st->*f != 0 ? st->*f : dense;
+}
+
+gdn_status check_linear_io(const gdn_linear_dims* d, const void* q, const void* k, const void* v, const gdn_linear_strides* st,
+                           const float* log_decay) {
+  GDN_REQUIRE(log_decay != nullptr && aligned(log_decay, 4), GDN_EINVAL, "log_decay is NULL or misaligned");
+  GDN_REQUIRE(q && k && v, GDN_EINVAL, "q, k or v is NULL");
+  GDN_REQUIRE(aligned(q, 16) && aligned(k, 16) && aligned(v, 16), GDN_EINVAL, "q, k or v is not 16-byte aligned");
+  if (st != nullptr) {
+    GDN_TRY(check_token_stride(st->q, (int64_t)d->num_q_heads * d->dk, 8, "q"));
+    GDN_TRY(check_token_stride(st->k, (int64_t)d->num_k_heads * d->dk, 8, "k"));
+    GDN_TRY(check_token_stride(st->v, (int64_t)d->num_v_heads * d->dv, 8, "v"));
+  }
+  return GDN_OK;
+}
+
+gdn_status check_linear_sizes(const gdn_linear_dims* d, int32_t N, int64_t total, int roles) {
+  GDN_TRY(check_linear_dims(d));
+  GDN_REQUIRE(N >= 0 && total >= 0, GDN_EINVAL, "N=%d and total_tokens=%lld must be >= 0", N, (long long)total);
+  GDN_REQUIRE(total <= INT32_MAX, GDN_EINVAL, "total_tokens=%lld exceeds the 32-bit cu_seqlens", (long long)total);
+  GDN_REQUIRE(N > 0 || total == 0, GDN_EINVAL, "%lld tokens in no sequence", (long long)total);
+  const gdn::LinPlan p = gdn::linear_plan(N, total, d->num_heads, roles);
+  const int64_t slots = p.seg_chunks > 0 ? gdn::scan_slots(N, total, (int64_t)p.seg_chunks * 64) : N;
+  const int64_t items = slots * d->num_heads * 256;  // threads along x of the largest launch
+  GDN_REQUIRE(items <= UINT32_MAX, GDN_EUNSUPPORTED,
+              "N=%d and total_tokens=%lld make a launch of %lld threads: at most 2^32 - 1 are supported", N, (long long)total, (long long)items);
+  if (roles > 1) {
+    const int64_t sum = total * d->num_heads * (d->dk / 4);
+    GDN_REQUIRE(sum <= UINT32_MAX, GDN_EUNSUPPORTED, "total_tokens=%lld make a launch of %lld threads: at most 2^32 - 1 are supported",
+                (long long)total, (long long)sum);
+  }
+  return GDN_OK;
+}
+
+struct LinWs {
+  size_t seg[2], each[3], bytes;  // segment states forward and in reverse; every state's own dq, dk and dv where heads are shared
+  gdn::LinPlan plan;
+};
+
+LinWs linear_ws(const gdn_linear_dims* d, int32_t N, int64_t total, bool backward) {
+  LinWs w{};
+  Carve c;
+  const size_t H = d->num_heads;
+  w.plan = gdn::linear_plan(N, total, d->num_heads, backward ? 3 : 1);
+  if (w.plan.seg_chunks > 0) {
+    const size_t segs = gdn::scan_slots(N, total, (int64_t)w.plan.seg_chunks * 64);
+    for (int i = 0; i < (backward ? 2 : 1); ++i) w.seg[i] = c.take(segs * H * d->dk * d->dv * 4);
+  }
+  const int heads[3] = {d->num_q_heads, d->num_k_heads, d->num_v_heads};
+  for (int i = 0; backward && i < 3; ++i)
+    if (heads[i] != d->num_heads) w.each[i] = c.take((size_t)total * H * d->dk * 4);
+  w.bytes = c.used;
+  return w;
+}
+
+gdn_status check_linear_scan(const gdn_linear_dims* d, const int32_t* cu, int64_t total, const void* q, const void* k, const void* v,
+                             const gdn_linear_strides* st, const float* log_decay, const gdn_pool* state, const int32_t* slot_map) {
+  GDN_REQUIRE(cu != nullptr && aligned(cu, 4), GDN_EINVAL, "cu_seqlens is NULL or misaligned");
+  GDN_REQUIRE(log_decay != nullptr && aligned(log_decay, 4), GDN_EINVAL, "log_decay is NULL or misaligned");
+  if (total > 0) GDN_TRY(check_linear_io(d, q, k, v, st, log_decay));
+  GDN_REQUIRE((state != nullptr) == (slot_map != nullptr), GDN_EINVAL, "the state pool and slot_map come together or not at all");
+  if (state != nullptr) {
+    GDN_TRY(check_pool(state, "state"));
+    GDN_REQUIRE(aligned(slot_map, 4), GDN_EINVAL, "slot_map is misaligned");
+  }
+  return GDN_OK;
+}
+
+// A tensor of a walk: its address, distance between tokens, and the states that share a head of it.
+struct LinTensor {
+  const void* p;
+  int64_t ts;
+  int share;
+};
+
+gdn::LinRole linear_role(const LinTensor& read, const LinTensor& write, const LinTensor& in, bool rev, bool transposed) {
+  gdn::LinRole r{};
+  r.read = read.p;
+  r.write = write.p;
+  r.in = in.p;
+  r.read_ts = read.ts;
+  r.write_ts = write.ts;
+  r.in_ts = in.ts;
+  r.read_share = read.share;
+  r.write_share = write.share;
+  r.in_share = in.share;
+  r.rev = rev;
+  r.transposed = transposed;
+  return r;
+}
+
+struct LinInputs {
+  LinTensor q, k, v;
+};
+
+LinInputs linear_inputs(const gdn_linear_dims* d, const void* q, const void* k, const void* v, const gdn_linear_strides* st) {
+  return {{q, linear_stride(st, &gdn_linear_strides::q, (int64_t)d->num_q_heads * d->dk), d->num_heads / d->num_q_heads},
+          {k, linear_stride(st, &gdn_linear_strides::k, (int64_t)d->num_k_heads * d->dk), d->num_heads / d->num_k_heads},
+          {v, linear_stride(st, &gdn_linear_strides::v, (int64_t)d->num_v_heads * d->dv), d->num_heads / d->num_v_heads}};
+}
+
+gdn::LinScanArgs linear_args(const gdn_linear_dims* d, int32_t N, const int32_t* cu, int64_t total, int in_dt, const float* log_decay,
+                             const gdn_pool* state, const int32_t* slot_map, const LinWs& w) {
+  gdn::LinScanArgs a{};
+  a.log_decay = log_decay;
+  a.cu = cu;
+  if (state != nullptr) {
+    a.live = slot_map;
+    a.live_slots = state->num_slots;
+  }
+  a.total = total;
+  a.N = N;
+  a.H = d->num_heads;
+  a.in_dt = in_dt;
+  a.scale = linear_scale(d);
+  a.seg_chunks = w.plan.seg_chunks;
+  a.whole = w.plan.whole;
+  return a;
+}
+
+}  // namespace
+
+gdn_status gdn_linear_decode_step(const gdn_linear_dims* dims, int32_t B, const void* q, const void* k, const void* v,
+                                  gdn_dtype in_dtype, const gdn_linear_strides* strides, const float* log_decay,
+                                  const gdn_pool* state, const int32_t* slot_map, void* out, gdn_dtype out_dtype, void* stream) {
+  GDN_TRY(check_linear_dims(dims));
+  GDN_REQUIRE(B >= 0, GDN_EINVAL, "B=%d must be >= 0", B);
+  // a tile takes up to 512 threads, and a launch fewer than 2^32
+  GDN_REQUIRE((int64_t)B * dims->num_heads * 512 <= UINT32_MAX, GDN_EUNSUPPORTED, "B * H exceeds the grid limit");
+  GDN_TRY(check_dtypes(in_dtype, out_dtype));
+  if (B == 0) return ok();  // nothing is read or written
+  GDN_TRY(check_linear_io(dims, q, k, v, strides, log_decay));
+  GDN_REQUIRE(out != nullptr && aligned(out, dtype_bytes(out_dtype)), GDN_EINVAL, "out is NULL or misaligned for out_dtype");
+  GDN_TRY(check_pool(state, "state"));
+  GDN_REQUIRE(slot_map != nullptr && aligned(slot_map, 4), GDN_EINVAL, "slot_map is NULL or misaligned");
+  const LinInputs t = linear_inputs(dims, q, k, v, strides);
+  gdn::LinStepArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.log_decay = log_decay;
+  a.pool = state->base;
+  a.slot_map = slot_map;
+  a.out = out;
+  a.num_slots = state->num_slots;
+  a.q_ts = t.q.ts;
+  a.k_ts = t.k.ts;
+  a.v_ts = t.v.ts;
+  a.B = B;
+  a.H = dims->num_heads;
+  a.q_share = t.q.share;
+  a.k_share = t.k.share;
+  a.v_share = t.v.share;
+  a.in_dt = in_dtype;
+  a.out_dt = out_dtype;
+  a.scale = linear_scale(dims);
+  return launched(gdn::launch_linear_step(a, state->dtype, dims->dk, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_linear_scan_workspace_bytes(const gdn_linear_dims* dims, int32_t N, int64_t total_tokens) {
+  if (check_linear_sizes(dims, N, total_tokens, 1) != GDN_OK || N == 0) return 0;
+  return linear_ws(dims, N, total_tokens, false).bytes;
+}
+
+gdn_status gdn_linear_scan(const gdn_linear_dims* dims, int32_t N, const int32_t* cu_seqlens, int64_t total_tokens, const void* q,
+                           const void* k, const void* v, gdn_dtype in_dtype, const gdn_linear_strides* strides,
+                           const float* log_decay, const gdn_pool* state, const int32_t* slot_map, void* out, gdn_dtype out_dtype,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  GDN_TRY(check_linear_sizes(dims, N, total_tokens, 1));
+  GDN_TRY(check_dtypes(in_dtype, out_dtype));
+  if (N == 0 || total_tokens == 0) return ok();  // nothing is read or written
+  GDN_TRY(check_linear_scan(dims, cu_seqlens, total_tokens, q, k, v, strides, log_decay, state, slot_map));
+  GDN_REQUIRE(out != nullptr && aligned(out, 16), GDN_EINVAL, "out is NULL or not 16-byte aligned");
+  const LinWs w = linear_ws(dims, N, total_tokens, false);
+  GDN_TRY(check_scan_ws(workspace, workspace_bytes, w.bytes));
+  gdn::LinScanArgs a = linear_args(dims, N, cu_seqlens, total_tokens, in_dtype, log_decay, state, slot_map, w);
+  const LinInputs t = linear_inputs(dims, q, k, v, strides);
+  gdn::LinRole& r = a.role[0] = linear_role(t.q, t.k, t.v, false, false);
+  r.out = out;
+  r.out_dt = out_dtype;
+  if (state != nullptr) r.init = r.fin = gdn::ScanStates{state->base, slot_map, (int32_t)state->dtype};
+  if (workspace != nullptr) r.seg = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.seg[0]);
+  return launched(gdn::launch_linear_scan(a, in_dtype == GDN_BF16 && out_dtype == GDN_BF16, dims->dk, 1, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_linear_scan_backward_workspace_bytes(const gdn_linear_dims* dims, int32_t N, int64_t total_tokens) {
+  if (check_linear_sizes(dims, N, total_tokens, 3) != GDN_OK || N == 0) return 0;
+  return linear_ws(dims, N, total_tokens, true).bytes;
+}
+
+gdn_status gdn_linear_scan_backward(const gdn_linear_dims* dims, int32_t N, const int32_t* cu_seqlens, int64_t total_tokens,
+                                    const void* q, const void* k, const void* v, gdn_dtype in_dtype,
+                                    const gdn_linear_strides* strides, const float* log_decay, const gdn_pool* init,
+                                    const int32_t* slot_map, const void* dout, const float* dfinal, void* dq, void* dk, void* dv,
+                                    float* dinit, void* workspace, size_t workspace_bytes, void* stream) {
+  GDN_TRY(check_linear_sizes(dims, N, total_tokens, 3));
+  GDN_TRY(check_dtypes(in_dtype, in_dtype));
+  if (N == 0) return ok();  // nothing is read or written
+  GDN_TRY(check_linear_scan(dims, cu_seqlens, total_tokens, q, k, v, strides, log_decay, init, slot_map));
+  if (total_tokens > 0) {
+    GDN_REQUIRE(dout != nullptr && aligned(dout, 16), GDN_EINVAL, "dout is NULL or not 16-byte aligned");
+    GDN_REQUIRE(dq && dk && dv && aligned(dq, 16) && aligned(dk, 16) && aligned(dv, 16), GDN_EINVAL,
+                "dq, dk or dv is NULL or not 16-byte aligned");
+  }
+  GDN_REQUIRE(aligned(dfinal, 16) && aligned(dinit, 16), GDN_EINVAL, "dfinal or dinit is not 16-byte aligned");
+  const LinWs w = linear_ws(dims, N, total_tokens, true);
+  GDN_TRY(check_scan_ws(workspace, workspace_bytes, w.bytes));
+  char* const ws = static_cast<char*>(workspace);
+  gdn::LinScanArgs a = linear_args(dims, N, cu_seqlens, total_tokens, in_dtype, log_decay, init, slot_map, w);
+  const LinInputs t = linear_inputs(dims, q, k, v, strides);
+  const LinTensor o{dout, (int64_t)dims->num_heads * dims->dv, 1};
+  a.role[0] = linear_role(o, t.v, t.k, false, true);   // dq
+  a.role[1] = linear_role(t.k, t.q, o, true, false);   // dv
+  a.role[2] = linear_role(t.v, o, t.q, true, true);    // dk
+  if (init != nullptr) a.role[0].init = gdn::ScanStates{init->base, slot_map, (int32_t)init->dtype};
+  a.role[1].init = a.role[2].init = gdn::ScanStates{const_cast<float*>(dfinal), nullptr, GDN_F32};
+  a.role[1].fin = gdn::ScanStates{dinit, nullptr, GDN_F32};
+  if (ws != nullptr) {
+    a.role[0].seg = reinterpret_cast<float*>(ws + w.seg[0]);
+    a.role[1].seg = a.role[2].seg = reinterpret_cast<float*>(ws + w.seg[1]);
+  }
+  void* const grads[3] = {dq, dv, dk};
+  const size_t each[3] = {w.each[0], w.each[2], w.each[1]};
+  const int heads[3] = {dims->num_q_heads, dims->num_v_heads, dims->num_k_heads};
+  for (int i = 0; i < 3; ++i) {
+    const bool shared = heads[i] != dims->num_heads;
+    a.role[i].out = shared ? ws + each[i] : grads[i];
+    a.role[i].out_dt = shared ? (int)GDN_F32 : (int)in_dtype;
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = gdn::launch_linear_scan(a, in_dtype == GDN_BF16, dims->dk, 3, s);
+  for (int i = 0; i < 3 && e == hipSuccess && total_tokens > 0; ++i)
+    if (heads[i] != dims->num_heads)
+      e = gdn::launch_linear_sum(gdn::LinSumArgs{reinterpret_cast<const float*>(ws + each[i]), grads[i], total_tokens * heads[i] * (dims->dk / 4),
+                                                 dims->num_heads / heads[i], dims->dk, (int32_t)in_dtype}, s);
+  return launched(e);
+}
+
+// ------------------------------------------------------------------ norm and rotation of q and k
+namespace {
+
+gdn_status check_qk_dims(const gdn_qk_dims* d) {
+  GDN_REQUIRE(d != nullptr, GDN_EINVAL, "dims is NULL");
+  GDN_REQUIRE(d->tokens >= 0, GDN_EINVAL, "tokens=%lld must be >= 0", (long long)d->tokens);
+  GDN_REQUIRE(d->tokens <= INT32_MAX, GDN_EUNSUPPORTED, "tokens=%lld: at most 2^31 - 1 are supported", (long long)d->tokens);
+  GDN_REQUIRE(d->num_q_heads >= 1 && d->num_k_heads >= 1, GDN_EINVAL, "head counts must be >= 1 (Hq=%d Hk=%d)", d->num_q_heads, d->num_k_heads);
+  GDN_REQUIRE(d->head_dim >= 1, GDN_EINVAL, "head_dim=%d must be >= 1", d->head_dim);
+  GDN_REQUIRE(d->head_dim >= 16 && d->head_dim <= 256 && d->head_dim % 8 == 0, GDN_EUNSUPPORTED,
+              "head_dim=%d: multiples of 8 from 16 to 256 are supported", d->head_dim);
+  GDN_REQUIRE(d->rotary_dim >= 1 && d->rotary_dim <= d->head_dim && d->rotary_dim % 2 == 0, GDN_EINVAL,
+              "rotary_dim=%d must be even, from 2 to head_dim=%d", d->rotary_dim, d->head_dim);
+  GDN_REQUIRE(d->rotary_dim % 8 == 0, GDN_EUNSUPPORTED, "rotary_dim=%d: multiples of 8 are supported", d->rotary_dim);
+  GDN_REQUIRE((int64_t)d->num_q_heads * d->head_dim <= kMaxTokenStride && (int64_t)d->num_k_heads * d->head_dim <= kMaxTokenStride,
+              GDN_EUNSUPPORTED, "heads x head_dim must be at most 2^22");
+  GDN_REQUIRE(d->num_axes >= 1, GDN_EINVAL, "num_axes=%d must be >= 1", d->num_axes);
+  GDN_REQUIRE(d->num_axes <= 4, GDN_EUNSUPPORTED, "num_axes=%d: at most 4 are supported", d->num_axes);
+  for (int i = 0; d->pair_axis != nullptr && i < d->rotary_dim / 2; ++i)
+    GDN_REQUIRE(d->pair_axis[i] < d->num_axes, GDN_EINVAL, "pair %d follows axis %d of %d", i, d->pair_axis[i], d->num_axes);
+  return GDN_OK;
+}
+
+gdn_status check_qk_tensor(const void* p, int64_t stride, int heads, const gdn_qk_dims* d, const char* what) {
+  GDN_REQUIRE(p != nullptr && aligned(p, 16), GDN_EINVAL, "%s is NULL or not 16-byte aligned", what);
+  return check_token_stride(stride, (int64_t)heads * d->head_dim, 8, what);
+}
+
+gdn_status check_qk_params(const float* qw, const float* kw, float eps, const int32_t* positions, const float* inv_freq) {
+  GDN_REQUIRE(eps >= 0.f, GDN_EINVAL, "eps must be >= 0");
+  GDN_REQUIRE(qw != nullptr && kw != nullptr && aligned(qw, 4) && aligned(kw, 4), GDN_EINVAL, "q_weight or k_weight is NULL or misaligned");
+  GDN_REQUIRE(positions != nullptr && inv_freq != nullptr && aligned(positions, 4) && aligned(inv_freq, 4), GDN_EINVAL,
+              "positions or inv_freq is NULL or misaligned");
+  return GDN_OK;
+}
+
+gdn::QkArgs qk_args(const gdn_qk_dims* d, const void* q, int64_t qs, const void* k, int64_t ks, int dt, const float* qw, const float* kw,
+                    float eps, const int32_t* positions, const float* inv_freq, void* yq, int64_t yqs, void* yk, int64_t yks) {
+  gdn::QkArgs a{};
+  const int64_t wide[2] = {(int64_t)d->num_q_heads * d->head_dim, (int64_t)d->num_k_heads * d->head_dim};
+  a.x[0] = q;
+  a.x[1] = k;
+  a.x_ts[0] = qs != 0 ? qs : wide[0];
+  a.x_ts[1] = ks != 0 ? ks : wide[1];
+  a.y[0] = yq;
+  a.y[1] = yk;
+  a.y_ts[0] = yqs != 0 ? yqs : wide[0];
+  a.y_ts[1] = yks != 0 ? yks : wide[1];
+  a.w[0] = qw;
+  a.w[1] = kw;
+  a.pos = positions;
+  a.freq = inv_freq;
+  a.T = d->tokens;
+  a.heads[0] = d->num_q_heads;
+  a.heads[1] = d->num_k_heads;
+  a.d = d->head_dim;
+  a.rot = d->rotary_dim;
+  a.neighbours = d->neighbours != 0;
+  a.in_dt = dt;
+  a.eps = eps;
+  for (int i = 0; d->pair_axis != nullptr && i < d->rotary_dim / 2; ++i) a.axis[i / 16] |= (uint32_t)d->pair_axis[i] << 2 * (i % 16);
+  return a;
+}
+
+}  // namespace
+
+gdn_status gdn_qk_norm_rope(const gdn_qk_dims* dims, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            gdn_dtype in_dtype, const float* q_weight, const float* k_weight, float eps, const int32_t* positions,
+                            const float* inv_freq, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  GDN_TRY(check_qk_dims(dims));
+  GDN_TRY(check_dtypes(in_dtype, in_dtype));
+  if (dims->tokens == 0) return ok();  // nothing is read or written
+  GDN_TRY(check_qk_params(q_weight, k_weight, eps, positions, inv_freq));
+  GDN_TRY(check_qk_tensor(q, q_stride, dims->num_q_heads, dims, "q"));
+  GDN_TRY(check_qk_tensor(k, k_stride, dims->num_k_heads, dims, "k"));
+  GDN_TRY(check_qk_tensor(q_out, q_out_stride, dims->num_q_heads, dims, "q_out"));
+  GDN_TRY(check_qk_tensor(k_out, k_out_stride, dims->num_k_heads, dims, "k_out"));
+  const gdn::QkArgs a = qk_args(dims, q, q_stride, k, k_stride, in_dtype, q_weight, k_weight, eps, positions, inv_freq, q_out, q_out_stride,
+                                k_out, k_out_stride);
+  return launched(gdn::launch_qk(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t gdn_qk_norm_rope_backward_workspace_bytes(const gdn_qk_dims* dims) {
+  if (check_qk_dims(dims) != GDN_OK || dims->tokens == 0) return 0;
+  return (size_t)gdn::qk_bwd_blocks(dims->tokens, dims->num_q_heads + dims->num_k_heads, dims->head_dim) * 2 * dims->head_dim * sizeof(float);
+}
+
+gdn_status gdn_qk_norm_rope_backward(const gdn_qk_dims* dims, const void* dq_out, int64_t dq_out_stride, const void* dk_out,
+                                     int64_t dk_out_stride, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                     gdn_dtype in_dtype, const float* q_weight, const float* k_weight, float eps, const int32_t* positions,
+                                     const float* inv_freq, void* dq, int64_t dq_stride, void* dk, int64_t dk_stride, float* dq_weight,
+                                     float* dk_weight, void* workspace, size_t workspace_bytes, void* stream) {
+  GDN_TRY(check_qk_dims(dims));
+  GDN_TRY(check_dtypes(in_dtype, in_dtype));
+  GDN_REQUIRE(dq_weight != nullptr && dk_weight != nullptr && aligned(dq_weight, 4) && aligned(dk_weight, 4), GDN_EINVAL,
+              "dq_weight or dk_weight is NULL or misaligned");
+  if (dims->tokens > 0) {
+    GDN_TRY(check_qk_params(q_weight, k_weight, eps, positions, inv_freq));
+    GDN_TRY(check_qk_tensor(q, q_stride, dims->num_q_heads, dims, "q"));
+    GDN_TRY(check_qk_tensor(k, k_stride, dims->num_k_heads, dims, "k"));
+    GDN_TRY(check_qk_tensor(dq_out, dq_out_stride, dims->num_q_heads, dims, "dq_out"));
+    GDN_TRY(check_qk_tensor(dk_out, dk_out_stride, dims->num_k_heads, dims, "dk_out"));
+    GDN_TRY(check_qk_tensor(dq, dq_stride, dims->num_q_heads, dims, "dq"));
+    GDN_TRY(check_qk_tensor(dk, dk_stride, dims->num_k_heads, dims, "dk"));
+    GDN_TRY(check_scan_ws(workspace, workspace_bytes, gdn_qk_norm_rope_backward_workspace_bytes(dims)));
+  }
+  gdn::QkArgs a = qk_args(dims, q, q_stride, k, k_stride, in_dtype, q_weight, k_weight, eps, positions, inv_freq, dq, dq_stride, dk, dk_stride);
+  a.dy[0] = dq_out;
+  a.dy[1] = dk_out;
+  a.dy_ts[0] = dq_out_stride != 0 ? dq_out_stride : (int64_t)dims->num_q_heads * dims->head_dim;
+  a.dy_ts[1] = dk_out_stride != 0 ? dk_out_stride : (int64_t)dims->num_k_heads * dims->head_dim;
+  a.part = static_cast<float*>(workspace);
+  a.dw[0] = dq_weight;
+  a.dw[1] = dk_weight;
+  return launched(gdn::launch_qk_bwd(a, static_cast<hipStream_t>(stream)));
+}

@@ -188,6 +188,77 @@ struct NormArgs {
   float eps;
 };
 
+// One token of linear attention.  Strides are in elements between tokens.
+struct LinStepArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* log_decay;
+  void* pool;          // [num_slots, H, D, D]
+  const int32_t* slot_map;
+  void* out;           // [B, H, D]
+  int64_t num_slots, q_ts, k_ts, v_ts;
+  int32_t B, H, q_share, k_share, v_share;  // states that share a query, key or value head
+  int32_t in_dt, out_dt;
+  float scale;
+};
+
+// A walk of linear attention over a chunk's tokens: out_t = sum over tokens up to t (in reverse, from t on) of
+// scale e^{g |t - j|} (read_t . write_j) in_j, with the state of all write_j in_j^T behind it.  Forward: o (read q, write k, in v)
+// and dq (read dout, write v, in k); in reverse: dv (read k, write q, in dout) and dk (read v, write dout, in q).
+struct LinRole {
+  const void* read;
+  const void* write;
+  const void* in;
+  void* out;           // [T, H, D] dense
+  int64_t read_ts, write_ts, in_ts;
+  int32_t read_share, write_share, in_share;  // states that share a head
+  int32_t rev;
+  int32_t transposed;  // the walk's state [write][in] is the transpose of the one in memory, [dk][dv]
+  int32_t out_dt;
+  ScanStates init, fin;
+  float* seg;          // [segment slots][H][dk][dv] states at the segments' starts
+};
+
+struct LinScanArgs {
+  LinRole role[3];
+  const float* log_decay;
+  const int32_t* cu;    // [N + 1]
+  const int32_t* live;  // slot of each sequence: outside [0, live_slots) marks a padded one; or null
+  int64_t live_slots, total;
+  int32_t N, H, in_dt;
+  float scale;
+  int32_t seg_chunks, whole;  // LinPlan
+  int32_t local;              // the segments' first walk
+};
+
+// Sums the gradients of the states that share a head.
+struct LinSumArgs {
+  const float* each;  // [T, heads, share, D]
+  void* out;          // [T, heads, D]
+  int64_t items;      // T heads D / 4
+  int32_t share, D, out_dt;
+};
+
+// The norm and rotation of queries (index 0) and keys (1), forward (x to y) or backward (dy and x to y).
+struct QkArgs {
+  const void* x[2];
+  const void* dy[2];
+  void* y[2];
+  const float* w[2];
+  const int32_t* pos;  // [axes][T]
+  const float* freq;
+  float* part;         // [blocks][2][d] partial weight gradients
+  float* dw[2];
+  int64_t x_ts[2], dy_ts[2], y_ts[2];
+  int64_t T;
+  int32_t heads[2];
+  int32_t d, rot, neighbours, in_dt;
+  int32_t tokens;      // of a workgroup's turn
+  float eps;
+  uint32_t axis[8];    // two bits a pair
+};
+
 // Each returns hipSuccess or the launch error.
 hipError_t launch_decode(const DecodeArgs& a, int state_dt, int D, hipStream_t s);
 // state_dt: dtype of the checkpoint pool a.d.pool; with a.read_pool set the
@@ -222,6 +293,19 @@ hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
 bool norm_slice_fits(int n);
 int norm_bwd_blocks(int64_t rows, int N, int groups);
 int64_t norm_sum_work_items(int N);  // threads of the kernel that adds dw and db: fewer than 2^32
+hipError_t launch_linear_step(const LinStepArgs& a, int state_dt, int D, hipStream_t s);
+// How a walk is cut: chunks of 64 tokens a segment (0: whole sequences), and the most segments that a sequence may have and
+// stay whole.
+struct LinPlan {
+  int seg_chunks, whole;
+};
+LinPlan linear_plan(int64_t N, int64_t total, int H, int roles);
+hipError_t launch_linear_scan(LinScanArgs a, bool bf, int D, int roles, hipStream_t s);
+// The segments' states of role 0 (and role 1 where `both`), then the roles' outputs.
+hipError_t launch_linear_sum(const LinSumArgs& a, hipStream_t s);
+hipError_t launch_qk(QkArgs a, hipStream_t s);
+hipError_t launch_qk_bwd(QkArgs a, hipStream_t s);
+int qk_bwd_blocks(int64_t T, int heads, int d);
 size_t m2_lds_bytes(int P, int N, int L, int T, int heads_per_group);
 
 // Dynamic LDS of the speculative-decode kernel; launches need <= kSpecMaxLds.

@@ -1,0 +1,521 @@
+// Linear attention with a fixed decay a head over packed sequences, forward
+// and backward.
+//
+// Per head, S_t = e^g S_{t-1} + k_t v_t^T and o_t = scale S_t^T q_t.  Over a
+// chunk of 64 tokens (i, j from 0) with S before it and p[m] = e^{g m}:
+//     o_i = scale (p[i+1] S^T q_i + sum_{j<=i} p[i-j] (q_i.k_j) v_j)
+//     S'  = p[64] S + sum_j p[63-j] k_j v_j^T.
+// The gradients are walks of the same form with the tensors in other places:
+// with do the gradient of o and dS that of the state behind a chunk,
+//     dq_i = scale (p[i+1] S do_i + sum_{j<=i} p[i-j] (do_i.v_j) k_j)
+//     dv_j = p[63-j] dS^T k_j + scale sum_{i>=j} p[i-j] (k_j.q_i) do_i
+//     dk_j = p[63-j] dS  v_j + scale sum_{i>=j} p[i-j] (v_j.do_i) q_i
+//     dS  <- p[64] dS + scale sum_i p[i+1] q_i do_i^T.
+// So one kernel has a read, a write and an input tensor (q, k, v for o) and a
+// direction, and a backward pass runs three of these walks side by side.  The
+// p[m] are a table of 65 numbers for all chunks; exponents never grow.
+//
+// A workgroup walks one head of a sequence (or segment) with the state in
+// accumulators, transposed so that it meets the read vectors straight from
+// them: lane l holds the rows 8 (l / 16) + .. of column l % 16.  All operands
+// of a chunk lie in LDS as they do in memory, row by row; operands that run
+// over tokens are read transposed (the 16-bit transposing LDS reads), so nothing
+// is stored twice.  Blocks of 8 values of a row are permuted by the row's number
+// so that both kinds of reads meet all banks.  The next chunk is fetched into
+// registers under the work on this one.
+//
+// Where there are too few walks for the chip, sequences are cut into segments:
+// a first walk finds each segment's own end state, a small kernel chains them,
+// and the second walk starts every segment from its true state.
+//
+// Rounding (bf16 inputs and outputs): products of two inputs are exact in FP32.
+// The state is FP32, and its updates take the weighted inputs in three bf16
+// terms, all their 24 bits, with exact write vectors.  For the output alone the
+// state and the weighted products are taken in two bf16 terms, to 2^-16 of each,
+// where the output's own rounding is 2^-9.  Any other types take the FP32 MFMA
+// throughout.
+#include <algorithm>
+
+#include "gdn_m2scan.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int Q = kScanChunk;
+
+template <bool BF, int D, bool OUT>
+struct LinGeom {
+  typedef typename Frag<BF>::E E;
+  static constexpr int PT = D == 128 ? 2 : 1;          // 16-column tiles of a wave
+  static constexpr int NW = D / (16 * PT);             // waves
+  static constexpr int THREADS = 64 * NW;
+  static constexpr int NT = D / 16, KB = (D + 31) / 32;
+  static constexpr int LD = BF ? D : D + 4;            // rows of the operands
+  static constexpr int LDP = Q + (BF ? 8 : 4);         // rows of the weighted products
+  static constexpr int TERMS = BF ? 2 : 1;             // of those
+  static constexpr int W0 = OUT ? Q * LD : 0, X0 = W0 + Q * LD, P0 = X0 + Q * LD;
+  static constexpr int ELEMS = P0 + (OUT ? TERMS * Q * LDP : 0);
+  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + (Q + 4) * 4;
+  static constexpr int VPR = D / 8;                    // 8-element vectors of a row
+  static constexpr int SV = Q * VPR / THREADS;         // and those that a thread stages of an operand
+  static_assert(SV * THREADS == Q * VPR && ELEMS * sizeof(E) % 16 == 0, "whole vectors");
+};
+
+// Where the 8-value block c of row t lies: blocks are permuted by the row, so
+// that 16 rows of one block, and 4 rows of 4 blocks, meet all banks.
+template <bool BF, int D>
+__device__ __forceinline__ int block_at(int t, int c) {
+  if constexpr (!BF) return t * (D + 4) + 8 * c;
+  const int f = D == 128 ? (t & 3) << 2 | (t >> 2 & 3) : D == 64 ? (t >> 1 & 1) << 2 | (t >> 2 & 3) : D == 32 ? t >> 2 & 3 : t >> 3 & 1;
+  return t * D + ((c ^ f) << 3);
+}
+
+// Four 16-bit values of one column, from four rows of 16 columns of which lane
+// l of 16 points at row l / 4, columns 4 (l % 4) and on.
+__device__ __forceinline__ u32x2 read_transposed(const uint16_t* p) {
+  typedef short i16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) i16x4* Lds;
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(const_cast<uint16_t*>(p))));
+}
+
+template <bool BF, int D, bool OUT>
+__global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 128 ? 2 : 1)) gdn_linear_walk_kernel(const LinScanArgs a) {
+  using W = LinGeom<BF, D, OUT>;
+  typedef typename W::E E;
+  constexpr int PT = W::PT, NW = W::NW, NT = W::NT, KB = W::KB, LD = W::LD, LDP = W::LDP, THREADS = W::THREADS, VPR = W::VPR, SV = W::SV;
+  extern __shared__ __align__(16) unsigned char smem[];
+  E* const s_r = reinterpret_cast<E*>(smem);
+  E* const s_w = reinterpret_cast<E*>(smem) + W::W0;
+  E* const s_x = reinterpret_cast<E*>(smem) + W::X0;
+  E* const s_p = reinterpret_cast<E*>(smem) + W::P0;  // [TERMS][64][LDP]
+  float* const s_e = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E));  // p[0..64]
+
+  const LinRole& ro = a.role[blockIdx.y];
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool rev = ro.rev;
+  const int u = a.seg_chunks > 0 ? (int)blockIdx.x : xcd_unit(blockIdx.x, gridDim.x);
+  const int slot = u / a.H, h = u - slot * a.H;
+  Piece sg;
+  if (a.seg_chunks > 0) {
+    sg = find_piece(a.cu, a.N, a.total, slot, a.seg_chunks * Q);
+    if (sg.seq < 0) return;
+    if (sg.count <= a.whole) {  // its first segment's workgroup takes it whole
+      if (sg.index > 0) return;
+      sg.count = 1;
+    }
+  } else {
+    sg.seq = slot;
+    sg.begin = token_at(a.cu, slot, a.total);
+    sg.len = max(token_at(a.cu, slot + 1, a.total) - sg.begin, (int64_t)0);
+    sg.index = 0;
+    sg.count = 1;
+  }
+  const bool last_seg = rev ? sg.index == 0 : sg.index == sg.count - 1;
+  if (a.local && last_seg) return;  // nothing starts from this segment's end
+  const int chunks = (int)((sg.len + Q - 1) / Q);
+  const int c_lo = sg.index * a.seg_chunks;
+  const int c_hi = sg.count > 1 ? min(chunks, c_lo + a.seg_chunks) : chunks;
+  const int p0 = wave * 16 * PT;  // the wave's columns
+  const int64_t out_ts = (int64_t)a.H * D;
+
+  if (!state_live(a.live, a.live_slots, sg.seq)) {  // a padded sequence: zero outputs, no state
+    if (OUT)
+      for (int64_t i = tid; i < (int64_t)(c_hi - c_lo) * Q * D; i += THREADS) {
+        const int64_t t = sg.begin + (int64_t)c_lo * Q + i / D;
+        if (t < sg.begin + sg.len) store_elem(ro.out, t * out_ts + h * D + i % D, 0.f, ro.out_dt);
+      }
+    if (OUT && ro.fin.base != nullptr && ro.fin.slots == nullptr && last_seg)
+      for (int i = tid; i < D * D; i += THREADS) store_elem(ro.fin.base, ((int64_t)sg.seq * a.H + h) * D * D + i, 0.f, ro.fin.dtype);
+    return;
+  }
+
+  for (int m = tid; m <= Q; m += THREADS)  // a product of 0 and an infinite decay is to be 0
+    s_e[m] = (float)exp2(fmax((double)a.log_decay[h], -1e300) * 1.4426950408889634 * m);
+
+  // The state S[nt][pt][r]: its row (a value of the write vector) is row_of(nt, 4 q + r), its column p0 + 16 pt + l16.
+  f32x4 S[NT][PT];
+  auto row_of = [&](int nt, int m) { return D == 16 ? m : 32 * (nt >> 1) + 8 * (m >> 2) + 4 * (nt & 1) + (m & 3); };
+  const int64_t sn = ro.transposed ? 1 : D, sp = ro.transposed ? D : 1;
+  const int64_t state_at = 4 * q * (D == 16 ? 1 : 2) * sn + (p0 + l16) * sp;  // of S[0][0][0]
+  auto load_as = [&](const void* base, int64_t unit, auto type) __attribute__((always_inline)) {  // all loads before the first use
+    constexpr int DT = decltype(type)::value;
+    uint32_t e[NT][PT][4];
+    const int64_t at = (unit * a.H + h) * D * D + state_at;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) e[nt][pt][r] = in_bits<DT>(base, at + row_of(nt, r) * sn + 16 * pt * sp);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+        S[nt][pt] = f32x4{in_value<DT>(e[nt][pt][0]), in_value<DT>(e[nt][pt][1]), in_value<DT>(e[nt][pt][2]), in_value<DT>(e[nt][pt][3])};
+  };
+  auto store_as = [&](void* base, int64_t unit, auto type) __attribute__((always_inline)) {
+    constexpr int DT = decltype(type)::value;
+    const int64_t at = (unit * a.H + h) * D * D + state_at;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) store_elem(base, at + row_of(nt, r) * sn + 16 * pt * sp, S[nt][pt][r], DT);
+  };
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int pt = 0; pt < PT; ++pt) S[nt][pt] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // ---- a chunk's operands: from memory a chunk ahead, in registers, then to LDS
+  Frag<BF> vr[OUT ? SV : 1], vw[SV], vx[SV];
+  const int st = tid / VPR, sc = tid % VPR;  // the thread's first row, and its block of the row
+  auto fetch_one = [&](Frag<BF> (&v)[SV], const void* base, int64_t ts, int64_t t0, int head, int len) __attribute__((always_inline)) {
+    if constexpr (BF) {
+      const auto w = window(base, t0 * ts + head * D, 2, 2 * ((len - 1) * ts + D));
+      const int off = 2 * (st * (int)ts + 8 * sc);
+#pragma unroll
+      for (int k = 0; k < SV; ++k) v[k].v = __builtin_amdgcn_raw_buffer_load_b128(w, off + 2 * k * (THREADS / VPR) * (int)ts, 0, 0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < SV; ++k) {
+        const int t = st + k * (THREADS / VPR);
+        v[k] = Frag<BF>::zero();
+        if (t < len) v[k] = frag_from<BF>(base, t0 * ts + head * D, t * (uint32_t)ts + 8 * sc, a.in_dt);
+      }
+    }
+  };
+  auto fetch = [&](int c) __attribute__((always_inline)) {
+    const int64_t t0 = sg.begin + (int64_t)c * Q;
+    const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
+    if constexpr (OUT) fetch_one(vr, ro.read, ro.read_ts, t0, h / ro.read_share, len);
+    fetch_one(vw, ro.write, ro.write_ts, t0, h / ro.write_share, len);
+    fetch_one(vx, ro.in, ro.in_ts, t0, h / ro.in_share, len);
+  };
+  auto commit = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < SV; ++k) {
+      const int at = block_at<BF, D>(st + k * (THREADS / VPR), sc);
+      if constexpr (OUT) *reinterpret_cast<Frag<BF>*>(s_r + at) = vr[k];
+      *reinterpret_cast<Frag<BF>*>(s_w + at) = vw[k];
+      *reinterpret_cast<Frag<BF>*>(s_x + at) = vx[k];
+    }
+  };
+  // ---- fragments
+  // row t, the values of block kb in the order of the state's rows
+  auto row_frag = [&](const E* s, int t, int kb) __attribute__((always_inline)) {
+    if constexpr (D >= 32) return Frag<BF>::load(s + block_at<BF, D>(t, 4 * kb + q));
+    Frag<BF> f = Frag<BF>::zero();
+    const E* p = s + block_at<BF, D>(t, q >> 1) + 4 * (q & 1);
+    if constexpr (BF) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+      f.v[0] = v[0];
+      f.v[1] = v[1];
+    } else {
+      f.a = *reinterpret_cast<const f32x4*>(p);
+    }
+    return f;
+  };
+  // tokens 32 ks + 8 q and on of the column that lane l16 gets from four blocks of four columns, of which it points at `col`
+  auto column_frag = [&](const E* s, int ks, int col, int mine) __attribute__((always_inline)) {
+    if constexpr (BF) {
+      const int t = 32 * ks + 8 * q + (l16 >> 2);
+      const u32x2 v0 = read_transposed(s + block_at<BF, D>(t, col >> 3) + (col & 4));
+      const u32x2 v1 = read_transposed(s + block_at<BF, D>(t + 4, col >> 3) + (col & 4));
+      return Frag<BF>{u32x4{v0[0], v0[1], v1[0], v1[1]}};
+    } else {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = s[(32 * ks + 8 * q + e) * LD + mine];
+      return Frag<BF>::round(f);
+    }
+  };
+  auto write_frag = [&](int nt, int ks) __attribute__((always_inline)) { return column_frag(s_w, ks, row_of(nt, 4 * (l16 & 3)), row_of(nt, l16)); };
+  auto in_frag = [&](int pt, int ks) __attribute__((always_inline)) { return column_frag(s_x, ks, p0 + 16 * pt + 4 * (l16 & 3), p0 + 16 * pt + l16); };
+
+  if (OUT)  // the products beyond the diagonal that share an operand with one on it stay zero
+    for (int i = tid; i < W::TERMS * Q * LDP; i += THREADS) s_p[i] = 0;
+  const int steps = c_hi - c_lo;
+  if (steps > 0) fetch(rev ? c_hi - 1 : c_lo);
+  if (!a.local && (sg.count > 1 || ro.init.base != nullptr)) {
+    const bool cut = sg.count > 1;
+    const void* const base = cut ? ro.seg : ro.init.base;
+    const int64_t unit = cut ? slot : ro.init.slots != nullptr ? ro.init.slots[sg.seq] : sg.seq;
+    const int dt = cut ? (int)GDN_F32 : ro.init.dtype;
+    if (dt == GDN_F32) load_as(base, unit, std::integral_constant<int, GDN_F32>{});
+    else if (dt == GDN_BF16) load_as(base, unit, std::integral_constant<int, GDN_BF16>{});
+    else load_as(base, unit, std::integral_constant<int, GDN_F16>{});
+  }
+
+  for (int step = 0; step < steps; ++step) {
+    const int c = rev ? c_hi - 1 - step : c_lo + step;
+    const int64_t t0 = sg.begin + (int64_t)c * Q;
+    const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
+
+    __syncthreads();  // the chunk before is done with LDS
+    commit();
+    __syncthreads();
+    __builtin_amdgcn_sched_barrier(0);
+    fetch(min(max(rev ? c - 1 : c + 1, c_lo), c_hi - 1));
+    __builtin_amdgcn_sched_barrier(0);
+
+    Frag<BF> xf[2][PT];
+    if constexpr (OUT) {
+      // the weighted products of read and write vectors, 16 x 16 tiles on and below the diagonal (above it in reverse)
+      for (int t = wave; t < 10; t += NW) {
+        const int i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t - i * (i + 1) / 2;
+        const int rt = rev ? j : i, ct = rev ? i : j;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) acc = frag_mma(acc, row_frag(s_w, 16 * ct + l16, kb), row_frag(s_r, 16 * rt + l16, kb));
+        float f[4];
+        const int at = 16 * rt + l16, from = 16 * ct + 4 * q;  // token of the read vector, first of the write vectors
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int m = rev ? from + r - at : at - from - r;
+          f[r] = m >= 0 ? acc[r] * a.scale * s_e[max(m, 0)] : 0.f;
+        }
+        E* d = s_p + at * LDP + from;
+        if constexpr (BF) {
+          const u32x2 high = {pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
+          *reinterpret_cast<u32x2*>(d) = high;
+          bf16_rest(high[0], f[0], f[1]);
+          bf16_rest(high[1], f[2], f[3]);
+          *reinterpret_cast<u32x2*>(d + Q * LDP) = u32x2{pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
+        } else {
+          *reinterpret_cast<f32x4*>(d) = f32x4{f[0], f[1], f[2], f[3]};
+        }
+      }
+      // the state's part of the output, transposed: acc[pt][rt][r] = (column 16 pt + 4 q + r, token 16 rt + l16)
+      f32x4 acc[PT][4];
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) acc[pt][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        typedef Split<BF, 2> Terms;
+        Terms sf[PT];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] = S[2 * kb][pt][e];
+            f[4 + e] = 2 * kb + 1 < NT ? S[2 * kb + 1 < NT ? 2 * kb + 1 : 0][pt][e] : 0.f;
+          }
+          sf[pt] = Terms::of(f);
+        }
+        Frag<BF> rf[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) rf[rt] = row_frag(s_r, 16 * rt + l16, kb);
+#pragma unroll
+        for (int k = Terms::K - 1; k >= 0; --k)
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], sf[pt].t[k], rf[rt]);
+      }
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const int t = 16 * rt + l16;
+        const float f = rev ? s_e[max(len - 1 - t, 0)] : a.scale * s_e[t + 1];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) acc[pt][rt] *= f;
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) xf[ks][pt] = in_frag(pt, ks);
+      __syncthreads();  // the products are there
+#pragma unroll
+      for (int k = W::TERMS - 1; k >= 0; --k)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) {
+            if (rev ? (ks == 0 && rt >= 2) : (ks == 1 && rt < 2)) continue;  // all beyond the diagonal
+            const Frag<BF> pf = Frag<BF>::load(s_p + (k * Q + 16 * rt + l16) * LDP + 32 * ks + 8 * q);
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[ks][pt], pf);
+          }
+      if (BF && ro.out_dt == GDN_BF16) {
+        const auto w = window(ro.out, t0 * out_ts + h * D + p0, 2, 2 * ((len - 1) * out_ts + 16 * PT));
+        const int off = 2 * (l16 * (int)out_ts + 4 * q);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) {
+            const f32x4 v = acc[pt][rt];
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2<GDN_BF16>(v[0], v[1]), pack2<GDN_BF16>(v[2], v[3])}, w,
+                                                  off + 2 * (16 * rt * (int)out_ts + 16 * pt), 0, 0);
+          }
+      } else {
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const int t = 16 * rt + l16;
+          if (t < len)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) {
+              const float v[4] = {acc[pt][rt][0], acc[pt][rt][1], acc[pt][rt][2], acc[pt][rt][3]};
+              store_vec<4>(ro.out, (t0 + t) * out_ts + h * D + p0 + 16 * pt + 4 * q, v, ro.out_dt, true);
+            }
+        }
+      }
+    }
+
+    // the state after the chunk
+    const float dec = s_e[len];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) S[nt][pt] *= dec;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      if (32 * ks >= len) continue;
+      float wgt[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int t = 32 * ks + 8 * q + e;
+        wgt[e] = rev ? a.scale * s_e[t + 1] : t < len ? s_e[max(len - 1 - t, 0)] : 0.f;
+      }
+      Split<BF> xs[PT];
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        float f[8];
+        if constexpr (OUT) xf[ks][pt].widen(f);
+        else in_frag(pt, ks).widen(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= wgt[e];
+        xs[pt] = Split<BF>::of(f);
+      }
+      constexpr int NG = NT < 4 ? NT : 4;  // tiles at a time, their terms apart: a product never follows the one it adds to
+#pragma unroll
+      for (int ng = 0; ng < NT; ng += NG) {
+        Frag<BF> wf[NG];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) wf[i] = write_frag(ng + i, ks);
+#pragma unroll
+        for (int k = Split<BF>::K - 1; k >= 0; --k)
+#pragma unroll
+          for (int i = 0; i < NG; ++i)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) S[ng + i][pt] = frag_mma(S[ng + i][pt], wf[i], xs[pt].t[k]);
+      }
+    }
+  }
+
+  if (a.local || (ro.fin.base != nullptr && last_seg && (rev || sg.len > 0))) {
+    void* const base = a.local ? ro.seg : ro.fin.base;
+    const int64_t unit = a.local ? slot : ro.fin.slots != nullptr ? ro.fin.slots[sg.seq] : sg.seq;
+    const int dt = a.local ? (int)GDN_F32 : ro.fin.dtype;
+    if (dt == GDN_F32) store_as(base, unit, std::integral_constant<int, GDN_F32>{});
+    else if (dt == GDN_BF16) store_as(base, unit, std::integral_constant<int, GDN_BF16>{});
+    else store_as(base, unit, std::integral_constant<int, GDN_F16>{});
+  }
+}
+
+// ------------------------------------------------------------------ chain
+// Turns the segments' own end states into the states they start from, in
+// place: per (sequence, head), four state elements a thread.
+__global__ void __launch_bounds__(256) gdn_linear_chain_kernel(const LinScanArgs a, int elems, int parts) {
+  const LinRole& ro = a.role[blockIdx.y];
+  const int unit = blockIdx.x / parts, seq = unit / a.H, h = unit - seq * a.H;
+  const int i = ((blockIdx.x - unit * parts) * 256 + threadIdx.x) * 4;
+  if (i >= elems || !state_live(a.live, a.live_slots, seq)) return;
+  const int P = a.seg_chunks * Q;
+  const int64_t b = token_at(a.cu, seq, a.total), e = token_at(a.cu, seq + 1, a.total);
+  const int count = (int)max((e - b + P - 1) / P, (int64_t)1);
+  if (count <= a.whole) return;
+  f32x4 S = {0.f, 0.f, 0.f, 0.f};
+  if (ro.init.base != nullptr) {
+    float f[4];
+    load_vec<4>(ro.init.base, ((ro.init.slots != nullptr ? ro.init.slots[seq] : (int64_t)seq) * a.H + h) * elems + i, ro.init.dtype, f);
+    S = f32x4{f[0], f[1], f[2], f[3]};
+  }
+  const double g = fmax((double)a.log_decay[h], -1e300) * 1.4426950408889634;
+  const float whole = (float)exp2(g * P);
+  const float tail = (float)exp2(g * (double)(e - b - (int64_t)(count - 1) * P));  // the sequence's last segment
+  const int64_t s0 = seq + b / P;
+  for (int k = 0; k < count; ++k) {
+    const int at = ro.rev ? count - 1 - k : k;
+    f32x4* p = reinterpret_cast<f32x4*>(ro.seg + ((s0 + at) * a.H + h) * elems + i);
+    if (k + 1 < count) {
+      const f32x4 own = *p;
+      *p = S;
+      S = S * (at == count - 1 ? tail : whole) + own;
+    } else {
+      *p = S;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ shared heads
+__global__ void __launch_bounds__(256) gdn_linear_sum_kernel(const LinSumArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.items) return;
+  const int v = a.D / 4;
+  const int64_t head = i / v;  // of all tokens
+  const float* p = a.each + head * a.share * a.D + (i - head * v) * 4;
+  f32x4 sum = *reinterpret_cast<const f32x4*>(p);
+  for (int k = 1; k < a.share; ++k) sum += *reinterpret_cast<const f32x4*>(p + (int64_t)k * a.D);
+  const float f[4] = {sum[0], sum[1], sum[2], sum[3]};
+  store_vec<4>(a.out, i * 4, f, a.out_dt, true);
+}
+
+template <bool BF, int D, bool OUT>
+hipError_t walk(const LinScanArgs& a, int roles, hipStream_t s) {
+  using W = LinGeom<BF, D, OUT>;
+  const int64_t slots = a.seg_chunks > 0 ? scan_slots(a.N, a.total, (int64_t)a.seg_chunks * Q) : a.N;
+  auto* k = gdn_linear_walk_kernel<BF, D, OUT>;
+  static std::atomic<uint64_t> allowed{0};
+  const hipError_t e = allow_lds(reinterpret_cast<const void*>(k), W::LDS, allowed);
+  if (e != hipSuccess) return e;
+  k<<<dim3((unsigned)(slots * a.H), (unsigned)roles), W::THREADS, W::LDS, s>>>(a);
+  return hipGetLastError();
+}
+
+template <bool OUT>
+hipError_t walk_any(const LinScanArgs& a, bool bf, int D, int roles, hipStream_t s) {
+  if (bf) return D == 16 ? walk<true, 16, OUT>(a, roles, s) : D == 32 ? walk<true, 32, OUT>(a, roles, s) : D == 64 ? walk<true, 64, OUT>(a, roles, s) : walk<true, 128, OUT>(a, roles, s);
+  return D == 16 ? walk<false, 16, OUT>(a, roles, s) : D == 32 ? walk<false, 32, OUT>(a, roles, s) : D == 64 ? walk<false, 64, OUT>(a, roles, s) : walk<false, 128, OUT>(a, roles, s);
+}
+
+}  // namespace
+
+LinPlan linear_plan(int64_t N, int64_t total, int H, int roles) {
+  LinPlan p{0, 1};
+  const int64_t chunks = (total + Q - 1) / Q, walks = N * H * roles;
+  if (walks < 512 && chunks > 8) {
+    const int64_t per = chunks * H * roles / 1024 + 1;
+    p.seg_chunks = (int)std::max<int64_t>(4, per);
+  }
+  return p;
+}
+
+// The walks of roles 0 and on; backward, roles 1 and 2 go the same way over the
+// same states, so the segments' first walk and the chain take roles 0 and 1.
+hipError_t launch_linear_scan(LinScanArgs a, bool bf, int D, int roles, hipStream_t s) {
+  if (a.seg_chunks > 0) {
+    const int passes = std::min(roles, 2);
+    a.local = 1;
+    hipError_t e = walk_any<false>(a, bf, D, passes, s);
+    if (e != hipSuccess) return e;
+    const int parts = (D * D + 1023) / 1024;
+    gdn_linear_chain_kernel<<<dim3((unsigned)((int64_t)a.N * a.H * parts), (unsigned)passes), 256, 0, s>>>(a, D * D, parts);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.local = 0;
+  }
+  return walk_any<true>(a, bf, D, roles, s);
+}
+
+hipError_t launch_linear_sum(const LinSumArgs& a, hipStream_t s) {
+  gdn_linear_sum_kernel<<<(unsigned)((a.items + 255) / 256), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace gdn

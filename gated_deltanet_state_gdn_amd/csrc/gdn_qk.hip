@@ -1,0 +1,310 @@
+// RMS norm of every head of the queries and keys and the rotation by the
+// token's position behind it, in one pass, and its reverse.
+//
+// Per head of d values, with r = (mean x^2 + eps)^-1/2 and n = x r w, pair i of
+// the first `rot` values turns by the angle p f_i:
+//     (a, b) -> (a cos - b sin, b cos + a sin).
+// In reverse the gradient turns back, dn = rot(dy, -angle), and with xh = x r
+//     dw = sum dn xh,   dx = r (dn w - xh mean(dn w xh)),
+// where mean(dn w xh) = r mean(dn w x): both sums of a row are taken at once.
+//
+// A row (one head of one token) lies on d / 8 lanes rounded up to a power of
+// two, 8 values a lane as two vectors of 4: those of four pairs, so a rotation
+// never leaves its lane.  A workgroup takes a few tokens at a time: first its
+// threads form the tokens' cosines and sines, one pair a thread, in LDS (the
+// angle in FP64, reduced to a quarter turn before it is rounded to FP32), then
+// its rows of lanes go over all heads of these tokens, so that a token's angles
+// are formed once for all its heads.
+#include <algorithm>
+
+#include "gdn_device.h"
+#include "gdn_launch.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kQkThreads = 256;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over LPR neighbouring lanes, in every one of them.
+template <int LPR>
+__device__ __forceinline__ float lanes_sum(float x) {
+  if constexpr (LPR >= 2) x = dpp_add<0xB1>(x);    // lane ^ 1
+  if constexpr (LPR >= 4) x = dpp_add<0x4E>(x);    // lane ^ 2
+  if constexpr (LPR >= 8) x = dpp_add<0x141>(x);   // mirrored in 8: the other quad
+  if constexpr (LPR >= 16) x = dpp_add<0x140>(x);  // mirrored in 16: the other half
+  if constexpr (LPR >= 32) {
+    const unsigned a = __builtin_bit_cast(unsigned, x);
+    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    unsigned r0 = r[0], r1 = r[1];
+    asm volatile("" : "+v"(r0), "+v"(r1));
+    x = __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+  }
+  return x;
+}
+
+// cos and sin of p f: turns in FP64, of which the whole and then the quarter
+// ones are dropped exactly; what is left, at most an eighth, is rounded to
+// FP32.
+__device__ __forceinline__ void cos_sin(int p, float f, float& c, float& s) {
+  double t = (double)p * (double)f * 0.15915494309189533577;
+  t = 4.0 * (t - rint(t));
+  const double quarter = rint(t);
+  float sr, cr;
+  sincospif(0.5f * (float)(t - quarter), &sr, &cr);
+  const int k = (int)quarter;
+  c = k & 1 ? sr : cr;
+  s = k & 1 ? cr : sr;
+  if ((k + 1) & 2) c = -c;
+  if (k & 2) s = -s;
+}
+
+template <int IDT, int LPR, bool NB, bool BWD>
+__global__ void __launch_bounds__(kQkThreads) gdn_qk_kernel(const QkArgs a) {
+  constexpr int G = kQkThreads / LPR;  // rows at a time
+  constexpr int U = 4;                 // and times that many in flight
+  extern __shared__ __align__(16) float s_turn[];  // [tokens][2][rot / 2]; backward also [G][d]
+  const int tid = threadIdx.x, r = tid % LPR, row0 = tid / LPR + G * blockIdx.y, step = G * gridDim.y;
+  const int half = a.rot / 2, d = a.d;
+  const bool on = 8 * r < d, turned = 8 * r < a.rot;
+  // the lane's two vectors of 4
+  const int o1 = !on ? 0 : NB || !turned ? 8 * r : 4 * r, o2 = !on ? 4 : NB || !turned ? 8 * r + 4 : half + 4 * r;
+  float acc[BWD ? 2 : 1][8];
+  if constexpr (BWD)
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[s][e] = 0.f;
+  float w[2][8];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[s][e] = a.w[s][o1 + e];
+      w[s][4 + e] = a.w[s][o2 + e];
+    }
+  const float inv_d = 1.f / (float)d;
+
+  for (int64_t t0 = (int64_t)blockIdx.x * a.tokens; t0 < a.T; t0 += (int64_t)gridDim.x * a.tokens) {
+    const int n = (int)min((int64_t)a.tokens, a.T - t0);
+    if (BWD) __syncthreads();  // the tokens before are done with
+    for (int i = tid; i < n * half; i += kQkThreads) {
+      const int t = i / half, p = i - t * half;
+      const int axis = (a.axis[p >> 4] >> (2 * (p & 15))) & 3;
+      float c, s;
+      cos_sin(a.pos[axis * a.T + t0 + t], a.freq[p], c, s);
+      s_turn[2 * t * half + p] = c;
+      s_turn[(2 * t + 1) * half + p] = BWD ? -s : s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int heads = a.heads[s], rows = n * heads;
+      const int dt = step / heads, dh = step - dt * heads;
+      int t = row0 / heads, h = row0 - t * heads;
+      for (int row = row0; row < rows; row += U * step) {
+        int at[U], ah[U];
+        InVec<IDT, 4> x1[U], x2[U], g1[BWD ? U : 1], g2[BWD ? U : 1];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          at[u] = t;
+          ah[u] = h;
+          t += dt;
+          h += dh;
+          if (h >= heads) {
+            h -= heads;
+            ++t;
+          }
+          const int64_t tok = t0 + min(at[u], n - 1);  // rows past the last are loaded as its token's
+          const int64_t xo = tok * a.x_ts[s] + (int64_t)ah[u] * d;
+          x1[u].load(a.x[s], xo + o1);
+          x2[u].load(a.x[s], xo + o2);
+          if constexpr (BWD) {
+            const int64_t go = tok * a.dy_ts[s] + (int64_t)ah[u] * d;
+            g1[u].load(a.dy[s], go + o1);
+            g2[u].load(a.dy[s], go + o2);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (row + u * step >= rows) break;
+          float x[8], y[8];
+          {
+            float f[4], f2[4];
+            x1[u].widen(f);
+            x2[u].widen(f2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[e] = on ? f[e] : 0.f;
+              x[4 + e] = on ? f2[e] : 0.f;
+            }
+          }
+          const float* cs = s_turn + 2 * at[u] * half + 4 * (turned ? r : 0);
+          float c[4], sn[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            c[e] = turned ? cs[e] : 1.f;
+            sn[e] = turned ? cs[half + e] : 0.f;
+          }
+          auto turn = [&](float (&v)[8]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = NB ? 2 * e : e, j = NB ? 2 * e + 1 : 4 + e;
+              const float p = v[i], q = v[j];
+              v[i] = p * c[e] - q * sn[e];
+              v[j] = q * c[e] + p * sn[e];
+            }
+          };
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+          if constexpr (!BWD) {
+            const float rstd = rsqrtf(lanes_sum<LPR>(sum) * inv_d + a.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = x[e] * rstd * w[s][e];
+            turn(y);
+          } else {
+            float f[4], f2[4];
+            g1[u].widen(f);
+            g2[u].widen(f2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[e] = on ? f[e] : 0.f;
+              y[4 + e] = on ? f2[e] : 0.f;
+            }
+            turn(y);
+            float dot = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = fmaf(y[e] * w[s][e], x[e], dot);
+            const float rstd = rsqrtf(lanes_sum<LPR>(sum) * inv_d + a.eps);
+            const float m = lanes_sum<LPR>(dot) * rstd * inv_d;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float xh = x[e] * rstd;
+              acc[BWD ? s : 0][e] = fmaf(y[e], xh, acc[BWD ? s : 0][e]);
+              y[e] = rstd * fmaf(-xh, m, y[e] * w[s][e]);
+            }
+          }
+          if (on) {
+            const int64_t yo = (t0 + at[u]) * a.y_ts[s] + (int64_t)ah[u] * d;
+            const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+            store_vec<4>(a.y[s], yo + o1, lo, IDT, true);
+            store_vec<4>(a.y[s], yo + o2, hi, IDT, true);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (BWD) {
+    // the workgroup's sums over its rows of lanes, in order
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      __syncthreads();
+      float* row = s_turn + (tid / LPR) * d;
+      if (on)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          row[o1 + e] = acc[s][e];
+          row[o2 + e] = acc[s][4 + e];
+        }
+      __syncthreads();
+      if (tid < d) {
+        float sum = 0.f;
+        for (int g = 0; g < G; ++g) sum += s_turn[g * d + tid];
+        a.part[((int64_t)blockIdx.x * 2 + s) * d + tid] = sum;
+      }
+    }
+  }
+}
+
+// Adds the workgroups' partial weight gradients in a fixed order: 16 columns a
+// workgroup, a 16th of the workgroups' sums a row of threads.
+__global__ void __launch_bounds__(256) gdn_qk_sum_kernel(const QkArgs a, int blocks) {
+  __shared__ float s_sum[16][17];
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4, col = blockIdx.x * 16 + x, d = a.d;
+  float sum = 0.f;
+  if (col < 2 * d)
+    for (int b = y; b < blocks; b += 16) sum += a.part[(int64_t)b * 2 * d + col];
+  s_sum[y][x] = sum;
+  __syncthreads();
+  if (y == 0 && col < 2 * d) {
+    for (int k = 1; k < 16; ++k) sum += s_sum[k][x];
+    (col < d ? a.dw[0] : a.dw[1])[col < d ? col : col - d] = sum;
+  }
+}
+
+int lanes_of_row(int d) {
+  int l = 2;
+  while (8 * l < d) l *= 2;
+  return l;
+}
+
+// Tokens of a workgroup's turn: eight rounds of its rows, so that angles and
+// the barrier behind them are shared, but enough workgroups for the chip.
+int turn_tokens(int64_t T, int heads, int d) {
+  const int rows = kQkThreads / lanes_of_row(d);
+  int64_t t = std::min<int64_t>(16, std::max(1, 8 * rows / heads));
+  return (int)std::max<int64_t>(1, std::min(t, T / 2048));
+}
+
+template <int IDT, int LPR, bool BWD>
+hipError_t launch(const QkArgs& a, dim3 grid, size_t lds, hipStream_t s) {
+  if (a.neighbours) gdn_qk_kernel<IDT, LPR, true, BWD><<<grid, kQkThreads, lds, s>>>(a);
+  else gdn_qk_kernel<IDT, LPR, false, BWD><<<grid, kQkThreads, lds, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int IDT, bool BWD>
+hipError_t launch_lanes(const QkArgs& a, dim3 grid, size_t lds, hipStream_t s) {
+  switch (lanes_of_row(a.d)) {
+    case 2: return launch<IDT, 2, BWD>(a, grid, lds, s);
+    case 4: return launch<IDT, 4, BWD>(a, grid, lds, s);
+    case 8: return launch<IDT, 8, BWD>(a, grid, lds, s);
+    case 16: return launch<IDT, 16, BWD>(a, grid, lds, s);
+    default: return launch<IDT, 32, BWD>(a, grid, lds, s);
+  }
+}
+
+template <bool BWD>
+hipError_t launch_type(const QkArgs& a, dim3 grid, size_t lds, hipStream_t s) {
+  if (a.in_dt == GDN_F32) return launch_lanes<GDN_F32, BWD>(a, grid, lds, s);
+  if (a.in_dt == GDN_BF16) return launch_lanes<GDN_BF16, BWD>(a, grid, lds, s);
+  return launch_lanes<GDN_F16, BWD>(a, grid, lds, s);
+}
+
+}  // namespace
+
+hipError_t launch_qk(QkArgs a, hipStream_t s) {
+  const int heads = a.heads[0] + a.heads[1], rows = kQkThreads / lanes_of_row(a.d);
+  a.tokens = turn_tokens(a.T, heads, a.d);
+  dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens));
+  // few tokens: their heads on several workgroups
+  if (a.T < 512) grid.y = (unsigned)std::min((std::max(a.heads[0], a.heads[1]) + rows - 1) / rows, 64);
+  return launch_type<false>(a, grid, (size_t)a.tokens * a.rot * 4, s);
+}
+
+// Workgroups of the backward pass, each with a partial sum of the weights'
+// gradients: four a compute unit.
+int qk_bwd_blocks(int64_t T, int heads, int d) {
+  const int t = turn_tokens(T, heads, d);
+  return (int)std::min<int64_t>((T + t - 1) / t, 1024);
+}
+
+hipError_t launch_qk_bwd(QkArgs a, hipStream_t s) {
+  const int blocks = a.T > 0 ? qk_bwd_blocks(a.T, a.heads[0] + a.heads[1], a.d) : 0;
+  if (blocks > 0) {
+    a.tokens = turn_tokens(a.T, a.heads[0] + a.heads[1], a.d);
+    const size_t lds = std::max((size_t)a.tokens * a.rot * 4, (size_t)(kQkThreads / lanes_of_row(a.d)) * a.d * 4);
+    const hipError_t e = launch_type<true>(a, dim3((unsigned)blocks), lds, s);
+    if (e != hipSuccess) return e;
+  }
+  gdn_qk_sum_kernel<<<(2 * a.d + 15) / 16, 256, 0, s>>>(a, blocks);
+  return hipGetLastError();
+}
+
+}  // namespace gdn

@@ -486,6 +486,145 @@ gdn_status gdn_layer_norm_backward(const gdn_norm_dims* dims, const void* dy, in
                                    void* dz, int64_t dz_stride, float* dw, float* db, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
+/* -------------------------------------------------------- linear attention
+ * Linear attention whose state decays by a fixed factor a head (retention,
+ * "lightning" attention): with H states of dk x dv and, per token, a query and
+ * a key (dk) and a value (dv),
+ *     S_t = e^{g_h} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
+ * log_decay, float32 [H], holds g_h, usually <= 0 (-infinity: no memory); it is
+ * a constant of the layer and has no gradient here.  q, k and v may have fewer
+ * heads than there are states: state h reads query head h / (H / Hq), key head
+ * h / (H / Hk) and value head h / (H / Hv).  State pools are
+ * [num_slots, H, dk, dv], as those of the gated delta rule, and the three calls
+ * go on from each other's states. */
+typedef struct {
+  int32_t num_heads;   /* H, the heads of o */
+  int32_t num_q_heads; /* each divides H */
+  int32_t num_k_heads;
+  int32_t num_v_heads;
+  int32_t dk; /* dk == dv in {16, 32, 64, 128} */
+  int32_t dv;
+  float scale; /* <= 0 selects dk^-1/2 */
+} gdn_linear_dims;
+
+/* Distances between tokens in elements, for inputs that are slices of wider
+ * rows; 0 stands for dense.  Multiples of 8, at most 2^22. */
+typedef struct {
+  int64_t q; /* >= Hq dk */
+  int64_t k; /* >= Hk dk */
+  int64_t v; /* >= Hv dv */
+} gdn_linear_strides;
+
+/* One token for B sequences: q [B, Hq, dk], k [B, Hk, dk], v [B, Hv, dv]
+ * in_dtype, 16-byte aligned; strides NULL: all dense; out [B, H, dv]. */
+gdn_status gdn_linear_decode_step(const gdn_linear_dims* dims, int32_t B, const void* q,
+                                  const void* k, const void* v, gdn_dtype in_dtype,
+                                  const gdn_linear_strides* strides, const float* log_decay,
+                                  const gdn_pool* state, const int32_t* slot_map, void* out,
+                                  gdn_dtype out_dtype, void* stream);
+
+/* N packed variable-length sequences.
+ *   cu_seqlens  device int32 [N+1], non-decreasing, cu_seqlens[0] = 0,
+ *               cu_seqlens[N] = total_tokens
+ *   q, k, v     [total_tokens, Hq (Hk, Hv), dk (dk, dv)] in_dtype, 16-byte
+ *               aligned; strides NULL: all dense
+ *   state       sequence s starts from slot slot_map[s] and its final state is
+ *               written back there, rounded once per call; a zero-length
+ *               sequence leaves its slot untouched; a slot outside the pool
+ *               marks a padded sequence (zero outputs).  NULL (and slot_map
+ *               NULL): zero initial states, and none kept
+ *   out         [total_tokens, H, dv] out_dtype, dense, 16-byte aligned
+ *   workspace   device scratch of at least the queried size, 256-byte aligned,
+ *               not read before it is written; calls that share one must not
+ *               overlap
+ * bf16 inputs with a bf16 out run on the bf16 matrix instructions (FP32 state
+ * and sums; the state and the decay-weighted products of queries and keys meet
+ * o in two bf16 terms, to 2^-16 of each, and the gradients are formed alike);
+ * any other pair of types runs in FP32 throughout.  Within 64 tokens a NaN or
+ * infinity also reaches earlier tokens of its own sequence. */
+size_t gdn_linear_scan_workspace_bytes(const gdn_linear_dims* dims, int32_t N, int64_t total_tokens);
+gdn_status gdn_linear_scan(const gdn_linear_dims* dims, int32_t N, const int32_t* cu_seqlens,
+                           int64_t total_tokens, const void* q, const void* k, const void* v,
+                           gdn_dtype in_dtype, const gdn_linear_strides* strides,
+                           const float* log_decay, const gdn_pool* state, const int32_t* slot_map,
+                           void* out, gdn_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Gradients of gdn_linear_scan from dout and the forward call's inputs.
+ *   init, slot_map  the states that the forward call started from, as they
+ *               were before it (read only), or both NULL for zero states
+ *   dout        [total_tokens, H, dv] in_dtype, dense, 16-byte aligned
+ *   dfinal      float32 [N, H, dk, dv], gradient of the final states, or NULL
+ *   dq, dk, dv  dense, in_dtype, shaped as the inputs, 16-byte aligned; a shared
+ *               head's gradient is the sum over its states, in a fixed order
+ *               (equal calls give equal bits)
+ *   dinit       float32 [N, H, dk, dv], gradient of the initial states, or NULL
+ * A padded sequence has zero gradients; of a zero-length one dinit is dfinal.
+ * The workspace holds, for each input whose heads are shared, FP32 gradients of
+ * every state's own. */
+size_t gdn_linear_scan_backward_workspace_bytes(const gdn_linear_dims* dims, int32_t N,
+                                                int64_t total_tokens);
+gdn_status gdn_linear_scan_backward(const gdn_linear_dims* dims, int32_t N,
+                                    const int32_t* cu_seqlens, int64_t total_tokens, const void* q,
+                                    const void* k, const void* v, gdn_dtype in_dtype,
+                                    const gdn_linear_strides* strides, const float* log_decay,
+                                    const gdn_pool* init, const int32_t* slot_map, const void* dout,
+                                    const float* dfinal, void* dq, void* dk, void* dv, float* dinit,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------- norm and rotation of q and k
+ * What stands between the projections and a recurrence (or attention): every
+ * head of q and k is normed and rotated by its token's position, in one pass.
+ * With r = (mean(x^2) + eps)^-1/2 over the head's values, n = x r w, and pair i
+ * of the first rotary_dim values (a, b) turned by the angle
+ * positions[axis of i][token] inv_freq[i]:
+ *     (a, b) -> (a cos - b sin, b cos + a sin);
+ * the values behind rotary_dim are left as normed.  Pair i is (i, i +
+ * rotary_dim / 2), or with `neighbours` (2 i, 2 i + 1).  FP32 math; the angle is
+ * formed in FP64, so far positions lose nothing. */
+typedef struct {
+  int64_t tokens;
+  int32_t num_q_heads, num_k_heads; /* >= 1 */
+  int32_t head_dim;   /* a multiple of 8 in [16, 256] */
+  int32_t rotary_dim; /* a multiple of 8 in [8, head_dim] */
+  int32_t neighbours; /* 0: halves of the rotary values pair up, otherwise neighbours */
+  int32_t num_axes;   /* rows of positions, 1 to 4 */
+  const uint8_t* pair_axis; /* HOST pointer, [rotary_dim / 2]: the axis of each pair, < num_axes; NULL: axis 0 */
+} gdn_qk_dims;
+
+/*   q, k       [tokens, heads, head_dim] in_dtype, 16-byte aligned; strides
+ *              between tokens in elements, multiples of 8, 0 stands for dense
+ *   q_weight, k_weight  float32 [head_dim]
+ *   positions  device int32 [num_axes, tokens]
+ *   inv_freq   device float32 [rotary_dim / 2]
+ *   q_out, k_out  shaped and aligned as q and k, in_dtype, with strides of their
+ *              own; q_out may be q and k_out k, element for element
+ * tokens == 0 is a no-op. */
+gdn_status gdn_qk_norm_rope(const gdn_qk_dims* dims, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, gdn_dtype in_dtype, const float* q_weight,
+                            const float* k_weight, float eps, const int32_t* positions,
+                            const float* inv_freq, void* q_out, int64_t q_out_stride, void* k_out,
+                            int64_t k_out_stride, void* stream);
+
+/* Gradients from those of its results (dq_out, dk_out, in_dtype) and the forward
+ * call's inputs.
+ *   dq, dk     in_dtype; dq may be dq_out or q, dk dk_out or k, element for
+ *              element
+ *   dq_weight, dk_weight  float32 [head_dim], summed over all tokens and heads
+ *              in a fixed order (equal calls give equal bits)
+ *   workspace  device scratch of at least the queried size, 256-byte aligned,
+ *              not read before it is written
+ * tokens == 0 writes zeros to dq_weight and dk_weight. */
+size_t gdn_qk_norm_rope_backward_workspace_bytes(const gdn_qk_dims* dims);
+gdn_status gdn_qk_norm_rope_backward(const gdn_qk_dims* dims, const void* dq_out,
+                                     int64_t dq_out_stride, const void* dk_out, int64_t dk_out_stride,
+                                     const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                     gdn_dtype in_dtype, const float* q_weight, const float* k_weight,
+                                     float eps, const int32_t* positions, const float* inv_freq,
+                                     void* dq, int64_t dq_stride, void* dk, int64_t dk_stride,
+                                     float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* gdn_status_string(gdn_status status);
 

@@ -7,3 +7,5 @@ from .gdn_oracle import *  # noqa: F401,F403
 from .mamba2_oracle import *  # noqa: F401,F403
 from .norm_oracle import *  # noqa: F401,F403
 from .mamba2_scan_oracle import *  # noqa: F401,F403
+from .linear_oracle import *  # noqa: F401,F403
+from .qk_oracle import *  # noqa: F401,F403

@@ -803,7 +803,8 @@ def gdn_layer_norm_backward(dy, x, weight, mean, rstd, bias=None, gate=None, gro
 
 # ------------------------------------------------------------------ linear attention
 class _launch_on:
-    """The stream's handle for a launch whose tensors all lie on x's GPU, which is made the current one meanwhile."""
+    """The stream's handle for a launch whose tensors all lie on x's GPU (others may be None), which is made the current one
+    meanwhile."""
 
     __slots__ = ("stream", "tensors", "guard")
 
@@ -812,15 +813,35 @@ class _launch_on:
 
     def __enter__(self):
         torch = _torch()
-        gpu = self.tensors[0].get_device()
-        if gpu >= 0 and gpu != torch.cuda.current_device():
+        x = self.tensors[0]
+        gpu = x.get_device()
+        if gpu < 0:
+            raise ValueError(f"tensors must lie on a GPU, not on {x.device}")
+        for t in self.tensors:
+            if t is not None and t.get_device() != gpu:
+                raise ValueError(f"all tensors must lie on {x.device}, not on {t.device}")
+        if gpu != torch.cuda.current_device():
             self.guard = torch.cuda.device(gpu)
             self.guard.__enter__()
-        return _on_gpu(self.stream, *self.tensors)
+        if self.stream is None:
+            return torch._C._cuda_getCurrentRawStream(gpu)
+        return _stream(self.stream)
 
     def __exit__(self, *error):
         if self.guard is not None:
             self.guard.__exit__(*error)
+
+
+def _head_rows(t, shape, dtype, what, copies=None, stream=None):
+    """(pointer, token stride) of a tensor [T, heads, d] whose tokens may be apart; an expanded one is copied if `copies` are kept."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    step, head, one = t.stride()
+    if one == 1 and head == shape[2] and step >= shape[1] * head and shape[0] > 1:
+        return t.data_ptr(), step
+    return _token_rows(t, shape[1:], dtype, what, copies, stream)
 
 
 class LinearScanGrads(NamedTuple):
@@ -838,11 +859,9 @@ def _linear_args(q, k, v, log_decay, scale, copies, stream):
     T, Hq, dk = q.shape
     Hk, Hv, dv = k.shape[1], v.shape[1], v.shape[2]
     dtype = q.dtype
-    pq, sq = _token_rows(q, (Hq, dk), dtype, "q", copies, stream)
-    pk, sk = _token_rows(k, (Hk, dk), dtype, "k", copies, stream)
-    pv, sv = _token_rows(v, (Hv, dv), dtype, "v", copies, stream)
-    if not T == k.shape[0] == v.shape[0]:
-        raise ValueError("q, k and v must have the same number of tokens")
+    pq, sq = _head_rows(q, (T, Hq, dk), dtype, "q", copies, stream)
+    pk, sk = _head_rows(k, (T, Hk, dk), dtype, "k", copies, stream)
+    pv, sv = _head_rows(v, (T, Hv, dv), dtype, "v", copies, stream)
     if scale is not None and not 0.0 < scale < float("inf"):
         raise ValueError(f"scale must be positive and finite, not {scale}")
     H = int(log_decay.shape[0])
@@ -870,7 +889,7 @@ def gdn_linear_decode_step(q, k, v, log_decay, pool, slot_map, scale=None, out=N
     shape = (B, dims.num_heads, dims.dv)
     fresh = []
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or torch.float32, device=q.device)
+        out = q.new_empty(shape, dtype=out_dtype or torch.float32)
         fresh.append(out)
     elif out.shape != shape:
         raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
@@ -920,13 +939,12 @@ def gdn_linear_scan(q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, sc
     sequence s goes on from slot slot_map[s] and leaves its final state there; without, from zero states.  Returns
     o [T, H, dv] in out_dtype (q's by default).  Autograd does not record it: gradients come from
     gdn_linear_scan_backward."""
-    torch = _torch()
     _says_no_graph("gdn_linear_scan", q, k, v, pool)
     copies, fresh = [], []
     dims, N, T, args = _linear_scan_args(q, k, v, log_decay, cu_seqlens, pool, slot_map, scale, copies, stream)
     shape = (T, dims.num_heads, dims.dv)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=q.device)
+        out = q.new_empty(shape, dtype=out_dtype)
         fresh.append(out)
     elif out.shape != shape:
         raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
@@ -985,9 +1003,7 @@ def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, neighbours, axe
         raise ValueError("q and k must be [tokens, heads, head_dim]")
     T, Hq, d = q.shape
     Hk, dtype = k.shape[1], q.dtype
-    rq, rk = _token_rows(q, (Hq, d), dtype, "q", copies, stream), _token_rows(k, (Hk, d), dtype, "k", copies, stream)
-    if k.shape[0] != T:
-        raise ValueError("q and k must have the same number of tokens")
+    rq, rk = _head_rows(q, (T, Hq, d), dtype, "q", copies, stream), _head_rows(k, (T, Hk, d), dtype, "k", copies, stream)
     _f32(q_weight, (d,), "q_weight"), _f32(k_weight, (d,), "k_weight")
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be float32 [rotary_dim / 2]")
@@ -1014,19 +1030,16 @@ def gdn_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, ne
     height, width) positions is int32 [axes, T] and `axes` names the row that each of the P pairs follows.  Tokens may
     be apart (slices of wider rows; an expanded tensor is copied).  Returns (q, k) anew, or in q_out and k_out, which may be q and k.
     Autograd does not record it: gradients come from gdn_qk_norm_rope_backward."""
-    torch = _torch()
     _says_no_graph("gdn_qk_norm_rope", q, k, q_weight, k_weight)
     copies, fresh = [], []
     dims, rows, params = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, neighbours, axes, copies, stream)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = q.new_empty(q.shape)
         fresh.append(q_out)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        k_out = k.new_empty(k.shape)
         fresh.append(k_out)
-    outs = (*_token_rows(q_out, q.shape[1:], q.dtype, "q_out"), *_token_rows(k_out, k.shape[1:], q.dtype, "k_out"))
-    if q_out.shape[0] != q.shape[0] or k_out.shape[0] != q.shape[0]:
-        raise ValueError("q_out and k_out must have as many tokens as q and k")
+    outs = (*_head_rows(q_out, q.shape, q.dtype, "q_out"), *_head_rows(k_out, k.shape, q.dtype, "k_out"))
     _keep_for_stream(fresh + copies, stream)
     with _launch_on(stream, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out) as handle:
         _check(lib().gdn_qk_norm_rope(ctypes.byref(dims), *rows, *params, *outs, handle))
@@ -1039,10 +1052,8 @@ def gdn_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, position
     torch = _torch()
     copies = []
     dims, rows, params = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, neighbours, axes, copies, stream)
-    if dq_out.shape != q.shape or dk_out.shape != k.shape:
-        raise ValueError("dq_out and dk_out must be shaped as q and k")
-    dys = (*_token_rows(dq_out, q.shape[1:], q.dtype, "dq_out", copies, stream),
-           *_token_rows(dk_out, k.shape[1:], q.dtype, "dk_out", copies, stream))
+    dys = (*_head_rows(dq_out, q.shape, q.dtype, "dq_out", copies, stream),
+           *_head_rows(dk_out, k.shape, q.dtype, "dk_out", copies, stream))
     new = lambda shape, t: torch.empty(shape, dtype=t, device=q.device)  # noqa: E731
     d = q.shape[2:]
     grads = QkGrads(new(q.shape, q.dtype), new(k.shape, q.dtype), new(d, torch.float32), new(d, torch.float32))

@@ -67,7 +67,6 @@ __device__ __forceinline__ void cos_sin(int p, float f, float& c, float& s) {
 template <int IDT, int LPR, bool NB, bool BWD>
 __global__ void __launch_bounds__(kQkThreads) gdn_qk_kernel(const QkArgs a) {
   constexpr int G = kQkThreads / LPR;  // rows at a time
-  constexpr int U = 4;                 // and times that many in flight
   extern __shared__ __align__(16) float s_turn[];  // [tokens][2][rot / 2]; backward also [G][d]
   const int tid = threadIdx.x, r = tid % LPR, row0 = tid / LPR + G * blockIdx.y, step = G * gridDim.y;
   const int half = a.rot / 2, d = a.d;
@@ -90,112 +89,117 @@ __global__ void __launch_bounds__(kQkThreads) gdn_qk_kernel(const QkArgs a) {
     }
   const float inv_d = 1.f / (float)d;
 
-  for (int64_t t0 = (int64_t)blockIdx.x * a.tokens; t0 < a.T; t0 += (int64_t)gridDim.x * a.tokens) {
+  const int64_t turns = (a.T + a.tokens - 1) / a.tokens;
+  const int dt0 = step / a.heads[0], dh0 = step - dt0 * a.heads[0], dt1 = step / a.heads[1], dh1 = step - dt1 * a.heads[1];
+  for (int64_t turn_at = blockIdx.x; turn_at < turns; turn_at += gridDim.x) {
+    const int64_t t0 = turn_at * a.tokens;
     const int n = (int)min((int64_t)a.tokens, a.T - t0);
+    struct Row {
+      int t, h;
+      InVec<IDT, 4> x1, x2, g1, g2;
+    } row, next;
+    auto load = [&](Row& q, int s) __attribute__((always_inline)) {
+      const int64_t xo = (t0 + q.t) * a.x_ts[s] + (int64_t)q.h * d;
+      q.x1.load(a.x[s], xo + o1);
+      q.x2.load(a.x[s], xo + o2);
+      if constexpr (BWD) {
+        const int64_t go = (t0 + q.t) * a.dy_ts[s] + (int64_t)q.h * d;
+        q.g1.load(a.dy[s], go + o1);
+        q.g2.load(a.dy[s], go + o2);
+      }
+    };
+    next.t = row0 / a.heads[0];
+    next.h = row0 - next.t * a.heads[0];
+    if (row0 < n * a.heads[0]) load(next, 0);  // on its way while the angles are formed
     if (BWD) __syncthreads();  // the tokens before are done with
     for (int i = tid; i < n * half; i += kQkThreads) {
-      const int t = i / half, p = i - t * half;
+      const int k = i / half, p = i - k * half;
       const int axis = (a.axis[p >> 4] >> (2 * (p & 15))) & 3;
       float c, s;
-      cos_sin(a.pos[axis * a.T + t0 + t], a.freq[p], c, s);
-      s_turn[2 * t * half + p] = c;
-      s_turn[(2 * t + 1) * half + p] = BWD ? -s : s;
+      cos_sin(a.pos[axis * a.T + t0 + k], a.freq[p], c, s);
+      s_turn[2 * k * half + p] = c;
+      s_turn[(2 * k + 1) * half + p] = BWD ? -s : s;
     }
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int heads = a.heads[s], rows = n * heads;
-      const int dt = step / heads, dh = step - dt * heads;
-      int t = row0 / heads, h = row0 - t * heads;
-      for (int row = row0; row < rows; row += U * step) {
-        int at[U], ah[U];
-        InVec<IDT, 4> x1[U], x2[U], g1[BWD ? U : 1], g2[BWD ? U : 1];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          at[u] = t;
-          ah[u] = h;
-          t += dt;
-          h += dh;
-          if (h >= heads) {
-            h -= heads;
-            ++t;
-          }
-          const int64_t tok = t0 + min(at[u], n - 1);  // rows past the last are loaded as its token's
-          const int64_t xo = tok * a.x_ts[s] + (int64_t)ah[u] * d;
-          x1[u].load(a.x[s], xo + o1);
-          x2[u].load(a.x[s], xo + o2);
-          if constexpr (BWD) {
-            const int64_t go = tok * a.dy_ts[s] + (int64_t)ah[u] * d;
-            g1[u].load(a.dy[s], go + o1);
-            g2[u].load(a.dy[s], go + o2);
-          }
+      const int rows = n * a.heads[s];
+      if (s == 1) {
+        next.t = row0 / a.heads[1];
+        next.h = row0 - next.t * a.heads[1];
+        if (row0 < rows) load(next, 1);
+      }
+      for (int i = row0; i < rows; i += step) {
+        row = next;
+        next.t += s == 0 ? dt0 : dt1;
+        next.h += s == 0 ? dh0 : dh1;
+        if (next.h >= a.heads[s]) {
+          next.h -= a.heads[s];
+          ++next.t;
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (row + u * step >= rows) break;
-          float x[8], y[8];
-          {
-            float f[4], f2[4];
-            x1[u].widen(f);
-            x2[u].widen(f2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[e] = on ? f[e] : 0.f;
-              x[4 + e] = on ? f2[e] : 0.f;
-            }
-          }
-          const float* cs = s_turn + 2 * at[u] * half + 4 * (turned ? r : 0);
-          float c[4], sn[4];
+        if (i + step < rows) load(next, s);
+        float x[8], y[8];
+        {
+          float f[4], f2[4];
+          row.x1.widen(f);
+          row.x2.widen(f2);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            c[e] = turned ? cs[e] : 1.f;
-            sn[e] = turned ? cs[half + e] : 0.f;
+            x[e] = on ? f[e] : 0.f;
+            x[4 + e] = on ? f2[e] : 0.f;
           }
-          auto turn = [&](float (&v)[8]) {
+        }
+        const float* cs = s_turn + 2 * row.t * half + 4 * (turned ? r : 0);
+        float c[4], sn[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = NB ? 2 * e : e, j = NB ? 2 * e + 1 : 4 + e;
-              const float p = v[i], q = v[j];
-              v[i] = p * c[e] - q * sn[e];
-              v[j] = q * c[e] + p * sn[e];
-            }
-          };
-          float sum = 0.f;
+        for (int e = 0; e < 4; ++e) {
+          c[e] = turned ? cs[e] : 1.f;
+          sn[e] = turned ? cs[half + e] : 0.f;
+        }
+        auto turn = [&](float (&v)[8]) __attribute__((always_inline)) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-          if constexpr (!BWD) {
-            const float rstd = rsqrtf(lanes_sum<LPR>(sum) * inv_d + a.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e] * rstd * w[s][e];
-            turn(y);
-          } else {
-            float f[4], f2[4];
-            g1[u].widen(f);
-            g2[u].widen(f2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[e] = on ? f[e] : 0.f;
-              y[4 + e] = on ? f2[e] : 0.f;
-            }
-            turn(y);
-            float dot = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dot = fmaf(y[e] * w[s][e], x[e], dot);
-            const float rstd = rsqrtf(lanes_sum<LPR>(sum) * inv_d + a.eps);
-            const float m = lanes_sum<LPR>(dot) * rstd * inv_d;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float xh = x[e] * rstd;
-              acc[BWD ? s : 0][e] = fmaf(y[e], xh, acc[BWD ? s : 0][e]);
-              y[e] = rstd * fmaf(-xh, m, y[e] * w[s][e]);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const int i = NB ? 2 * e : e, j = NB ? 2 * e + 1 : 4 + e;
+            const float p = v[i], q = v[j];
+            v[i] = p * c[e] - q * sn[e];
+            v[j] = q * c[e] + p * sn[e];
           }
-          if (on) {
-            const int64_t yo = (t0 + at[u]) * a.y_ts[s] + (int64_t)ah[u] * d;
-            const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
-            store_vec<4>(a.y[s], yo + o1, lo, IDT, true);
-            store_vec<4>(a.y[s], yo + o2, hi, IDT, true);
+        };
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+        if constexpr (!BWD) {
+          const float rstd = rsqrtf(lanes_sum<LPR>(sum) * inv_d + a.eps);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = x[e] * rstd * w[s][e];
+          turn(y);
+        } else {
+          float f[4], f2[4];
+          row.g1.widen(f);
+          row.g2.widen(f2);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = on ? f[e] : 0.f;
+            y[4 + e] = on ? f2[e] : 0.f;
           }
+          turn(y);
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot = fmaf(y[e] * w[s][e], x[e], dot);
+          const float rstd = rsqrtf(lanes_sum<LPR>(sum) * inv_d + a.eps);
+          const float m = lanes_sum<LPR>(dot) * rstd * inv_d;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float xh = x[e] * rstd;
+            acc[BWD ? s : 0][e] = fmaf(y[e], xh, acc[BWD ? s : 0][e]);
+            y[e] = rstd * fmaf(-xh, m, y[e] * w[s][e]);
+          }
+        }
+        if (on) {
+          const int64_t yo = (t0 + row.t) * a.y_ts[s] + (int64_t)row.h * d;
+          const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+          store_vec<4>(a.y[s], yo + o1, lo, IDT, true);
+          store_vec<4>(a.y[s], yo + o2, hi, IDT, true);
         }
       }
     }
@@ -223,18 +227,29 @@ __global__ void __launch_bounds__(kQkThreads) gdn_qk_kernel(const QkArgs a) {
 }
 
 // Adds the workgroups' partial weight gradients in a fixed order: 16 columns a
-// workgroup, a 16th of the workgroups' sums a row of threads.
-__global__ void __launch_bounds__(256) gdn_qk_sum_kernel(const QkArgs a, int blocks) {
-  __shared__ float s_sum[16][17];
+// workgroup, a 64th of the workgroups' sums a row of threads, four in flight.
+__global__ void __launch_bounds__(1024) gdn_qk_sum_kernel(const QkArgs a, int blocks) {
+  __shared__ float s_sum[64][17];
   const int x = threadIdx.x & 15, y = threadIdx.x >> 4, col = blockIdx.x * 16 + x, d = a.d;
   float sum = 0.f;
-  if (col < 2 * d)
-    for (int b = y; b < blocks; b += 16) sum += a.part[(int64_t)b * 2 * d + col];
+  if (col < 2 * d) {
+    const float* p = a.part + col;
+    for (int b = y; b < blocks; b += 4 * 64) {
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = b + 64 * k < blocks ? p[(int64_t)(b + 64 * k) * 2 * d] : 0.f;
+      sum += (f[0] + f[1]) + (f[2] + f[3]);
+    }
+  }
   s_sum[y][x] = sum;
   __syncthreads();
-  if (y == 0 && col < 2 * d) {
-    for (int k = 1; k < 16; ++k) sum += s_sum[k][x];
-    (col < d ? a.dw[0] : a.dw[1])[col < d ? col : col - d] = sum;
+  if (threadIdx.x < 64) {  // a column a row of 16 lanes' place, 16 sums each
+    const int c = threadIdx.x & 15, k0 = threadIdx.x >> 4;
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) sum += s_sum[k0 + 4 * k][c];
+    sum = xor_sum_from<16>(sum);
+    if (k0 == 0 && col < 2 * d) (col < d ? a.dw[0] : a.dw[1])[col < d ? col : col - d] = sum;
   }
 }
 
@@ -245,12 +260,13 @@ int lanes_of_row(int d) {
 }
 
 // Tokens of a workgroup's turn: eight rounds of its rows, so that angles and
-// the barrier behind them are shared, but enough workgroups for the chip.
-int turn_tokens(int64_t T, int heads, int d) {
+// the barrier behind them are shared, but as many workgroups as given.
+int turn_tokens(int64_t T, int heads, int d, int workgroups) {
   const int rows = kQkThreads / lanes_of_row(d);
-  int64_t t = std::min<int64_t>(16, std::max(1, 8 * rows / heads));
-  return (int)std::max<int64_t>(1, std::min(t, T / 2048));
+  const int64_t t = std::min<int64_t>(16, std::max(1, 8 * rows / heads));
+  return (int)std::max<int64_t>(1, std::min(t, (T + workgroups - 1) / workgroups));
 }
+constexpr int kQkForward = 4096, kQkBackward = 1024;
 
 template <int IDT, int LPR, bool BWD>
 hipError_t launch(const QkArgs& a, dim3 grid, size_t lds, hipStream_t s) {
@@ -281,7 +297,7 @@ hipError_t launch_type(const QkArgs& a, dim3 grid, size_t lds, hipStream_t s) {
 
 hipError_t launch_qk(QkArgs a, hipStream_t s) {
   const int heads = a.heads[0] + a.heads[1], rows = kQkThreads / lanes_of_row(a.d);
-  a.tokens = turn_tokens(a.T, heads, a.d);
+  a.tokens = turn_tokens(a.T, heads, a.d, kQkForward);
   dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens));
   // few tokens: their heads on several workgroups
   if (a.T < 512) grid.y = (unsigned)std::min((std::max(a.heads[0], a.heads[1]) + rows - 1) / rows, 64);
@@ -291,19 +307,19 @@ hipError_t launch_qk(QkArgs a, hipStream_t s) {
 // Workgroups of the backward pass, each with a partial sum of the weights'
 // gradients: four a compute unit.
 int qk_bwd_blocks(int64_t T, int heads, int d) {
-  const int t = turn_tokens(T, heads, d);
-  return (int)std::min<int64_t>((T + t - 1) / t, 1024);
+  const int t = turn_tokens(T, heads, d, kQkBackward);
+  return (int)std::min<int64_t>((T + t - 1) / t, kQkBackward);
 }
 
 hipError_t launch_qk_bwd(QkArgs a, hipStream_t s) {
   const int blocks = a.T > 0 ? qk_bwd_blocks(a.T, a.heads[0] + a.heads[1], a.d) : 0;
   if (blocks > 0) {
-    a.tokens = turn_tokens(a.T, a.heads[0] + a.heads[1], a.d);
+    a.tokens = turn_tokens(a.T, a.heads[0] + a.heads[1], a.d, kQkBackward);
     const size_t lds = std::max((size_t)a.tokens * a.rot * 4, (size_t)(kQkThreads / lanes_of_row(a.d)) * a.d * 4);
     const hipError_t e = launch_type<true>(a, dim3((unsigned)blocks), lds, s);
     if (e != hipSuccess) return e;
   }
-  gdn_qk_sum_kernel<<<(2 * a.d + 15) / 16, 256, 0, s>>>(a, blocks);
+  gdn_qk_sum_kernel<<<(2 * a.d + 15) / 16, 1024, 0, s>>>(a, blocks);
   return hipGetLastError();
 }
 

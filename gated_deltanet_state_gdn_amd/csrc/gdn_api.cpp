@@ -1034,7 +1034,7 @@ gdn_status check_linear_sizes(const gdn_linear_dims* d, int32_t N, int64_t total
   GDN_REQUIRE(N > 0 || total == 0, GDN_EINVAL, "%lld tokens in no sequence", (long long)total);
   const gdn::LinPlan p = gdn::linear_plan(N, total, d->num_heads, roles);
   const int64_t slots = p.seg_chunks > 0 ? gdn::scan_slots(N, total, (int64_t)p.seg_chunks * 64) : N;
-  const int64_t items = slots * d->num_heads * 256;  // threads along x of the largest launch
+  const int64_t items = (slots + 8) * d->num_heads * roles * 256;  // threads of the largest launch
   GDN_REQUIRE(items <= UINT32_MAX, GDN_EUNSUPPORTED,
               "N=%d and total_tokens=%lld make a launch of %lld threads: at most 2^32 - 1 are supported", N, (long long)total, (long long)items);
   if (roles > 1) {

@@ -229,7 +229,8 @@ struct LinScanArgs {
   int32_t N, H, in_dt;
   float scale;
   int32_t seg_chunks, whole;  // LinPlan
-  int32_t local;              // the segments' first walk
+  int32_t slots;              // segment slots, or sequences
+  int32_t roles, bunch;       // of the launch; neighbouring heads that read from one
 };
 
 // Sums the gradients of the states that share a head.

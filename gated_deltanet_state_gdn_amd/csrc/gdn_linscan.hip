@@ -47,16 +47,20 @@ constexpr int Q = kScanChunk;
 template <bool BF, int D, bool OUT>
 struct LinGeom {
   typedef typename Frag<BF>::E E;
-  static constexpr int PT = D == 128 ? 2 : 1;          // 16-column tiles of a wave
+  static constexpr int PT = D < 128 ? 1 : 2;           // 16-column tiles of a wave
   static constexpr int NW = D / (16 * PT);             // waves
   static constexpr int THREADS = 64 * NW;
   static constexpr int NT = D / 16, KB = (D + 31) / 32;
   static constexpr int LD = BF ? D : D + 4;            // rows of the operands
-  static constexpr int LDP = Q + (BF ? 8 : 4);         // rows of the weighted products
-  static constexpr int TERMS = BF ? 2 : 1;             // of those
-  static constexpr int W0 = OUT ? Q * LD : 0, X0 = W0 + Q * LD, P0 = X0 + Q * LD;
-  static constexpr int ELEMS = P0 + (OUT ? TERMS * Q * LDP : 0);
-  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + (Q + 4) * 4;
+  // The weighted products, 16 rows of reading tokens at a time: two blocks of rows meet 32 writing tokens, two meet all 64.
+  static constexpr int LDN = 32 + (BF ? 8 : 4), LDF = Q + (BF ? 8 : 4);
+  static constexpr int TERMS = BF ? 2 : 1, PE = 32 * (LDN + LDF);
+  static constexpr int TPW = (10 + NW - 1) / NW;       // 16 x 16 tiles of them that a wave forms
+  // read vectors, inputs (twice without outputs), write vectors twice, products
+  static constexpr int X0 = OUT ? Q * LD : 0, W0 = X0 + (OUT ? 1 : 2) * Q * LD, P0 = W0 + 2 * Q * LD;
+  static constexpr int ELEMS = P0 + (OUT ? TERMS * PE : 0);
+  static constexpr int TABLE = 80 + 2 * 128;           // floats: 15 zeros, scale p[0..64]; p[63], .., p[0], 64 zeros, and that times scale
+  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + TABLE * 4;
   static constexpr int VPR = D / 8;                    // 8-element vectors of a row
   static constexpr int SV = Q * VPR / THREADS;         // and those that a thread stages of an operand
   static_assert(SV * THREADS == Q * VPR && ELEMS * sizeof(E) % 16 == 0, "whole vectors");
@@ -80,23 +84,35 @@ __device__ __forceinline__ u32x2 read_transposed(const uint16_t* p) {
 }
 
 template <bool BF, int D, bool OUT>
-__global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 128 ? 2 : 1)) gdn_linear_walk_kernel(const LinScanArgs a) {
+__global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128 ? 2 : 1)) gdn_linear_walk_kernel(const LinScanArgs a) {
   using W = LinGeom<BF, D, OUT>;
   typedef typename W::E E;
-  constexpr int PT = W::PT, NW = W::NW, NT = W::NT, KB = W::KB, LD = W::LD, LDP = W::LDP, THREADS = W::THREADS, VPR = W::VPR, SV = W::SV;
+  constexpr int PT = W::PT, NW = W::NW, NT = W::NT, KB = W::KB, LD = W::LD, THREADS = W::THREADS, VPR = W::VPR, SV = W::SV, TPW = W::TPW;
   extern __shared__ __align__(16) unsigned char smem[];
   E* const s_r = reinterpret_cast<E*>(smem);
-  E* const s_w = reinterpret_cast<E*>(smem) + W::W0;
   E* const s_x = reinterpret_cast<E*>(smem) + W::X0;
-  E* const s_p = reinterpret_cast<E*>(smem) + W::P0;  // [TERMS][64][LDP]
-  float* const s_e = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E));  // p[0..64]
+  E* const s_w = reinterpret_cast<E*>(smem) + W::W0;  // [2]
+  E* const s_p = reinterpret_cast<E*>(smem) + W::P0;  // [TERMS]
+  // tables: s_a[m] = scale p[m] for m to 64, and zero for -15 <= m < 0; s_b[i] = p[63 - i], and zero for 64 <= i < 128;
+  // s_c = scale s_b
+  float* const s_a = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E)) + 15;
+  float* const s_b = s_a + 65;
+  float* const s_c = s_b + 128;
 
-  const LinRole& ro = a.role[blockIdx.y];
-  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
+  // The roles and the heads that share a tensor's head are neighbours on one XCD (workgroup i of a launch goes to XCD i mod 8).
+  // Whole sequences: each XCD takes a run of them.  Segments: round the XCDs, as the slots behind a sequence that is not cut
+  // have no work.
+  const int inner = a.bunch * a.roles, groups = a.H / a.bunch;
+  const int at_x = blockIdx.x & 7, at_k = blockIdx.x >> 3;
+  const int u = a.seg_chunks > 0 ? ((at_k / inner) * 8 + at_x) * inner + at_k % inner : xcd_unit(blockIdx.x, gridDim.x);
+  const int group = u / inner, in_group = u - group * inner;
+  const int slot = group / groups;
+  if (slot >= a.slots) return;
+  const int h = (group - slot * groups) * a.bunch + in_group / a.roles;
+  const LinRole& ro = a.role[in_group % a.roles];
+  int tid = threadIdx.x, l16 = tid & 15, q = tid >> 4 & 3;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool rev = ro.rev;
-  const int u = a.seg_chunks > 0 ? (int)blockIdx.x : xcd_unit(blockIdx.x, gridDim.x);
-  const int slot = u / a.H, h = u - slot * a.H;
   Piece sg;
   if (a.seg_chunks > 0) {
     sg = find_piece(a.cu, a.N, a.total, slot, a.seg_chunks * Q);
@@ -113,7 +129,7 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 12
     sg.count = 1;
   }
   const bool last_seg = rev ? sg.index == 0 : sg.index == sg.count - 1;
-  if (a.local && last_seg) return;  // nothing starts from this segment's end
+  if (!OUT && last_seg) return;  // nothing starts from this segment's end
   const int chunks = (int)((sg.len + Q - 1) / Q);
   const int c_lo = sg.index * a.seg_chunks;
   const int c_hi = sg.count > 1 ? min(chunks, c_lo + a.seg_chunks) : chunks;
@@ -131,49 +147,10 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 12
     return;
   }
 
-  for (int m = tid; m <= Q; m += THREADS)  // a product of 0 and an infinite decay is to be 0
-    s_e[m] = (float)exp2(fmax((double)a.log_decay[h], -1e300) * 1.4426950408889634 * m);
-
-  // The state S[nt][pt][r]: its row (a value of the write vector) is row_of(nt, 4 q + r), its column p0 + 16 pt + l16.
-  f32x4 S[NT][PT];
-  auto row_of = [&](int nt, int m) { return D == 16 ? m : 32 * (nt >> 1) + 8 * (m >> 2) + 4 * (nt & 1) + (m & 3); };
-  const int64_t sn = ro.transposed ? 1 : D, sp = ro.transposed ? D : 1;
-  const int64_t state_at = 4 * q * (D == 16 ? 1 : 2) * sn + (p0 + l16) * sp;  // of S[0][0][0]
-  auto load_as = [&](const void* base, int64_t unit, auto type) __attribute__((always_inline)) {  // all loads before the first use
-    constexpr int DT = decltype(type)::value;
-    uint32_t e[NT][PT][4];
-    const int64_t at = (unit * a.H + h) * D * D + state_at;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) e[nt][pt][r] = in_bits<DT>(base, at + row_of(nt, r) * sn + 16 * pt * sp);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
-        S[nt][pt] = f32x4{in_value<DT>(e[nt][pt][0]), in_value<DT>(e[nt][pt][1]), in_value<DT>(e[nt][pt][2]), in_value<DT>(e[nt][pt][3])};
-  };
-  auto store_as = [&](void* base, int64_t unit, auto type) __attribute__((always_inline)) {
-    constexpr int DT = decltype(type)::value;
-    const int64_t at = (unit * a.H + h) * D * D + state_at;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) store_elem(base, at + row_of(nt, r) * sn + 16 * pt * sp, S[nt][pt][r], DT);
-  };
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int pt = 0; pt < PT; ++pt) S[nt][pt] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // ---- a chunk's operands: from memory a chunk ahead, in registers, then to LDS
+  // ---- a chunk's operands: from memory two chunks ahead, in registers, then to LDS one chunk ahead
   Frag<BF> vr[OUT ? SV : 1], vw[SV], vx[SV];
-  const int st = tid / VPR, sc = tid % VPR;  // the thread's first row, and its block of the row
-  auto fetch_one = [&](Frag<BF> (&v)[SV], const void* base, int64_t ts, int64_t t0, int head, int len) __attribute__((always_inline)) {
+  auto fetch_one = [&](auto& v, const void* base, int64_t ts, int64_t t0, int head, int len) __attribute__((always_inline)) {
+    const int st = tid / VPR, sc = tid % VPR;  // the thread's first row, and its block of the row
     if constexpr (BF) {
       const auto w = window(base, t0 * ts + head * D, 2, 2 * ((len - 1) * ts + D));
       const int off = 2 * (st * (int)ts + 8 * sc);
@@ -188,28 +165,107 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 12
       }
     }
   };
-  auto fetch = [&](int c) __attribute__((always_inline)) {
-    const int64_t t0 = sg.begin + (int64_t)c * Q;
+  const int steps = c_hi - c_lo;
+  const int hr = h / ro.read_share, hw = h / ro.write_share, hx = h / ro.in_share;
+  auto chunk_of = [&](int step) { return rev ? c_hi - 1 - min(step, steps - 1) : c_lo + min(step, steps - 1); };
+  auto fetch = [&](int step) __attribute__((always_inline)) {  // past the last: the last once more, for no one
+    const int64_t t0 = sg.begin + (int64_t)chunk_of(step) * Q;
     const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
-    if constexpr (OUT) fetch_one(vr, ro.read, ro.read_ts, t0, h / ro.read_share, len);
-    fetch_one(vw, ro.write, ro.write_ts, t0, h / ro.write_share, len);
-    fetch_one(vx, ro.in, ro.in_ts, t0, h / ro.in_share, len);
+    if constexpr (OUT) fetch_one(vr, ro.read, ro.read_ts, t0, hr, len);
+    fetch_one(vw, ro.write, ro.write_ts, t0, hw, len);
+    fetch_one(vx, ro.in, ro.in_ts, t0, hx, len);
   };
-  auto commit = [&]() __attribute__((always_inline)) {
+  auto commit = [&](int step) __attribute__((always_inline)) {
+    E* const w = s_w + (step & 1) * Q * LD;
+    E* const x = s_x + (OUT ? 0 : (step & 1) * Q * LD);
+    const int st = tid / VPR, sc = tid % VPR;
 #pragma unroll
     for (int k = 0; k < SV; ++k) {
       const int at = block_at<BF, D>(st + k * (THREADS / VPR), sc);
       if constexpr (OUT) *reinterpret_cast<Frag<BF>*>(s_r + at) = vr[k];
-      *reinterpret_cast<Frag<BF>*>(s_w + at) = vw[k];
-      *reinterpret_cast<Frag<BF>*>(s_x + at) = vx[k];
+      *reinterpret_cast<Frag<BF>*>(w + at) = vw[k];
+      *reinterpret_cast<Frag<BF>*>(x + at) = vx[k];
     }
   };
-  // ---- fragments
-  // row t, the values of block kb in the order of the state's rows
-  auto row_frag = [&](const E* s, int t, int kb) __attribute__((always_inline)) {
-    if constexpr (D >= 32) return Frag<BF>::load(s + block_at<BF, D>(t, 4 * kb + q));
+  if (steps > 0) fetch(0);
+
+  // an infinite decay times 0 tokens is to be 0
+  const double log2_decay = fmax((double)a.log_decay[h], -1e300) * 1.4426950408889634;
+  for (int m = tid - 15; m < 128; m += THREADS) {
+    const float p = (float)exp2(log2_decay * (m >= 0 && m <= Q ? m : 0));
+    if (m <= Q) s_a[m] = m >= 0 ? a.scale * p : 0.f;
+    if (m >= 0) {
+      const int i = m < Q ? Q - 1 - m : m;
+      s_b[i] = m < Q ? p : 0.f;
+      s_c[i] = m < Q ? a.scale * p : 0.f;
+    }
+  }
+  const float whole_decay = (float)exp2(log2_decay * Q);
+  if (OUT)  // the products beyond the diagonal that share an operand with one on it stay zero
+    for (int i = tid; i < W::TERMS * W::PE; i += THREADS) s_p[i] = 0;
+
+  // The state S[nt][pt][r]: its row (a value of the write vector) is row_of(nt, 4 q + r), its column column_of(pt, l16): eight
+  // neighbours of a row or column in a lane's registers, where a head has so many.
+  f32x4 S[NT][PT];
+  auto row_of = [&](int nt, int m) { return D == 16 ? m : 32 * (nt >> 1) + 8 * (m >> 2) + 4 * (nt & 1) + (m & 3); };
+  auto column_of = [&](int pt, int m) { return p0 + (PT == 1 ? m : 8 * (m >> 2) + 4 * pt + (m & 3)); };
+  // its elements in memory: one lane offset, and a uniform one an element
+  const int sn = ro.transposed ? 1 : D, sp = ro.transposed ? D : 1;
+  const int state_at = row_of(0, 4 * q) * sn + column_of(0, l16) * sp;
+  auto load_as = [&](const void* base, int64_t unit, auto type) __attribute__((always_inline)) {
+    constexpr int DT = decltype(type)::value, EB = DT == GDN_F32 ? 4 : 2;
+    const auto w = window(base, (unit * a.H + h) * D * D, EB, EB * D * D);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        float f[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int at = EB * (row_of(nt, r) * sn + 4 * pt * sp);
+          if constexpr (EB == 4) f[r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(w, EB * state_at, at, 0));
+          else f[r] = in_value<DT>(__builtin_amdgcn_raw_buffer_load_b16(w, EB * state_at, at, 0));
+        }
+        S[nt][pt] = f32x4{f[0], f[1], f[2], f[3]};
+      }
+  };
+  auto store_as = [&](void* base, int64_t unit, auto type) __attribute__((always_inline)) {
+    constexpr int DT = decltype(type)::value, EB = DT == GDN_F32 ? 4 : 2;
+    const auto w = window(base, (unit * a.H + h) * D * D, EB, EB * D * D);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int at = EB * (row_of(nt, r) * sn + 4 * pt * sp);
+          const float f = S[nt][pt][r];
+          if constexpr (EB == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, f), w, EB * state_at, at, 0);
+          else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack2<DT == GDN_F32 ? GDN_BF16 : DT>(f, 0.f), w, EB * state_at, at, 0);
+        }
+  };
+  if (OUT && (sg.count > 1 || ro.init.base != nullptr)) {
+    const bool cut = sg.count > 1;
+    const void* const base = cut ? ro.seg : ro.init.base;
+    const int64_t unit = cut ? slot : ro.init.slots != nullptr ? ro.init.slots[sg.seq] : sg.seq;
+    const int dt = cut ? (int)GDN_F32 : ro.init.dtype;
+    if (dt == GDN_F32) load_as(base, unit, std::integral_constant<int, GDN_F32>{});
+    else if (dt == GDN_BF16) load_as(base, unit, std::integral_constant<int, GDN_BF16>{});
+    else load_as(base, unit, std::integral_constant<int, GDN_F16>{});
+  } else {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) S[nt][pt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // ---- fragments.  The lane's places in the first block of 32 columns (see block_at); `along` goes on by whole such blocks.
+  auto along = [](int at, int kb) __attribute__((always_inline)) { return BF ? at ^ (32 * kb) : at + 32 * kb; };
+  // row 16 rt + l16, the values of block kb in the order of the state's rows
+  auto row_frag = [&](const E* s, int rt, int kb) __attribute__((always_inline)) {
+    if constexpr (D >= 32) return Frag<BF>::load(s + 16 * rt * LD + along(block_at<BF, D>(l16, q), kb));
     Frag<BF> f = Frag<BF>::zero();
-    const E* p = s + block_at<BF, D>(t, q >> 1) + 4 * (q & 1);
+    const E* p = s + 16 * rt * LD + block_at<BF, D>(l16, q >> 1) + 4 * (q & 1);
     if constexpr (BF) {
       const u32x2 v = *reinterpret_cast<const u32x2*>(p);
       f.v[0] = v[0];
@@ -219,77 +275,112 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 12
     }
     return f;
   };
-  // tokens 32 ks + 8 q and on of the column that lane l16 gets from four blocks of four columns, of which it points at `col`
-  auto column_frag = [&](const E* s, int ks, int col, int mine) __attribute__((always_inline)) {
+  // tokens 32 ks + 8 q and on of a column a lane: l16's of sixteen, of which lanes point at four each.  A tile of the state's rows:
+  auto write_frag = [&](const E* s, int nt, int ks) __attribute__((always_inline)) {
     if constexpr (BF) {
-      const int t = 32 * ks + 8 * q + (l16 >> 2);
-      const u32x2 v0 = read_transposed(s + block_at<BF, D>(t, col >> 3) + (col & 4));
-      const u32x2 v1 = read_transposed(s + block_at<BF, D>(t + 4, col >> 3) + (col & 4));
-      return Frag<BF>{u32x4{v0[0], v0[1], v1[0], v1[1]}};
+      const int t = 8 * q + (l16 >> 2), c = l16 & 3;
+      u32x2 v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = D == 16 ? block_at<BF, D>(t + 4 * h, c >> 1) + 4 * (c & 1) : along(block_at<BF, D>(t + 4 * h, c), nt >> 1) + 4 * (nt & 1);
+        v[h] = read_transposed(s + 32 * ks * LD + at);
+      }
+      return Frag<BF>{u32x4{v[0][0], v[0][1], v[1][0], v[1][1]}};
     } else {
       float f[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = s[(32 * ks + 8 * q + e) * LD + mine];
+      for (int e = 0; e < 8; ++e) f[e] = s[(32 * ks + 8 * q + e) * LD + row_of(nt, l16)];
       return Frag<BF>::round(f);
     }
   };
-  auto write_frag = [&](int nt, int ks) __attribute__((always_inline)) { return column_frag(s_w, ks, row_of(nt, 4 * (l16 & 3)), row_of(nt, l16)); };
-  auto in_frag = [&](int pt, int ks) __attribute__((always_inline)) { return column_frag(s_x, ks, p0 + 16 * pt + 4 * (l16 & 3), p0 + 16 * pt + l16); };
+  // and of the wave's columns
+  auto in_frag = [&](int step, int pt, int ks) __attribute__((always_inline)) {
+    const E* const s = s_x + (OUT ? 0 : (step & 1) * Q * LD) + 32 * ks * LD;
+    if constexpr (BF) {
+      const int t = 8 * q + (l16 >> 2), c = l16 & 3;
+      u32x2 v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = PT == 1 ? block_at<BF, D>(t + 4 * h, 2 * wave + (c >> 1)) + 4 * (c & 1) : along(block_at<BF, D>(t + 4 * h, c), wave) + 4 * pt;
+        v[h] = read_transposed(s + at);
+      }
+      return Frag<BF>{u32x4{v[0][0], v[0][1], v[1][0], v[1][1]}};
+    } else {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = s[(8 * q + e) * LD + column_of(pt, l16)];
+      return Frag<BF>::round(f);
+    }
+  };
 
-  if (OUT)  // the products beyond the diagonal that share an operand with one on it stay zero
-    for (int i = tid; i < W::TERMS * Q * LDP; i += THREADS) s_p[i] = 0;
-  const int steps = c_hi - c_lo;
-  if (steps > 0) fetch(rev ? c_hi - 1 : c_lo);
-  if (!a.local && (sg.count > 1 || ro.init.base != nullptr)) {
-    const bool cut = sg.count > 1;
-    const void* const base = cut ? ro.seg : ro.init.base;
-    const int64_t unit = cut ? slot : ro.init.slots != nullptr ? ro.init.slots[sg.seq] : sg.seq;
-    const int dt = cut ? (int)GDN_F32 : ro.init.dtype;
-    if (dt == GDN_F32) load_as(base, unit, std::integral_constant<int, GDN_F32>{});
-    else if (dt == GDN_BF16) load_as(base, unit, std::integral_constant<int, GDN_BF16>{});
-    else load_as(base, unit, std::integral_constant<int, GDN_F16>{});
+  // ---- the weighted products: the wave's 16 x 16 tiles on and below the diagonal (above it in reverse).  A lane has four writing
+  // tokens of one reading token.  The last tile goes to several waves where the tiles do not go round.
+  int prt[TPW], pct[TPW];
+#pragma unroll
+  for (int k = 0; k < TPW; ++k) {
+    const int t = min(wave + k * NW, 9);
+    const int i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t - i * (i + 1) / 2;
+    prt[k] = rev ? j : i;
+    pct[k] = rev ? i : j;
   }
+  // where the products of block rt of reading tokens and the half `ks` of the writing ones begin, for the lane's row of the block
+  const int turn = rev ? 1 : 0;
+  auto product_row = [&](int rt, int ks) __attribute__((always_inline)) {
+    const bool all = (rt >> 1) != turn;  // meets all 64 writing tokens, others the 32 of their own half
+    return all ? 32 * W::LDN + ((rt & 1) * 16 + l16) * W::LDF + 32 * ks : ((rt & 1) * 16 + l16) * W::LDN;
+  };
+  auto products = [&](int step) __attribute__((always_inline)) {
+    const E* const w = s_w + (step & 1) * Q * LD;
+    f32x4 acc[TPW];
+#pragma unroll
+    for (int k = 0; k < TPW; ++k) acc[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int k = 0; k < TPW; ++k) acc[k] = frag_mma(acc[k], row_frag(w, pct[k], kb), row_frag(s_r, prt[k], kb));
+#pragma unroll
+    for (int k = 0; k < TPW; ++k) {
+      const int rt = prt[k], ct = pct[k], m0 = 16 * rt + l16 - 16 * ct - 4 * q;
+      const float* const p = (rev ? s_a : s_c + Q - 1) - m0;  // scale p[|m0 - r|] on the diagonal and to its one side, zero on the other
+      float f[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) f[r] = acc[k][r] * p[r];
+      E* d = s_p + product_row(rt, ct >> 1) + 16 * (ct & 1) + 4 * q;
+      if constexpr (BF) {
+        const u32x2 high = {pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
+        *reinterpret_cast<u32x2*>(d) = high;
+        bf16_rest(high[0], f[0], f[1]);
+        bf16_rest(high[1], f[2], f[3]);
+        *reinterpret_cast<u32x2*>(d + W::PE) = u32x2{pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
+      } else {
+        *reinterpret_cast<f32x4*>(d) = f32x4{f[0], f[1], f[2], f[3]};
+      }
+    }
+  };
 
-  for (int step = 0; step < steps; ++step) {
-    const int c = rev ? c_hi - 1 - step : c_lo + step;
-    const int64_t t0 = sg.begin + (int64_t)c * Q;
-    const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
-
-    __syncthreads();  // the chunk before is done with LDS
-    commit();
+  if (steps > 0) {
+    commit(0);
+    fetch(1);
     __syncthreads();
-    __builtin_amdgcn_sched_barrier(0);
-    fetch(min(max(rev ? c - 1 : c + 1, c_lo), c_hi - 1));
-    __builtin_amdgcn_sched_barrier(0);
-
+    if constexpr (OUT) products(0);
+  }
+  for (int step = 0; step < steps; ++step) {
+    const int64_t t0 = sg.begin + (int64_t)chunk_of(step) * Q;
+    const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
+    // the lane's places are not known to be the ones of the chunk before: what follows from them is formed anew, in a few
+    // instructions, where it would otherwise be kept in registers that the loop has not got
+    asm volatile("" : "+v"(tid));
+    tid &= THREADS - 1;
+    l16 = tid & 15;
+    q = tid >> 4 & 3;
+    // what tokens see of the state, and how much of their input reaches the next
+    const float* const tell = rev ? s_b + Q - len : s_a + 1;
+    const float* const keep = rev ? s_a + 1 : s_b + Q - len;
+    // In reverse blocks of 16 tokens and halves of 32 go in the order 2 3 0 1 and 1 0, so that the half of the writing tokens
+    // that reading tokens do not meet has the same place.
     Frag<BF> xf[2][PT];
     if constexpr (OUT) {
-      // the weighted products of read and write vectors, 16 x 16 tiles on and below the diagonal (above it in reverse)
-      for (int t = wave; t < 10; t += NW) {
-        const int i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t - i * (i + 1) / 2;
-        const int rt = rev ? j : i, ct = rev ? i : j;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) acc = frag_mma(acc, row_frag(s_w, 16 * ct + l16, kb), row_frag(s_r, 16 * rt + l16, kb));
-        float f[4];
-        const int at = 16 * rt + l16, from = 16 * ct + 4 * q;  // token of the read vector, first of the write vectors
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int m = rev ? from + r - at : at - from - r;
-          f[r] = m >= 0 ? acc[r] * a.scale * s_e[max(m, 0)] : 0.f;
-        }
-        E* d = s_p + at * LDP + from;
-        if constexpr (BF) {
-          const u32x2 high = {pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
-          *reinterpret_cast<u32x2*>(d) = high;
-          bf16_rest(high[0], f[0], f[1]);
-          bf16_rest(high[1], f[2], f[3]);
-          *reinterpret_cast<u32x2*>(d + Q * LDP) = u32x2{pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
-        } else {
-          *reinterpret_cast<f32x4*>(d) = f32x4{f[0], f[1], f[2], f[3]};
-        }
-      }
-      // the state's part of the output, transposed: acc[pt][rt][r] = (column 16 pt + 4 q + r, token 16 rt + l16)
+      // the state's part of the output, transposed: acc[pt][i][r] = (column column_of(pt, 4 q + r), token 16 (i ^ 2 turn) + l16)
       f32x4 acc[PT][4];
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt)
@@ -298,6 +389,9 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 12
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         typedef Split<BF, 2> Terms;
+        Frag<BF> rf[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) rf[rt] = row_frag(s_r, rt ^ 2 * turn, kb);
         Terms sf[PT];
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
@@ -309,9 +403,6 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 12
           }
           sf[pt] = Terms::of(f);
         }
-        Frag<BF> rf[4];
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) rf[rt] = row_frag(s_r, 16 * rt + l16, kb);
 #pragma unroll
         for (int k = Terms::K - 1; k >= 0; --k)
 #pragma unroll
@@ -320,76 +411,94 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 12
             for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], sf[pt].t[k], rf[rt]);
       }
 #pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) xf[ks][pt] = in_frag(step, pt, ks ^ turn);
+#pragma unroll
       for (int rt = 0; rt < 4; ++rt) {
-        const int t = 16 * rt + l16;
-        const float f = rev ? s_e[max(len - 1 - t, 0)] : a.scale * s_e[t + 1];
+        const float f = tell[16 * (rt ^ 2 * turn) + l16];
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) acc[pt][rt] *= f;
       }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-        for (int pt = 0; pt < PT; ++pt) xf[ks][pt] = in_frag(pt, ks);
-      __syncthreads();  // the products are there
+      __syncthreads();  // the products are there, and read vectors and inputs done with
+      Frag<BF> pf[W::TERMS][6];  // blocks 0 to 3 with the first half of the writing tokens, 2 and 3 with the second
 #pragma unroll
       for (int k = W::TERMS - 1; k >= 0; --k)
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+        for (int i = 0; i < 6; ++i)
+          pf[k][i] = Frag<BF>::load(s_p + k * W::PE + product_row((i - 2 * (i >= 4)) ^ 2 * turn, (i >= 4) ^ turn) + 8 * q);
+      commit(step + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(step + 2);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int rt = 0; rt < 4; ++rt) {
-            if (rev ? (ks == 0 && rt >= 2) : (ks == 1 && rt < 2)) continue;  // all beyond the diagonal
-            const Frag<BF> pf = Frag<BF>::load(s_p + (k * Q + 16 * rt + l16) * LDP + 32 * ks + 8 * q);
+      for (int k = W::TERMS - 1; k >= 0; --k)
 #pragma unroll
-            for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[ks][pt], pf);
-          }
+        for (int i = 0; i < 6; ++i) {
+          const int ks = i >= 4, rt = i - 2 * ks;
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[ks][pt], pf[k][i]);
+        }
       if (BF && ro.out_dt == GDN_BF16) {
         const auto w = window(ro.out, t0 * out_ts + h * D + p0, 2, 2 * ((len - 1) * out_ts + 16 * PT));
-        const int off = 2 * (l16 * (int)out_ts + 4 * q);
+        const int off = 2 * (l16 * (int)out_ts + 4 * PT * q);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
+        for (int rt = 0; rt < 4; ++rt) {
+          uint32_t v[2 * PT];
 #pragma unroll
           for (int pt = 0; pt < PT; ++pt) {
-            const f32x4 v = acc[pt][rt];
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2<GDN_BF16>(v[0], v[1]), pack2<GDN_BF16>(v[2], v[3])}, w,
-                                                  off + 2 * (16 * rt * (int)out_ts + 16 * pt), 0, 0);
+            v[2 * pt] = pack2<GDN_BF16>(acc[pt][rt][0], acc[pt][rt][1]);
+            v[2 * pt + 1] = pack2<GDN_BF16>(acc[pt][rt][2], acc[pt][rt][3]);
           }
+          if constexpr (PT == 2) __builtin_amdgcn_raw_buffer_store_b128(u32x4{v[0], v[1], v[2], v[3]}, w, off + 32 * (rt ^ 2 * turn) * (int)out_ts, 0, 0);
+          else __builtin_amdgcn_raw_buffer_store_b64(u32x2{v[0], v[1]}, w, off + 32 * (rt ^ 2 * turn) * (int)out_ts, 0, 0);
+        }
       } else {
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-          const int t = 16 * rt + l16;
+          const int t = 16 * (rt ^ 2 * turn) + l16;
           if (t < len)
 #pragma unroll
             for (int pt = 0; pt < PT; ++pt) {
               const float v[4] = {acc[pt][rt][0], acc[pt][rt][1], acc[pt][rt][2], acc[pt][rt][3]};
-              store_vec<4>(ro.out, (t0 + t) * out_ts + h * D + p0 + 16 * pt + 4 * q, v, ro.out_dt, true);
+              store_vec<4>(ro.out, (t0 + t) * out_ts + h * D + p0 + 4 * PT * q + 4 * pt, v, ro.out_dt, true);
             }
         }
       }
+    } else {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) xf[ks][pt] = in_frag(step, pt, ks ^ turn);
+      commit(step + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(step + 2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (OUT) {
+      __syncthreads();  // the next operands are there, and the products done with
+      products(step + 1);
     }
 
     // the state after the chunk
-    const float dec = s_e[len];
+    const E* const w = s_w + (step & 1) * Q * LD;
+    const float dec = len == Q ? whole_decay : s_b[Q - 1 - len];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt) S[nt][pt] *= dec;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      if (32 * ks >= len) continue;
-      float wgt[8];
+      float wt[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int t = 32 * ks + 8 * q + e;
-        wgt[e] = rev ? a.scale * s_e[t + 1] : t < len ? s_e[max(len - 1 - t, 0)] : 0.f;
-      }
+      for (int e = 0; e < 8; ++e) wt[e] = keep[32 * (ks ^ turn) + 8 * q + e];
       Split<BF> xs[PT];
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt) {
         float f[8];
-        if constexpr (OUT) xf[ks][pt].widen(f);
-        else in_frag(pt, ks).widen(f);
+        xf[ks][pt].widen(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= wgt[e];
+        for (int e = 0; e < 8; ++e) f[e] *= wt[e];
         xs[pt] = Split<BF>::of(f);
       }
       constexpr int NG = NT < 4 ? NT : 4;  // tiles at a time, their terms apart: a product never follows the one it adds to
@@ -397,7 +506,7 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 12
       for (int ng = 0; ng < NT; ng += NG) {
         Frag<BF> wf[NG];
 #pragma unroll
-        for (int i = 0; i < NG; ++i) wf[i] = write_frag(ng + i, ks);
+        for (int i = 0; i < NG; ++i) wf[i] = write_frag(w, ng + i, ks ^ turn);
 #pragma unroll
         for (int k = Split<BF>::K - 1; k >= 0; --k)
 #pragma unroll
@@ -406,12 +515,13 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF && D == 12
             for (int pt = 0; pt < PT; ++pt) S[ng + i][pt] = frag_mma(S[ng + i][pt], wf[i], xs[pt].t[k]);
       }
     }
+    if constexpr (!OUT) __syncthreads();  // the next operands are there, and these done with
   }
 
-  if (a.local || (ro.fin.base != nullptr && last_seg && (rev || sg.len > 0))) {
-    void* const base = a.local ? ro.seg : ro.fin.base;
-    const int64_t unit = a.local ? slot : ro.fin.slots != nullptr ? ro.fin.slots[sg.seq] : sg.seq;
-    const int dt = a.local ? (int)GDN_F32 : ro.fin.dtype;
+  if (!OUT || (ro.fin.base != nullptr && last_seg && (rev || sg.len > 0))) {
+    void* const base = OUT ? ro.fin.base : ro.seg;
+    const int64_t unit = !OUT ? slot : ro.fin.slots != nullptr ? ro.fin.slots[sg.seq] : sg.seq;
+    const int dt = OUT ? ro.fin.dtype : (int)GDN_F32;
     if (dt == GDN_F32) store_as(base, unit, std::integral_constant<int, GDN_F32>{});
     else if (dt == GDN_BF16) store_as(base, unit, std::integral_constant<int, GDN_BF16>{});
     else store_as(base, unit, std::integral_constant<int, GDN_F16>{});
@@ -467,21 +577,21 @@ __global__ void __launch_bounds__(256) gdn_linear_sum_kernel(const LinSumArgs a)
 }
 
 template <bool BF, int D, bool OUT>
-hipError_t walk(const LinScanArgs& a, int roles, hipStream_t s) {
+hipError_t walk(const LinScanArgs& a, hipStream_t s) {
   using W = LinGeom<BF, D, OUT>;
-  const int64_t slots = a.seg_chunks > 0 ? scan_slots(a.N, a.total, (int64_t)a.seg_chunks * Q) : a.N;
   auto* k = gdn_linear_walk_kernel<BF, D, OUT>;
   static std::atomic<uint64_t> allowed{0};
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(k), W::LDS, allowed);
   if (e != hipSuccess) return e;
-  k<<<dim3((unsigned)(slots * a.H), (unsigned)roles), W::THREADS, W::LDS, s>>>(a);
+  const int64_t inner = a.bunch * a.roles, units = (int64_t)a.slots * a.H * a.roles;
+  k<<<(unsigned)(a.seg_chunks > 0 ? (units + 8 * inner - 1) / (8 * inner) * (8 * inner) : units), W::THREADS, W::LDS, s>>>(a);
   return hipGetLastError();
 }
 
 template <bool OUT>
-hipError_t walk_any(const LinScanArgs& a, bool bf, int D, int roles, hipStream_t s) {
-  if (bf) return D == 16 ? walk<true, 16, OUT>(a, roles, s) : D == 32 ? walk<true, 32, OUT>(a, roles, s) : D == 64 ? walk<true, 64, OUT>(a, roles, s) : walk<true, 128, OUT>(a, roles, s);
-  return D == 16 ? walk<false, 16, OUT>(a, roles, s) : D == 32 ? walk<false, 32, OUT>(a, roles, s) : D == 64 ? walk<false, 64, OUT>(a, roles, s) : walk<false, 128, OUT>(a, roles, s);
+hipError_t walk_any(const LinScanArgs& a, bool bf, int D, hipStream_t s) {
+  if (bf) return D == 16 ? walk<true, 16, OUT>(a, s) : D == 32 ? walk<true, 32, OUT>(a, s) : D == 64 ? walk<true, 64, OUT>(a, s) : walk<true, 128, OUT>(a, s);
+  return D == 16 ? walk<false, 16, OUT>(a, s) : D == 32 ? walk<false, 32, OUT>(a, s) : D == 64 ? walk<false, 64, OUT>(a, s) : walk<false, 128, OUT>(a, s);
 }
 
 }  // namespace
@@ -499,18 +609,20 @@ LinPlan linear_plan(int64_t N, int64_t total, int H, int roles) {
 // The walks of roles 0 and on; backward, roles 1 and 2 go the same way over the
 // same states, so the segments' first walk and the chain take roles 0 and 1.
 hipError_t launch_linear_scan(LinScanArgs a, bool bf, int D, int roles, hipStream_t s) {
+  a.slots = (int32_t)(a.seg_chunks > 0 ? scan_slots(a.N, a.total, (int64_t)a.seg_chunks * Q) : a.N);
+  a.bunch = 1;
+  for (int i = 0; i < roles; ++i) a.bunch = std::max({a.bunch, a.role[i].read_share, a.role[i].write_share, a.role[i].in_share});
   if (a.seg_chunks > 0) {
-    const int passes = std::min(roles, 2);
-    a.local = 1;
-    hipError_t e = walk_any<false>(a, bf, D, passes, s);
+    const int passes = a.roles = std::min(roles, 2);
+    hipError_t e = walk_any<false>(a, bf, D, s);
     if (e != hipSuccess) return e;
     const int parts = (D * D + 1023) / 1024;
     gdn_linear_chain_kernel<<<dim3((unsigned)((int64_t)a.N * a.H * parts), (unsigned)passes), 256, 0, s>>>(a, D * D, parts);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    a.local = 0;
   }
-  return walk_any<true>(a, bf, D, roles, s);
+  a.roles = roles;
+  return walk_any<true>(a, bf, D, s);
 }
 
 hipError_t launch_linear_sum(const LinSumArgs& a, hipStream_t s) {

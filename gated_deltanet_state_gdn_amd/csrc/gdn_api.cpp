@@ -1027,14 +1027,19 @@ gdn_status check_linear_io(const gdn_linear_dims* d, const void* q, const void* 
   return GDN_OK;
 }
 
+// Segments behind the sequences' first, at most.
+int64_t linear_extras(const gdn_linear_dims* d, int32_t N, int64_t total, bool bf, int roles) {
+  const gdn::LinPlan p = gdn::linear_plan(N, total, d->num_heads, d->dk, bf, roles);
+  return p.seg_chunks > 0 ? total / ((int64_t)p.seg_chunks * 64) : 0;
+}
+
 gdn_status check_linear_sizes(const gdn_linear_dims* d, int32_t N, int64_t total, int roles) {
   GDN_TRY(check_linear_dims(d));
   GDN_REQUIRE(N >= 0 && total >= 0, GDN_EINVAL, "N=%d and total_tokens=%lld must be >= 0", N, (long long)total);
   GDN_REQUIRE(total <= INT32_MAX, GDN_EINVAL, "total_tokens=%lld exceeds the 32-bit cu_seqlens", (long long)total);
   GDN_REQUIRE(N > 0 || total == 0, GDN_EINVAL, "%lld tokens in no sequence", (long long)total);
-  const gdn::LinPlan p = gdn::linear_plan(N, total, d->num_heads, roles);
-  const int64_t slots = p.seg_chunks > 0 ? gdn::scan_slots(N, total, (int64_t)p.seg_chunks * 64) : N;
-  const int64_t items = (slots + 8) * d->num_heads * roles * 256;  // threads of the largest launch
+  const int64_t extras = std::max(linear_extras(d, N, total, true, roles), linear_extras(d, N, total, false, roles));
+  const int64_t items = (N + extras + 16) * d->num_heads * roles * 256;  // threads of the largest launch
   GDN_REQUIRE(items <= UINT32_MAX, GDN_EUNSUPPORTED,
               "N=%d and total_tokens=%lld make a launch of %lld threads: at most 2^32 - 1 are supported", N, (long long)total, (long long)items);
   if (roles > 1) {
@@ -1050,13 +1055,16 @@ struct LinWs {
   gdn::LinPlan plan;
 };
 
-LinWs linear_ws(const gdn_linear_dims* d, int32_t N, int64_t total, bool backward) {
+// For calls of either kind of types, which may be cut in different ways.
+LinWs linear_ws(const gdn_linear_dims* d, int32_t N, int64_t total, bool backward, bool bf) {
   LinWs w{};
   Carve c;
   const size_t H = d->num_heads;
-  w.plan = gdn::linear_plan(N, total, d->num_heads, backward ? 3 : 1);
-  if (w.plan.seg_chunks > 0) {
-    const size_t segs = gdn::scan_slots(N, total, (int64_t)w.plan.seg_chunks * 64);
+  const int roles = backward ? 3 : 1;
+  w.plan = gdn::linear_plan(N, total, d->num_heads, d->dk, bf, roles);
+  const int64_t extras = std::max(linear_extras(d, N, total, true, roles), linear_extras(d, N, total, false, roles));
+  if (extras > 0) {
+    const size_t segs = N + extras;
     for (int i = 0; i < (backward ? 2 : 1); ++i) w.seg[i] = c.take(segs * H * d->dk * d->dv * 4);
   }
   const int heads[3] = {d->num_q_heads, d->num_k_heads, d->num_v_heads};
@@ -1172,7 +1180,7 @@ gdn_status gdn_linear_decode_step(const gdn_linear_dims* dims, int32_t B, const 
 
 size_t gdn_linear_scan_workspace_bytes(const gdn_linear_dims* dims, int32_t N, int64_t total_tokens) {
   if (check_linear_sizes(dims, N, total_tokens, 1) != GDN_OK || N == 0) return 0;
-  return linear_ws(dims, N, total_tokens, false).bytes;
+  return linear_ws(dims, N, total_tokens, false, true).bytes;
 }
 
 gdn_status gdn_linear_scan(const gdn_linear_dims* dims, int32_t N, const int32_t* cu_seqlens, int64_t total_tokens, const void* q,
@@ -1184,7 +1192,8 @@ gdn_status gdn_linear_scan(const gdn_linear_dims* dims, int32_t N, const int32_t
   if (N == 0 || total_tokens == 0) return ok();  // nothing is read or written
   GDN_TRY(check_linear_scan(dims, cu_seqlens, total_tokens, q, k, v, strides, log_decay, state, slot_map));
   GDN_REQUIRE(out != nullptr && aligned(out, 16), GDN_EINVAL, "out is NULL or not 16-byte aligned");
-  const LinWs w = linear_ws(dims, N, total_tokens, false);
+  const bool bf = in_dtype == GDN_BF16 && out_dtype == GDN_BF16;
+  const LinWs w = linear_ws(dims, N, total_tokens, false, bf);
   GDN_TRY(check_scan_ws(workspace, workspace_bytes, w.bytes));
   gdn::LinScanArgs a = linear_args(dims, N, cu_seqlens, total_tokens, in_dtype, log_decay, state, slot_map, w);
   const LinInputs t = linear_inputs(dims, q, k, v, strides);
@@ -1193,12 +1202,12 @@ gdn_status gdn_linear_scan(const gdn_linear_dims* dims, int32_t N, const int32_t
   r.out_dt = out_dtype;
   if (state != nullptr) r.init = r.fin = gdn::ScanStates{state->base, slot_map, (int32_t)state->dtype};
   if (workspace != nullptr) r.seg = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.seg[0]);
-  return launched(gdn::launch_linear_scan(a, in_dtype == GDN_BF16 && out_dtype == GDN_BF16, dims->dk, 1, static_cast<hipStream_t>(stream)));
+  return launched(gdn::launch_linear_scan(a, bf, dims->dk, 1, static_cast<hipStream_t>(stream)));
 }
 
 size_t gdn_linear_scan_backward_workspace_bytes(const gdn_linear_dims* dims, int32_t N, int64_t total_tokens) {
   if (check_linear_sizes(dims, N, total_tokens, 3) != GDN_OK || N == 0) return 0;
-  return linear_ws(dims, N, total_tokens, true).bytes;
+  return linear_ws(dims, N, total_tokens, true, true).bytes;
 }
 
 gdn_status gdn_linear_scan_backward(const gdn_linear_dims* dims, int32_t N, const int32_t* cu_seqlens, int64_t total_tokens,
@@ -1216,7 +1225,7 @@ gdn_status gdn_linear_scan_backward(const gdn_linear_dims* dims, int32_t N, cons
                 "dq, dk or dv is NULL or not 16-byte aligned");
   }
   GDN_REQUIRE(aligned(dfinal, 16) && aligned(dinit, 16), GDN_EINVAL, "dfinal or dinit is not 16-byte aligned");
-  const LinWs w = linear_ws(dims, N, total_tokens, true);
+  const LinWs w = linear_ws(dims, N, total_tokens, true, in_dtype == GDN_BF16);
   GDN_TRY(check_scan_ws(workspace, workspace_bytes, w.bytes));
   char* const ws = static_cast<char*>(workspace);
   gdn::LinScanArgs a = linear_args(dims, N, cu_seqlens, total_tokens, in_dtype, log_decay, init, slot_map, w);

@@ -217,7 +217,7 @@ struct LinRole {
   int32_t transposed;  // the walk's state [write][in] is the transpose of the one in memory, [dk][dv]
   int32_t out_dt;
   ScanStates init, fin;
-  float* seg;          // [segment slots][H][dk][dv] states at the segments' starts
+  float* seg;          // [N + extras][H][dk][dv] states at the segments' starts
 };
 
 struct LinScanArgs {
@@ -229,8 +229,8 @@ struct LinScanArgs {
   int32_t N, H, in_dt;
   float scale;
   int32_t seg_chunks, whole;  // LinPlan
-  int32_t slots;              // segment slots, or sequences
-  int32_t roles, bunch;       // of the launch; neighbouring heads that read from one
+  int32_t extras;             // slots of the segments behind the sequences' first
+  int32_t roles, bunch, runs; // of the launch; neighbouring heads that read from one; workgroups in runs
 };
 
 // Sums the gradients of the states that share a head.
@@ -300,7 +300,7 @@ hipError_t launch_linear_step(const LinStepArgs& a, int state_dt, int D, hipStre
 struct LinPlan {
   int seg_chunks, whole;
 };
-LinPlan linear_plan(int64_t N, int64_t total, int H, int roles);
+LinPlan linear_plan(int64_t N, int64_t total, int H, int D, bool bf, int roles);
 hipError_t launch_linear_scan(LinScanArgs a, bool bf, int D, int roles, hipStream_t s);
 // The segments' states of role 0 (and role 1 where `both`), then the roles' outputs.
 hipError_t launch_linear_sum(const LinSumArgs& a, hipStream_t s);

@@ -83,6 +83,34 @@ __device__ __forceinline__ u32x2 read_transposed(const uint16_t* p) {
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(const_cast<uint16_t*>(p))));
 }
 
+// Segments behind a sequence's first: segment c > 0 of sequence s has the slot floor(cu[s] / P) + c - 1, distinct for all
+// sequences, since P (ceil(len / P) - 1) < len.  A slot's sequence, if it has one, is the last with floor(cu[s] / P) <= slot.
+__device__ __forceinline__ Piece whole_sequence(const int32_t* cu, int64_t total, int seq) {
+  Piece p;
+  p.seq = seq;
+  p.begin = token_at(cu, seq, total);
+  p.len = max(token_at(cu, seq + 1, total) - p.begin, (int64_t)0);
+  p.index = 0;
+  p.count = 1;
+  return p;
+}
+
+__device__ __forceinline__ Piece find_other_segment(const int32_t* cu, int N, int64_t total, int slot, int P) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = N;  // the answer lies in [lo, hi): s = 0 always qualifies
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) >> 6;
+    const int s = lo + lane * step;
+    const int n = __popcll(__ballot(s < hi && cu[min(s, N)] / P <= slot));
+    const int nlo = lo + (n - 1) * step;  // the condition holds on a prefix, and for lane 0
+    hi = __builtin_amdgcn_readfirstlane(min(hi, nlo + step));
+    lo = __builtin_amdgcn_readfirstlane(nlo);
+  }
+  Piece p = whole_sequence(cu, total, lo);
+  p.index = slot - (int)(p.begin / P) + 1;
+  return p;
+}
+
 template <bool BF, int D, bool OUT>
 __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128 ? 2 : 1)) gdn_linear_walk_kernel(const LinScanArgs a) {
   using W = LinGeom<BF, D, OUT>;
@@ -99,34 +127,34 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
   float* const s_b = s_a + 65;
   float* const s_c = s_b + 128;
 
-  // The roles and the heads that share a tensor's head are neighbours on one XCD (workgroup i of a launch goes to XCD i mod 8).
-  // Whole sequences: each XCD takes a run of them.  Segments: round the XCDs, as the slots behind a sequence that is not cut
-  // have no work.
+  // Places: all sequences' first segments (or the sequences whole), then the other segments.  The roles, and the heads that
+  // share a tensor's head, are neighbours on one XCD (workgroup i of a launch goes to XCD i mod 8).  Where the first segments
+  // are most of the work, each XCD takes a run of them, so that a chunk's heads share its L2; the others, whose places are not
+  // all used, go round the XCDs.
   const int inner = a.bunch * a.roles, groups = a.H / a.bunch;
-  const int at_x = blockIdx.x & 7, at_k = blockIdx.x >> 3;
-  const int u = a.seg_chunks > 0 ? ((at_k / inner) * 8 + at_x) * inner + at_k % inner : xcd_unit(blockIdx.x, gridDim.x);
+  const int runs = a.runs, padded = (runs + 7) & ~7;
+  int u;
+  if ((int)blockIdx.x < padded) {
+    if ((int)blockIdx.x >= runs) return;
+    u = xcd_unit(blockIdx.x, runs);
+  } else {
+    const int i = blockIdx.x - padded, k = i >> 3;
+    u = runs + ((k / inner) * 8 + (i & 7)) * inner + k % inner;
+  }
   const int group = u / inner, in_group = u - group * inner;
-  const int slot = group / groups;
-  if (slot >= a.slots) return;
-  const int h = (group - slot * groups) * a.bunch + in_group / a.roles;
+  const int place = group / groups;
+  if (place >= a.N + a.extras) return;
+  const bool first = place < a.N;
+  const int h = (group - place * groups) * a.bunch + in_group / a.roles;
   const LinRole& ro = a.role[in_group % a.roles];
   int tid = threadIdx.x, l16 = tid & 15, q = tid >> 4 & 3;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool rev = ro.rev;
-  Piece sg;
+  Piece sg = first ? whole_sequence(a.cu, a.total, place) : find_other_segment(a.cu, a.N, a.total, place - a.N, a.seg_chunks * Q);
   if (a.seg_chunks > 0) {
-    sg = find_piece(a.cu, a.N, a.total, slot, a.seg_chunks * Q);
-    if (sg.seq < 0) return;
-    if (sg.count <= a.whole) {  // its first segment's workgroup takes it whole
-      if (sg.index > 0) return;
-      sg.count = 1;
-    }
-  } else {
-    sg.seq = slot;
-    sg.begin = token_at(a.cu, slot, a.total);
-    sg.len = max(token_at(a.cu, slot + 1, a.total) - sg.begin, (int64_t)0);
-    sg.index = 0;
-    sg.count = 1;
+    sg.count = (int)((sg.len + a.seg_chunks * Q - 1) / (a.seg_chunks * Q));
+    if (sg.count <= a.whole) sg.count = 1;  // its first segment's workgroup takes it whole
+    if (sg.index > 0 && sg.index >= sg.count) return;
   }
   const bool last_seg = rev ? sg.index == 0 : sg.index == sg.count - 1;
   if (!OUT && last_seg) return;  // nothing starts from this segment's end
@@ -247,7 +275,7 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
   if (OUT && (sg.count > 1 || ro.init.base != nullptr)) {
     const bool cut = sg.count > 1;
     const void* const base = cut ? ro.seg : ro.init.base;
-    const int64_t unit = cut ? slot : ro.init.slots != nullptr ? ro.init.slots[sg.seq] : sg.seq;
+    const int64_t unit = cut ? place : ro.init.slots != nullptr ? ro.init.slots[sg.seq] : sg.seq;
     const int dt = cut ? (int)GDN_F32 : ro.init.dtype;
     if (dt == GDN_F32) load_as(base, unit, std::integral_constant<int, GDN_F32>{});
     else if (dt == GDN_BF16) load_as(base, unit, std::integral_constant<int, GDN_BF16>{});
@@ -520,7 +548,7 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
 
   if (!OUT || (ro.fin.base != nullptr && last_seg && (rev || sg.len > 0))) {
     void* const base = OUT ? ro.fin.base : ro.seg;
-    const int64_t unit = !OUT ? slot : ro.fin.slots != nullptr ? ro.fin.slots[sg.seq] : sg.seq;
+    const int64_t unit = !OUT ? place : ro.fin.slots != nullptr ? ro.fin.slots[sg.seq] : sg.seq;
     const int dt = OUT ? ro.fin.dtype : (int)GDN_F32;
     if (dt == GDN_F32) store_as(base, unit, std::integral_constant<int, GDN_F32>{});
     else if (dt == GDN_BF16) store_as(base, unit, std::integral_constant<int, GDN_BF16>{});
@@ -549,10 +577,9 @@ __global__ void __launch_bounds__(256) gdn_linear_chain_kernel(const LinScanArgs
   const double g = fmax((double)a.log_decay[h], -1e300) * 1.4426950408889634;
   const float whole = (float)exp2(g * P);
   const float tail = (float)exp2(g * (double)(e - b - (int64_t)(count - 1) * P));  // the sequence's last segment
-  const int64_t s0 = seq + b / P;
   for (int k = 0; k < count; ++k) {
     const int at = ro.rev ? count - 1 - k : k;
-    f32x4* p = reinterpret_cast<f32x4*>(ro.seg + ((s0 + at) * a.H + h) * elems + i);
+    f32x4* p = reinterpret_cast<f32x4*>(ro.seg + ((at == 0 ? seq : a.N + b / P + at - 1) * a.H + h) * elems + i);
     if (k + 1 < count) {
       const f32x4 own = *p;
       *p = S;
@@ -577,14 +604,15 @@ __global__ void __launch_bounds__(256) gdn_linear_sum_kernel(const LinSumArgs a)
 }
 
 template <bool BF, int D, bool OUT>
-hipError_t walk(const LinScanArgs& a, hipStream_t s) {
+hipError_t walk(LinScanArgs a, hipStream_t s) {
   using W = LinGeom<BF, D, OUT>;
+  a.runs = a.seg_chunks > 0 && a.whole == 1 ? 0 : a.N * a.H * a.roles;
   auto* k = gdn_linear_walk_kernel<BF, D, OUT>;
   static std::atomic<uint64_t> allowed{0};
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(k), W::LDS, allowed);
   if (e != hipSuccess) return e;
-  const int64_t inner = a.bunch * a.roles, units = (int64_t)a.slots * a.H * a.roles;
-  k<<<(unsigned)(a.seg_chunks > 0 ? (units + 8 * inner - 1) / (8 * inner) * (8 * inner) : units), W::THREADS, W::LDS, s>>>(a);
+  const int64_t inner = a.bunch * a.roles, all = ((int64_t)a.N + a.extras) * a.H * a.roles;
+  k<<<(unsigned)((a.runs + 7) / 8 * 8 + (all - a.runs + 8 * inner - 1) / (8 * inner) * (8 * inner)), W::THREADS, W::LDS, s>>>(a);
   return hipGetLastError();
 }
 
@@ -596,12 +624,28 @@ hipError_t walk_any(const LinScanArgs& a, bool bf, int D, hipStream_t s) {
 
 }  // namespace
 
-LinPlan linear_plan(int64_t N, int64_t total, int H, int roles) {
+// The host knows how many sequences and tokens there are, not how long each sequence is.  In steps of a chunk, `room`
+// workgroups at a time, sequences of equal lengths take `whole`; cut in segments of `per` chunks, of which ragged ones make a
+// few more, `cut`: a start and end of some three steps among them, and two fifths for the segments' first walk and the chain.
+LinPlan linear_plan(int64_t N, int64_t total, int H, int D, bool bf, int roles) {
   LinPlan p{0, 1};
   const int64_t chunks = (total + Q - 1) / Q, walks = N * H * roles;
-  if (walks < 512 && chunks > 8) {
-    const int64_t per = chunks * H * roles / 1024 + 1;
-    p.seg_chunks = (int)std::max<int64_t>(4, per);
+  if (chunks <= 8) return p;
+  const int64_t room = !bf && D >= 64 ? 224 : 512;
+  const int64_t length = (chunks + N - 1) / N;
+  auto rounds = [&](int64_t w) { return (w + room - 1) / room; };
+  double best = (double)(rounds(walks) * length) * (2 * walks <= room ? 0.65 : 1.0);
+  for (int64_t per = std::max<int64_t>(4, length / 128); per < length; per += per / 32 + 1) {
+    const int64_t segs = std::max(N * ((length + per - 1) / per), (4 * chunks + N * per + 4 * per - 1) / (4 * per));
+    const double cut = (double)(rounds(segs * H * roles) * (per + 3)) * 1.4;
+    if (cut < best) {
+      best = cut;
+      p.seg_chunks = (int)per;
+    }
+  }
+  if (p.seg_chunks == 0 && N > 1 && walks <= 4 * room && chunks >= 2 * N && chunks * H * roles >= 4 * room) {
+    p.seg_chunks = (int)std::max<int64_t>(4, length);
+    p.whole = 2;
   }
   return p;
 }
@@ -609,7 +653,8 @@ LinPlan linear_plan(int64_t N, int64_t total, int H, int roles) {
 // The walks of roles 0 and on; backward, roles 1 and 2 go the same way over the
 // same states, so the segments' first walk and the chain take roles 0 and 1.
 hipError_t launch_linear_scan(LinScanArgs a, bool bf, int D, int roles, hipStream_t s) {
-  a.slots = (int32_t)(a.seg_chunks > 0 ? scan_slots(a.N, a.total, (int64_t)a.seg_chunks * Q) : a.N);
+  a.extras = a.seg_chunks > 0 ? (int32_t)(a.total / (a.seg_chunks * Q)) : 0;
+  if (a.extras == 0) a.seg_chunks = 0;  // no sequence is longer than a segment
   a.bunch = 1;
   for (int i = 0; i < roles; ++i) a.bunch = std::max({a.bunch, a.role[i].read_share, a.role[i].write_share, a.role[i].in_share});
   if (a.seg_chunks > 0) {

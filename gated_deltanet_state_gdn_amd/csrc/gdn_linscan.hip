@@ -71,7 +71,8 @@ struct LinGeom {
 template <bool BF, int D>
 __device__ __forceinline__ int block_at(int t, int c) {
   if constexpr (!BF) return t * (D + 4) + 8 * c;
-  const int f = D == 128 ? (t & 3) << 2 | (t >> 2 & 3) : D == 64 ? (t >> 1 & 1) << 2 | (t >> 2 & 3) : D == 32 ? t >> 2 & 3 : t >> 3 & 1;
+  const int g = ((t >> 2 ^ t >> 3) & 1) << 1 | (t >> 3 & 1);
+  const int f = D == 128 ? (t & 3) << 2 | g : D == 64 ? (t >> 1 & 1) << 2 | g : D == 32 ? g : t >> 3 & 1;
   return t * D + ((c ^ f) << 3);
 }
 
@@ -82,6 +83,9 @@ __device__ __forceinline__ u32x2 read_transposed(const uint16_t* p) {
   typedef __attribute__((address_space(3))) i16x4* Lds;
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(const_cast<uint16_t*>(p))));
 }
+
+// A decay in powers of two; an infinite one is left finite, so that over 0 tokens it is 0.
+__device__ __forceinline__ double log2_of_decay(float g) { return 1.4426950408889634 * (g == -INFINITY ? -1e300 : (double)g); }
 
 // Segments behind a sequence's first: segment c > 0 of sequence s has the slot floor(cu[s] / P) + c - 1, distinct for all
 // sequences, since P (ceil(len / P) - 1) < len.  A slot's sequence, if it has one, is the last with floor(cu[s] / P) <= slot.
@@ -195,8 +199,9 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
   };
   const int steps = c_hi - c_lo;
   const int hr = h / ro.read_share, hw = h / ro.write_share, hx = h / ro.in_share;
-  auto chunk_of = [&](int step) { return rev ? c_hi - 1 - min(step, steps - 1) : c_lo + min(step, steps - 1); };
-  auto fetch = [&](int step) __attribute__((always_inline)) {  // past the last: the last once more, for no one
+  auto chunk_of = [&](int step) { return rev ? c_hi - 1 - step : c_lo + step; };
+  auto fetch = [&](int step) __attribute__((always_inline)) {
+    if (step >= steps) return;
     const int64_t t0 = sg.begin + (int64_t)chunk_of(step) * Q;
     const int len = (int)min((int64_t)Q, sg.begin + sg.len - t0);
     if constexpr (OUT) fetch_one(vr, ro.read, ro.read_ts, t0, hr, len);
@@ -204,6 +209,7 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
     fetch_one(vx, ro.in, ro.in_ts, t0, hx, len);
   };
   auto commit = [&](int step) __attribute__((always_inline)) {
+    if (step >= steps) return;
     E* const w = s_w + (step & 1) * Q * LD;
     E* const x = s_x + (OUT ? 0 : (step & 1) * Q * LD);
     const int st = tid / VPR, sc = tid % VPR;
@@ -215,12 +221,15 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
       *reinterpret_cast<Frag<BF>*>(x + at) = vx[k];
     }
   };
-  if (steps > 0) fetch(0);
+  fetch(0);
 
-  // an infinite decay times 0 tokens is to be 0
-  const double log2_decay = fmax((double)a.log_decay[h], -1e300) * 1.4426950408889634;
+  const double log2_decay = log2_of_decay(a.log_decay[h]);
+  auto power = [&](int m) __attribute__((always_inline)) {  // p[m]: the exponent's whole part apart, so the rest loses nothing
+    const double x = log2_decay * m, n = fmin(fmax(rint(x), -400.0), 400.0);
+    return ldexpf(exp2f((float)(x - n)), (int)n);
+  };
   for (int m = tid - 15; m < 128; m += THREADS) {
-    const float p = (float)exp2(log2_decay * (m >= 0 && m <= Q ? m : 0));
+    const float p = power(m >= 0 && m <= Q ? m : 0);
     if (m <= Q) s_a[m] = m >= 0 ? a.scale * p : 0.f;
     if (m >= 0) {
       const int i = m < Q ? Q - 1 - m : m;
@@ -228,7 +237,7 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
       s_c[i] = m < Q ? a.scale * p : 0.f;
     }
   }
-  const float whole_decay = (float)exp2(log2_decay * Q);
+  const float whole_decay = power(Q);
   if (OUT)  // the products beyond the diagonal that share an operand with one on it stay zero
     for (int i = tid; i < W::TERMS * W::PE; i += THREADS) s_p[i] = 0;
 
@@ -358,6 +367,7 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
     return all ? 32 * W::LDN + ((rt & 1) * 16 + l16) * W::LDF + 32 * ks : ((rt & 1) * 16 + l16) * W::LDN;
   };
   auto products = [&](int step) __attribute__((always_inline)) {
+    if (step >= steps) return;
     const E* const w = s_w + (step & 1) * Q * LD;
     f32x4 acc[TPW];
 #pragma unroll
@@ -574,7 +584,7 @@ __global__ void __launch_bounds__(256) gdn_linear_chain_kernel(const LinScanArgs
     load_vec<4>(ro.init.base, ((ro.init.slots != nullptr ? ro.init.slots[seq] : (int64_t)seq) * a.H + h) * elems + i, ro.init.dtype, f);
     S = f32x4{f[0], f[1], f[2], f[3]};
   }
-  const double g = fmax((double)a.log_decay[h], -1e300) * 1.4426950408889634;
+  const double g = log2_of_decay(a.log_decay[h]);
   const float whole = (float)exp2(g * P);
   const float tail = (float)exp2(g * (double)(e - b - (int64_t)(count - 1) * P));  // the sequence's last segment
   for (int k = 0; k < count; ++k) {

@@ -935,11 +935,14 @@ def gdn_linear_scan(q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, sc
                     workspace=None, stream=None):
     """Linear attention with a fixed decay a head over packed sequences: q [T, Hq, dk]; k [T, Hk, dk]; v [T, Hv, dv];
     log_decay float32 [H], a constant without a gradient; cu_seqlens int32 [N+1] (device); Hq, Hk and Hv divide H.
+    Rows from cu_seqlens[N] on are neither read nor written.
     Tokens may be apart (slices of wider rows; an expanded tensor is copied).  With a pool [slots, H, dk, dv] and slot_map int32 [N],
     sequence s goes on from slot slot_map[s] and leaves its final state there; without, from zero states.  Returns
     o [T, H, dv] in out_dtype (q's by default).  Autograd does not record it: gradients come from
     gdn_linear_scan_backward."""
     _says_no_graph("gdn_linear_scan", q, k, v, pool)
+    if log_decay.requires_grad and _torch().is_grad_enabled():
+        warnings.warn("gdn_linear_scan takes log_decay as a constant: no call gives its gradient", stacklevel=2)
     copies, fresh = [], []
     dims, N, T, args = _linear_scan_args(q, k, v, log_decay, cu_seqlens, pool, slot_map, scale, copies, stream)
     shape = (T, dims.num_heads, dims.dv)
@@ -958,7 +961,8 @@ def gdn_linear_scan(q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, sc
 def gdn_linear_scan_backward(do, q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, dfinal=None, scale=None,
                              workspace=None, stream=None) -> LinearScanGrads:
     """Gradients of gdn_linear_scan for do [T, H, dv] in q's dtype (and dfinal, float32 [N, H, dk, dv], of the final
-    states).  pool and slot_map give the states that the forward call started from, as they were before it."""
+    states).  pool and slot_map give the states that the forward call started from, as they were before it.  Rows from
+    cu_seqlens[N] on are not written."""
     torch = _torch()
     copies = []
     dims, N, T, args = _linear_scan_args(q, k, v, log_decay, cu_seqlens, pool, slot_map, scale, copies, stream)

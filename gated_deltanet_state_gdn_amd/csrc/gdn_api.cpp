@@ -1003,7 +1003,7 @@ gdn_status check_linear_dims(const gdn_linear_dims* d) {
   GDN_REQUIRE(d->dk >= 1 && d->dv >= 1, GDN_EINVAL, "head dims must be >= 1 (dk=%d dv=%d)", d->dk, d->dv);
   GDN_REQUIRE(d->dk == d->dv && (d->dk == 16 || d->dk == 32 || d->dk == 64 || d->dk == 128), GDN_EUNSUPPORTED,
               "head dims dk=%d dv=%d: compiled for dk == dv in {16, 32, 64, 128}", d->dk, d->dv);
-  GDN_REQUIRE(!(d->scale > 0.f) || d->scale <= 3.4028235e38f, GDN_EINVAL, "scale must be finite");
+  GDN_REQUIRE(d->scale <= 3.4028235e38f, GDN_EINVAL, "scale must be finite");  // and not a NaN
   GDN_REQUIRE((int64_t)d->num_heads * d->dk <= kMaxTokenStride, GDN_EUNSUPPORTED, "H dk must be at most 2^22");
   return GDN_OK;
 }
@@ -1040,7 +1040,7 @@ gdn_status check_linear_sizes(const gdn_linear_dims* d, int32_t N, int64_t total
   GDN_REQUIRE(N > 0 || total == 0, GDN_EINVAL, "%lld tokens in no sequence", (long long)total);
   const int64_t extras = std::max(linear_extras(d, N, total, true, roles), linear_extras(d, N, total, false, roles));
   const int64_t items = (N + extras + 16) * d->num_heads * roles * 256;  // threads of the largest launch
-  GDN_REQUIRE(items <= UINT32_MAX, GDN_EUNSUPPORTED,
+  GDN_REQUIRE(items <= UINT32_MAX || (total == 0 && roles == 1), GDN_EUNSUPPORTED,
               "N=%d and total_tokens=%lld make a launch of %lld threads: at most 2^32 - 1 are supported", N, (long long)total, (long long)items);
   if (roles > 1) {
     const int64_t sum = total * d->num_heads * (d->dk / 4);
@@ -1253,8 +1253,8 @@ gdn_status gdn_linear_scan_backward(const gdn_linear_dims* dims, int32_t N, cons
   hipError_t e = gdn::launch_linear_scan(a, in_dtype == GDN_BF16, dims->dk, 3, s);
   for (int i = 0; i < 3 && e == hipSuccess && total_tokens > 0; ++i)
     if (heads[i] != dims->num_heads)
-      e = gdn::launch_linear_sum(gdn::LinSumArgs{reinterpret_cast<const float*>(ws + each[i]), grads[i], total_tokens * heads[i] * (dims->dk / 4),
-                                                 dims->num_heads / heads[i], dims->dk, (int32_t)in_dtype}, s);
+      e = gdn::launch_linear_sum(gdn::LinSumArgs{reinterpret_cast<const float*>(ws + each[i]), grads[i], cu_seqlens, total_tokens * heads[i] * (dims->dk / 4),
+                                                 N, heads[i], dims->num_heads / heads[i], dims->dk, (int32_t)in_dtype}, s);
   return launched(e);
 }
 

@@ -237,8 +237,9 @@ struct LinScanArgs {
 struct LinSumArgs {
   const float* each;  // [T, heads, share, D]
   void* out;          // [T, heads, D]
+  const int32_t* cu;  // [N + 1]
   int64_t items;      // T heads D / 4
-  int32_t share, D, out_dt;
+  int32_t N, heads, share, D, out_dt;
 };
 
 // The norm and rotation of queries (index 0) and keys (1), forward (x to y) or backward (dy and x to y).
@@ -302,7 +303,6 @@ struct LinPlan {
 };
 LinPlan linear_plan(int64_t N, int64_t total, int H, int D, bool bf, int roles);
 hipError_t launch_linear_scan(LinScanArgs a, bool bf, int D, int roles, hipStream_t s);
-// The segments' states of role 0 (and role 1 where `both`), then the roles' outputs.
 hipError_t launch_linear_sum(const LinSumArgs& a, hipStream_t s);
 hipError_t launch_qk(QkArgs a, hipStream_t s);
 hipError_t launch_qk_bwd(QkArgs a, hipStream_t s);

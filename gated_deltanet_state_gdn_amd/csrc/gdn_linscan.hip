@@ -606,6 +606,7 @@ __global__ void __launch_bounds__(256) gdn_linear_sum_kernel(const LinSumArgs a)
   if (i >= a.items) return;
   const int v = a.D / 4;
   const int64_t head = i / v;  // of all tokens
+  if (head / a.heads >= a.cu[a.N]) return;  // behind the last sequence
   const float* p = a.each + head * a.share * a.D + (i - head * v) * 4;
   f32x4 sum = *reinterpret_cast<const f32x4*>(p);
   for (int k = 1; k < a.share; ++k) sum += *reinterpret_cast<const f32x4*>(p + (int64_t)k * a.D);

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kQkThreads) gdn_qk_kernel(const QkArgs a) {
     next.t = row0 / a.heads[0];
     next.h = row0 - next.t * a.heads[0];
     if (row0 < n * a.heads[0]) load(next, 0);  // on its way while the angles are formed
-    if (BWD) __syncthreads();  // the tokens before are done with
+    if (turn_at != blockIdx.x) __syncthreads();  // the tokens before are done with
     for (int i = tid; i < n * half; i += kQkThreads) {
       const int k = i / half, p = i - k * half;
       const int axis = (a.axis[p >> 4] >> (2 * (p & 15))) & 3;
@@ -298,7 +298,7 @@ hipError_t launch_type(const QkArgs& a, dim3 grid, size_t lds, hipStream_t s) {
 hipError_t launch_qk(QkArgs a, hipStream_t s) {
   const int heads = a.heads[0] + a.heads[1], rows = kQkThreads / lanes_of_row(a.d);
   a.tokens = turn_tokens(a.T, heads, a.d, kQkForward);
-  dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens));
+  dim3 grid((unsigned)std::min<int64_t>((a.T + a.tokens - 1) / a.tokens, 1 << 20));
   // few tokens: their heads on several workgroups
   if (a.T < 512) grid.y = (unsigned)std::min((std::max(a.heads[0], a.heads[1]) + rows - 1) / rows, 64);
   return launch_type<false>(a, grid, (size_t)a.tokens * a.rot * 4, s);

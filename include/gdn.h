@@ -525,7 +525,8 @@ gdn_status gdn_linear_decode_step(const gdn_linear_dims* dims, int32_t B, const 
 
 /* N packed variable-length sequences.
  *   cu_seqlens  device int32 [N+1], non-decreasing, cu_seqlens[0] = 0,
- *               cu_seqlens[N] = total_tokens
+ *               cu_seqlens[N] <= total_tokens; rows behind the last sequence are
+ *               neither read nor written (gradients' rows included)
  *   q, k, v     [total_tokens, Hq (Hk, Hv), dk (dk, dv)] in_dtype, 16-byte
  *               aligned; strides NULL: all dense
  *   state       sequence s starts from slot slot_map[s] and its final state is
@@ -533,7 +534,8 @@ gdn_status gdn_linear_decode_step(const gdn_linear_dims* dims, int32_t B, const 
  *               sequence leaves its slot untouched; a slot outside the pool
  *               marks a padded sequence (zero outputs).  NULL (and slot_map
  *               NULL): zero initial states, and none kept
- *   out         [total_tokens, H, dv] out_dtype, dense, 16-byte aligned
+ *   out         [total_tokens, H, dv] out_dtype, dense, 16-byte aligned, apart
+ *               from the inputs
  *   workspace   device scratch of at least the queried size, 256-byte aligned,
  *               not read before it is written; calls that share one must not
  *               overlap
@@ -598,7 +600,8 @@ typedef struct {
  *   positions  device int32 [num_axes, tokens]
  *   inv_freq   device float32 [rotary_dim / 2]
  *   q_out, k_out  shaped and aligned as q and k, in_dtype, with strides of their
- *              own; q_out may be q and k_out k, element for element
+ *              own; q_out may be q and k_out k, element for element, and apart
+ *              from the inputs otherwise
  * tokens == 0 is a no-op. */
 gdn_status gdn_qk_norm_rope(const gdn_qk_dims* dims, const void* q, int64_t q_stride, const void* k,
                             int64_t k_stride, gdn_dtype in_dtype, const float* q_weight,

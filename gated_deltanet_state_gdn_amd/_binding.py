@@ -935,7 +935,7 @@ def gdn_linear_scan(q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, sc
                     workspace=None, stream=None):
     """Linear attention with a fixed decay a head over packed sequences: q [T, Hq, dk]; k [T, Hk, dk]; v [T, Hv, dv];
     log_decay float32 [H], a constant without a gradient; cu_seqlens int32 [N+1] (device); Hq, Hk and Hv divide H.
-    Rows from cu_seqlens[N] on are neither read nor written.
+    Rows in front of cu_seqlens[0] and from cu_seqlens[N] on are neither read nor written.
     Tokens may be apart (slices of wider rows; an expanded tensor is copied).  With a pool [slots, H, dk, dv] and slot_map int32 [N],
     sequence s goes on from slot slot_map[s] and leaves its final state there; without, from zero states.  Returns
     o [T, H, dv] in out_dtype (q's by default).  Autograd does not record it: gradients come from

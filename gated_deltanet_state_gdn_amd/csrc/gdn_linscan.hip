@@ -89,6 +89,7 @@ __device__ __forceinline__ double log2_of_decay(float g) { return 1.442695040888
 
 // Segments behind a sequence's first: segment c > 0 of sequence s has the slot floor(cu[s] / P) + c - 1, distinct for all
 // sequences, since P (ceil(len / P) - 1) < len.  A slot's sequence, if it has one, is the last with floor(cu[s] / P) <= slot.
+// Slots in front of the first sequence come out with an index below 1.
 __device__ __forceinline__ Piece whole_sequence(const int32_t* cu, int64_t total, int seq) {
   Piece p;
   p.seq = seq;
@@ -101,12 +102,12 @@ __device__ __forceinline__ Piece whole_sequence(const int32_t* cu, int64_t total
 
 __device__ __forceinline__ Piece find_other_segment(const int32_t* cu, int N, int64_t total, int slot, int P) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, hi = N;  // the answer lies in [lo, hi): s = 0 always qualifies
+  int lo = 0, hi = N;  // the answer lies in [lo, hi), or is s = 0
   while (hi - lo > 1) {
     const int step = (hi - lo + 63) >> 6;
     const int s = lo + lane * step;
     const int n = __popcll(__ballot(s < hi && cu[min(s, N)] / P <= slot));
-    const int nlo = lo + (n - 1) * step;  // the condition holds on a prefix, and for lane 0
+    const int nlo = lo + max(n - 1, 0) * step;  // the condition holds on a prefix
     hi = __builtin_amdgcn_readfirstlane(min(hi, nlo + step));
     lo = __builtin_amdgcn_readfirstlane(nlo);
   }
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
   if (a.seg_chunks > 0) {
     sg.count = (int)((sg.len + a.seg_chunks * Q - 1) / (a.seg_chunks * Q));
     if (sg.count <= a.whole) sg.count = 1;  // its first segment's workgroup takes it whole
-    if (sg.index > 0 && sg.index >= sg.count) return;
+    if (!first && (sg.index < 1 || sg.index >= sg.count)) return;
   }
   const bool last_seg = rev ? sg.index == 0 : sg.index == sg.count - 1;
   if (!OUT && last_seg) return;  // nothing starts from this segment's end
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(256) gdn_linear_sum_kernel(const LinSumArgs a)
   if (i >= a.items) return;
   const int v = a.D / 4;
   const int64_t head = i / v;  // of all tokens
-  if (head / a.heads >= a.cu[a.N]) return;  // behind the last sequence
+  if (head / a.heads < a.cu[0] || head / a.heads >= a.cu[a.N]) return;  // in no sequence
   const float* p = a.each + head * a.share * a.D + (i - head * v) * 4;
   f32x4 sum = *reinterpret_cast<const f32x4*>(p);
   for (int k = 1; k < a.share; ++k) sum += *reinterpret_cast<const f32x4*>(p + (int64_t)k * a.D);

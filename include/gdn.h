@@ -524,9 +524,10 @@ gdn_status gdn_linear_decode_step(const gdn_linear_dims* dims, int32_t B, const 
                                   gdn_dtype out_dtype, void* stream);
 
 /* N packed variable-length sequences.
- *   cu_seqlens  device int32 [N+1], non-decreasing, cu_seqlens[0] = 0,
- *               cu_seqlens[N] <= total_tokens; rows behind the last sequence are
- *               neither read nor written (gradients' rows included)
+ *   cu_seqlens  device int32 [N+1], non-decreasing, cu_seqlens[0] >= 0,
+ *               cu_seqlens[N] <= total_tokens; rows in front of the first
+ *               sequence and behind the last are neither read nor written
+ *               (gradients' rows included)
  *   q, k, v     [total_tokens, Hq (Hk, Hv), dk (dk, dv)] in_dtype, 16-byte
  *               aligned; strides NULL: all dense
  *   state       sequence s starts from slot slot_map[s] and its final state is

@@ -80,29 +80,31 @@ def test_rotation_past_32_bits():
     assert torch.equal(back.dq[-50:], end.dq) and torch.equal(back.dk[-50:], end.dk)
 
 
+@pytest.mark.parametrize("front", [0, 200])
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_rows_behind_the_last_sequence(dt):
-    """A batch with room behind its last sequence: those rows are not read (they are NaN) and outputs not written."""
+def test_rows_of_no_sequence(dt, front):
+    """A batch with room behind its last sequence and in front of its first: those rows are not read (they are NaN) and outputs
+    not written."""
     import torch
     import gated_deltanet_state_gdn_amd as gdn
     t = torch.bfloat16 if dt == "bf16" else torch.float32
-    T, used = 900, 730
+    T, used = 900 + front, 730 + front
     g = torch.Generator(device=DEV).manual_seed(4)
     q, k, v, do = (torch.randn((T, h, 64), generator=g, device=DEV).to(t) for h in (4, 2, 1, 4))
     for x in (q, k, v, do):
-        x[used:] = float("nan")
-    cu = torch.tensor([0, 700, used], dtype=torch.int32, device=DEV)
+        x[:front] = x[used:] = float("nan")
+    cu = torch.tensor([front, 700 + front, used], dtype=torch.int32, device=DEV)
     out = torch.full((T, 4, 64), 7.0, device=DEV, dtype=t)
     gdn.gdn_linear_scan(q, k, v, slopes(4), cu, out=out)
-    assert (out[used:] == 7).all()
+    assert (out[:front] == 7).all() and (out[used:] == 7).all()
     # the host counts with all rows, so the cuts differ: only the order of FP32 sums
-    cut = lambda x: x[:used].contiguous()  # noqa: E731
-    want = gdn.gdn_linear_scan(cut(q), cut(k), cut(v), slopes(4), cu)
+    cut = lambda x: x[front:used].contiguous()  # noqa: E731
+    want = gdn.gdn_linear_scan(cut(q), cut(k), cut(v), slopes(4), cu - front)
     got = gdn.gdn_linear_scan_backward(do, q, k, v, slopes(4), cu)
-    ref = gdn.gdn_linear_scan_backward(cut(do), cut(q), cut(k), cut(v), slopes(4), cu)
+    ref = gdn.gdn_linear_scan_backward(cut(do), cut(q), cut(k), cut(v), slopes(4), cu - front)
     step = 2.0 ** -7 if dt == "bf16" else 2.0 ** -14
     for a, b in ((out, want), (got.dq, ref.dq), (got.dk, ref.dk), (got.dv, ref.dv)):
-        a, b = a[:used].float(), b.float()
+        a, b = a[front:used].float(), b.float()
         assert ((a - b).abs() <= step * (b.abs() + b.abs().mean())).all()
 
 

@@ -5,8 +5,12 @@
 // A workgroup takes CW columns of a D x D tile (D, or fewer where there are few
 // tiles, as columns never meet): each lane owns VEC neighbouring columns, a
 // wave RPW rows a pass, and the whole part is in flight before any arithmetic.
-// q and k are staged in LDS while it comes.  What bounds it is the state's way
-// from and to memory.
+// q and k are staged in LDS while it comes.
+//
+// What bounds it is the state's way from and to memory: 256 sequences of 32
+// heads of 128 x 128 in FP32 take 195 us, 5.5 TB/s of states read and written
+// where a large copy reaches 4.7.  One sequence of 32 heads is all latency,
+// 3.3 us of which the launch alone is some 2.
 #include "gdn_device.h"
 #include "gdn_launch.h"
 
@@ -112,11 +116,14 @@ template <int SDT, int D>
 hipError_t launch_in(const LinStepArgs& a, hipStream_t s) {
   auto go = [&](auto type) -> hipError_t {
     constexpr int IDT = decltype(type)::value;
-    if constexpr (D >= 64) {
+    // Up to a tile for every second compute unit, parts of rows that are still 128 bytes: 32 FP32 tiles in four parts 3.3 us
+    // and whole 4.4, 128 tiles 4.5 and 5.2, 192 tiles 5.8 and 5.7; 32 BF16 tiles in two parts 3.5 and whole 3.8, 128 tiles 4.2
+    // and 4.4, 192 tiles 5.1 both.  Shorter parts lose (64 x 64 tiles in four parts: 32 tiles 2.6 whole, 3.5).
+    if constexpr (D == 128) {
       int cus = 0;
       const hipError_t e = device_cus(&cus);
       if (e != hipSuccess) return e;
-      if ((int64_t)a.B * a.H < 2 * cus) return launch_part<SDT, D, D / 4, IDT>(a, s);
+      if (2 * (int64_t)a.B * a.H <= cus) return launch_part<SDT, D, SDT == GDN_F32 ? D / 4 : D / 2, IDT>(a, s);
     }
     return launch_part<SDT, D, D, IDT>(a, s);
   };

@@ -266,7 +266,10 @@ int turn_tokens(int64_t T, int heads, int d, int workgroups) {
   const int64_t t = std::min<int64_t>(16, std::max(1, 8 * rows / heads));
   return (int)std::max<int64_t>(1, std::min(t, (T + workgroups - 1) / workgroups));
 }
-constexpr int kQkForward = 4096, kQkBackward = 1024;
+// Forward (4096 tokens of 32 and 8 heads of 128: 19.9 us with 2048 workgroups, 21.3 with 4096, 18.9 with 1024, but 2500 tokens
+// 12.9, 13.7 and 13.7; 16,384 tokens of 64 and 8 heads take 113 with any).  Backward, four a compute unit, which are all there
+// at once (16,384 tokens: 178 us with 1024, 190 with 768, 199 with 1536, 182 with 2048).
+constexpr int kQkForward = 2048, kQkBackward = 1024;
 
 template <int IDT, int LPR, bool BWD>
 hipError_t launch(const QkArgs& a, dim3 grid, size_t lds, hipStream_t s) {
@@ -299,13 +302,14 @@ hipError_t launch_qk(QkArgs a, hipStream_t s) {
   const int heads = a.heads[0] + a.heads[1], rows = kQkThreads / lanes_of_row(a.d);
   a.tokens = turn_tokens(a.T, heads, a.d, kQkForward);
   dim3 grid((unsigned)std::min<int64_t>((a.T + a.tokens - 1) / a.tokens, 1 << 20));
-  // few tokens: their heads on several workgroups
+  // few tokens: their heads on several workgroups (32 and 8 heads of 128: one token 3.4 us and without 3.8, 511 tokens 5.6 and
+  // 6.0, but 1024 tokens 8.5 and 7.8)
   if (a.T < 512) grid.y = (unsigned)std::min((std::max(a.heads[0], a.heads[1]) + rows - 1) / rows, 64);
   return launch_type<false>(a, grid, (size_t)a.tokens * a.rot * 4, s);
 }
 
 // Workgroups of the backward pass, each with a partial sum of the weights'
-// gradients: four a compute unit.
+// gradients.
 int qk_bwd_blocks(int64_t T, int heads, int d) {
   const int t = turn_tokens(T, heads, d, kQkBackward);
   return (int)std::min<int64_t>((T + t - 1) / t, kQkBackward);

@@ -21,19 +21,34 @@
 // of a chunk lie in LDS as they do in memory, row by row; operands that run
 // over tokens are read transposed (the 16-bit transposing LDS reads), so nothing
 // is stored twice.  Blocks of 8 values of a row are permuted by the row's number
-// so that both kinds of reads meet all banks.  The next chunk is fetched into
-// registers under the work on this one.
+// so that both kinds of reads meet all banks (611 cycles of conflicts a chunk of
+// 128 x 128, where rows permuted for 16 lanes in a row had 1257).  The chunk
+// behind the next is fetched into registers, and the next one put into LDS, under
+// the work on this one: two barriers a chunk.  80 KB of LDS, so that two
+// workgroups fit a compute unit.
 //
 // Where there are too few walks for the chip, sequences are cut into segments:
 // a first walk finds each segment's own end state, a small kernel chains them,
 // and the second walk starts every segment from its true state.
 //
+// What bounds it: 16 sequences of 2048 tokens x 32 heads of 128 in BF16 take 320
+// us, 3.4 TB/s of inputs and outputs.  A chunk of two workgroups on a compute
+// unit takes 10 us; its memory traffic alone takes 7.6, its arithmetic alone 8.5
+// (matrix units busy 35% of the time, vector units 43%, LDS 33%), and three
+// waves on two SIMDs do not lay one wholly under the other.  Heads of 64 reach
+// 4.1 TB/s.  In FP32 one workgroup fits a compute unit and the matrix units are
+// busy 47%: 16 x 1024 tokens x 32 heads of 64 take 211 us.  Eight waves of 16
+// columns, in place of four of 32, took 362 us for 324 (the read vectors are
+// then read twice as often); three workgroups a compute unit in the segments'
+// first walk, with one buffer each, gained nothing.
+//
 // Rounding (bf16 inputs and outputs): products of two inputs are exact in FP32.
 // The state is FP32, and its updates take the weighted inputs in three bf16
 // terms, all their 24 bits, with exact write vectors.  For the output alone the
 // state and the weighted products are taken in two bf16 terms, to 2^-16 of each,
-// where the output's own rounding is 2^-9.  Any other types take the FP32 MFMA
-// throughout.
+// where the output's own rounding is 2^-8.  (Updates in two terms take 5% less,
+// and a state that had 24 bits would have 16.)  Any other types take the FP32
+// MFMA throughout.
 #include <algorithm>
 
 #include "gdn_m2scan.h"
@@ -639,6 +654,16 @@ hipError_t walk_any(const LinScanArgs& a, bool bf, int D, hipStream_t s) {
 // The host knows how many sequences and tokens there are, not how long each sequence is.  In steps of a chunk, `room`
 // workgroups at a time, sequences of equal lengths take `whole`; cut in segments of `per` chunks, of which ragged ones make a
 // few more, `cut`: a start and end of some three steps among them, and two fifths for the segments' first walk and the chain.
+// A lone workgroup on a compute unit takes 0.65 of the time that each of two takes.  In FP32 from 64 on one fits, and 224 leave
+// some for what ragged lengths add (256 places filled exactly took 219 to 342 us from call to call, with room 255 to 270).
+// Measured, us whole / cut: forward in heads of 128, 4 x 4096 tokens x 32 heads 325 / 237, prompts of 1024 to 8192 x 32 650 / 270
+// (segments of 23 chunks; of 16 304, of 32 365), 8 x 2048 x 32 182 / 207, so whole; one of 16,384 x 16 heads of 64 697 / 76;
+// backward in heads of 128, 4 x 4096 x 32 497 / 536 and more, one of 16,385 x 16 1466 / 385 (26 chunks; 16: 400); FP32, one of 4099 x 24
+// heads of 64 358 / 83, 4 x 2048 x 16 of 128 498 / 262.
+// What would stay whole by that and has several sequences for the chip's places may hold long ones among short: there segments
+// have the mean length, and a sequence up to two of them long stays whole.  16 sequences of 33 to 8192 tokens x 32 heads of 128 take
+// 672 us whole and 240 so, of 64 364 and 115, 20 of 0 to 1500 80 and 61; equal lengths pay for launches that find nothing to do
+// (16 x 1024 x 32 heads of 64 75 and 80, backward 4 x 4096 x 32 of 128 497 and 511).
 LinPlan linear_plan(int64_t N, int64_t total, int H, int D, bool bf, int roles) {
   LinPlan p{0, 1};
   const int64_t chunks = (total + Q - 1) / Q, walks = N * H * roles;

@@ -14,7 +14,14 @@
 // threads form the tokens' cosines and sines, one pair a thread, in LDS (the
 // angle in FP64, reduced to a quarter turn before it is rounded to FP32), then
 // its rows of lanes go over all heads of these tokens, so that a token's angles
-// are formed once for all its heads.
+// are formed once for all its heads.  A row is fetched under the one before it.
+//
+// What bounds it is memory: 20,408 tokens of 32 and 16 heads of 128 take 95 us,
+// 5.3 TB/s, and back 16,384 of 32 and 32 take 153, 5.3 TB/s, where a large copy
+// reaches 4.7 (vector units are active 75 and 69% of the time).  Four and two
+// rows in flight in place of one took 104 and 177 us (registers, so fewer
+// waves); rows are never kept for a second pass.  Three tokens take 4.5 us, all
+// latency: loads, the angles and the barrier behind them, a row, its store.
 #include <algorithm>
 
 #include "gdn_device.h"

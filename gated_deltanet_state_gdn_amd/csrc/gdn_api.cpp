@@ -1029,8 +1029,8 @@ gdn_status check_linear_io(const gdn_linear_dims* d, const void* q, const void* 
 
 // Segments behind the sequences' first, at most.
 int64_t linear_extras(const gdn_linear_dims* d, int32_t N, int64_t total, bool bf, int roles) {
-  const gdn::LinPlan p = gdn::linear_plan(N, total, d->num_heads, d->dk, bf, roles);
-  return p.seg_chunks > 0 ? total / ((int64_t)p.seg_chunks * 64) : 0;
+  const int chunks = gdn::linear_plan(N, total, d->num_heads, d->dk, bf, roles);
+  return chunks > 0 ? total / ((int64_t)chunks * 64) : 0;
 }
 
 gdn_status check_linear_sizes(const gdn_linear_dims* d, int32_t N, int64_t total, int roles) {
@@ -1052,7 +1052,7 @@ gdn_status check_linear_sizes(const gdn_linear_dims* d, int32_t N, int64_t total
 
 struct LinWs {
   size_t seg[2], each[3], bytes;  // segment states forward and in reverse; every state's own dq, dk and dv where heads are shared
-  gdn::LinPlan plan;
+  int seg_chunks;
 };
 
 // For calls of either kind of types, which may be cut in different ways.
@@ -1061,7 +1061,7 @@ LinWs linear_ws(const gdn_linear_dims* d, int32_t N, int64_t total, bool backwar
   Carve c;
   const size_t H = d->num_heads;
   const int roles = backward ? 3 : 1;
-  w.plan = gdn::linear_plan(N, total, d->num_heads, d->dk, bf, roles);
+  w.seg_chunks = gdn::linear_plan(N, total, d->num_heads, d->dk, bf, roles);
   const int64_t extras = std::max(linear_extras(d, N, total, true, roles), linear_extras(d, N, total, false, roles));
   if (extras > 0) {
     const size_t segs = N + extras;
@@ -1134,8 +1134,7 @@ gdn::LinScanArgs linear_args(const gdn_linear_dims* d, int32_t N, const int32_t*
   a.H = d->num_heads;
   a.in_dt = in_dt;
   a.scale = linear_scale(d);
-  a.seg_chunks = w.plan.seg_chunks;
-  a.whole = w.plan.whole;
+  a.seg_chunks = w.seg_chunks;
   return a;
 }
 

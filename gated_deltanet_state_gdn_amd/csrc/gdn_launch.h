@@ -228,9 +228,9 @@ struct LinScanArgs {
   int64_t live_slots, total;
   int32_t N, H, in_dt;
   float scale;
-  int32_t seg_chunks, whole;  // LinPlan
+  int32_t seg_chunks;         // linear_plan
   int32_t extras;             // slots of the segments behind the sequences' first
-  int32_t roles, bunch, runs; // of the launch; neighbouring heads that read from one; workgroups in runs
+  int32_t roles, bunch;       // of the launch; neighbouring heads that read from one
 };
 
 // Sums the gradients of the states that share a head.
@@ -296,12 +296,8 @@ bool norm_slice_fits(int n);
 int norm_bwd_blocks(int64_t rows, int N, int groups);
 int64_t norm_sum_work_items(int N);  // threads of the kernel that adds dw and db: fewer than 2^32
 hipError_t launch_linear_step(const LinStepArgs& a, int state_dt, int D, hipStream_t s);
-// How a walk is cut: chunks of 64 tokens a segment (0: whole sequences), and the most segments that a sequence may have and
-// stay whole.
-struct LinPlan {
-  int seg_chunks, whole;
-};
-LinPlan linear_plan(int64_t N, int64_t total, int H, int D, bool bf, int roles);
+// How a walk is cut: chunks of 64 tokens a segment (0: whole sequences).
+int linear_plan(int64_t N, int64_t total, int H, int D, bool bf, int roles);
 hipError_t launch_linear_scan(LinScanArgs a, bool bf, int D, int roles, hipStream_t s);
 hipError_t launch_linear_sum(const LinSumArgs& a, hipStream_t s);
 hipError_t launch_qk(QkArgs a, hipStream_t s);

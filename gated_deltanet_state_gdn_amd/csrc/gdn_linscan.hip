@@ -148,18 +148,18 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
   float* const s_c = s_b + 128;
 
   // Places: all sequences' first segments (or the sequences whole), then the other segments.  The roles, and the heads that
-  // share a tensor's head, are neighbours on one XCD (workgroup i of a launch goes to XCD i mod 8).  Where the first segments
-  // are most of the work, each XCD takes a run of them, so that a chunk's heads share its L2; the others, whose places are not
-  // all used, go round the XCDs.
+  // share a tensor's head, are neighbours on one XCD (workgroup i of a launch goes to XCD i mod 8).  Of whole sequences each
+  // XCD takes a run, whose heads' tokens share its L2 (64 x 2048 tokens x 32 heads of 64 520 us, round the XCDs 548; of 128 no
+  // difference).  Segments, whose places are not all used, go round the XCDs.
   const int inner = a.bunch * a.roles, groups = a.H / a.bunch;
-  const int runs = a.runs, padded = (runs + 7) & ~7;
   int u;
-  if ((int)blockIdx.x < padded) {
-    if ((int)blockIdx.x >= runs) return;
-    u = xcd_unit(blockIdx.x, runs);
+  if (a.seg_chunks == 0) {
+    const int units = a.N * a.H * a.roles;
+    if ((int)blockIdx.x >= units) return;
+    u = xcd_unit(blockIdx.x, units);
   } else {
-    const int i = blockIdx.x - padded, k = i >> 3;
-    u = runs + ((k / inner) * 8 + (i & 7)) * inner + k % inner;
+    const int k = blockIdx.x >> 3;
+    u = ((k / inner) * 8 + (blockIdx.x & 7)) * inner + k % inner;
   }
   const int group = u / inner, in_group = u - group * inner;
   const int place = group / groups;
@@ -173,7 +173,6 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
   Piece sg = first ? whole_sequence(a.cu, a.total, place) : find_other_segment(a.cu, a.N, a.total, place - a.N, a.seg_chunks * Q);
   if (a.seg_chunks > 0) {
     sg.count = (int)((sg.len + a.seg_chunks * Q - 1) / (a.seg_chunks * Q));
-    if (sg.count <= a.whole) sg.count = 1;  // its first segment's workgroup takes it whole
     if (!first && (sg.index < 1 || sg.index >= sg.count)) return;
   }
   const bool last_seg = rev ? sg.index == 0 : sg.index == sg.count - 1;
@@ -593,7 +592,7 @@ __global__ void __launch_bounds__(256) gdn_linear_chain_kernel(const LinScanArgs
   const int P = a.seg_chunks * Q;
   const int64_t b = token_at(a.cu, seq, a.total), e = token_at(a.cu, seq + 1, a.total);
   const int count = (int)max((e - b + P - 1) / P, (int64_t)1);
-  if (count <= a.whole) return;
+  if (count <= 1) return;
   f32x4 S = {0.f, 0.f, 0.f, 0.f};
   if (ro.init.base != nullptr) {
     float f[4];
@@ -631,15 +630,14 @@ __global__ void __launch_bounds__(256) gdn_linear_sum_kernel(const LinSumArgs a)
 }
 
 template <bool BF, int D, bool OUT>
-hipError_t walk(LinScanArgs a, hipStream_t s) {
+hipError_t walk(const LinScanArgs& a, hipStream_t s) {
   using W = LinGeom<BF, D, OUT>;
-  a.runs = a.seg_chunks > 0 && a.whole == 1 ? 0 : a.N * a.H * a.roles;
   auto* k = gdn_linear_walk_kernel<BF, D, OUT>;
   static std::atomic<uint64_t> allowed{0};
   const hipError_t e = allow_lds(reinterpret_cast<const void*>(k), W::LDS, allowed);
   if (e != hipSuccess) return e;
-  const int64_t inner = a.bunch * a.roles, all = ((int64_t)a.N + a.extras) * a.H * a.roles;
-  k<<<(unsigned)((a.runs + 7) / 8 * 8 + (all - a.runs + 8 * inner - 1) / (8 * inner) * (8 * inner)), W::THREADS, W::LDS, s>>>(a);
+  const int64_t all = ((int64_t)a.N + a.extras) * a.H * a.roles, ways = 8 * (a.seg_chunks > 0 ? a.bunch * a.roles : 1);
+  k<<<(unsigned)((all + ways - 1) / ways * ways), W::THREADS, W::LDS, s>>>(a);
   return hipGetLastError();
 }
 
@@ -657,34 +655,34 @@ hipError_t walk_any(const LinScanArgs& a, bool bf, int D, hipStream_t s) {
 // A lone workgroup on a compute unit takes 0.65 of the time that each of two takes.  In FP32 from 64 on one fits, and 224 leave
 // some for what ragged lengths add (256 places filled exactly took 219 to 342 us from call to call, with room 255 to 270).
 // Measured, us whole / cut: forward in heads of 128, 4 x 4096 tokens x 32 heads 325 / 237, prompts of 1024 to 8192 x 32 650 / 270
-// (segments of 23 chunks; of 16 304, of 32 365), 8 x 2048 x 32 182 / 207, so whole; one of 16,384 x 16 heads of 64 697 / 76;
-// backward in heads of 128, 4 x 4096 x 32 497 / 536 and more, one of 16,385 x 16 1466 / 385 (26 chunks; 16: 400); FP32, one of 4099 x 24
-// heads of 64 358 / 83, 4 x 2048 x 16 of 128 498 / 262.
-// What would stay whole by that and has several sequences for the chip's places may hold long ones among short: there segments
-// have the mean length, and a sequence up to two of them long stays whole.  16 sequences of 33 to 8192 tokens x 32 heads of 128 take
-// 672 us whole and 240 so, of 64 364 and 115, 20 of 0 to 1500 80 and 61; equal lengths pay for launches that find nothing to do
-// (16 x 1024 x 32 heads of 64 75 and 80, backward 4 x 4096 x 32 of 128 497 and 511).
-LinPlan linear_plan(int64_t N, int64_t total, int H, int D, bool bf, int roles) {
-  LinPlan p{0, 1};
+// (segments of 23 chunks; of 16 304, of 32 365), 8 x 2048 x 32 182 / 207, so whole; one of 16,384 x 16 heads of 64 697 / 76, 4 x 960 x 8
+// 46 / 31; backward in heads of 128, 4 x 4096 x 32 497 / 536 and more, one of 16,385 x 16 1466 / 385 (26 chunks; 16: 400); FP32, one
+// of 4099 x 24 heads of 64 358 / 83, 4 x 2048 x 16 of 128 498 / 262.
+// Several sequences that would stay whole by that may be long ones among short.  They are cut at a quarter above their mean
+// length, which leaves nearly equal ones whole (16 of 905 to 1150 tokens x 32 heads of 64: 87 us, whole 81, at the mean length
+// 115), or at five chunks where the chip is empty.  Whole / so: 16 of 33 to 8192 x 32 heads of 128 672 / 250, 16 of 100 to 2300 x 32 of
+// 128 218 / 212 and of 64 backward x 16 133 / 126, 20 of 0 to 1500 x 32 of 64 75 / 60 and x 8 70 / 36, 6 of 60 to 1600 x 16 76 / 36.
+// Equal lengths pay for two launches that find nothing to do: 20 of 215 tokens x 8 heads 18 / 24, 16 x 1024 x 32 73 / 84, backward
+// 4 x 4096 x 32 of 128 491 / 519.
+int linear_plan(int64_t N, int64_t total, int H, int D, bool bf, int roles) {
+  int seg_chunks = 0;
   const int64_t chunks = (total + Q - 1) / Q, walks = N * H * roles;
-  if (chunks <= 8) return p;
+  if (chunks <= 8) return 0;
   const int64_t room = !bf && D >= 64 ? 224 : 512;
   const int64_t length = (chunks + N - 1) / N;
   auto rounds = [&](int64_t w) { return (w + room - 1) / room; };
   double best = (double)(rounds(walks) * length) * (2 * walks <= room ? 0.65 : 1.0);
   for (int64_t per = std::max<int64_t>(4, length / 128); per < length; per += per / 32 + 1) {
     const int64_t segs = std::max(N * ((length + per - 1) / per), (4 * chunks + N * per + 4 * per - 1) / (4 * per));
-    const double cut = (double)(rounds(segs * H * roles) * (per + 3)) * 1.4;
+    const double cut = rounds(segs * H * roles) * (per + 3.5) * (2 * segs * H * roles <= room ? 0.65 : 1.0) * 1.4;
     if (cut < best) {
       best = cut;
-      p.seg_chunks = (int)per;
+      seg_chunks = (int)per;
     }
   }
-  if (p.seg_chunks == 0 && N > 1 && walks <= 4 * room && chunks >= 2 * N && chunks * H * roles >= 4 * room) {
-    p.seg_chunks = (int)std::max<int64_t>(4, length);
-    p.whole = 2;
-  }
-  return p;
+  if (seg_chunks == 0 && N > 1 && walks <= 4 * room && chunks >= 2 * N)
+    seg_chunks = (int)(4 * walks <= room ? 5 : std::max<int64_t>(5, length + length / 4));
+  return seg_chunks;
 }
 
 // The walks of roles 0 and on; backward, roles 1 and 2 go the same way over the

@@ -109,7 +109,7 @@ def test_rows_of_no_sequence(dt, front):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("H,lens,cuts", [(40, [1500] + [20] * 9 + [0, 700], (0, 1)), (300, [64, 900, 1, 65, 130], (1, 0)),
+@pytest.mark.parametrize("H,lens,cuts", [(40, [1500] + [20] * 9 + [0, 700], (1, 1)), (300, [64, 900, 1, 65, 130], (1, 0)),
                                          (40, [6000] + [20] * 20 + [0, 700], (1, 0)), (32, [6000] + [33] * 7, (1, 1))])
 def test_ragged_batches_in_segments(H, lens, cuts, dt):
     """Batches whose long sequences alone are cut, against one sequence a call."""

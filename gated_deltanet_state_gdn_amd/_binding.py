@@ -935,7 +935,7 @@ def gdn_linear_scan(q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, sc
                     workspace=None, stream=None):
     """Linear attention with a fixed decay a head over packed sequences: q [T, Hq, dk]; k [T, Hk, dk]; v [T, Hv, dv];
     log_decay float32 [H], a constant without a gradient; cu_seqlens int32 [N+1] (device); Hq, Hk and Hv divide H.
-    Rows in front of cu_seqlens[0] and from cu_seqlens[N] on are neither read nor written.
+    Rows in front of cu_seqlens[0] and from cu_seqlens[N] on are neither read nor written: in a new tensor they hold anything.
     Tokens may be apart (slices of wider rows; an expanded tensor is copied).  With a pool [slots, H, dk, dv] and slot_map int32 [N],
     sequence s goes on from slot slot_map[s] and leaves its final state there; without, from zero states.  Returns
     o [T, H, dv] in out_dtype (q's by default).  Autograd does not record it: gradients come from
@@ -961,8 +961,8 @@ def gdn_linear_scan(q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, sc
 def gdn_linear_scan_backward(do, q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, dfinal=None, scale=None,
                              workspace=None, stream=None) -> LinearScanGrads:
     """Gradients of gdn_linear_scan for do [T, H, dv] in q's dtype (and dfinal, float32 [N, H, dk, dv], of the final
-    states).  pool and slot_map give the states that the forward call started from, as they were before it.  Rows from
-    cu_seqlens[N] on are not written."""
+    states).  pool and slot_map give the states that the forward call started from, as they were before it.  Rows of
+    no sequence are not written: clear them before sums over all rows."""
     torch = _torch()
     copies = []
     dims, N, T, args = _linear_scan_args(q, k, v, log_decay, cu_seqlens, pool, slot_map, scale, copies, stream)

@@ -145,3 +145,55 @@ def test_ragged_batches_in_segments(H, lens, cuts, dt):
         close(pool[s], p[0], "f32", f"state of {n}")
         for name, u, w in zip(grads._fields, grads, b):
             close(u[s] if name == "dinit" else u[at], w[0] if name == "dinit" else w, "f32" if name == "dinit" else dt, f"{name} of {n}")
+
+
+def test_two_graphs_of_one_workspace():
+    """A forward and a backward call captured apart, with one workspace, replayed in turn and each twice in a row."""
+    import torch
+    import gated_deltanet_state_gdn_amd as gdn
+    g = torch.Generator(device=DEV).manual_seed(6)
+    T, cu = 2100, torch.tensor([0, 1500, 1600, 2100], dtype=torch.int32, device=DEV)
+    q, k, v, do = (torch.randn((T, h, 64), generator=g, device=DEV).bfloat16() for h in (4, 2, 1, 4))
+    need = [gdn._binding._linear_workspace(back, 4, 4, 2, 1, 64, 3, T) for back in (False, True)]
+    assert all(need)
+    ws = torch.empty(max(need), dtype=torch.uint8, device=DEV)
+    calls = [lambda: [gdn.gdn_linear_scan(q, k, v, slopes(4), cu, workspace=ws)],
+             lambda: list(gdn.gdn_linear_scan_backward(do, q, k, v, slopes(4), cu, workspace=ws)[:3])]
+    want = [[t.clone() for t in f()] for f in calls]
+    graphs, outs = [], []
+    for f in calls:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            f()
+        torch.cuda.current_stream().wait_stream(s)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(f())
+    for turn, i in enumerate((0, 1, 0, 1, 1, 0, 0)):
+        for t in outs[i]:
+            t.fill_(float("nan"))
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i])), turn
+        assert all(torch.equal(a, b) for f, w in zip(calls, want) for a, b in zip(f(), w)), turn
+
+
+def test_expanded_inputs_on_another_stream():
+    """Copies and outputs that the call makes belong to the stream it runs on, also when memory is used again at once."""
+    import torch
+    import gated_deltanet_state_gdn_amd as gdn
+    g = torch.Generator(device=DEV).manual_seed(7)
+    T, cu = 1400, torch.tensor([0, 900, 1400], dtype=torch.int32, device=DEV)
+    row = torch.randn((1, 4, 64), generator=g, device=DEV).bfloat16()
+    q, k, v = (torch.randn((T, 4, 64), generator=g, device=DEV).bfloat16() for _ in range(3))
+    want = gdn.gdn_linear_scan_backward(row.expand(T, 4, 64).contiguous(), q, k, v, slopes(4), cu)
+    decay = slopes(4)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(4):
+        got = gdn.gdn_linear_scan_backward(row.expand(T, 4, 64), q, k, v, decay, cu, stream=s)
+        junk = [torch.full((T, 4, 64), 3.0, device=DEV, dtype=torch.bfloat16) for _ in range(4)]
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
+        del junk

@@ -243,9 +243,11 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
     const double x = log2_decay * m, n = fmin(fmax(rint(x), -400.0), 400.0);
     return ldexpf(exp2f((float)(x - n)), (int)n);
   };
+  // Powers past the sequence's length meet rows of zeros alone, and are zero: where the state grows they may be infinite.
+  const int most = (int)min((int64_t)Q, sg.len);
   for (int m = tid - 15; m < 128; m += THREADS) {
-    const float p = power(m >= 0 && m <= Q ? m : 0);
-    if (m <= Q) s_a[m] = m >= 0 ? a.scale * p : 0.f;
+    const float p = m >= 0 && m <= most ? power(m) : 0.f;
+    if (m <= Q) s_a[m] = a.scale * p;
     if (m >= 0) {
       const int i = m < Q ? Q - 1 - m : m;
       s_b[i] = m < Q ? p : 0.f;

@@ -43,12 +43,14 @@
 // first walk, with one buffer each, gained nothing.
 //
 // Rounding (bf16 inputs and outputs): products of two inputs are exact in FP32.
-// The state is FP32, and its updates take the weighted inputs in three bf16
-// terms, all their 24 bits, with exact write vectors.  For the output alone the
-// state and the weighted products are taken in two bf16 terms, to 2^-16 of each,
-// where the output's own rounding is 2^-8.  (Updates in two terms take 5% less,
-// and a state that had 24 bits would have 16.)  Any other types take the FP32
-// MFMA throughout.
+// The state is FP32.  Wherever the matrix instructions take an FP32 number, that
+// is the weighted inputs of an update, the state and the weighted products that
+// an output reads, they take it in three bf16 terms, all its 24 bits, beside
+// exact inputs.  (Two terms of what outputs read take 7% less for prompts and 11%
+// for gradients, but outputs are then 1.0e-4 of their size from an FP32 scan's,
+// where the order of sums alone leaves 0.3e-4, and sums over shared heads have 16
+// bits.)  The wave that forms a product also splits it, once for the four that
+// read it.  Any other types take the FP32 MFMA throughout.
 #include <algorithm>
 
 #include "gdn_m2scan.h"
@@ -67,15 +69,14 @@ struct LinGeom {
   static constexpr int THREADS = 64 * NW;
   static constexpr int NT = D / 16, KB = (D + 31) / 32;
   static constexpr int LD = BF ? D : D + 4;            // rows of the operands
-  // The weighted products, 16 rows of reading tokens at a time: two blocks of rows meet 32 writing tokens, two meet all 64.
-  static constexpr int LDN = 32 + (BF ? 8 : 4), LDF = Q + (BF ? 8 : 4);
-  static constexpr int TERMS = BF ? 2 : 1, PE = 32 * (LDN + LDF);
+  // The weighted products: ten tiles of 16 x 16, each as 32 cells of 8 writing tokens of one reading token, in three bf16 terms or in
+  // FP32.  Cells are 48 bytes apart, 12 banks, so that 16 of them meet all banks.
+  static constexpr int CELL = 48, TILE = 32 * CELL, PB = OUT ? 10 * TILE : 0;
   static constexpr int TPW = (10 + NW - 1) / NW;       // 16 x 16 tiles of them that a wave forms
   // read vectors, inputs (twice without outputs), write vectors twice, products
-  static constexpr int X0 = OUT ? Q * LD : 0, W0 = X0 + (OUT ? 1 : 2) * Q * LD, P0 = W0 + 2 * Q * LD;
-  static constexpr int ELEMS = P0 + (OUT ? TERMS * PE : 0);
-  static constexpr int TABLE = 80 + 2 * 128;           // floats: 15 zeros, scale p[0..64]; p[63], .., p[0], 64 zeros, and that times scale
-  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + TABLE * 4;
+  static constexpr int X0 = OUT ? Q * LD : 0, W0 = X0 + (OUT ? 1 : 2) * Q * LD, ELEMS = W0 + 2 * Q * LD;
+  static constexpr int TABLE = 64 + 64 + 16 + 68;      // floats: p[63], .., p[0]; scale p[63], .., scale p[0]; zeros; scale p[0..64]
+  static constexpr size_t LDS = (size_t)ELEMS * sizeof(E) + PB + TABLE * 4;
   static constexpr int VPR = D / 8;                    // 8-element vectors of a row
   static constexpr int SV = Q * VPR / THREADS;         // and those that a thread stages of an operand
   static_assert(SV * THREADS == Q * VPR && ELEMS * sizeof(E) % 16 == 0, "whole vectors");
@@ -140,12 +141,12 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
   E* const s_r = reinterpret_cast<E*>(smem);
   E* const s_x = reinterpret_cast<E*>(smem) + W::X0;
   E* const s_w = reinterpret_cast<E*>(smem) + W::W0;  // [2]
-  E* const s_p = reinterpret_cast<E*>(smem) + W::P0;  // [TERMS]
-  // tables: s_a[m] = scale p[m] for m to 64, and zero for -15 <= m < 0; s_b[i] = p[63 - i], and zero for 64 <= i < 128;
-  // s_c = scale s_b
-  float* const s_a = reinterpret_cast<float*>(smem + (size_t)W::ELEMS * sizeof(E)) + 15;
-  float* const s_b = s_a + 65;
-  float* const s_c = s_b + 128;
+  unsigned char* const s_p = smem + (size_t)W::ELEMS * sizeof(E);
+  // tables: s_a[m] = scale p[m] for m to 64, and zero for -16 <= m < 0; s_b[i] = p[63 - i], and numbers that meet zeros alone behind
+  // them; s_c[i] = scale p[63 - i], and zero for 64 <= i < 80
+  float* const s_b = reinterpret_cast<float*>(s_p + W::PB);
+  float* const s_c = s_b + 64;
+  float* const s_a = s_c + 80;
 
   // Places: all sequences' first segments (or the sequences whole), then the other segments.  The roles, and the heads that
   // share a tensor's head, are neighbours on one XCD (workgroup i of a launch goes to XCD i mod 8).  Of whole sequences each
@@ -245,18 +246,15 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
   };
   // Powers past the sequence's length meet rows of zeros alone, and are zero: where the state grows they may be infinite.
   const int most = (int)min((int64_t)Q, sg.len);
-  for (int m = tid - 15; m < 128; m += THREADS) {
+  for (int m = tid - 16; m <= Q; m += THREADS) {
     const float p = m >= 0 && m <= most ? power(m) : 0.f;
-    if (m <= Q) s_a[m] = a.scale * p;
-    if (m >= 0) {
-      const int i = m < Q ? Q - 1 - m : m;
-      s_b[i] = m < Q ? p : 0.f;
-      s_c[i] = m < Q ? a.scale * p : 0.f;
+    s_a[m] = a.scale * p;
+    if (m >= 0 && m < Q) {
+      s_b[Q - 1 - m] = p;
+      s_c[Q - 1 - m] = a.scale * p;
     }
   }
   const float whole_decay = power(Q);
-  if (OUT)  // the products beyond the diagonal that share an operand with one on it stay zero
-    for (int i = tid; i < W::TERMS * W::PE; i += THREADS) s_p[i] = 0;
 
   // The state S[nt][pt][r]: its row (a value of the write vector) is row_of(nt, 4 q + r), its column column_of(pt, l16): eight
   // neighbours of a row or column in a lane's registers, where a head has so many.
@@ -369,20 +367,15 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
 
   // ---- the weighted products: the wave's 16 x 16 tiles on and below the diagonal (above it in reverse).  A lane has four writing
   // tokens of one reading token.  The last tile goes to several waves where the tiles do not go round.
+  // Tiles lie in the order in which they are read (see below), whose rows and columns stand in two bits a tile.
+  const int turn = rev ? 1 : 0;
   int prt[TPW], pct[TPW];
 #pragma unroll
   for (int k = 0; k < TPW; ++k) {
-    const int t = min(wave + k * NW, 9);
-    const int i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, j = t - i * (i + 1) / 2;
-    prt[k] = rev ? j : i;
-    pct[k] = rev ? i : j;
+    const int t = 2 * min(wave + k * NW, 9);
+    prt[k] = (rev ? 0x4143a : 0xfbe94) >> t & 3;  // forward 0 1 1 2 2 3 3 2 3 3, in reverse 2 2 3 0 0 1 1 0 0 1
+    pct[k] = (rev ? 0x53bbe : 0xe9110) >> t & 3;  // forward 0 0 1 0 1 0 1 2 2 3, in reverse 2 3 3 2 3 2 3 0 1 1
   }
-  // where the products of block rt of reading tokens and the half `ks` of the writing ones begin, for the lane's row of the block
-  const int turn = rev ? 1 : 0;
-  auto product_row = [&](int rt, int ks) __attribute__((always_inline)) {
-    const bool all = (rt >> 1) != turn;  // meets all 64 writing tokens, others the 32 of their own half
-    return all ? 32 * W::LDN + ((rt & 1) * 16 + l16) * W::LDF + 32 * ks : ((rt & 1) * 16 + l16) * W::LDN;
-  };
   auto products = [&](int step) __attribute__((always_inline)) {
     if (step >= steps) return;
     const E* const w = s_w + (step & 1) * Q * LD;
@@ -400,15 +393,19 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
       float f[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) f[r] = acc[k][r] * p[r];
-      E* d = s_p + product_row(rt, ct >> 1) + 16 * (ct & 1) + 4 * q;
+      unsigned char* const cell = s_p + min(wave + k * NW, 9) * W::TILE + (16 * (q >> 1) + l16) * W::CELL;
       if constexpr (BF) {
-        const u32x2 high = {pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
-        *reinterpret_cast<u32x2*>(d) = high;
-        bf16_rest(high[0], f[0], f[1]);
-        bf16_rest(high[1], f[2], f[3]);
-        *reinterpret_cast<u32x2*>(d + W::PE) = u32x2{pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const u32x2 term = {pack2<GDN_BF16>(f[0], f[1]), pack2<GDN_BF16>(f[2], f[3])};
+          *reinterpret_cast<u32x2*>(cell + 16 * i + 8 * (q & 1)) = term;
+          if (i < 2) {
+            bf16_rest(term[0], f[0], f[1]);
+            bf16_rest(term[1], f[2], f[3]);
+          }
+        }
       } else {
-        *reinterpret_cast<f32x4*>(d) = f32x4{f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<f32x4*>(cell + 16 * (q & 1)) = f32x4{f[0], f[1], f[2], f[3]};
       }
     }
   };
@@ -443,7 +440,7 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
         for (int rt = 0; rt < 4; ++rt) acc[pt][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        typedef Split<BF, 2> Terms;
+        typedef Split<BF> Terms;
         Frag<BF> rf[4];
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) rf[rt] = row_frag(s_r, rt ^ 2 * turn, kb);
@@ -476,24 +473,33 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
         for (int pt = 0; pt < PT; ++pt) acc[pt][rt] *= f;
       }
       __syncthreads();  // the products are there, and read vectors and inputs done with
-      Frag<BF> pf[W::TERMS][6];  // blocks 0 to 3 with the first half of the writing tokens, 2 and 3 with the second
-#pragma unroll
-      for (int k = W::TERMS - 1; k >= 0; --k)
-#pragma unroll
-        for (int i = 0; i < 6; ++i)
-          pf[k][i] = Frag<BF>::load(s_p + k * W::PE + product_row((i - 2 * (i >= 4)) ^ 2 * turn, (i >= 4) ^ turn) + 8 * q);
       commit(step + 1);
       __builtin_amdgcn_sched_barrier(0);
       fetch(step + 2);
       __builtin_amdgcn_sched_barrier(0);
+      // Blocks 0 to 3 of reading tokens with the first half of the writing ones, 2 and 3 with the second: 12 pairs of a block and 16
+      // writing tokens, of which two lie beyond the diagonal.  They have no tile, and their lanes read zeros.
+      const unsigned char* const at = s_p + (q >> 1) * W::TILE + (16 * (q & 1) + l16) * W::CELL;
+      const unsigned char* const zeros = reinterpret_cast<const unsigned char*>(s_a - 16);
 #pragma unroll
-      for (int k = W::TERMS - 1; k >= 0; --k)
+      for (int i = 0; i < 6; i += 2) {  // two blocks at a time, so that a product never follows the one it adds to
+        const int ks = i >= 4, rt = i - 2 * ks;
+        constexpr int first[6] = {0, 1, 3, 5, 7, 8}, K = Split<BF>::K;
+        Frag<BF> pf[2][K];
 #pragma unroll
-        for (int i = 0; i < 6; ++i) {
-          const int ks = i >= 4, rt = i - 2 * ks;
+        for (int j = 0; j < 2; ++j) {
+          const bool none = i != 2 && (j == 0 ? !rev && q >= 2 : rev && q < 2);
+          const unsigned char* const p = none ? zeros : at + first[i + j] * W::TILE;
 #pragma unroll
-          for (int pt = 0; pt < PT; ++pt) acc[pt][rt] = frag_mma(acc[pt][rt], xf[ks][pt], pf[k][i]);
+          for (int k = 0; k < K; ++k) pf[j][k] = Frag<BF>::load(reinterpret_cast<const E*>(p + 16 * k));
         }
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) acc[pt][rt + j] = frag_mma(acc[pt][rt + j], xf[ks][pt], pf[j][k]);
+      }
       if (BF && ro.out_dt == GDN_BF16) {
         const auto w = window(ro.out, t0 * out_ts + h * D + p0, 2, 2 * ((len - 1) * out_ts + 16 * PT));
         const int off = 2 * (l16 * (int)out_ts + 4 * PT * q);

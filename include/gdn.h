@@ -542,9 +542,8 @@ gdn_status gdn_linear_decode_step(const gdn_linear_dims* dims, int32_t B, const 
  *               not read before it is written; calls that share one must not
  *               overlap
  * bf16 inputs with a bf16 out run on the bf16 matrix instructions (FP32 state
- * and sums; the state and the decay-weighted products of queries and keys meet
- * o in two bf16 terms, to 2^-16 of each, and the gradients are formed alike);
- * any other pair of types runs in FP32 throughout.  Within 64 tokens a NaN or
+ * and sums; FP32 numbers enter products in three bf16 terms, all their 24 bits,
+ * for o and for the gradients); any other pair of types runs in FP32 throughout.  Within 64 tokens a NaN or
  * infinity also reaches earlier tokens of its own sequence. */
 size_t gdn_linear_scan_workspace_bytes(const gdn_linear_dims* dims, int32_t N, int64_t total_tokens);
 gdn_status gdn_linear_scan(const gdn_linear_dims* dims, int32_t N, const int32_t* cu_seqlens,

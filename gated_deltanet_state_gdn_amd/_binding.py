@@ -8,6 +8,7 @@ an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -204,19 +205,31 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _keep_for_stream(tensors, stream):
-    """Buffers this binding allocated on the current stream but hands to a launch on another
-    stream are marked as used there, so the caching allocator does not give their memory to a
-    later allocation on the current stream while the launch may still run."""
-    torch = _torch()
+def _other_stream(stream, device):
+    """The stream that a call runs on, where it is not the device's current one."""
     if stream is None:
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-    if s.cuda_stream == torch.cuda.current_stream().cuda_stream:
-        return
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
+        return None
+    cuda, handle = _torch().cuda, _stream(stream)
+    if handle == cuda.current_stream(device).cuda_stream:
+        return None
+    if isinstance(stream, cuda.Stream):
+        return stream
+    return cuda.ExternalStream(handle, device=device) if handle else cuda.default_stream(device)
+
+
+def _new(like, shape, dtype, stream, result=True):
+    """A tensor for a call on `stream`, from that stream's memory.  The current stream's may be memory that work queued there still
+    uses, which the call would not wait for.  A result is marked as used on the current stream too, where the caller goes on with it,
+    so that it is not given to a later call before that is done; a workspace goes back to its own stream."""
+    other = _other_stream(stream, like.device) if stream is not None else None
+    if other is None:
+        return like.new_empty(shape, dtype=dtype)
+    cuda = _torch().cuda
+    with cuda.stream(other):
+        t = like.new_empty(shape, dtype=dtype)
+    if result:
+        t.record_stream(cuda.current_stream(like.device))
+    return t
 
 
 def _dims(Hk, Hv, dk, dv, scale):
@@ -267,8 +280,7 @@ def gdn_decode_step(q, k, v, a, b, A_log, dt_bias, pool, slot_map, out=None, out
     B, Hk, dk = q.shape
     Hv, dv = v.shape[1], v.shape[2]
     if out is None:
-        out = torch.empty((B, Hv, dv), dtype=out_dtype or torch.float32, device=q.device)
-        _keep_for_stream([out], stream)
+        out = _new(q, (B, Hv, dv), out_dtype or torch.float32, stream)
     dims = _dims(Hk, Hv, dk, dv, scale)
     _check(lib().gdn_decode_step(ctypes.byref(dims), B, _ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype),
                                  ctypes.byref(_gates(a, b, A_log, dt_bias)), ctypes.byref(_pool(pool)),
@@ -284,8 +296,7 @@ def gdn_spec_decode(q, k, v, a, b, A_log, dt_bias, pool, src_slots, dst_slots, o
     B, T, Hk, dk = q.shape
     Hv, dv = v.shape[2], v.shape[3]
     if out is None:
-        out = torch.empty((B, T, Hv, dv), dtype=out_dtype or torch.float32, device=q.device)
-        _keep_for_stream([out], stream)
+        out = _new(q, (B, T, Hv, dv), out_dtype or torch.float32, stream)
     dims = _dims(Hk, Hv, dk, dv, scale)
     _check(lib().gdn_spec_decode(ctypes.byref(dims), B, T, _ptr(q), _ptr(k), _ptr(v), dtype_code(q.dtype),
                                  ctypes.byref(_gates(a, b, A_log, dt_bias)), ctypes.byref(_pool(pool)),
@@ -323,15 +334,10 @@ def gdn_copy_state_blocks(tensors, src_slots, dst_slots, stream=None, table=None
     if len(tensors) == 0 or n == 0:
         return
     if table is None:
-        if stream is None or isinstance(stream, torch.cuda.Stream):
-            # upload on the stream the copy runs on, so the kernel is ordered after it
-            with torch.cuda.stream(stream or torch.cuda.current_stream()):
-                table = make_state_table(tensors, src_slots.device)
-            if stream is not None:
-                table[0].record_stream(stream)
-        else:  # a raw stream handle: finish the upload before enqueueing
+        # uploaded on the stream the copy runs on, from its memory, so the kernel and whoever gets that memory next come behind it
+        other = _other_stream(stream, src_slots.device)
+        with torch.cuda.stream(other) if other is not None else contextlib.nullcontext():
             table = make_state_table(tensors, src_slots.device)
-            torch.cuda.current_stream().synchronize()
     dev_table, P, max_bytes = table
     _check(lib().gdn_copy_state_blocks(_ptr(dev_table), P, max_bytes, _ptr(src_slots), _ptr(dst_slots), n,
                                        _stream(stream)))
@@ -350,12 +356,10 @@ def gdn_chunk_prefill(q, k, v, a, b, A_log, dt_bias, pool, slot_map, cu_seqlens,
     Hv, dv = v.shape[1], v.shape[2]
     N = int(cu_seqlens.shape[0]) - 1
     if out is None:
-        out = torch.empty((T, Hv, dv), dtype=out_dtype or torch.float32, device=q.device)
-        _keep_for_stream([out], stream)
+        out = _new(q, (T, Hv, dv), out_dtype or torch.float32, stream)
     need = gdn_chunk_prefill_workspace_bytes(Hk, Hv, dk, dv, N, T, chunk)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _keep_for_stream([workspace], stream)
+        workspace = _new(q, need, torch.uint8, stream, result=False)
     ws_ptr = _ptr(workspace) if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     dims = _dims(Hk, Hv, dk, dv, scale)
@@ -379,12 +383,10 @@ def gdn_replay_decode(q, k, v, a, b, A_log, dt_bias, ckpt, slot_map, ring: Ring,
     B, T, Hk, dk = q.shape
     Hv, dv = v.shape[2], v.shape[3]
     if out is None:
-        out = torch.empty((B, T, Hv, dv), dtype=out_dtype or torch.float32, device=q.device)
-        _keep_for_stream([out], stream)
+        out = _new(q, (B, T, Hv, dv), out_dtype or torch.float32, stream)
     need = gdn_replay_workspace_bytes(Hk, Hv, dk, dv, B, T)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _keep_for_stream([workspace], stream)
+        workspace = _new(q, need, torch.uint8, stream, result=False)
     ws_ptr = _ptr(workspace) if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     dims = _dims(Hk, Hv, dk, dv, scale)
@@ -484,8 +486,7 @@ def gdn_mamba2_decode_step(x, Bm, Cm, dt, A_log, dt_bias, D, pool, slot_map, out
     B, H, d = x.shape
     G, n = Bm.shape[1], Bm.shape[2]
     if out is None:
-        out = torch.empty((B, H, d), dtype=out_dtype or torch.float32, device=x.device)
-        _keep_for_stream([out], stream)
+        out = _new(x, (B, H, d), out_dtype or torch.float32, stream)
     dims = gdn_m2_dims(H, G, d, n)
     _check(lib().gdn_mamba2_decode_step(ctypes.byref(dims), B, _ptr(x), _ptr(Bm), _ptr(Cm), dtype_code(x.dtype),
                                         ctypes.byref(_m2_params(dt, A_log, dt_bias, D)), ctypes.byref(_pool(pool)),
@@ -500,8 +501,7 @@ def gdn_mamba2_replay_decode(x, Bm, Cm, dt, A_log, dt_bias, D, ckpt, slot_map, r
     B, T, H, d = x.shape
     G, n = Bm.shape[2], Bm.shape[3]
     if out is None:
-        out = torch.empty((B, T, H, d), dtype=out_dtype or torch.float32, device=x.device)
-        _keep_for_stream([out], stream)
+        out = _new(x, (B, T, H, d), out_dtype or torch.float32, stream)
     dims = gdn_m2_dims(H, G, d, n)
     rs = ring.c_struct()
     _check(lib().gdn_mamba2_replay_decode(ctypes.byref(dims), B, T, _ptr(x), _ptr(Bm), _ptr(Cm), dtype_code(x.dtype),
@@ -571,12 +571,9 @@ def _one_row(t):
 
 def _own_rows(t, copies, stream):
     """A copy of an input whose rows are all one, made on the call's stream and kept in `copies` until the launch."""
-    torch = _torch()
-    if stream is None:
+    other = _other_stream(stream, t.device)
+    with _torch().cuda.stream(other) if other is not None else contextlib.nullcontext():
         t = t.contiguous()
-    else:
-        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
-            t = t.contiguous()
     copies.append(t)
     return t.data_ptr(), 0
 
@@ -658,18 +655,14 @@ def gdn_mamba2_scan(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool=None, slo
     _says_no_graph("gdn_mamba2_scan", x, Bm, Cm, dt, A_log, dt_bias, D, pool)
     copies = []
     T, N, dims, args = _scan_args(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, copies, stream)
-    fresh = []
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        fresh.append(out)
+        out = _new(x, x.shape, out_dtype, stream)
     elif out.shape != x.shape:
         raise ValueError(f"out must be {tuple(x.shape)}, not {tuple(out.shape)}")
     if workspace is None:
         need = _scan_workspace(False, dims.num_heads, dims.num_groups, dims.headdim, dims.dstate, N, T)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-            fresh.append(workspace)
-    _keep_for_stream(fresh, stream)
+            workspace = _new(x, need, torch.uint8, stream, result=False)
     _check(lib().gdn_mamba2_scan(*args, _ptr(out), dtype_code(out.dtype), _ptr(workspace) if workspace is not None else None,
                                  workspace.nbytes if workspace is not None else 0,
                                  _on_gpu(stream, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, out, workspace)))
@@ -688,17 +681,14 @@ def gdn_mamba2_scan_backward(dy, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, p
         raise ValueError(f"dy must be {x.dtype} of shape {tuple(x.shape)}, not {dy.dtype} {tuple(dy.shape)}")
     pdy = _own_rows(dy, copies, stream)[0] if not dy.is_contiguous() and _one_row(dy) else _ptr(dy)
     _f32(dfinal, (N, H, d, n), "dfinal")
-    new = lambda shape, t: torch.empty(shape, dtype=t, device=x.device)  # noqa: E731
+    new = lambda shape, t: _new(x, shape, t, stream)  # noqa: E731
     f32 = torch.float32
     grads = M2ScanGrads(new((T, H, d), x.dtype), new((T, G, n), x.dtype), new((T, G, n), x.dtype), new((T, H), x.dtype),
                         new((H,), f32), new((H,), f32), new((H,), f32), new((N, H, d, n), f32) if pool is not None else None)
-    fresh = list(grads)
     if workspace is None:
         need = _scan_workspace(True, H, G, d, n, N, T)
         if need:
-            workspace = new((need,), torch.uint8)
-            fresh.append(workspace)
-    _keep_for_stream(fresh, stream)
+            workspace = _new(x, need, torch.uint8, stream, result=False)
     _check(lib().gdn_mamba2_scan_backward(
         *args, pdy, _ptr(dfinal) if dfinal is not None else None, *(_ptr(t) for t in grads[:7]),
         _ptr(grads.dinit) if pool is not None else None, _ptr(workspace) if workspace is not None else None,
@@ -755,15 +745,12 @@ def gdn_layer_norm(x, weight, bias=None, gate=None, groups=1, eps=1e-5, rms=Fals
     _says_no_graph("gdn_layer_norm", x, weight, bias, gate)
     dims = _norm_dims(x, groups, rms, gate, gate_after)
     _f32(weight, x.shape[1:], "weight"), _f32(bias, x.shape[1:], "bias")
-    fresh, copies = [], []
+    copies = []
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        fresh.append(out)
+        out = _new(x, x.shape, out_dtype, stream)
     mean = rstd = None
     if save_stats:
-        mean, rstd = torch.empty((2, x.shape[0], groups), dtype=torch.float32, device=x.device)
-        fresh += [mean, rstd]
-    _keep_for_stream(fresh, stream)
+        mean, rstd = _new(x, (2, x.shape[0], groups), torch.float32, stream)
     _check(lib().gdn_layer_norm(ctypes.byref(dims), *_rows(x, x.shape, x.dtype, "x", copies, stream),
                                 *_rows(gate, x.shape, x.dtype, "gate", copies, stream), dtype_code(x.dtype), _ptr(weight),
                                 _ptr(bias) if bias is not None else None, float(eps),
@@ -781,16 +768,13 @@ def gdn_layer_norm_backward(dy, x, weight, mean, rstd, bias=None, gate=None, gro
     dims = _norm_dims(x, groups, rms, gate, gate_after)
     _f32(weight, x.shape[1:], "weight"), _f32(bias, x.shape[1:], "bias")
     _f32(mean, (x.shape[0], groups), "mean"), _f32(rstd, (x.shape[0], groups), "rstd")
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dz = torch.empty(x.shape, dtype=x.dtype, device=x.device) if gate is not None else None
-    dw = torch.empty(x.shape[1:], dtype=torch.float32, device=x.device)
-    db = torch.empty_like(dw) if bias is not None else None
-    fresh, copies = [dx, dz, dw, db], []
+    new = lambda shape, t: _new(x, shape, t, stream)  # noqa: E731
+    dx, dz = new(x.shape, x.dtype), new(x.shape, x.dtype) if gate is not None else None
+    dw, db = new(x.shape[1:], torch.float32), new(x.shape[1:], torch.float32) if bias is not None else None
+    copies = []
     need = int(lib().gdn_layer_norm_backward_workspace_bytes(ctypes.byref(dims)))
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        fresh.append(workspace)
-    _keep_for_stream(fresh, stream)
+        workspace = _new(x, need, torch.uint8, stream, result=False)
     _check(lib().gdn_layer_norm_backward(
         ctypes.byref(dims), *_rows(dy, x.shape, x.dtype, "dy", copies, stream), *_rows(x, x.shape, x.dtype, "x", copies, stream),
         *_rows(gate, x.shape, x.dtype, "gate", copies, stream), dtype_code(x.dtype), _ptr(weight),
@@ -887,14 +871,11 @@ def gdn_linear_decode_step(q, k, v, log_decay, pool, slot_map, scale=None, out=N
     copies = []
     dims, B, args = _linear_args(q, k, v, log_decay, scale, copies, stream)
     shape = (B, dims.num_heads, dims.dv)
-    fresh = []
     if out is None:
-        out = q.new_empty(shape, dtype=out_dtype or torch.float32)
-        fresh.append(out)
+        out = _new(q, shape, out_dtype or torch.float32, stream)
     elif out.shape != shape:
         raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
     state, slots = _linear_pool(pool, slot_map, dims, B)
-    _keep_for_stream(fresh + copies, stream)
     with _launch_on(stream, q, k, v, log_decay, pool, slot_map, out) as handle:
         _check(lib().gdn_linear_decode_step(ctypes.byref(dims), B, *args, state, slots, _ptr(out), dtype_code(out.dtype), handle))
     return out
@@ -920,14 +901,13 @@ def _linear_scan_args(q, k, v, log_decay, cu_seqlens, pool, slot_map, scale, cop
     return dims, N, T, [ctypes.byref(dims), N, _ptr(cu_seqlens), T, *args, state, slots]
 
 
-def _linear_scratch(backward, dims, N, T, workspace, device, fresh):
+def _linear_scratch(backward, dims, N, T, workspace, q, stream):
     """(tensor, pointer, bytes) of the workspace given, or of one made for the call."""
     if workspace is None:
         need = _linear_workspace(backward, dims.num_heads, dims.num_q_heads, dims.num_k_heads, dims.num_v_heads, dims.dk, N, T)
         if not need:
             return None, None, 0
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
-        fresh.append(workspace)
+        workspace = _new(q, need, _torch().uint8, stream, result=False)
     return workspace, _ptr(workspace), workspace.nbytes
 
 
@@ -943,16 +923,14 @@ def gdn_linear_scan(q, k, v, log_decay, cu_seqlens, pool=None, slot_map=None, sc
     _says_no_graph("gdn_linear_scan", q, k, v, pool)
     if log_decay.requires_grad and _torch().is_grad_enabled():
         warnings.warn("gdn_linear_scan takes log_decay as a constant: no call gives its gradient", stacklevel=2)
-    copies, fresh = [], []
+    copies = []
     dims, N, T, args = _linear_scan_args(q, k, v, log_decay, cu_seqlens, pool, slot_map, scale, copies, stream)
     shape = (T, dims.num_heads, dims.dv)
     if out is None:
-        out = q.new_empty(shape, dtype=out_dtype)
-        fresh.append(out)
+        out = _new(q, shape, out_dtype, stream)
     elif out.shape != shape:
         raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
-    workspace, pw, nw = _linear_scratch(False, dims, N, T, workspace, q.device, fresh)
-    _keep_for_stream(fresh + copies, stream)
+    workspace, pw, nw = _linear_scratch(False, dims, N, T, workspace, q, stream)
     with _launch_on(stream, q, k, v, log_decay, cu_seqlens, pool, slot_map, out, workspace) as handle:
         _check(lib().gdn_linear_scan(*args, _ptr(out), dtype_code(out.dtype), pw, nw, handle))
     return out
@@ -971,12 +949,10 @@ def gdn_linear_scan_backward(do, q, k, v, log_decay, cu_seqlens, pool=None, slot
         raise ValueError(f"do must be {q.dtype} of shape {(T, H, d)}, not {do.dtype} {tuple(do.shape)}")
     pdo = _own_rows(do, copies, stream)[0] if not do.is_contiguous() and _one_row(do) else _ptr(do)
     _f32(dfinal, (N, H, dims.dk, d), "dfinal")
-    new = lambda shape, t: torch.empty(shape, dtype=t, device=q.device)  # noqa: E731
+    new = lambda shape, t: _new(q, shape, t, stream)  # noqa: E731
     grads = LinearScanGrads(new(q.shape, q.dtype), new(k.shape, q.dtype), new(v.shape, q.dtype),
                             new((N, H, dims.dk, d), torch.float32) if pool is not None else None)
-    fresh = list(grads)
-    workspace, pw, nw = _linear_scratch(True, dims, N, T, workspace, q.device, fresh)
-    _keep_for_stream(fresh + copies, stream)
+    workspace, pw, nw = _linear_scratch(True, dims, N, T, workspace, q, stream)
     with _launch_on(stream, q, do, k, v, log_decay, cu_seqlens, pool, slot_map, dfinal, workspace) as handle:
         _check(lib().gdn_linear_scan_backward(
             *args, pdo, _ptr(dfinal) if dfinal is not None else None, *(_ptr(t) for t in grads[:3]),
@@ -1035,16 +1011,13 @@ def gdn_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, ne
     be apart (slices of wider rows; an expanded tensor is copied).  Returns (q, k) anew, or in q_out and k_out, which may be q and k.
     Autograd does not record it: gradients come from gdn_qk_norm_rope_backward."""
     _says_no_graph("gdn_qk_norm_rope", q, k, q_weight, k_weight)
-    copies, fresh = [], []
+    copies = []
     dims, rows, params = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, neighbours, axes, copies, stream)
     if q_out is None:
-        q_out = q.new_empty(q.shape)
-        fresh.append(q_out)
+        q_out = _new(q, q.shape, None, stream)
     if k_out is None:
-        k_out = k.new_empty(k.shape)
-        fresh.append(k_out)
+        k_out = _new(k, k.shape, None, stream)
     outs = (*_head_rows(q_out, q.shape, q.dtype, "q_out"), *_head_rows(k_out, k.shape, q.dtype, "k_out"))
-    _keep_for_stream(fresh + copies, stream)
     with _launch_on(stream, q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out) as handle:
         _check(lib().gdn_qk_norm_rope(ctypes.byref(dims), *rows, *params, *outs, handle))
     return q_out, k_out
@@ -1058,15 +1031,12 @@ def gdn_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, position
     dims, rows, params = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, neighbours, axes, copies, stream)
     dys = (*_head_rows(dq_out, q.shape, q.dtype, "dq_out", copies, stream),
            *_head_rows(dk_out, k.shape, q.dtype, "dk_out", copies, stream))
-    new = lambda shape, t: torch.empty(shape, dtype=t, device=q.device)  # noqa: E731
+    new = lambda shape, t: _new(q, shape, t, stream)  # noqa: E731
     d = q.shape[2:]
     grads = QkGrads(new(q.shape, q.dtype), new(k.shape, q.dtype), new(d, torch.float32), new(d, torch.float32))
-    fresh = list(grads)
     need = int(lib().gdn_qk_norm_rope_backward_workspace_bytes(ctypes.byref(dims)))
     if workspace is None and need:
-        workspace = new((need,), torch.uint8)
-        fresh.append(workspace)
-    _keep_for_stream(fresh + copies, stream)
+        workspace = _new(q, need, torch.uint8, stream, result=False)
     with _launch_on(stream, q, k, dq_out, dk_out, q_weight, k_weight, positions, inv_freq, workspace) as handle:
         _check(lib().gdn_qk_norm_rope_backward(
             ctypes.byref(dims), *dys, *rows, *params, grads.dq.data_ptr(), 0, grads.dk.data_ptr(), 0, _ptr(grads.dq_weight),

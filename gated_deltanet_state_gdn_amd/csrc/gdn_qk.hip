@@ -12,7 +12,8 @@
 // two, 8 values a lane as two vectors of 4: those of four pairs, so a rotation
 // never leaves its lane.  A workgroup takes a few tokens at a time: first its
 // threads form the tokens' cosines and sines, one pair a thread, in LDS (the
-// angle in FP64, reduced to a quarter turn before it is rounded to FP32), then
+// angle's turns as a sum of two FP64 numbers, reduced to a quarter turn before
+// they are rounded to FP32), then
 // its rows of lanes go over all heads of these tokens, so that a token's angles
 // are formed once for all its heads.  A row is fetched under the one before it.
 //
@@ -55,12 +56,19 @@ __device__ __forceinline__ float lanes_sum(float x) {
   return x;
 }
 
-// cos and sin of p f: turns in FP64, of which the whole and then the quarter
-// ones are dropped exactly; what is left, at most an eighth, is rounded to
-// FP32.
+// cos and sin of p f: turns, of which the whole and then the quarter ones are
+// dropped exactly; what is left, at most an eighth, is rounded to FP32.  The
+// product and 1 / (2 pi) are sums of two FP64 numbers each: single ones would be
+// off by up to 2^-22 radians where p f is 2^31, several steps of a sine.  (No
+// product may be fused with the subtraction behind it here: its rest is added
+// apart.)
 __device__ __forceinline__ void cos_sin(int p, float f, float& c, float& s) {
-  double t = (double)p * (double)f * 0.15915494309189533577;
-  t = 4.0 * (t - rint(t));
+#pragma clang fp contract(off)
+  constexpr double kTurns = 0x1.45f306dc9c883p-3, kTurnsRest = -0x1.6b01ec5417056p-57;  // 1 / (2 pi), and what it leaves
+  const double x = (double)p * (double)f, x_rest = fma((double)p, (double)f, -x);
+  double t = x * kTurns;
+  const double t_rest = fma(x, kTurns, -t) + fma(x_rest, kTurns, x * kTurnsRest);
+  t = 4.0 * ((t - rint(t)) + t_rest);
   const double quarter = rint(t);
   float sr, cr;
   sincospif(0.5f * (float)(t - quarter), &sr, &cr);

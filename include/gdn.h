@@ -584,7 +584,8 @@ gdn_status gdn_linear_scan_backward(const gdn_linear_dims* dims, int32_t N,
  *     (a, b) -> (a cos - b sin, b cos + a sin);
  * the values behind rotary_dim are left as normed.  Pair i is (i, i +
  * rotary_dim / 2), or with `neighbours` (2 i, 2 i + 1).  FP32 math; the angle is
- * formed in FP64, so far positions lose nothing. */
+ * formed to more than FP64's bits before it is reduced, so far positions lose
+ * nothing. */
 typedef struct {
   int64_t tokens;
   int32_t num_q_heads, num_k_heads; /* >= 1 */

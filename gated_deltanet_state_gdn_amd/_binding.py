@@ -1024,8 +1024,9 @@ def gdn_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, ne
 
 
 def gdn_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, neighbours=False,
-                              axes=None, workspace=None, stream=None) -> QkGrads:
-    """Gradients of gdn_qk_norm_rope from those of its results, in q's dtype, and its inputs."""
+                              axes=None, workspace=None, stream=None, dq=None, dk=None) -> QkGrads:
+    """Gradients of gdn_qk_norm_rope from those of its results, in q's dtype, and its inputs.  Those of q and k come anew, or in dq and
+    dk: slices of a joint projection's gradient, or dq_out or q and dk_out or k themselves."""
     torch = _torch()
     copies = []
     dims, rows, params = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, eps, neighbours, axes, copies, stream)
@@ -1033,13 +1034,15 @@ def gdn_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, position
            *_head_rows(dk_out, k.shape, q.dtype, "dk_out", copies, stream))
     new = lambda shape, t: _new(q, shape, t, stream)  # noqa: E731
     d = q.shape[2:]
-    grads = QkGrads(new(q.shape, q.dtype), new(k.shape, q.dtype), new(d, torch.float32), new(d, torch.float32))
+    dq, dk = new(q.shape, q.dtype) if dq is None else dq, new(k.shape, q.dtype) if dk is None else dk
+    outs = (*_head_rows(dq, q.shape, q.dtype, "dq"), *_head_rows(dk, k.shape, q.dtype, "dk"))
+    grads = QkGrads(dq, dk, new(d, torch.float32), new(d, torch.float32))
     need = int(lib().gdn_qk_norm_rope_backward_workspace_bytes(ctypes.byref(dims)))
     if workspace is None and need:
         workspace = _new(q, need, torch.uint8, stream, result=False)
-    with _launch_on(stream, q, k, dq_out, dk_out, q_weight, k_weight, positions, inv_freq, workspace) as handle:
+    with _launch_on(stream, q, k, dq_out, dk_out, q_weight, k_weight, positions, inv_freq, dq, dk, workspace) as handle:
         _check(lib().gdn_qk_norm_rope_backward(
-            ctypes.byref(dims), *dys, *rows, *params, grads.dq.data_ptr(), 0, grads.dk.data_ptr(), 0, _ptr(grads.dq_weight),
+            ctypes.byref(dims), *dys, *rows, *params, *outs, _ptr(grads.dq_weight),
             _ptr(grads.dk_weight), _ptr(workspace) if workspace is not None else None,
             workspace.nbytes if workspace is not None else 0, handle))
     return grads

@@ -553,13 +553,14 @@ def _on_gpu(stream, x, *others):
     return _stream(stream)
 
 
-def _says_no_graph(name, *inputs):
-    """Warns where autograd would be expected to record the call, which it cannot."""
+def _says_no_graph(name, *inputs, instead=None):
+    """Warns where autograd would be expected to record the call, which it cannot, and names what gives gradients."""
     if _torch().is_grad_enabled():
         for t in inputs:
             if t is not None and t.requires_grad:
-                warnings.warn(f"{name} records no gradients: its result has no graph, although an input requires grad.  Call it in a "
-                              f"torch.autograd.Function with {name}_backward, or under torch.no_grad()", stacklevel=3)
+                instead = instead or f"Call it in a torch.autograd.Function with {name}_backward"
+                warnings.warn(f"{name} records no gradients: its result has no graph, although an input requires grad.  {instead}, "
+                              "or under torch.no_grad()", stacklevel=3)
                 return
 
 
@@ -866,8 +867,10 @@ def _linear_pool(pool, slot_map, dims, N):
 def gdn_linear_decode_step(q, k, v, log_decay, pool, slot_map, scale=None, out=None, out_dtype=None, stream=None):
     """One token of linear attention for each of B sequences: S <- e^g S + k v^T, o = scale S^T q.  q [B, Hq, dk];
     k [B, Hk, dk]; v [B, Hv, dv]; log_decay float32 [H]; pool [slots, H, dk, dv]; Hq, Hk and Hv divide H.  Tokens may
-    be apart (slices of wider rows).  Returns o [B, H, dv], float32 by default."""
+    be apart (slices of wider rows).  Returns o [B, H, dv], float32 by default.  There is no gradient of single tokens."""
     torch = _torch()
+    _says_no_graph("gdn_linear_decode_step", q, k, v, log_decay, pool,
+                   instead="Train through gdn_linear_scan and gdn_linear_scan_backward, and call it with detached tensors")
     copies = []
     dims, B, args = _linear_args(q, k, v, log_decay, scale, copies, stream)
     shape = (B, dims.num_heads, dims.dv)

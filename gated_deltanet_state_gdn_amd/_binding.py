@@ -847,8 +847,8 @@ def _linear_args(q, k, v, log_decay, scale, copies, stream):
     pq, sq = _head_rows(q, (T, Hq, dk), dtype, "q", copies, stream)
     pk, sk = _head_rows(k, (T, Hk, dk), dtype, "k", copies, stream)
     pv, sv = _head_rows(v, (T, Hv, dv), dtype, "v", copies, stream)
-    if scale is not None and not 0.0 < scale < float("inf"):
-        raise ValueError(f"scale must be positive and finite, not {scale}")
+    if scale is not None and not 0.0 < ctypes.c_float(scale).value < float("inf"):  # as FP32: zero would stand for dk^-1/2
+        raise ValueError(f"scale must be positive and finite in float32, not {scale}")
     H = int(log_decay.shape[0])
     _f32(log_decay, (H,), "log_decay")
     dims = gdn_linear_dims(H, Hq, Hk, Hv, dk, dv, float(scale) if scale is not None else 0.0)

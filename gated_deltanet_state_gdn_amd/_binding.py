@@ -541,16 +541,34 @@ class M2ScanGrads(NamedTuple):
     dinit: object  # [N, H, d, n], or None without a pool
 
 
-def _on_gpu(stream, x, *others):
-    """The stream's handle for a launch, once all its tensors are known to lie on x's GPU (others may be None): the library
-    takes their addresses as they are."""
-    gpu = x.get_device()
-    if gpu < 0:
-        raise ValueError(f"tensors must lie on a GPU, not on {x.device}")
-    for t in others:
-        if t is not None and t.get_device() != gpu:
-            raise ValueError(f"all tensors must lie on {x.device}, not on {t.device}")
-    return _stream(stream)
+class _launch_on:
+    """The stream's handle for a launch whose tensors all lie on x's GPU (others may be None): the library takes their addresses as they
+    are.  That GPU is made the current one meanwhile."""
+
+    __slots__ = ("stream", "tensors", "guard")
+
+    def __init__(self, stream, *tensors):
+        self.stream, self.tensors, self.guard = stream, tensors, None
+
+    def __enter__(self):
+        torch = _torch()
+        x = self.tensors[0]
+        gpu = x.get_device()
+        if gpu < 0:
+            raise ValueError(f"tensors must lie on a GPU, not on {x.device}")
+        for t in self.tensors:
+            if t is not None and t.get_device() != gpu:
+                raise ValueError(f"all tensors must lie on {x.device}, not on {t.device}")
+        if gpu != torch.cuda.current_device():
+            self.guard = torch.cuda.device(gpu)
+            self.guard.__enter__()
+        if self.stream is None:
+            return torch._C._cuda_getCurrentRawStream(gpu)
+        return _stream(self.stream)
+
+    def __exit__(self, *error):
+        if self.guard is not None:
+            self.guard.__exit__(*error)
 
 
 def _says_no_graph(name, *inputs, instead=None):
@@ -664,9 +682,9 @@ def gdn_mamba2_scan(x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool=None, slo
         need = _scan_workspace(False, dims.num_heads, dims.num_groups, dims.headdim, dims.dstate, N, T)
         if need:
             workspace = _new(x, need, torch.uint8, stream, result=False)
-    _check(lib().gdn_mamba2_scan(*args, _ptr(out), dtype_code(out.dtype), _ptr(workspace) if workspace is not None else None,
-                                 workspace.nbytes if workspace is not None else 0,
-                                 _on_gpu(stream, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, out, workspace)))
+    with _launch_on(stream, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, out, workspace) as handle:
+        _check(lib().gdn_mamba2_scan(*args, _ptr(out), dtype_code(out.dtype), _ptr(workspace) if workspace is not None else None,
+                                     workspace.nbytes if workspace is not None else 0, handle))
     return out
 
 
@@ -690,11 +708,11 @@ def gdn_mamba2_scan_backward(dy, x, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, p
         need = _scan_workspace(True, H, G, d, n, N, T)
         if need:
             workspace = _new(x, need, torch.uint8, stream, result=False)
-    _check(lib().gdn_mamba2_scan_backward(
-        *args, pdy, _ptr(dfinal) if dfinal is not None else None, *(_ptr(t) for t in grads[:7]),
-        _ptr(grads.dinit) if pool is not None else None, _ptr(workspace) if workspace is not None else None,
-        workspace.nbytes if workspace is not None else 0,
-        _on_gpu(stream, x, dy, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, dfinal, workspace)))
+    with _launch_on(stream, x, dy, Bm, Cm, dt, A_log, dt_bias, D, cu_seqlens, pool, slot_map, dfinal, workspace) as handle:
+        _check(lib().gdn_mamba2_scan_backward(
+            *args, pdy, _ptr(dfinal) if dfinal is not None else None, *(_ptr(t) for t in grads[:7]),
+            _ptr(grads.dinit) if pool is not None else None, _ptr(workspace) if workspace is not None else None,
+            workspace.nbytes if workspace is not None else 0, handle))
     return grads
 
 
@@ -752,12 +770,12 @@ def gdn_layer_norm(x, weight, bias=None, gate=None, groups=1, eps=1e-5, rms=Fals
     mean = rstd = None
     if save_stats:
         mean, rstd = _new(x, (2, x.shape[0], groups), torch.float32, stream)
-    _check(lib().gdn_layer_norm(ctypes.byref(dims), *_rows(x, x.shape, x.dtype, "x", copies, stream),
-                                *_rows(gate, x.shape, x.dtype, "gate", copies, stream), dtype_code(x.dtype), _ptr(weight),
-                                _ptr(bias) if bias is not None else None, float(eps),
-                                *_rows(out, x.shape, out.dtype, "out"), dtype_code(out.dtype),
-                                _ptr(mean) if save_stats else None, _ptr(rstd) if save_stats else None,
-                                _on_gpu(stream, x, gate, weight, bias, out)))
+    args = (ctypes.byref(dims), *_rows(x, x.shape, x.dtype, "x", copies, stream), *_rows(gate, x.shape, x.dtype, "gate", copies, stream),
+            dtype_code(x.dtype), _ptr(weight), _ptr(bias) if bias is not None else None, float(eps),
+            *_rows(out, x.shape, out.dtype, "out"), dtype_code(out.dtype), _ptr(mean) if save_stats else None,
+            _ptr(rstd) if save_stats else None)
+    with _launch_on(stream, x, gate, weight, bias, out) as handle:
+        _check(lib().gdn_layer_norm(*args, handle))
     return (out, mean, rstd) if save_stats else out
 
 
@@ -776,47 +794,17 @@ def gdn_layer_norm_backward(dy, x, weight, mean, rstd, bias=None, gate=None, gro
     need = int(lib().gdn_layer_norm_backward_workspace_bytes(ctypes.byref(dims)))
     if workspace is None and need:
         workspace = _new(x, need, torch.uint8, stream, result=False)
-    _check(lib().gdn_layer_norm_backward(
-        ctypes.byref(dims), *_rows(dy, x.shape, x.dtype, "dy", copies, stream), *_rows(x, x.shape, x.dtype, "x", copies, stream),
-        *_rows(gate, x.shape, x.dtype, "gate", copies, stream), dtype_code(x.dtype), _ptr(weight),
-        _ptr(bias) if bias is not None else None, _ptr(mean), _ptr(rstd), *_rows(dx, x.shape, x.dtype, "dx"),
-        *_rows(dz, x.shape, x.dtype, "dgate"), _ptr(dw), _ptr(db) if db is not None else None,
-        _ptr(workspace) if workspace is not None else None,
-        workspace.nbytes if workspace is not None else 0, _on_gpu(stream, x, dy, gate, weight, bias, mean, rstd, workspace)))
+    args = (ctypes.byref(dims), *_rows(dy, x.shape, x.dtype, "dy", copies, stream), *_rows(x, x.shape, x.dtype, "x", copies, stream),
+            *_rows(gate, x.shape, x.dtype, "gate", copies, stream), dtype_code(x.dtype), _ptr(weight),
+            _ptr(bias) if bias is not None else None, _ptr(mean), _ptr(rstd), *_rows(dx, x.shape, x.dtype, "dx"),
+            *_rows(dz, x.shape, x.dtype, "dgate"), _ptr(dw), _ptr(db) if db is not None else None,
+            _ptr(workspace) if workspace is not None else None, workspace.nbytes if workspace is not None else 0)
+    with _launch_on(stream, x, dy, gate, weight, bias, mean, rstd, workspace) as handle:
+        _check(lib().gdn_layer_norm_backward(*args, handle))
     return LayerNormGrads(dx, dw, db, dz)
 
 
 # ------------------------------------------------------------------ linear attention
-class _launch_on:
-    """The stream's handle for a launch whose tensors all lie on x's GPU (others may be None), which is made the current one
-    meanwhile."""
-
-    __slots__ = ("stream", "tensors", "guard")
-
-    def __init__(self, stream, *tensors):
-        self.stream, self.tensors, self.guard = stream, tensors, None
-
-    def __enter__(self):
-        torch = _torch()
-        x = self.tensors[0]
-        gpu = x.get_device()
-        if gpu < 0:
-            raise ValueError(f"tensors must lie on a GPU, not on {x.device}")
-        for t in self.tensors:
-            if t is not None and t.get_device() != gpu:
-                raise ValueError(f"all tensors must lie on {x.device}, not on {t.device}")
-        if gpu != torch.cuda.current_device():
-            self.guard = torch.cuda.device(gpu)
-            self.guard.__enter__()
-        if self.stream is None:
-            return torch._C._cuda_getCurrentRawStream(gpu)
-        return _stream(self.stream)
-
-    def __exit__(self, *error):
-        if self.guard is not None:
-            self.guard.__exit__(*error)
-
-
 def _head_rows(t, shape, dtype, what, copies=None, stream=None):
     """(pointer, token stride) of a tensor [T, heads, d] whose tokens may be apart; an expanded one is copied if `copies` are kept."""
     if t.shape != shape or t.dtype != dtype:

@@ -21,8 +21,8 @@
 // of a chunk lie in LDS as they do in memory, row by row; operands that run
 // over tokens are read transposed (the 16-bit transposing LDS reads), so nothing
 // is stored twice.  Blocks of 8 values of a row are permuted by the row's number
-// so that both kinds of reads meet all banks (611 cycles of conflicts a chunk of
-// 128 x 128, where rows permuted for 16 lanes in a row had 1257).  The chunk
+// so that both kinds of reads meet all banks (464 cycles of conflicts a chunk of
+// 128 x 128; rows permuted for 16 lanes in a row have some 650 more).  The chunk
 // behind the next is fetched into registers, and the next one put into LDS, under
 // the work on this one: two barriers a chunk.  80 KB of LDS, so that two
 // workgroups fit a compute unit.
@@ -31,16 +31,19 @@
 // a first walk finds each segment's own end state, a small kernel chains them,
 // and the second walk starts every segment from its true state.
 //
-// What bounds it: 16 sequences of 2048 tokens x 32 heads of 128 in BF16 take 320
-// us, 3.4 TB/s of inputs and outputs.  A chunk of two workgroups on a compute
-// unit takes 10 us; its memory traffic alone takes 7.6, its arithmetic alone 8.5
-// (matrix units busy 35% of the time, vector units 43%, LDS 33%), and three
-// waves on two SIMDs do not lay one wholly under the other.  Heads of 64 reach
-// 4.1 TB/s.  In FP32 one workgroup fits a compute unit and the matrix units are
-// busy 47%: 16 x 1024 tokens x 32 heads of 64 take 211 us.  Eight waves of 16
-// columns, in place of four of 32, took 362 us for 324 (the read vectors are
-// then read twice as often); three workgroups a compute unit in the segments'
-// first walk, with one buffer each, gained nothing.
+// What bounds it: 16 sequences of 2048 tokens x 32 heads of 128 in BF16 take 318
+// us, 3.4 TB/s of inputs and outputs where a large copy reaches 4.7.  No unit is at
+// its limit (matrix units busy 39% of the time, vector units 45%, LDS 26%): the
+// four waves of a workgroup meet at two barriers a chunk, which takes 10 us, and
+// two workgroups on a compute unit do not lay all loads, splits and products under
+// one another.  That is this schedule's bound, not a floor.  Heads of 64 reach 3.8
+// TB/s (64 x 2048 tokens x 32 heads 572 us).  In FP32 one workgroup fits a compute
+// unit from heads of 64 on and the matrix units are busy 52%: 16 x 1024 tokens x
+// 32 heads of 64 take 202 us, 16 x 2048 x 32 of 128 956.  FP16 runs as FP32, its
+// values widened as they come: 1384 us for those.  Eight waves of 16 columns, in
+// place of four of 32, took 362 us for 324 (the read vectors are then read twice
+// as often); three workgroups a compute unit in the segments' first walk, with
+// one buffer each, gained nothing.
 //
 // Rounding (bf16 inputs and outputs): products of two inputs are exact in FP32.
 // The state is FP32.  Wherever the matrix instructions take an FP32 number, that
@@ -150,8 +153,8 @@ __global__ void __launch_bounds__((LinGeom<BF, D, OUT>::THREADS), (BF || D < 128
 
   // Places: all sequences' first segments (or the sequences whole), then the other segments.  The roles, and the heads that
   // share a tensor's head, are neighbours on one XCD (workgroup i of a launch goes to XCD i mod 8).  Of whole sequences each
-  // XCD takes a run, whose heads' tokens share its L2 (64 x 2048 tokens x 32 heads of 64 520 us, round the XCDs 548; of 128 no
-  // difference).  Segments, whose places are not all used, go round the XCDs.
+  // XCD takes a run, whose heads' tokens share its L2 (256 x 512 tokens x 32 heads of 32 263 us, round the XCDs 332, of 64 498 and
+  // 520; of 128, and 64 x 2048 of 64, no difference).  Segments, whose places are not all used, go round the XCDs.
   const int inner = a.bunch * a.roles, groups = a.H / a.bunch;
   int u;
   if (a.seg_chunks == 0) {
@@ -662,16 +665,20 @@ hipError_t walk_any(const LinScanArgs& a, bool bf, int D, hipStream_t s) {
 // few more, `cut`: a start and end of some three steps among them, and two fifths for the segments' first walk and the chain.
 // A lone workgroup on a compute unit takes 0.65 of the time that each of two takes.  In FP32 from 64 on one fits, and 224 leave
 // some for what ragged lengths add (256 places filled exactly took 219 to 342 us from call to call, with room 255 to 270).
-// Measured, us whole / cut: forward in heads of 128, 4 x 4096 tokens x 32 heads 325 / 237, prompts of 1024 to 8192 x 32 650 / 270
-// (segments of 23 chunks; of 16 304, of 32 365), 8 x 2048 x 32 182 / 207, so whole; one of 16,384 x 16 heads of 64 697 / 76, 4 x 960 x 8
-// 46 / 31; backward in heads of 128, 4 x 4096 x 32 497 / 536 and more, one of 16,385 x 16 1466 / 385 (26 chunks; 16: 400); FP32, one
-// of 4099 x 24 heads of 64 358 / 83, 4 x 2048 x 16 of 128 498 / 262.
+// Measured, us whole / cut: forward in heads of 128, 4 x 4096 tokens x 32 heads 350 / 258, prompts of 1024 to 8192 x 32 660 / 299
+// (segments of 23 chunks; of 16 325, of 32 400), 8 x 2048 x 32 181 / 209, so whole; one of 16,384 x 16 heads of 64 666 / 79, 4 x 960 x 8
+// 44 / 30; backward in heads of 128, 4 x 4096 x 32 523 / 545 and more, one of 16,385 x 16 1483 / 400 (segments of 16: 370); FP32, one
+// of 4099 x 24 heads of 64 345 / 82, 4 x 2048 x 16 of 128 462 / 261.
 // Several sequences that would stay whole by that may be long ones among short.  They are cut at a quarter above their mean
-// length, which leaves nearly equal ones whole (16 of 905 to 1150 tokens x 32 heads of 64: 87 us, whole 81, at the mean length
-// 115), or at five chunks where the chip is empty.  Whole / so: 16 of 33 to 8192 x 32 heads of 128 672 / 250, 16 of 100 to 2300 x 32 of
-// 128 218 / 212 and of 64 backward x 16 133 / 126, 20 of 0 to 1500 x 32 of 64 75 / 60 and x 8 70 / 36, 6 of 60 to 1600 x 16 76 / 36.
-// Equal lengths pay for two launches that find nothing to do: 20 of 215 tokens x 8 heads 18 / 24, 16 x 1024 x 32 73 / 84, backward
-// 4 x 4096 x 32 of 128 491 / 519.
+// length, which leaves nearly equal ones whole (16 of 905 to 1150 tokens x 32 heads of 64: 86 us, whole 77, at the mean length
+// 105), or at five chunks where the chip is empty.  Whole / so: 16 of 33 to 8192 x 32 heads of 128 689 / 301, 16 of 100 to 2300 x 32 of
+// 128 239 / 230 and of 64 backward x 16 136 / 126, 20 of 0 to 1500 x 32 of 64 73 / 56 and x 8 67 / 33, 6 of 60 to 1600 x 16 70 / 35.
+// Equal lengths pay for two launches that find nothing to do: 20 of 215 tokens x 8 heads 18 / 24, 16 x 1024 x 32 of 64 78 / 88, 8 x 2048
+// x 32 of 128 181 / 191, backward 4 x 4096 x 32 of 128 523 / 526.
+// Above four times `room` walks, or below two chunks a sequence, batches stay whole, and a long sequence among many short ones is one
+// walk: forward in 32 heads of 128 one of 8192 tokens with 63 of 200 takes 326 us (whole 705), with 64 of them 704 (394 in segments of
+// 23 chunks), in 8 heads one of 8192 with 64 single tokens 635 (139 in segments of 16); backward one of 16,384 with 20 of 100 822 (whole
+// 3169), with 21 of them 3166 (816 in segments of 26).
 int linear_plan(int64_t N, int64_t total, int H, int D, bool bf, int roles) {
   int seg_chunks = 0;
   const int64_t chunks = (total + Q - 1) / Q, walks = N * H * roles;

@@ -19,7 +19,7 @@
 //
 // What bounds it is memory: 20,408 tokens of 32 and 16 heads of 128 take 95 us,
 // 5.3 TB/s, and back 16,384 of 32 and 32 take 153, 5.3 TB/s, where a large copy
-// reaches 4.7 (vector units are active 75 and 69% of the time).  Four and two
+// reaches 4.7 (vector units are active 77 and 68% of the time).  Four and two
 // rows in flight in place of one took 104 and 177 us (registers, so fewer
 // waves); rows are never kept for a second pass.  Three tokens take 4.5 us, all
 // latency: loads, the angles and the barrier behind them, a row, its store.

@@ -492,8 +492,9 @@ gdn_status gdn_layer_norm_backward(const gdn_norm_dims* dims, const void* dy, in
  * a key (dk) and a value (dv),
  *     S_t = e^{g_h} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
  * log_decay, float32 [H], holds g_h, usually <= 0 (-infinity: no memory; where
- * it is positive the state grows, and e^{g_h n} has to lie in FP32's range for a
- * sequence of n tokens); it is a constant of the layer and has no gradient here.  q, k and v may have fewer
+ * it is positive the state grows, and e^{g_h n}, also times scale, has to lie in
+ * FP32's range for a sequence of n tokens); it is a constant of the layer and has
+ * no gradient here.  q, k and v may have fewer
  * heads than there are states: state h reads query head h / (H / Hq), key head
  * h / (H / Hk) and value head h / (H / Hv).  State pools are
  * [num_slots, H, dk, dv], as those of the gated delta rule, and the three calls

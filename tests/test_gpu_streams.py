@@ -98,3 +98,26 @@ def test_beside_queued_work(name):
         del junk
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(kept, want)), "a result in use was written"
+
+
+@pytest.mark.parametrize("name", ["linear_scan", "linear_scan_backward", "qk", "qk_backward", "norm_backward", "mamba2_scan_backward"])
+def test_captured_on_a_second_stream(name):
+    """A graph whose call runs on a stream beside the capturing one, and joins it: every replay as the eager call."""
+    say(f"captured on a second stream: {name}")
+    call = calls()[name]
+    want = [t.clone() for t in tensors(call())]
+    side = torch.cuda.Stream()
+    call(stream=side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        outs = tensors(call(stream=side))
+        torch.cuda.current_stream().wait_stream(side)
+    for turn in range(4):
+        for t in outs:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), turn
+        assert all(torch.equal(a, b) for a, b in zip(tensors(call()), want)), turn
